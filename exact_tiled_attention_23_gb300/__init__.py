@@ -10,7 +10,9 @@ and only marshal arguments through ctypes.  The torch conveniences on top:
 * ``forward_from_host()`` -- the same for CPU tensors, copies overlapped with
   the computation;
 * ``backward()`` -- dQ, dK, dV by recomputation;
-* ``attention()`` -- a differentiable torch operation (forward + backward).
+* ``attention()`` -- a differentiable torch operation (forward + backward);
+* ``PagedKV`` with ``kv_append()``, ``forward_paged()`` and
+  ``forward_shared_prefix()`` -- generation over a paged key/value cache.
 
 Every step of the computation runs in the library's CUDA kernels; there is no
 other code path, and calling without the built library raises.
@@ -30,7 +32,9 @@ __all__ = ["FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "
            "fa_fwd_splitkv_noalloc", "FA_NOALLOC_SCRATCH_BYTES", "fa_fwd_f16",
            "fa_bwd", "fa_bwd_f16", "fa_bwd_workspace_bytes", "backward", "attention",
            "fa_fwd_from_host", "fa_fwd_from_host_auto_groups", "FA_MAX_HOST_GROUPS", "forward_from_host",
-           "forward", "build"]
+           "forward", "build", "fa_paged_kv", "fa_rows", "fa_kv_append", "fa_fwd_paged",
+           "fa_fwd_paged_workspace_bytes", "fa_fwd_shared_prefix", "fa_fwd_shared_prefix_workspace_bytes",
+           "PagedKV", "kv_append", "forward_paged", "forward_shared_prefix"]
 
 FA_OK = 0
 FA_ERR_INVALID_ARG = 1
@@ -49,6 +53,21 @@ class FAError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = int(status)
         super().__init__(f"{what}: {fa_status_string(status)}")
+
+
+class fa_paged_kv(ctypes.Structure):
+    """A paged key/value cache as the C entry points take it (include/fa.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("stride_slot", ctypes.c_int64), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
+                ("seq_len", ctypes.c_void_p)]
+
+
+class fa_rows(ctypes.Structure):
+    """A strided [B, H, N, D] array as the C entry points take it (include/fa.h)."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -108,6 +127,20 @@ def load():
         lib.fa_fwd_from_host.restype = i32
         lib.fa_fwd_from_host_auto_groups.argtypes = [i32, i32, i32, i32]
         lib.fa_fwd_from_host_auto_groups.restype = i32
+        cache_p, rows_p = ctypes.POINTER(fa_paged_kv), ctypes.POINTER(fa_rows)
+        lib.fa_kv_append.argtypes = [cache_p, rows_p, rows_p, rows_p, rows_p, i32, i32, i32, vp, i32, i32,
+                                     ctypes.c_int64, i32, vp]
+        lib.fa_kv_append.restype = i32
+        lib.fa_fwd_paged.argtypes = [rows_p, cache_p, rows_p, vp, i32, i32, i32, i32, f32, i32, vp,
+                                     ctypes.c_size_t, vp]
+        lib.fa_fwd_paged.restype = i32
+        lib.fa_fwd_paged_workspace_bytes.argtypes = [cache_p, i32, i32, i32]
+        lib.fa_fwd_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_fwd_shared_prefix.argtypes = [rows_p, cache_p, vp, i32, rows_p, vp, i32, i32, i32, i32, f32, i32,
+                                             vp, ctypes.c_size_t, vp]
+        lib.fa_fwd_shared_prefix.restype = i32
+        lib.fa_fwd_shared_prefix_workspace_bytes.argtypes = [cache_p, i32, i32, i32, i32]
+        lib.fa_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
         return lib
 
@@ -190,6 +223,36 @@ def fa_fwd_splitkv_auto_splits(B, H, N, D) -> int:
 
 def fa_fwd_kernel_choice(B, H, N, D) -> int:
     return int(load().fa_fwd_kernel_choice(B, H, N, D))
+
+
+def fa_kv_append(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, interleaved, position_offset, f16,
+                 stream) -> int:
+    """New tokens into a paged cache; `cache` is an fa_paged_kv, K, V, Q and
+    Q_out are fa_rows (Q and Q_out may be None)."""
+    return int(load().fa_kv_append(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, int(rot_dim),
+                                   int(bool(interleaved)), int(position_offset), int(bool(f16)), stream))
+
+
+def fa_fwd_paged(Q, cache, O, LSE, B, Hq, T, causal, scale, f16, workspace, workspace_bytes, stream) -> int:
+    """Forward over a paged cache; Q and O are fa_rows, `cache` an fa_paged_kv."""
+    return int(load().fa_fwd_paged(Q, cache, O, LSE, B, Hq, T, int(bool(causal)), float(scale),
+                                   int(bool(f16)), workspace, int(workspace_bytes), stream))
+
+
+def fa_fwd_paged_workspace_bytes(cache, B, Hq, T) -> int:
+    return int(load().fa_fwd_paged_workspace_bytes(cache, B, Hq, T))
+
+
+def fa_fwd_shared_prefix(Q, cache, prefix_table, prefix_len, O, LSE, B, Hq, T, causal, scale, f16, workspace,
+                         workspace_bytes, stream) -> int:
+    """fa_fwd_paged behind a prefix that all sequences share."""
+    return int(load().fa_fwd_shared_prefix(Q, cache, prefix_table, int(prefix_len), O, LSE, B, Hq, T,
+                                           int(bool(causal)), float(scale), int(bool(f16)), workspace,
+                                           int(workspace_bytes), stream))
+
+
+def fa_fwd_shared_prefix_workspace_bytes(cache, prefix_len, B, Hq, T) -> int:
+    return int(load().fa_fwd_shared_prefix_workspace_bytes(cache, int(prefix_len), B, Hq, T))
 
 
 def fa_status_string(status: int) -> str:
@@ -361,6 +424,210 @@ def backward(q, k, v, o, do, lse, causal: bool = True, scale=None, kv_len=None, 
     if st != FA_OK:
         raise FAError(st, "fa_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------- paged cache
+class PagedKV:
+    """A paged key/value cache: a pool of pages and the pages of each sequence.
+
+    k_cache, v_cache: bf16 or fp16 CUDA tensors [pages, Hkv, page_size, D] of
+    one shape and one set of strides, the last dimension contiguous (a
+    [pages, page_size, Hkv, D] pool is passed as its transpose(1, 2)).
+    block_table: int32 [B, W], the pages of each sequence in order.  seq_len:
+    int32 [B], keys per sequence.  The caller updates the contents of both in
+    place; the object checks the tensors once and keeps them alive.
+    """
+
+    def __init__(self, k_cache, v_cache, block_table, seq_len):
+        import torch
+
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+            raise ValueError("k_cache, v_cache must have one shape [pages, Hkv, page_size, D] and one set of strides")
+        if k_cache.dtype != v_cache.dtype or k_cache.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("k_cache, v_cache must share dtype bfloat16 or float16")
+        if k_cache.stride(3) != 1:
+            raise ValueError("the last dimension of the caches must be contiguous")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2:
+            raise ValueError("block_table must be an int32 tensor [B, W]")
+        B, W = block_table.shape
+        if W > 1 and block_table.stride(1) != 1:
+            raise ValueError("the rows of block_table must be contiguous")
+        if seq_len.dtype != torch.int32 or seq_len.dim() != 1 or seq_len.numel() != B or not seq_len.is_contiguous():
+            raise ValueError("seq_len must be a contiguous int32 tensor with B entries")
+        if not k_cache.is_cuda or any(x.device != k_cache.device for x in (v_cache, block_table, seq_len)):
+            raise ValueError("the caches, block_table and seq_len must be CUDA tensors of one device")
+        self.k_cache, self.v_cache, self.block_table, self.seq_len = k_cache, v_cache, block_table, seq_len
+        pages, Hkv, page_size, D = k_cache.shape
+        self.batch, self.Hkv, self.D, self.dtype, self.device = B, Hkv, D, k_cache.dtype, k_cache.device
+        sp, sh, ss, _ = k_cache.stride()
+        # the stride of a dimension of one entry is never followed
+        self.c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
+                             ss if page_size > 1 else 0, pages, page_size, Hkv, D, block_table.data_ptr(),
+                             block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
+
+
+def _followable(x):
+    """Whether the paged kernels can read `x` through its strides."""
+    s = x.stride()
+    return s[3] == 1 and not ((s[0] | s[1] | s[2]) & 7) and not (x.data_ptr() & 15)
+
+
+def _paged_input(x, what, cache, H, T=None):
+    """fa_rows of a [B, H, T, D] input, and the tensor it points into."""
+    shape = x.shape
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.D or (H is not None and shape[1] != H) or \
+            (T is not None and shape[2] != T):
+        raise ValueError(f"{what} must have shape [B, {H if H is not None else 'Hq'}, T, D] to match the cache")
+    if x.dtype != cache.dtype or x.device != cache.device:
+        raise ValueError(f"{what} must have the cache's dtype and device")
+    if not _followable(x):
+        x = x.clone(memory_format=_contiguous_format())
+    s = x.stride()
+    return fa_rows(x.data_ptr(), s[0], s[1], s[2]), x
+
+
+def _paged_output(out, what, like, cache):
+    """fa_rows of an output like the [B, H, T, D] tensor `like`, and the tensor."""
+    if out is None:
+        out = like.new_empty(like.shape)
+    elif out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError(f"{what} must be a tensor like q")
+    elif not _followable(out):
+        raise ValueError(f"{what} must have a contiguous last dimension, strides that are multiples of 8 and "
+                         "16-byte alignment")
+    s = out.stride()
+    return fa_rows(out.data_ptr(), s[0], s[1], s[2]), out
+
+
+def _contiguous_format():
+    import torch
+    return torch.contiguous_format
+
+
+def _on_stream(fn, device, stream, args):
+    """fn(*args, stream pointer) with `device` current; torch's allocations and
+    copies go to `stream` too when one is given."""
+    import torch
+
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(device):
+            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream or 0, device=device)
+    if stream.device != device:
+        raise ValueError("stream must belong to the cache's device")
+    with torch.cuda.stream(stream):
+        return fn(*args, stream.cuda_stream)
+
+
+def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, position_offset: int = 0,
+              q_out=None, stream=None):
+    """Put the keys and values of T new tokens per sequence into a PagedKV,
+    turned by their positions, and return the queries turned likewise (None
+    without q).
+
+    k, v: [B, Hkv, T, D], q: [B, Hq, T, D], any strides (a [B, T, H, D]
+    projection's transpose(1, 2) is read in place).  cache.seq_len already
+    counts the new tokens.  inv_freq: float32 CUDA tensor of the angles per
+    position, one per pair (2 * numel <= D elements of a head turn), or None
+    for no rotation; pairs are (p, p + numel), or neighbours if interleaved.
+    position_offset: position of a sequence's first key.  Runs asynchronously
+    on `stream` (default: torch's current stream).
+    """
+    return _on_stream(_kv_append, cache.device, stream, (cache, k, v, q, inv_freq, interleaved, position_offset, q_out))
+
+
+def _kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out, stream):
+    import torch
+
+    T = k.shape[2] if k.dim() == 4 else None
+    ck, k = _paged_input(k, "k", cache, cache.Hkv)
+    cv, v = _paged_input(v, "v", cache, cache.Hkv, T)
+    Hq, cq, co = 0, None, None
+    if q is not None:
+        cq, q = _paged_input(q, "q", cache, None, T)
+        Hq = q.shape[1]
+        co, q_out = _paged_output(q_out, "q_out", q, cache)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rot, freq = 0, None
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != cache.device:
+            raise ValueError("inv_freq must be a float32 tensor of one dimension on the cache's device")
+        inv_freq = inv_freq.contiguous()
+        rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
+    st = fa_kv_append(cache.c, ck, cv, cq, co, cache.batch, Hq, T, freq, rot, interleaved, position_offset,
+                      cache.dtype == torch.float16, stream)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv_append")
+    return q_out
+
+
+def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None, return_lse: bool = True,
+                  workspace=None, stream=None):
+    """O, LSE = attention of q [B, Hq, T, D] over a PagedKV.
+
+    Hq is a multiple of the cache's Hkv.  causal: the queries are the last T
+    tokens of their sequences; otherwise each sees all seq_len keys.  Queries
+    that see no key get O = 0 and LSE = -inf.  The other arguments are
+    forward()'s; q may have any strides, and out too (last dimension
+    contiguous).  The workspace (a CUDA tensor of at least
+    fa_fwd_paged_workspace_bytes bytes) is allocated here when not given.
+    """
+    return _on_stream(_forward_paged, cache.device, stream,
+                      (q, cache, None, 0, causal, scale, out, lse, return_lse, workspace))
+
+
+def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool = True, scale=None, out=None,
+                          lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """forward_paged() for sequences that begin with the same prefix_len keys.
+
+    prefix_table: int32 CUDA tensor with the prefix's pages in order (of the
+    same pool); the cache's block_table and seq_len give what follows it.  The
+    prefix is read once for the whole batch.  The workspace takes
+    fa_fwd_shared_prefix_workspace_bytes bytes.
+    """
+    return _on_stream(_forward_paged, cache.device, stream,
+                      (q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace))
+
+
+def _forward_paged(q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace, stream):
+    import torch
+
+    cq, q = _paged_input(q, "q", cache, None)
+    B, Hq, T, D = q.shape
+    if Hq % max(1, cache.Hkv):
+        raise ValueError("the query heads must be a multiple of the cache's key heads")
+    pages = None
+    if prefix_table is not None:
+        if prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or prefix_table.device != cache.device:
+            raise ValueError("prefix_table must be an int32 tensor of one dimension on the cache's device")
+        prefix_len = int(prefix_len)
+        if prefix_len < 0 or prefix_len > prefix_table.numel() * cache.c.page_size:
+            raise ValueError("prefix_len must lie in [0, what prefix_table's pages hold]")
+        prefix_table = prefix_table.contiguous()
+        pages = prefix_table.data_ptr()
+    co, out = _paged_output(out, "out", q, cache)
+    if lse is not None:
+        if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != cache.device or \
+                not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
+    elif return_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    need = fa_fwd_shared_prefix_workspace_bytes(cache.c, prefix_len, B, Hq, T)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, lse.data_ptr() if lse is not None else None,
+                              B, Hq, T, causal, float("nan") if scale is None else float(scale),
+                              cache.dtype == torch.float16, workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), stream)
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_shared_prefix" if prefix_table is not None else "fa_fwd_paged")
+    return (out, lse) if return_lse else out
 
 
 # ------------------------------------------------------------- autograd

@@ -1,0 +1,287 @@
+// fa_paged_api.cu -- the C ABI of the paged-cache operators: argument checks,
+// workspace layout and launches.  Declared in include/fa.h.
+//
+// Every check that can fail runs before any launch, so a rejected call has no
+// side effect.  The library allocates no device memory.
+#include "fa.h"
+#include "fa_internal.h"
+#include "fa_paged.h"
+
+#include <cmath>
+#include <cstdint>
+
+namespace {
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Strides that 16-byte accesses can follow.
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+// A [B, H, T, D] view: a pointer that 16-byte accesses can use, and strides.
+// Outputs may not have two elements at one address.
+bool rows_ok(const fa_rows *r, int B, int H, int T, int D, bool output)
+{
+    if (!r || !r->ptr || !aligned(r->ptr, 16)) return false;
+    if (!stride_ok(r->stride_b) || !stride_ok(r->stride_h) || !stride_ok(r->stride_n)) return false;
+    if (!output) return true;
+    return (B <= 1 || r->stride_b >= D) && (H <= 1 || r->stride_h >= D) && (T <= 1 || r->stride_n >= D);
+}
+
+fa_status check_cache(const fa_paged_kv *c, int B)
+{
+    if (!c) return FA_ERR_INVALID_ARG;
+    if (c->D <= 0 || c->Hkv <= 0 || c->num_pages < 0 || c->page_size <= 0 || c->table_width < 0) return FA_ERR_INVALID_ARG;
+    if (c->D % 8 != 0 || (c->D > 128 && c->D != 256)) return FA_ERR_UNSUPPORTED;
+    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID_ARG;
+    if (!stride_ok(c->stride_page) || !stride_ok(c->stride_head) || !stride_ok(c->stride_slot)) return FA_ERR_INVALID_ARG;
+    if ((c->num_pages > 1 && c->stride_page < c->D) || (c->Hkv > 1 && c->stride_head < c->D) ||
+        (c->page_size > 1 && c->stride_slot < c->D))
+        return FA_ERR_INVALID_ARG;
+    if (!c->seq_len || !aligned(c->seq_len, 4)) return FA_ERR_INVALID_ARG;
+    if (c->table_width > 0 && (!c->table || !aligned(c->table, 4))) return FA_ERR_INVALID_ARG;
+    if (B > 1 && c->table_stride < c->table_width) return FA_ERR_INVALID_ARG;
+    // positions inside a sequence are 32-bit numbers
+    if ((int64_t)c->table_width * c->page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+fa::PagedCache cache_of(const fa_paged_kv &c)
+{
+    fa::PagedCache r{};
+    r.k = static_cast<uint16_t *>(c.k);
+    r.v = static_cast<uint16_t *>(c.v);
+    r.s_page = c.stride_page;
+    r.s_head = c.stride_head;
+    r.s_slot = c.stride_slot;
+    r.table = c.table;
+    r.table_stride = c.table_stride;
+    r.table_width = c.table_width;
+    r.seq_len = c.seq_len;
+    r.num_pages = c.num_pages;
+    r.page_size = c.page_size;
+    r.Hkv = c.Hkv;
+    r.D = c.D;
+    return r;
+}
+
+void strides_of(int64_t (&s)[3], const fa_rows &r)
+{
+    s[0] = r.stride_b;
+    s[1] = r.stride_h;
+    s[2] = r.stride_n;
+}
+
+int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        sms = 148;
+    return sms;
+}
+
+size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// How one part of a call (the sequences' own keys, or a shared prefix) is cut
+// into tiles, and its piece of the workspace.
+struct Plan {
+    fa::Partials part{};
+    int64_t items = 0;      // tiles in all
+    int64_t ctas = 0;
+    size_t bytes = 0;
+    bool ok = true;
+
+    // rows: stacked query rows per (sequence, key head); keys: most keys of a sequence
+    Plan(int nseq, int Hkv, int64_t rows, int64_t keys, int D, bool stacked)
+    {
+        part.rows = fa::paged_rows_per_tile(D, rows);
+        const int64_t tiles = (rows + part.rows - 1) / part.rows;
+        items = (int64_t)nseq * Hkv * tiles;
+        if (rows > INT32_MAX / 2 || (int64_t)Hkv * tiles > INT32_MAX || items > INT32_MAX) {
+            ok = false;
+            return;
+        }
+        part.tiles = (int)tiles;
+        part.stacked = stacked;
+        part.fixed_len = stacked ? (int)keys : 0;
+        const int64_t chunks = items * ((keys + fa::kChunkKeys - 1) / fa::kChunkKeys);
+        ctas = (int64_t)sm_count() * fa::paged_rows_ctas_per_sm(D);
+        if (ctas > chunks) ctas = chunks > 0 ? chunks : 1;
+        const size_t slots = (size_t)(ctas + items);
+        bytes = 256 + round_up((size_t)items * 8) + round_up(slots * part.rows * 4) + round_up(slots * part.rows * D * 4);
+    }
+
+    // Places the piece at `at`; returns its end.
+    uint8_t *place(uint8_t *at, int D)
+    {
+        const size_t slots = (size_t)(ctas + items);
+        part.per_cta = reinterpret_cast<int64_t *>(at);
+        at += 256;
+        part.first_chunk = reinterpret_cast<int64_t *>(at);
+        at += round_up((size_t)items * 8);
+        part.lse = reinterpret_cast<float *>(at);
+        at += round_up(slots * part.rows * 4);
+        part.o = reinterpret_cast<float *>(at);
+        return at + round_up(slots * part.rows * D * 4);
+    }
+};
+
+// Sizes of a paged forward; `keys` is what a table row can hold.
+fa_status check_sizes(const fa_paged_kv *c, int B, int Hq, int T)
+{
+    if (B < 0 || Hq < 0 || T < 0) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_cache(c, B);
+    if (st != FA_OK) return st;
+    if (Hq % c->Hkv != 0) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * Hq > INT32_MAX || (int64_t)B * Hq * T > (int64_t)1 << 32) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_table, int prefix_len, const fa_rows *O,
+              float *LSE, int B, int Hq, int T, int causal, float scale, int f16, void *workspace,
+              size_t workspace_bytes, void *stream)
+{
+    fa_status st = check_sizes(c, B, Hq, T);
+    if (st != FA_OK) return st;
+    if (prefix_len < 0) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * Hq * T == 0) return FA_OK;
+    const int D = c->D;
+    if (!rows_ok(Q, B, Hq, T, D, false) || !rows_ok(O, B, Hq, T, D, true)) return FA_ERR_INVALID_ARG;
+    if (LSE && !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
+    if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4))) return FA_ERR_INVALID_ARG;
+    const int64_t own_keys = (int64_t)c->table_width * c->page_size;
+    if (own_keys + prefix_len > INT32_MAX) return FA_ERR_INVALID_ARG;
+    const int G = Hq / c->Hkv;
+    Plan own(B, c->Hkv, (int64_t)G * T, own_keys, D, false);
+    Plan front(1, c->Hkv, (int64_t)G * T * B, prefix_len, D, true);
+    if (!own.ok || (prefix_len > 0 && !front.ok)) return FA_ERR_INVALID_ARG;
+    const size_t need = own.bytes + (prefix_len > 0 ? front.bytes : 0);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    uint8_t *end = own.place(static_cast<uint8_t *>(workspace), D);
+    if (prefix_len > 0) front.place(end, D);
+
+    fa::PagedParams p{};
+    p.c = cache_of(*c);
+    p.q = static_cast<const uint16_t *>(Q->ptr);
+    strides_of(p.q_s, *Q);
+    p.o = static_cast<uint16_t *>(O->ptr);
+    strides_of(p.o_s, *O);
+    p.lse = LSE;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.G = G;
+    p.causal = causal ? 1 : 0;
+    p.f16 = f16 ? 1 : 0;
+    const bool given = scale > 0.f && !std::isinf(scale);
+    p.scale_log2 = (given ? scale : 1.0f / std::sqrt((float)D)) * 1.4426950408889634f;
+    p.joined = prefix_len > 0;
+
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    fa::MergeParams m{};
+    if (prefix_len > 0) {
+        fa::PagedParams f = p;
+        f.part = front.part;
+        f.c.table = prefix_table;
+        f.c.table_width = (int)((prefix_len + (int64_t)c->page_size - 1) / c->page_size);
+        f.c.table_stride = 0;
+        f.c.seq_len = nullptr;
+        f.c.fixed_len = prefix_len;
+        if (fa::launch_paged_rows(f, (int)front.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
+        m.src[m.n_src++] = front.part;
+    }
+    p.part = own.part;
+    if (fa::launch_paged_rows(p, (int)own.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
+    m.src[m.n_src++] = own.part;
+    m.seq_len = c->seq_len;
+    m.max_len = (int)own_keys;
+    m.o = p.o;
+    strides_of(m.o_s, *O);
+    m.lse = LSE;
+    m.B = B;
+    m.T = T;
+    m.Hq = Hq;
+    m.G = G;
+    m.D = D;
+    m.causal = p.causal;
+    m.f16 = p.f16;
+    m.joined = p.joined;
+    return fa::launch_paged_merge(m, cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_kv_append(const fa_paged_kv *cache, const fa_rows *K, const fa_rows *V, const fa_rows *Q,
+                       const fa_rows *Q_out, int B, int Hq, int T, const float *inv_freq, int rot_dim,
+                       int interleaved, int64_t position_offset, int f16, void *stream)
+{
+    if (B < 0 || T < 0 || Hq < 0) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_cache(cache, B);
+    if (st != FA_OK) return st;
+    if (rot_dim < 0 || rot_dim > cache->D || rot_dim % 2 != 0) return FA_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!inv_freq || !aligned(inv_freq, 4))) return FA_ERR_INVALID_ARG;
+    if (position_offset < 0 || position_offset > (int64_t)1 << 40) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * T > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * T == 0) return FA_OK;
+    const int D = cache->D;
+    if (!rows_ok(K, B, cache->Hkv, T, D, false) || !rows_ok(V, B, cache->Hkv, T, D, false)) return FA_ERR_INVALID_ARG;
+    const bool queries = Q && Hq > 0;
+    if (queries && (!rows_ok(Q, B, Hq, T, D, false) || !rows_ok(Q_out, B, Hq, T, D, true))) return FA_ERR_INVALID_ARG;
+    if ((int64_t)(queries ? Hq : 0) + cache->Hkv > INT32_MAX / D) return FA_ERR_INVALID_ARG;
+
+    fa::AppendParams p{};
+    p.c = cache_of(*cache);
+    p.k = static_cast<const uint16_t *>(K->ptr);
+    strides_of(p.k_s, *K);
+    p.v = static_cast<const uint16_t *>(V->ptr);
+    strides_of(p.v_s, *V);
+    if (queries) {
+        p.q = static_cast<const uint16_t *>(Q->ptr);
+        strides_of(p.q_s, *Q);
+        p.q_out = static_cast<uint16_t *>(Q_out->ptr);
+        strides_of(p.qo_s, *Q_out);
+    }
+    p.inv_freq = inv_freq;
+    p.offset = position_offset;
+    p.B = B;
+    p.T = T;
+    p.Hq = queries ? Hq : 0;
+    p.rot = rot_dim;
+    p.interleaved = interleaved ? 1 : 0;
+    p.f16 = f16 ? 1 : 0;
+    return fa::launch_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_kv *cache, int B, int Hq, int T)
+{
+    return fa_fwd_shared_prefix_workspace_bytes(cache, 0, B, Hq, T);
+}
+
+fa_status fa_fwd_paged(const fa_rows *Q, const fa_paged_kv *cache, const fa_rows *O, float *LSE, int B, int Hq, int T,
+                       int causal, float scale, int f16, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return run(Q, cache, nullptr, 0, O, LSE, B, Hq, T, causal, scale, f16, workspace, workspace_bytes, stream);
+}
+
+size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix_len, int B, int Hq, int T)
+{
+    if (check_sizes(cache, B, Hq, T) != FA_OK || prefix_len < 0 || (int64_t)B * Hq * T == 0) return 0;
+    const int G = Hq / cache->Hkv;
+    const Plan own(B, cache->Hkv, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, cache->D, false);
+    if (!own.ok) return 0;
+    if (prefix_len == 0) return own.bytes;
+    const Plan front(1, cache->Hkv, (int64_t)G * T * B, prefix_len, cache->D, true);
+    return front.ok ? own.bytes + front.bytes : 0;
+}
+
+fa_status fa_fwd_shared_prefix(const fa_rows *Q, const fa_paged_kv *cache, const int32_t *prefix_table, int prefix_len,
+                               const fa_rows *O, float *LSE, int B, int Hq, int T, int causal, float scale, int f16,
+                               void *workspace, size_t workspace_bytes, void *stream)
+{
+    return run(Q, cache, prefix_table, prefix_len, O, LSE, B, Hq, T, causal, scale, f16, workspace, workspace_bytes,
+               stream);
+}
+
+}  // extern "C"

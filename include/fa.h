@@ -320,6 +320,127 @@ fa_status fa_bwd_f16(const void *Q, const void *K, const void *V, const void *O,
 /* Bytes of workspace fa_bwd needs: B*H*N*(D + 1)*4 (0 for invalid sizes). */
 size_t fa_bwd_workspace_bytes(int B, int H, int N, int D);
 
+/*
+ * ---------------------------------------------------------------- paged cache
+ * The operators below serve generation: keys and values of earlier tokens stay
+ * in a cache, new tokens are appended, and few queries attend to many keys.
+ * The pages this library follows have no counterpart; the row mathematics is
+ * fa_fwd's.
+ *
+ * The cache is a pool of num_pages pages of page_size slots.  Key row (page,
+ * head, slot) is D contiguous 16-bit elements at
+ *     k + page * stride_page + head * stride_head + slot * stride_slot
+ * (elements; multiples of 8), and v likewise, so both [pages, Hkv, slots, D]
+ * and [pages, slots, Hkv, D] pools serve.  Key i of sequence b is slot
+ * i % page_size of page table[b * table_stride + i / page_size], for i <
+ * seq_len[b].  seq_len entries are clamped to [0, table_width * page_size] on
+ * the device.  A page number outside [0, num_pages) (-1, say, for a page that
+ * was given up) holds nothing: its keys are hidden and appends to it are
+ * dropped.  Slots at or past a sequence's length may hold anything; keys and
+ * values before it have to be finite.
+ *
+ * table and seq_len are device memory that the caller updates between calls;
+ * a captured graph reads their contents at replay.
+ */
+typedef struct fa_paged_kv {
+    void *k, *v;                 /* 16-byte aligned */
+    int64_t stride_page, stride_head, stride_slot;
+    int num_pages, page_size;
+    int Hkv, D;                  /* key heads; head dimension: a multiple of 8 up to 128, or 256 */
+    const int32_t *table;        /* [B, table_width] page numbers, rows table_stride entries apart */
+    int64_t table_stride;
+    int table_width;             /* table_width * page_size < 2^31 */
+    const int32_t *seq_len;      /* [B] keys per sequence, the call's own tokens included */
+} fa_paged_kv;
+
+/* A [B, H, N, D] array of 16-bit elements whose last dimension is contiguous:
+ * row (b, h, n) is at ptr + b * stride_b + h * stride_h + n * stride_n
+ * (elements; multiples of 8, >= 0).  ptr is 16-byte aligned.  Inputs may
+ * repeat rows through strides of 0; outputs may not. */
+typedef struct fa_rows {
+    void *ptr;
+    int64_t stride_b, stride_h, stride_n;
+} fa_rows;
+
+/*
+ * fa_kv_append -- keys and values of T new tokens per sequence into a paged
+ * cache, with the position rotation of keys and queries.
+ *
+ * seq_len already counts the new tokens: token t of sequence b is its key i =
+ * seq_len[b] - T + t, at position n = position_offset + i.  Tokens with i < 0
+ * do not exist (a shorter row of a padded batch is aligned at its end): they
+ * are not stored, and their query is set to zero.
+ *
+ * The first rot_dim elements of a head turn in pairs: pair p, of elements p
+ * and p + rot_dim / 2 (2p and 2p + 1 if interleaved), by the angle n *
+ * inv_freq[p].  The angle is kept modulo one turn in 64-bit fixed point, so
+ * far positions lose nothing; values are fp32 until they are rounded once.
+ *
+ *   K, V             [B, Hkv, T, D] new keys and values.
+ *   Q, Q_out         [B, Hq, T, D] queries and where to put them rotated, or
+ *                    Q = NULL for none.  Q_out may not overlap an input.
+ *   inv_freq         float [rot_dim / 2] device array, each in [-65536, 65536]
+ *                    (others give NaN).  NULL with rot_dim = 0: no rotation.
+ *   rot_dim          even, 0 <= rot_dim <= D.
+ *   position_offset  position of a sequence's first key, 0 .. 2^40 (the length
+ *                    of a shared prefix, say).
+ *   f16              elements are IEEE half (else bf16).
+ *
+ * Two tokens of one call that land on the same slot (tables that share a page
+ * there) leave it undefined.  One kernel; errors as fa_fwd.
+ */
+fa_status fa_kv_append(const fa_paged_kv *cache, const fa_rows *K, const fa_rows *V, const fa_rows *Q,
+                       const fa_rows *Q_out, int B, int Hq, int T, const float *inv_freq, int rot_dim,
+                       int interleaved, int64_t position_offset, int f16, void *stream);
+
+/*
+ * fa_fwd_paged -- fa_fwd over a paged cache: T query tokens per sequence, Hq
+ * query heads that share Hkv key heads (head h uses key head h / (Hq / Hkv)).
+ *
+ *   Q, O       [B, Hq, T, D].  O may not overlap Q or the cache.
+ *   LSE        float [B, Hq, T], contiguous, or NULL.
+ *   causal     nonzero: the queries are the last T tokens of their sequence;
+ *              query t sees the keys i <= seq_len[b] - T + t.  Queries before
+ *              the sequence's first token see none.  Zero: every query sees
+ *              all seq_len[b] keys.
+ *   scale      as in fa_fwd.
+ *   f16        elements are IEEE half (else bf16).
+ *   workspace  caller-owned device memory, 16-byte aligned, of at least
+ *              fa_fwd_paged_workspace_bytes bytes; its contents on entry do
+ *              not matter, and calls that may overlap need separate ones.
+ * Queries that see no key get O = +0.0 and LSE = -inf.  Results do not depend
+ * on timing: partial states are joined in a fixed order.  Returns as fa_fwd,
+ * and FA_ERR_INVALID_ARG for a missing, misaligned or too small workspace or
+ * an Hq that is no multiple of Hkv.
+ */
+fa_status fa_fwd_paged(const fa_rows *Q, const fa_paged_kv *cache, const fa_rows *O, float *LSE, int B, int Hq, int T,
+                       int causal, float scale, int f16, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_fwd_paged needs on the current device (0 for invalid
+ * or empty sizes).  They depend on the sizes, not on seq_len's contents. */
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_kv *cache, int B, int Hq, int T);
+
+/*
+ * fa_fwd_shared_prefix -- fa_fwd_paged for sequences that begin with the same
+ * prefix_len keys.  Key i of the prefix is slot i % page_size of page
+ * prefix_table[i / page_size] of the same pool; cache->table and seq_len give
+ * the keys that follow, each sequence's own.  The prefix's keys are read once
+ * for the whole batch, and every query that has a token sees all of them.
+ * prefix_len need not be a multiple of page_size.  Results equal fa_fwd_paged
+ * on tables that spell the whole sequence, to rounding.
+ *
+ *   prefix_table  int32 device array of ceil(prefix_len / page_size) pages.
+ *   prefix_len    >= 0, a host value (0: fa_fwd_paged).
+ * With causal set a query whose own index seq_len[b] - T + t is below 0 has
+ * no token and gets O = +0.0 and LSE = -inf.
+ */
+fa_status fa_fwd_shared_prefix(const fa_rows *Q, const fa_paged_kv *cache, const int32_t *prefix_table, int prefix_len,
+                               const fa_rows *O, float *LSE, int B, int Hq, int T, int causal, float scale, int f16,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_fwd_shared_prefix needs (0 for invalid or empty sizes). */
+size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix_len, int B, int Hq, int T);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *fa_status_string(fa_status s);
 
