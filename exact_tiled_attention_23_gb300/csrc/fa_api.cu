@@ -280,6 +280,26 @@ fa_status fwd16_with_tiles(const void *Q, const void *K, const void *V, void *O,
     return fwd16(Q, K, V, O, LSE, B, H, N, D, causal, scale, kv_len, stream, f16, tiles);
 }
 
+bool encode_tiled16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, bool f16)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+              const_cast<void *>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t wait_budget_ns() { return wait_limit_ns(); }
+
 }  // namespace fa
 
 extern "C" {
@@ -419,12 +439,12 @@ const char *fa_status_string(fa_status s)
 
 fa_status fa_device_status(void *stream)
 {
-    uint32_t v = 0, vb = 0, vd = 0, vh = 0;
+    uint32_t v = 0, vb = 0, vd = 0, vh = 0, vp = 0;
     if (fa::read_and_clear_status(static_cast<cudaStream_t>(stream), &v) != cudaSuccess ||
         fa::read_and_clear_status_bwd(&vb) != cudaSuccess || fa::read_and_clear_status_onetile(&vd) != cudaSuccess ||
-        fa::read_and_clear_status_halves(&vh) != cudaSuccess)
+        fa::read_and_clear_status_halves(&vh) != cudaSuccess || fa::read_and_clear_status_paged(&vp) != cudaSuccess)
         return FA_ERR_CUDA;
-    v |= vb | vd | vh;
+    v |= vb | vd | vh | vp;
     if (v) {
         g_last_detail = v;
         if (v & fa::kStatusTimeout) return FA_ERR_TIMEOUT;

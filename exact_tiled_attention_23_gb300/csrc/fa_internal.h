@@ -108,6 +108,15 @@ cudaError_t launch_bwd_bf16(const BwdParams &p, const CUtensorMap &tm_q, const C
                             const CUtensorMap &tm_v, const CUtensorMap &tm_do, const CUtensorMap &tm_dq,
                             cudaStream_t stream);
 
+// A tensor map over 16-bit elements with a box of 64 columns (128-byte
+// swizzle) by box[1..], zero fill outside; strides in bytes.  False if the
+// driver has none or refuses.
+bool encode_tiled16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, bool f16);
+
+// The budget of every bounded wait.
+uint64_t wait_budget_ns();
+
 // Read-and-clear of the device status word (synchronises `stream` first).
 cudaError_t read_and_clear_status(cudaStream_t stream, uint32_t *out);
 // The backward kernels' status word (call after read_and_clear_status).
@@ -116,5 +125,7 @@ cudaError_t read_and_clear_status_bwd(uint32_t *out);
 cudaError_t read_and_clear_status_onetile(uint32_t *out);
 // The split-row forward kernel's status word (call after read_and_clear_status).
 cudaError_t read_and_clear_status_halves(uint32_t *out);
+// The paged tensor-core kernel's status word (call after read_and_clear_status).
+cudaError_t read_and_clear_status_paged(uint32_t *out);
 
 }  // namespace fa

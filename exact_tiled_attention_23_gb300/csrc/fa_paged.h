@@ -4,6 +4,7 @@
 
 #include "fa.h"
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -34,19 +35,20 @@ struct AppendParams {
 };
 
 // Partial softmax states of row tiles, which the merge joins.  A tile is
-// `rows` stacked query rows of one (sequence, key head); tile i of the
-// nseq * Hkv * tiles ones has its states in a list of slots, each `rows`
-// normalised fp32 outputs of D columns and `rows` base-2 log-sum-exps.
+// `rows` stacked query rows of one (sequence, key head), in the order of
+// fa_paged_line.cuh.  Its states are in slots, each `rows` normalised fp32
+// outputs of D columns and `rows` base-2 log-sum-exps.
 struct Partials {
     float *o;              // [slots][rows][D]
     float *lse;            // [slots][rows]
     int rows;              // stacked query rows per tile
     int tiles;             // row tiles per (sequence, key head)
     int stacked;           // 1: one list of tiles for all sequences (a shared prefix)
-    // Slots of tile i: splits > 0: i * splits + s for s < splits.  splits = 0:
-    // k + i for the CTAs k that had a share of the tile's key chunks; they
-    // follow from the tile's first chunk and the chunks per CTA.
-    int splits;
+    int chunk;             // keys per chunk of the line
+    // Tile i has the slots k + i of the CTAs k that had a share of its chunks.
+    // They follow from the tile's first chunk and the chunks per CTA.  (Along
+    // the line, k and i never fall and one of them grows from share to share,
+    // so no two shares have one slot.)
     int64_t *first_chunk;  // [tiles in all]
     int64_t *per_cta;      // [1]
     int fixed_len;         // stacked: keys of the prefix
@@ -64,6 +66,7 @@ struct PagedParams {
     float scale_log2;
     int joined;                        // 1: every tile leaves its state in a slot for the merge
     Partials part;
+    int box_rows;                      // tensor-core kernel: key rows per copied box
     uint64_t wait_limit_ns;
 };
 
@@ -79,8 +82,9 @@ struct MergeParams {
     int joined;                        // 0: a tile that one CTA finished is written already
 };
 
-// Keys per chunk of the row kernel's work list.
+// Keys per chunk of the line: the row kernel's, and the tensor-core kernel's.
 constexpr int kChunkKeys = 64;
+constexpr int kBlockKeys = 128;
 
 // Query rows per tile, and CTAs per SM, of the row kernel.
 int paged_rows_per_tile(int D, int64_t rows);
@@ -88,6 +92,8 @@ int paged_rows_ctas_per_sm(int D);
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedParams &p, int ctas, cudaStream_t stream);
+cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                            cudaStream_t stream);
 cudaError_t launch_paged_merge(const MergeParams &p, cudaStream_t stream);
 
 }  // namespace fa

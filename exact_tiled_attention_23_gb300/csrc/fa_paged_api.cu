@@ -82,6 +82,23 @@ int sm_count()
 
 size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
+// Most stacked rows that the row kernel takes where the tensor-core kernel could.
+constexpr int64_t kMostRows = 32;
+
+// Key rows per box that the tensor-core kernel copies from this pool: the
+// largest power of two, 8 (the rows of a swizzle atom) to 128, that divides a
+// page.  0 where it cannot: other page sizes, D = 256 (its TMEM layout holds
+// two O tiles of at most 128 columns), strides past a tensor map's range.
+int tc_box_rows(const fa_paged_kv &c)
+{
+    if (c.D > 128 || c.page_size % 8 != 0 || c.num_pages <= 0) return 0;
+    const int64_t far = (int64_t)1 << 38;
+    if (c.stride_page >= far || c.stride_head >= far || c.stride_slot >= far) return 0;
+    int box = 8;
+    while (box < 128 && c.page_size % (2 * box) == 0) box *= 2;
+    return box;
+}
+
 // How one part of a call (the sequences' own keys, or a shared prefix) is cut
 // into tiles, and its piece of the workspace.
 struct Plan {
@@ -90,11 +107,15 @@ struct Plan {
     int64_t ctas = 0;
     size_t bytes = 0;
     bool ok = true;
+    int box = 0;            // key rows per box of the tensor-core kernel, 0: the row kernel
 
     // rows: stacked query rows per (sequence, key head); keys: most keys of a sequence
-    Plan(int nseq, int Hkv, int64_t rows, int64_t keys, int D, bool stacked)
+    Plan(int nseq, const fa_paged_kv &c, int64_t rows, int64_t keys, bool stacked)
     {
-        part.rows = fa::paged_rows_per_tile(D, rows);
+        const int Hkv = c.Hkv, D = c.D;
+        box = rows > kMostRows ? tc_box_rows(c) : 0;
+        part.rows = box ? 128 : fa::paged_rows_per_tile(D, rows);
+        part.chunk = box ? fa::kBlockKeys : fa::kChunkKeys;
         const int64_t tiles = (rows + part.rows - 1) / part.rows;
         items = (int64_t)nseq * Hkv * tiles;
         if (rows > INT32_MAX / 2 || (int64_t)Hkv * tiles > INT32_MAX || items > INT32_MAX) {
@@ -104,8 +125,8 @@ struct Plan {
         part.tiles = (int)tiles;
         part.stacked = stacked;
         part.fixed_len = stacked ? (int)keys : 0;
-        const int64_t chunks = items * ((keys + fa::kChunkKeys - 1) / fa::kChunkKeys);
-        ctas = (int64_t)sm_count() * fa::paged_rows_ctas_per_sm(D);
+        const int64_t chunks = items * ((keys + part.chunk - 1) / part.chunk);
+        ctas = (int64_t)sm_count() * (box ? 1 : fa::paged_rows_ctas_per_sm(D));
         if (ctas > chunks) ctas = chunks > 0 ? chunks : 1;
         const size_t slots = (size_t)(ctas + items);
         bytes = 256 + round_up((size_t)items * 8) + round_up(slots * part.rows * 4) + round_up(slots * part.rows * D * 4);
@@ -125,6 +146,26 @@ struct Plan {
         return at + round_up(slots * part.rows * D * 4);
     }
 };
+
+// One part's kernel.
+bool launch_part(fa::PagedParams p, const fa_paged_kv &c, const Plan &plan, cudaStream_t stream)
+{
+    p.part = plan.part;
+    if (!plan.box) return fa::launch_paged_rows(p, (int)plan.ctas, stream) == cudaSuccess;
+    // [D, slot, head, page]; the stride of a dimension of one entry is not followed
+    const uint64_t row = (uint64_t)c.D * 2;
+    const uint64_t dims[4] = {(uint64_t)c.D, (uint64_t)c.page_size, (uint64_t)c.Hkv, (uint64_t)c.num_pages};
+    const uint64_t strides[3] = {(uint64_t)c.stride_slot * 2, c.Hkv > 1 ? (uint64_t)c.stride_head * 2 : row,
+                                 c.num_pages > 1 ? (uint64_t)c.stride_page * 2 : row};
+    const uint32_t box[4] = {64, (uint32_t)plan.box, 1, 1};
+    CUtensorMap tk, tv;
+    if (!fa::encode_tiled16(&tk, c.k, 4, dims, strides, box, p.f16 != 0) ||
+        !fa::encode_tiled16(&tv, c.v, 4, dims, strides, box, p.f16 != 0))
+        return false;
+    p.box_rows = plan.box;
+    p.wait_limit_ns = fa::wait_budget_ns();
+    return fa::launch_paged_tc(p, tk, tv, (int)plan.ctas, stream) == cudaSuccess;
+}
 
 // Sizes of a paged forward; `keys` is what a table row can hold.
 fa_status check_sizes(const fa_paged_kv *c, int B, int Hq, int T)
@@ -152,8 +193,8 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     const int64_t own_keys = (int64_t)c->table_width * c->page_size;
     if (own_keys + prefix_len > INT32_MAX) return FA_ERR_INVALID_ARG;
     const int G = Hq / c->Hkv;
-    Plan own(B, c->Hkv, (int64_t)G * T, own_keys, D, false);
-    Plan front(1, c->Hkv, (int64_t)G * T * B, prefix_len, D, true);
+    Plan own(B, *c, (int64_t)G * T, own_keys, false);
+    Plan front(1, *c, (int64_t)G * T * B, prefix_len, true);
     if (!own.ok || (prefix_len > 0 && !front.ok)) return FA_ERR_INVALID_ARG;
     const size_t need = own.bytes + (prefix_len > 0 ? front.bytes : 0);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return FA_ERR_INVALID_ARG;
@@ -181,17 +222,15 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     fa::MergeParams m{};
     if (prefix_len > 0) {
         fa::PagedParams f = p;
-        f.part = front.part;
         f.c.table = prefix_table;
         f.c.table_width = (int)((prefix_len + (int64_t)c->page_size - 1) / c->page_size);
         f.c.table_stride = 0;
         f.c.seq_len = nullptr;
         f.c.fixed_len = prefix_len;
-        if (fa::launch_paged_rows(f, (int)front.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
+        if (!launch_part(f, *c, front, cs)) return FA_ERR_CUDA;
         m.src[m.n_src++] = front.part;
     }
-    p.part = own.part;
-    if (fa::launch_paged_rows(p, (int)own.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
+    if (!launch_part(p, *c, own, cs)) return FA_ERR_CUDA;
     m.src[m.n_src++] = own.part;
     m.seq_len = c->seq_len;
     m.max_len = (int)own_keys;
@@ -269,10 +308,10 @@ size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix
 {
     if (check_sizes(cache, B, Hq, T) != FA_OK || prefix_len < 0 || (int64_t)B * Hq * T == 0) return 0;
     const int G = Hq / cache->Hkv;
-    const Plan own(B, cache->Hkv, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, cache->D, false);
+    const Plan own(B, *cache, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, false);
     if (!own.ok) return 0;
     if (prefix_len == 0) return own.bytes;
-    const Plan front(1, cache->Hkv, (int64_t)G * T * B, prefix_len, cache->D, true);
+    const Plan front(1, *cache, (int64_t)G * T * B, prefix_len, true);
     return front.ok ? own.bytes + front.bytes : 0;
 }
 

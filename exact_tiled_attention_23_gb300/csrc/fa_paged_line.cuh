@@ -1,0 +1,162 @@
+// fa_paged_line.cuh -- the line of key chunks that the paged kernels share out.
+//
+// A group is one row tile of one sequence (its index is sequence * tiles + row
+// tile); each of the Hkv key heads has a tile of the group, with the same
+// number of chunks.  The line runs over groups, then key heads, then chunks;
+// every CTA takes an equal piece of it, whatever the sequences' lengths.
+#pragma once
+
+#include "fa_paged.h"
+
+namespace fa {
+
+__device__ __forceinline__ int keys_of_sequence(const PagedParams &p, int b)
+{
+    if (!p.c.seq_len) return p.c.fixed_len;
+    const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
+    const int n = p.c.seq_len[b];
+    return n < 0 ? 0 : (n > cap ? (int)cap : n);
+}
+
+// Keys that at least one row of row tile `rt` sees, of a sequence of `len`.
+__device__ __forceinline__ int keys_of_tile(int len, int rt, int rows, int R, int G, int T, bool causal)
+{
+    if (!causal) return len;
+    const int last = min((rt + 1) * rows, R) - 1;
+    return max(0, min(len, len - T + last / G + 1));
+}
+
+__device__ __forceinline__ int chunks_of(int keys, int chunk) { return (int)(((int64_t)keys + chunk - 1) / chunk); }
+
+// A place on the line.
+struct LineCursor {
+    int g, h;      // group, key head
+    int c, n;      // chunk, chunks of the tile
+    int keys;      // keys that the tile sees
+    int len;       // keys of the sequence
+};
+
+template <int kChunk>
+struct Line {
+    const PagedParams &p;
+    int R;         // stacked rows per (sequence, key head)
+    int groups;
+    bool masked;   // rows see different keys
+
+    __device__ __forceinline__ explicit Line(const PagedParams &q) : p(q)
+    {
+        R = p.G * p.T * (p.part.stacked ? p.B : 1);
+        groups = (p.part.stacked ? 1 : p.B) * p.part.tiles;
+        masked = p.causal && !p.part.stacked;
+    }
+
+    __device__ __forceinline__ void enter(LineCursor &u, int g) const
+    {
+        const int b = g / p.part.tiles;
+        u.g = g;
+        u.len = keys_of_sequence(p, b);
+        u.keys = keys_of_tile(u.len, g - b * p.part.tiles, p.part.rows, R, p.G, p.T, masked);
+        u.n = chunks_of(u.keys, kChunk);
+    }
+
+    // To the next chunk; past the line's end n is 0.
+    __device__ __forceinline__ void advance(LineCursor &u) const
+    {
+        if (++u.c < u.n) return;
+        u.c = 0;
+        if (++u.h < p.c.Hkv) return;
+        u.h = 0;
+        do {
+            if (u.g + 1 >= groups) {
+                u.n = 0;
+                return;
+            }
+            enter(u, u.g + 1);
+        } while (u.n == 0);
+    }
+
+    // This CTA's piece of the line: where it starts, its first chunk counted
+    // along the line and how many it has.  The whole CTA calls it; `scratch`
+    // holds kThreads / 32 + 2 numbers.  Thread i sums the chunks of a strip of
+    // groups, and the strips' prefix sums find the group to start in.
+    template <int kThreads>
+    __device__ __forceinline__ void share(int64_t *scratch, LineCursor &at, int64_t &first, int &count) const
+    {
+        constexpr int kWarps = kThreads / 32;
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        int64_t total, base = 0;
+        at.h = at.c = 0;
+        if (groups == 1) {
+            enter(at, 0);
+            total = (int64_t)at.n * p.c.Hkv;
+        } else {
+            const int strip = (groups + kThreads - 1) / kThreads;
+            const int g0 = min(tid * strip, groups), g1 = min(g0 + strip, groups);
+            int64_t sum = 0;
+            LineCursor u;
+            for (int g = g0; g < g1; ++g) {
+                enter(u, g);
+                sum += u.n;
+            }
+            int64_t scan = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, scan, d);
+                if (lane >= d) scan += v;
+            }
+            if (lane == 31) scratch[warp] = scan;
+            __syncthreads();
+            int64_t all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) scan += scratch[w];
+                all += scratch[w];
+            }
+            total = all * p.c.Hkv;
+            const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+            const int64_t start = per * blockIdx.x;
+            if (start < total && (scan - sum) * p.c.Hkv <= start && start < scan * p.c.Hkv) {
+                int64_t before = scan - sum;
+                int g = g0;
+                for (;; ++g) {
+                    enter(u, g);
+                    if (start < (before + u.n) * p.c.Hkv) break;
+                    before += u.n;
+                }
+                scratch[kWarps] = g;
+                scratch[kWarps + 1] = before * p.c.Hkv;
+            }
+            __syncthreads();
+            if (start < total) {
+                enter(at, (int)scratch[kWarps]);
+                base = scratch[kWarps + 1];
+            }
+        }
+        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+        if (blockIdx.x == 0 && tid == 0) *p.part.per_cta = per;
+        first = per * blockIdx.x;
+        const int64_t end = first + per < total ? first + per : total;
+        count = end > first ? (int)(end - first) : 0;
+        if (count > 0) {
+            at.h = (int)((first - base) / at.n);
+            at.c = (int)((first - base) - (int64_t)at.h * at.n);
+        }
+    }
+};
+
+// Row `idx` of the stacked rows of a tile's (sequence, key head): its place in
+// [B, H, T].
+struct RowPlace {
+    int b, hq, t;
+};
+
+__device__ __forceinline__ RowPlace row_place(const PagedParams &p, int b, int h, int idx)
+{
+    if (p.part.stacked) {
+        b = idx / (p.G * p.T);
+        idx -= b * p.G * p.T;
+    }
+    const int t = idx / p.G;
+    return RowPlace{b, h * p.G + idx - t * p.G, t};
+}
+
+}  // namespace fa

@@ -26,6 +26,7 @@
 // Keys at or past a sequence's length and keys of pages outside the pool are
 // never read; their shared-memory rows are zero and their scores -inf.
 #include "fa_paged.h"
+#include "fa_paged_line.cuh"
 #include "fa_tc_common.cuh"
 #include "sm103_ptx.cuh"
 
@@ -56,6 +57,7 @@ struct RowsLayout {
     static constexpr int kMaskOff = kStatOff + kStatBytes;        // valid keys of every stage
     static constexpr int kScanOff = kMaskOff + kWarps * kStages * 4;
     static constexpr int kSmemBytes = kScanOff + 128;
+    static_assert((kWarps + 2) * 8 <= 128, "scratch of the line's share");
     static_assert(kStageBytes >= 16 * DP * 4, "an output tile fits a stage");
     static_assert(kSmemBytes * (DP == 256 ? 1 : 2) + (DP == 256 ? 1 : 2) * 1024 <= 233472, "shared memory per SM");
 };
@@ -68,24 +70,6 @@ __device__ __forceinline__ uint32_t unit_at(int row, int unit)
 {
     return (uint32_t)(row * kRowBytes + ((unit ^ (row & 7)) << 4));
 }
-
-// Where a CTA is on the line of chunks.
-struct Cursor {
-    int b;         // sequence
-    int hr;        // key head * tiles + row tile
-    int c, n;      // chunk, chunks of this tile
-    int len;       // keys of the sequence
-};
-
-__device__ __forceinline__ int keys_of(const PagedParams &p, int b)
-{
-    if (!p.c.seq_len) return p.c.fixed_len;
-    const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
-    const int n = p.c.seq_len[b];
-    return n < 0 ? 0 : (n > cap ? (int)cap : n);
-}
-
-__device__ __forceinline__ int chunks_of(int len) { return (int)(((int64_t)len + kChunkKeys - 1) / kChunkKeys); }
 
 template <int DP, int MT, bool kF16>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel(const PagedParams p)
@@ -102,89 +86,17 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
     int64_t *s_scan = reinterpret_cast<int64_t *>(smem + Lay::kScanOff);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nseq = p.part.stacked ? 1 : p.B;
-    const int R = p.G * p.T * (p.part.stacked ? p.B : 1);      // stacked rows per (sequence, key head)
-    const int HR = p.c.Hkv * p.part.tiles;
-
-    // ---- this CTA's share of the line of chunks ---------------------------
-    // Thread i sums the chunks of a strip of sequences; the strips' prefix
-    // sums find the sequence that the share starts in.
-    Cursor at{0, 0, 0, 0, 0};
-    int64_t total, first;                           // chunks in all, first one of sequence at.b
-    if (nseq == 1) {
-        at.len = keys_of(p, 0);
-        at.n = chunks_of(at.len);
-        total = (int64_t)at.n * HR;
-        first = 0;
-    } else {
-        const int strip = (nseq + kThreads - 1) / kThreads;
-        const int b0 = min(tid * strip, nseq), b1 = min(b0 + strip, nseq);
-        int64_t sum = 0;
-        for (int b = b0; b < b1; ++b) sum += chunks_of(keys_of(p, b));
-        int64_t scan = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += v;
-        }
-        if (lane == 31) s_scan[warp] = scan;
-        __syncthreads();
-        int64_t all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) scan += s_scan[w];
-            all += s_scan[w];
-        }
-        total = all * HR;
-        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-        const int64_t start = per * blockIdx.x;
-        if (start < total && (scan - sum) * HR <= start && start < scan * HR) {
-            int64_t before = scan - sum;
-            int b = b0;
-            while (true) {
-                const int n = chunks_of(keys_of(p, b));
-                if (start < (before + n) * HR) break;
-                before += n;
-                ++b;
-            }
-            s_scan[8] = b;
-            s_scan[9] = before * HR;
-        }
-        __syncthreads();
-        at.b = (int)s_scan[8];
-        first = s_scan[9];
-    }
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (blockIdx.x == 0 && tid == 0) *p.part.per_cta = per;
-    const int64_t g0 = per * blockIdx.x;
-    const int64_t g1 = g0 + per < total ? g0 + per : total;
-    if (g0 >= g1) return;
-    at.len = keys_of(p, at.b);
-    at.n = chunks_of(at.len);
-    at.hr = (int)((g0 - first) / at.n);
-    at.c = (int)((g0 - first) % at.n);
-    const int steps = (int)(g1 - g0);
-
-    auto advance = [&](Cursor &u) {
-        if (++u.c < u.n) return;
-        u.c = 0;
-        if (++u.hr < HR) return;
-        u.hr = 0;
-        do {
-            if (++u.b >= nseq) { u.n = 0; u.len = 0; return; }
-            u.len = keys_of(p, u.b);
-            u.n = chunks_of(u.len);
-        } while (u.n == 0);
-    };
-    // Keys that no row of the cursor's tile sees are not read.
-    auto visible = [&](const Cursor &u) -> int {
-        if (!p.causal || p.part.stacked) return u.len;
-        const int last = min((u.hr % p.part.tiles + 1) * RM, R) - 1;
-        return min(u.len, u.len - p.T + last / p.G + 1);
-    };
+    const Line<kChunkKeys> line(p);
+    LineCursor at;
+    int64_t g0;
+    int steps;
+    line.share<kThreads>(s_scan, at, g0, steps);
+    if (steps == 0) return;
+    const int R = line.R;
 
     // ---- loads -----------------------------------------------------------
     const int kr = lane & 15;                       // the key of the step whose address this lane finds
-    Cursor ld = at;
+    LineCursor ld = at;
     int ld_left = steps;
     // The page number of a step's key is fetched one step before its use.
     int pg = -1, pg_slot = 0, pg_head = 0;
@@ -192,13 +104,13 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
         pg = -1;
         if (ld_left <= 0) return;
         const int key = ld.c * kChunkKeys + warp * kStepKeys + kr;
-        pg_head = ld.hr / p.part.tiles;
-        if (key < visible(ld)) {
+        pg_head = ld.h;
+        if (key < ld.keys) {
             const uint32_t which = (uint32_t)key / (uint32_t)p.c.page_size;
             pg_slot = key - (int)which * p.c.page_size;
-            pg = p.c.table[(int64_t)ld.b * p.c.table_stride + which];
+            pg = p.c.table[(int64_t)(ld.g / p.part.tiles) * p.c.table_stride + which];
         }
-        advance(ld);
+        line.advance(ld);
         --ld_left;
     };
     const uint32_t ring = s_base + Lay::kRingOff + warp * S * Lay::kStageBytes;
@@ -234,21 +146,17 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
     int stage = 0, done = 0;
     while (done < steps) {
         const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the share
-        const int h = at.hr / p.part.tiles, rt = at.hr % p.part.tiles;
-        const int row0 = rt * RM;
-        const int64_t tile = (int64_t)at.b * HR + at.hr;
+        const int b = at.g / p.part.tiles, row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
+        const int64_t tile = (int64_t)at.g * p.c.Hkv + h;
         const bool whole = count == at.n;
         if (at.c == 0 && tid == 0) p.part.first_chunk[tile] = g0 + done;
         // Q rows of the tile; rows past R and columns past D are zero
         for (int e = tid; e < RM * (DP / 8); e += kThreads) {
             const int row = e / (DP / 8), unit = e % (DP / 8);
-            int idx = row0 + row;
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (idx < R && unit * 8 < p.c.D) {
-                int b = at.b;
-                if (p.part.stacked) { b = idx / (p.G * p.T); idx -= b * p.G * p.T; }
-                w = *reinterpret_cast<const uint4 *>(p.q + (int64_t)b * p.q_s[0] + (int64_t)(h * p.G + idx % p.G) * p.q_s[1] +
-                                                     (int64_t)(idx / p.G) * p.q_s[2] + unit * 8);
+            if (row0 + row < R && unit * 8 < p.c.D) {
+                const RowPlace r = row_place(p, b, h, row0 + row);
+                w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
             }
             ptx::st_shared_v4(q_smem + unit_at<RB>(row, unit), w.x, w.y, w.z, w.w);
         }
@@ -256,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
             const int t = (row0 + i * 8 + qr) / p.G;
-            lim[i] = p.causal && !p.part.stacked ? at.len - p.T + t + 1 : at.len;
+            lim[i] = line.masked ? at.len - p.T + t + 1 : at.len;
         }
-        const int lim_all = p.causal && !p.part.stacked ? at.len - p.T + row0 / p.G + 1 : at.len;   // seen by every row
+        const int lim_all = line.masked ? at.len - p.T + row0 / p.G + 1 : at.len;   // seen by every row
         __syncthreads();
 
         float o[MT][NT][4], m[2 * MT], l[2 * MT];
@@ -419,17 +327,15 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                 const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[c] = empty ? 0.f : acc[c] * inv;
-                int idx = row0 + tr;
+                const int idx = row0 + tr;
                 if (idx >= R) continue;
                 const float lse2 = empty ? -INFINITY : top + log2f(sum);
                 if (direct) {
-                    int b = at.b;
-                    if (p.part.stacked) { b = idx / (p.G * p.T); idx -= b * p.G * p.T; }
-                    const int t = idx / p.G, hq = h * p.G + idx % p.G;
+                    const RowPlace r = row_place(p, b, h, idx);
                     if (col < p.c.D)
-                        *reinterpret_cast<uint2 *>(p.o + (int64_t)b * p.o_s[0] + (int64_t)hq * p.o_s[1] + (int64_t)t * p.o_s[2] + col) =
+                        *reinterpret_cast<uint2 *>(p.o + r.b * p.o_s[0] + r.hq * p.o_s[1] + r.t * p.o_s[2] + col) =
                             make_uint2(ptx::pack16x2<kF16>(acc[0], acc[1]), ptx::pack16x2<kF16>(acc[2], acc[3]));
-                    if (p.lse && col == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = lse2 * kLn2;
+                    if (p.lse && col == 0) p.lse[((int64_t)r.b * p.Hq + r.hq) * p.T + r.t] = lse2 * kLn2;
                 } else {
                     if (col < p.c.D)
                         *reinterpret_cast<float4 *>(p.part.o + (slot * RM + tr) * p.c.D + col) =
@@ -441,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
         }
         load(last_stage);
         at.c += count - 1;
-        advance(at);
+        line.advance(at);
         done += count;
     }
     ptx::cp_async_wait<0>();
@@ -481,7 +387,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const MergeParams p)
     const int h = hq / p.G;
     int len = p.seq_len[b];
     len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
-    const bool padding = p.causal && len - p.T + t < 0;        // no token at this place
+    const bool padding = p.causal && len - p.T + t < 0;        // no token here
 
     int64_t slot0[2];
     int count[2], tr[2];
@@ -491,22 +397,20 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const MergeParams p)
         if (s >= p.n_src || padding) continue;
         const Partials &src = p.src[s];
         const int idx = t * p.G + hq % p.G + (src.stacked ? b * p.G * p.T : 0);
-        const int keys = src.stacked ? src.fixed_len : len;
-        tr[s] = idx % src.rows;
-        const int64_t tile = ((int64_t)(src.stacked ? 0 : b) * (p.Hq / p.G) + h) * src.tiles + idx / src.rows;
-        if (keys == 0) continue;
-        if (src.splits) {
-            slot0[s] = tile * src.splits;
-            count[s] = src.splits;
-        } else {
-            const int64_t per = *src.per_cta, c0 = src.first_chunk[tile];
-            const int64_t k0 = c0 / per, k1 = (c0 + ((int64_t)keys + kChunkKeys - 1) / kChunkKeys - 1) / per;
-            slot0[s] = k0 + tile;
-            count[s] = (int)(k1 - k0 + 1);
-        }
+        const int rt = idx / src.rows;
+        tr[s] = idx - rt * src.rows;
+        const int64_t tile = ((int64_t)(src.stacked ? 0 : b) * src.tiles + rt) * (p.Hq / p.G) + h;
+        const int chunks = chunks_of(
+            keys_of_tile(src.stacked ? src.fixed_len : len, rt, src.rows, p.G * p.T, p.G, p.T, p.causal && !src.stacked),
+            src.chunk);
+        if (chunks == 0) continue;
+        const int64_t per = *src.per_cta, c0 = src.first_chunk[tile];
+        const int64_t k0 = c0 / per, k1 = (c0 + chunks - 1) / per;
+        slot0[s] = k0 + tile;
+        count[s] = (int)(k1 - k0 + 1);
     }
     // one CTA had the whole tile and wrote the row itself
-    if (!p.joined && !p.src[0].splits && count[0] == 1) return;
+    if (!p.joined && count[0] == 1) return;
 
     float top = -INFINITY;
     for (int s = 0; s < p.n_src; ++s)

@@ -1,0 +1,595 @@
+// fa_paged_tc.cu -- attention of many stacked query rows over a paged cache, on
+// the tensor cores.
+//
+// Serves the row tiles that the row kernel (fa_paged_rows.cu) would have to cut
+// into many: the rows of a whole batch over a shared prefix, and pieces of a
+// prompt.  A tile is 128 stacked query rows of one (sequence, key head); the
+// line of 128-key blocks of all tiles is cut into one equal piece per CTA
+// (fa_paged_line.cuh), one CTA per SM, and a tile that two or more CTAs had a
+// share of is joined by the merge.
+//
+// Within a block the work is laid out as in the split-row forward kernel
+// (fa_fwd_halves.cu): each row's 128 keys are split into halves of 64 with
+// separate online-softmax states, warps 4-7 and 8-11, and one thread each issues
+// S = Q K^T (warp 3) and O_h += P_h V_h (warp 1).  What is different:
+//
+//   * the roles run along the CTA's whole piece of the line without stopping
+//     at a tile's end: the rings, the score tile and the P tiles go on counting,
+//     Q has two buffers (warp 2 fetches the next tile's rows), and only O is
+//     handed over (o_final, o_read);
+//   * K and V come through the page table: every lane of warp 0 finds one box
+//     of a block (as many rows as divide a page, 8 to 128) and copies it.  A box
+//     past the tile's last key, or of a page outside the pool, is read past the
+//     tensor's end, which fills it with zeros;
+//   * a box that the sequence ends in brings whatever the page holds behind the
+//     last key, and 0 * NaN is NaN: warp 1 clears those rows of V before its
+//     products read them;
+//   * keys of pages outside the pool are hidden: a scan of the CTA's pages, done
+//     while the first copies fly, decides whether the blocks have to ask.
+//
+// P is rounded to 16 bits for the second product and O divided by the sum of
+// the rounded weights, as in fa_fwd: the tensor cores take 16-bit operands, and
+// a second product for the rounding's rest would cost a third of the rate.
+//
+// Every mbarrier wait is bounded; a wait that runs out records the site in
+// this file's status word, raises the CTA's abort flag, and every role drains
+// its copies / MMAs, frees TMEM and exits.
+#include "fa_fwd_softmax.cuh"
+#include "fa_internal.h"
+#include "fa_paged.h"
+#include "fa_paged_line.cuh"
+#include "fa_tc_common.cuh"
+#include "sm103_ptx.cuh"
+
+#include <cmath>
+
+namespace fa {
+
+__device__ uint32_t g_status_paged;
+
+namespace {
+
+constexpr int BM = 128;                   // query rows per tile (= TMEM lanes)
+constexpr int BN = kBlockKeys;            // keys per block
+constexpr int kHalf = 64;                 // keys of a block per softmax warpgroup
+constexpr int kThreads = 384;             // warp 0 K/V copies, 1 PV, 2 Q rows, 3 S, 4-11 softmax
+constexpr int kSoftmaxWarp0 = 4;
+constexpr int kChunkBytes = 128 * 128;    // 128 rows x 64 columns of 16 bits
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;             // S [0,128)
+constexpr uint32_t kColP = 128;           // P tiles [128,192), [192,256)
+constexpr uint32_t kColO = 256;           // O_A and O_B, D columns each
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D>
+struct TcLayout {
+    static constexpr int kChunks = D / 64;                      // 128-byte swizzle atoms per row
+    static constexpr int kTileBytes = kChunks * kChunkBytes;    // a Q, K or V tile
+    static constexpr int kRing = D == 128 ? 2 : 4;              // K slots, and V slots
+    static constexpr int kQOff = 0;                             // two Q buffers
+    static constexpr int kKOff = 2 * kTileBytes;
+    static constexpr int kVOff = kKOff + kRing * kTileBytes;
+    static constexpr int kXchOff = kVOff + kRing * kTileBytes;  // (m, l, l_o) of both halves
+    static constexpr int kXchBytes = 2 * 3 * BM * 4;
+    static constexpr int kBarOff = kXchOff + kXchBytes;
+    // q_full[2], q_empty[2], k_full/k_empty/v_full/v_empty[R], s_full, s_read,
+    // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
+    static constexpr int kBars = 4 + 4 * kRing + 2 + 4 + 4 + 4;
+    static constexpr int kScanOff = kBarOff + 512;
+    static constexpr int kSmemBytes = kScanOff + 128 + 1024;    // + alignment slack
+    __device__ static constexpr uint32_t col_o(int h) { return kColO + (uint32_t)(h * D); }
+    __device__ static constexpr uint32_t col_p(int buf, int h) { return kColP + (uint32_t)(buf * 64 + h * 32); }
+    static_assert(D == 64 || D == 128, "head dim");
+    static_assert(kColO + 2 * D <= kTmemCols, "TMEM columns");
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static_assert(kBars * 8 + 16 <= 512, "barrier area");
+    static_assert((kThreads / 32 + 2) * 8 <= 128, "scratch of the line's share");
+};
+
+// A role's way along the CTA's piece of the line.
+struct Walk {
+    LineCursor u;
+    int left;          // blocks from here to the end of the piece, this one included
+    bool begins;       // this block is the first of its tile in this piece
+    __device__ __forceinline__ bool ends() const { return left == 1 || u.c + 1 == u.n; }
+    __device__ __forceinline__ void next(const Line<BN> &line)
+    {
+        begins = u.c + 1 == u.n;
+        line.advance(u);
+        --left;
+    }
+    // Rows of this block's V that hold what lies behind the sequence's last
+    // key: from the length to the end of the box that it falls into.
+    __device__ __forceinline__ bool has_rest(int box_rows) const
+    {
+        return u.len < (int64_t)(u.c + 1) * BN && u.len % box_rows != 0 && u.len >= (int64_t)u.c * BN;
+    }
+};
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
+{
+    using Lay = TcLayout<D>;
+    constexpr int kChunks = Lay::kChunks, kTileBytes = Lay::kTileBytes, R = Lay::kRing;
+    constexpr int kQOff = Lay::kQOff, kKOff = Lay::kKOff, kVOff = Lay::kVOff;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
+    uint64_t *q_full = bars + 0;               // [2], 32 arrivals: the lanes that copy a tile's rows
+    uint64_t *q_empty = q_full + 2;            // [2]: every S product of the tile done
+    uint64_t *k_full = q_empty + 2;            // [R]
+    uint64_t *k_empty = k_full + R;            // [R]
+    uint64_t *v_full = k_empty + R;            // [R]
+    uint64_t *v_empty = v_full + R;            // [R]
+    uint64_t *s_full = v_empty + R;            // S of a block complete
+    uint64_t *s_read = s_full + 1;             // all softmax warps hold it in registers (8 arrivals)
+    uint64_t *p_full = s_read + 1;             // [half][P tile]: P_h stored (4 arrivals)
+    uint64_t *pv_done = p_full + 4;            // [half][P tile]: O_h += P_h V done
+    uint64_t *o_final = pv_done + 4;           // every product of a tile complete
+    uint64_t *o_read = o_final + 1;            // the softmax warps hold O (8 arrivals)
+    uint64_t *mma_drain = o_read + 1;
+    uint64_t *mma_drain_s = mma_drain + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Lay::kBars);
+    int *abort_word = reinterpret_cast<int *>(tmem_slot + 1);
+    int *hidden_word = abort_word + 1;
+    const Abort ab{abort_word, &g_status_paged};
+    const uint64_t limit = p.wait_limit_ns;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const Line<BN> line(p);
+    Walk walk;
+    int64_t g0;
+    line.template share<kThreads>(reinterpret_cast<int64_t *>(smem + Lay::kScanOff), walk.u, g0, walk.left);
+    if (walk.left == 0) return;
+    walk.begins = true;
+    const int blocks = walk.left;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Lay::kBars; ++i) {
+            uint32_t count = 1;
+            if (&bars[i] == s_read || &bars[i] == o_read) count = 8;              // one arrival per softmax warp
+            if (&bars[i] >= p_full && &bars[i] < p_full + 4) count = 4;           // the four warps of a half
+            if (&bars[i] >= q_full && &bars[i] < q_full + 2) count = 32;
+            ptx::mbar_init(&bars[i], count);
+        }
+        *abort_word = 0;
+        *hidden_word = 0;
+        ptx::fence_mbarrier_init();
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // Rows `first`, `first + step`, ... of a tile's Q into buffer `buf`, in the
+    // 128-byte-swizzled layout; rows past the last and columns past D are zero.
+    auto copy_q = [&](const LineCursor &u, int buf, int thread, int threads) {
+        const int b = u.g / p.part.tiles, row0 = (u.g - b * p.part.tiles) * BM;
+        constexpr int kUnits = D / 8;
+        const uint32_t dst = ptx::smem_u32(smem + kQOff + buf * kTileBytes);
+#pragma unroll 4
+        for (int e = thread; e < BM * kUnits; e += threads) {
+            const int row = e / kUnits, unit = e % kUnits;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (row0 + row < line.R && unit * 8 < p.c.D) {
+                const RowPlace r = row_place(p, b, u.h, row0 + row);
+                w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
+            }
+            ptx::st_shared_v4(dst + (unit / 8) * kChunkBytes + row * 128 + (((unit % 8) ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
+        }
+        ptx::fence_proxy_async_smem();
+    };
+
+    if (warp == 0) {
+        // ================= K and V copies =================
+        // In the order the products read them: K_0, K_1, V_0, K_2, V_1, ...
+        // Lane i < boxes finds and copies box i of a block.
+        const int box = p.box_rows, boxes = BN / box;
+        const uint32_t page_size = (uint32_t)p.c.page_size;
+        struct Box { int page, slot, h; };
+        auto find = [&](const LineCursor &u) -> Box {
+            Box r{p.c.num_pages, 0, u.h};                       // past the tensor's end: zeros
+            const int64_t key = (int64_t)u.c * BN + lane * box;
+            if (lane < boxes && key < u.keys) {
+                const uint32_t which = (uint32_t)key / page_size;
+                const int page = p.c.table[(int64_t)(u.g / p.part.tiles) * p.c.table_stride + which];
+                if (page >= 0 && page < p.c.num_pages) r.page = page;
+                r.slot = (int)((uint32_t)key - which * page_size);
+            }
+            return r;
+        };
+        auto load = [&](const CUtensorMap *tm, int off, uint64_t *full, uint64_t *empty, int t, const Box &x) -> bool {
+            const int slot = t % R;
+            if (t >= R && !__all_sync(0xffffffffu, wait_bounded(&empty[slot], ((t - R) / R) & 1, limit, kSiteSlotEmpty, ab)))
+                return false;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], kTileBytes);
+            __syncwarp();
+            if (lane < boxes)
+                for (int c = 0; c < kChunks; ++c)
+                    ptx::tma_load_4d(smem + off + slot * kTileBytes + c * kChunkBytes + lane * box * 128, tm, &full[slot],
+                                     c * 64, x.slot, x.h, x.page);
+            return true;
+        };
+        Box now = find(walk.u), then = now;
+        bool ok = load(&tm_k, kKOff, k_full, k_empty, 0, now);
+        int k_issued = ok ? 1 : 0, v_issued = 0;
+        for (int t = 0; t < blocks && ok; ++t) {
+            if (t + 1 < blocks) {
+                walk.next(line);
+                then = find(walk.u);
+                ok = load(&tm_k, kKOff, k_full, k_empty, t + 1, then);
+                k_issued += ok;
+            }
+            if (ok) {
+                ok = load(&tm_v, kVOff, v_full, v_empty, t, now);
+                v_issued += ok;
+            }
+            now = then;
+        }
+        // Drain: no copy may still be landing in shared memory at exit.
+        for (int t = k_issued > R ? k_issued - R : 0; t < k_issued; ++t)
+            wait_bounded(&k_full[t % R], (t / R) & 1, limit, kSiteDrain, ab, false);
+        for (int t = v_issued > R ? v_issued - R : 0; t < v_issued; ++t)
+            wait_bounded(&v_full[t % R], (t / R) & 1, limit, kSiteDrain, ab, false);
+    } else if (warp == 2) {
+        // ================= the next tiles' Q =================
+        // (the softmax warps fetch the first tile's)
+        for (int tile = 1;; ++tile) {
+            // to the first block of the next tile in this piece
+            const int skip = min(walk.u.n - walk.u.c, walk.left);
+            walk.left -= skip;
+            if (walk.left == 0) break;
+            walk.u.c += skip - 1;
+            line.advance(walk.u);
+            if (tile >= 2 && !__all_sync(0xffffffffu, wait_bounded(&q_empty[tile & 1], ((tile - 2) >> 1) & 1, limit,
+                                                                    kSiteSlotEmpty, ab)))
+                break;
+            copy_q(walk.u, tile & 1, lane, 32);
+            ptx::mbar_arrive(&q_full[tile & 1]);
+        }
+    } else if (warp == 3) {
+        // ================= S products =================
+        // S of block t into the score tile, once the softmax warps hold block
+        // t-1's in registers.
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc(BM, BN, 0, 0, kF16);
+            const uint64_t q_desc = make_sdesc(ptx::smem_u32(smem + kQOff), 16, 1024);
+            const uint64_t k_desc = make_sdesc(ptx::smem_u32(smem + kKOff), 16, 1024);
+            constexpr uint64_t kTileStep = kTileBytes >> 4;
+            int tile = -1;
+            for (int t = 0; t < blocks; ++t) {
+                bool ok = true;
+                if (walk.begins) {
+                    ++tile;
+                    ok = wait_bounded(&q_full[tile & 1], (tile >> 1) & 1, limit, kSiteQFull, ab);
+                }
+                ok = ok && wait_bounded(&k_full[t % R], (t / R) & 1, limit, kSiteSlotFull, ab);
+                if (ok && t > 0) ok = wait_bounded(s_read, (t - 1) & 1, limit, kSiteSFull, ab);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t qd = q_desc + (uint64_t)(tile & 1) * kTileStep;
+                const uint64_t kd = k_desc + (uint64_t)(t % R) * kTileStep;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)(((k / 4) * kChunkBytes + (k % 4) * 32) >> 4);
+                    ptx::mma_ss(tmem + kColS, qd + off, kd + off, idesc, k > 0);
+                }
+                ptx::mma_commit(s_full);
+                ptx::mma_commit(&k_empty[t % R]);
+                if (walk.ends()) ptx::mma_commit(&q_empty[tile & 1]);
+                if (t + 1 < blocks) walk.next(line);
+            }
+            ptx::mma_commit(mma_drain_s);
+            wait_bounded(mma_drain_s, 0, limit, kSiteDrain, ab, false);
+        }
+    } else if (warp == 1) {
+        // ================= PV products =================
+        // O_h += P_h V[64h ..]: K-steps 4h .. 4h+3 of the block, A from the
+        // half's 32 columns of P tile t % 2.  A tile's first products replace O,
+        // once the softmax warps hold the tile before.  Lane 0 waits and
+        // issues; the warp clears V behind a sequence's end together.
+        constexpr uint32_t idesc = make_idesc(BM, D, 0, 1, kF16);
+        const uint64_t v_desc = make_sdesc(ptx::smem_u32(smem + kVOff), kChunkBytes, 1024);
+        constexpr uint64_t kTileStep = kTileBytes >> 4;
+        int tile = 0;
+        for (int t = 0; t < blocks; ++t) {
+            const int buf = t & 1;
+            bool ok = true;
+            if (lane == 0) ok = wait_bounded(&v_full[t % R], (t / R) & 1, limit, kSiteSlotFull, ab);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (walk.has_rest(p.box_rows)) {
+                const int from = walk.u.len - walk.u.c * BN;
+                const int to = (from + p.box_rows - 1) / p.box_rows * p.box_rows;
+                const uint32_t v = ptx::smem_u32(smem + kVOff + (t % R) * kTileBytes);
+                __syncwarp();
+                for (int e = lane; e < (to - from) * kChunks * 8; e += 32) {
+                    const int row = from + e / (kChunks * 8), unit = e % (kChunks * 8);
+                    ptx::st_shared_v4(v + (unit / 8) * kChunkBytes + row * 128 + ((unit % 8) << 4), 0u, 0u, 0u, 0u);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) {
+                if (walk.begins && tile > 0) ok = wait_bounded(o_read, (tile - 1) & 1, limit, kSiteOFinal, ab);
+                const uint64_t vd = v_desc + (uint64_t)(t % R) * kTileStep;
+                for (int h = 0; h < 2 && ok; ++h) {
+                    ok = wait_bounded(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t to = tmem + Lay::col_o(h), tp = tmem + Lay::col_p(buf, h);
+#pragma unroll
+                    for (int k = 0; k < kHalf / 16; ++k)
+                        ptx::mma_ts(to, tp + k * 8, vd + (uint64_t)(((4 * h + k) * 2048) >> 4), idesc,
+                                    (!walk.begins || k > 0) ? 1u : 0u);
+                    ptx::mma_commit(&pv_done[h * 2 + buf]);
+                }
+                if (ok) {
+                    ptx::mma_commit(&v_empty[t % R]);
+                    if (walk.ends()) ptx::mma_commit(o_final);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            tile += walk.ends();
+            if (t + 1 < blocks) walk.next(line);
+        }
+        if (lane == 0) {
+            ptx::mma_commit(mma_drain);
+            wait_bounded(mma_drain, 0, limit, kSiteDrain, ab, false);
+        }
+        __syncwarp();
+    } else {
+        // ================= online softmax of one key half + epilogue =================
+        const int h = (warp - kSoftmaxWarp0) / 4;     // key half: columns 64h .. 64h+63 of every block
+        const int quarter = warp & 3;                 // TMEM lanes 32*quarter ..
+        const int r_local = quarter * 32 + lane;
+        const int thread = threadIdx.x - 32 * kSoftmaxWarp0;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + lane_off + kColS + (uint32_t)(h * kHalf);
+        const float sl2 = p.scale_log2;
+
+        // the first tile's Q, and whether any page of this piece is hidden
+        copy_q(walk.u, 0, thread, 256);
+        bool hidden = false;
+        {
+            Walk s = walk;
+            while (s.left > 0) {
+                const int count = min(s.u.n - s.u.c, s.left);
+                const uint32_t page_size = (uint32_t)p.c.page_size;
+                const uint32_t from = (uint32_t)(s.u.c * BN) / page_size;
+                const uint32_t last = (uint32_t)min((int64_t)s.u.keys, (int64_t)(s.u.c + count) * BN) - 1u;
+                const int32_t *table = p.c.table + (int64_t)(s.u.g / p.part.tiles) * p.c.table_stride;
+                for (uint32_t i = from + thread; i <= last / page_size; i += 256) {
+                    const int page = table[i];
+                    hidden = hidden || page < 0 || page >= p.c.num_pages;
+                }
+                s.u.c += count - 1;
+                s.left -= count;
+                if (s.left > 0) line.advance(s.u);
+            }
+        }
+        if (hidden) *hidden_word = 1;
+        // all of Q is in place: one warp makes the arrivals
+        ptx::bar_sync(1, 256);
+        if (warp == kSoftmaxWarp0) ptx::mbar_arrive(&q_full[0]);
+        hidden = *hidden_word != 0;
+
+        int t = 0;
+        bool ok = true;
+        for (int tile = 0; t < blocks; ++tile) {
+            const int count = min(walk.u.n - walk.u.c, walk.left);
+            const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
+            const int row = row0 + r_local;
+            const int lim = min(walk.u.len, line.masked ? walk.u.len - p.T + row / p.G + 1 : walk.u.len);
+            OnlineRow<D, kF16, kHalf> st;
+            for (int j = 0; j < count; ++j, ++t) {
+                const int buf = t & 1;
+                const uint32_t tP = tmem + lane_off + Lay::col_p(buf, h);
+                const uint32_t tO = tmem + lane_off + Lay::col_o(h);
+                const bool got = wait_bounded(s_full, t & 1, limit, kSiteSFull, ab);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                // whether the last reader of P tile `buf` is done: tested now,
+                // waited for below only if it was not
+                const bool p_free = t < 2 || ptx::mbar_test(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1);
+                ptx::tc_fence_after();
+                uint32_t s_raw[2][32];
+                ptx::tmem_ld32(tS, s_raw[0]);
+                ptx::tmem_ld32(tS + 32, s_raw[1]);
+                ptx::tmem_wait_ld();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(s_read);
+
+                const int64_t key0 = (int64_t)(walk.u.c + j) * BN + h * kHalf;
+                const int64_t vis = lim - key0;                   // columns k < vis are visible
+                if (vis < kHalf) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (c * 32 + k >= vis) s_raw[c][k] = f2u(-INFINITY);
+                }
+                if (hidden) {
+                    const int32_t *table = p.c.table + (int64_t)b * p.c.table_stride;
+                    uint64_t bad = 0;                             // one bit per key of this half
+                    for (int k = 0; k < kHalf; k += 8)            // a page holds a multiple of 8 keys
+                        if (key0 + k < walk.u.keys) {
+                            const int page = table[(uint32_t)(key0 + k) / (uint32_t)p.c.page_size];
+                            if (page < 0 || page >= p.c.num_pages) bad |= 0xffull << k;
+                        }
+                    if (bad) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if ((bad >> (c * 32 + k)) & 1) s_raw[c][k] = f2u(-INFINITY);
+                    }
+                }
+                bool hook_ok = true;
+                auto before_o = [&] {
+                    if (j > 0) {
+                        hook_ok = wait_bounded(&pv_done[h * 2 + ((t - 1) & 1)], ((t - 1) >> 1) & 1, limit, kSiteOFinal, ab) &&
+                                  hook_ok;
+                        ptx::tc_fence_after();
+                    }
+                };
+                auto before_p = [&] {
+                    if (!__all_sync(0xffffffffu, p_free)) {
+                        hook_ok = wait_bounded(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1, limit, kSiteOFinal, ab) && hook_ok;
+                        ptx::tc_fence_after();
+                    }
+                };
+                st.template block<1>(s_raw, sl2, j > 0, tP, tO, before_o, before_p);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&p_full[h * 2 + buf]);
+                if (!__all_sync(0xffffffffu, hook_ok)) {
+                    ok = false;
+                    break;
+                }
+            }
+
+            // ---- join the halves: m = max(m_A, m_B), w_h = 2^(m_h - m),
+            // O = (w_A O_A + w_B O_B) / (w_A l_oA + w_B l_oB)
+            bool have = ok;
+            if (have) have = wait_bounded(o_final, tile & 1, limit, kSiteOFinal, ab);
+            // all eight warps agree, so that the named barriers are reached by
+            // all of them or by none; the last tile's exchange is read, too
+            have = ptx::bar_and(1, 256, have);
+            if (!have) break;
+            ptx::tc_fence_after();
+            float *xch = reinterpret_cast<float *>(smem + Lay::kXchOff);   // [half][3][BM]
+            xch[(h * 3 + 0) * BM + r_local] = st.m_ref;
+            xch[(h * 3 + 1) * BM + r_local] = st.l;
+            xch[(h * 3 + 2) * BM + r_local] = st.l_o;
+            ptx::bar_sync(2, 256);
+            float mh[2], lh[2], loh[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mh[e] = xch[(e * 3 + 0) * BM + r_local];
+                lh[e] = xch[(e * 3 + 1) * BM + r_local];
+                loh[e] = xch[(e * 3 + 2) * BM + r_local];
+            }
+            const bool on[2] = {lh[0] != 0.f, lh[1] != 0.f};      // a NaN stays on and reaches the output
+            const float m = fmaxf(on[0] ? mh[0] : -INFINITY, on[1] ? mh[1] : -INFINITY);
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w[e] = on[e] ? ptx::ex2_approx(mh[e] - m) : 0.f;
+            const float l_all = w[0] * lh[0] + w[1] * lh[1];
+            const bool empty = !(on[0] || on[1]);
+            const float inv = empty ? 0.f : 1.f / (w[0] * loh[0] + w[1] * loh[1]);
+            const float c0 = w[0] * inv, c1 = w[1] * inv;
+            const float lse2 = empty ? -INFINITY : m + log2f(l_all);
+
+            // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
+            const bool direct = count == walk.u.n && !p.joined;
+            const int64_t tile_id = (int64_t)walk.u.g * p.c.Hkv + walk.u.h;
+            const int64_t at = ((int64_t)blockIdx.x + tile_id) * BM + r_local;
+            if (thread == 0 && walk.u.c == 0) p.part.first_chunk[tile_id] = g0 + (t - count);
+            uint16_t *o_row = nullptr;
+            const bool real = row < line.R;
+            if (real) {
+                const RowPlace r = row_place(p, b, walk.u.h, row);
+                o_row = p.o + r.b * p.o_s[0] + r.hq * p.o_s[1] + r.t * p.o_s[2];
+                if (h == 0) {
+                    if (!direct)
+                        p.part.lse[at] = lse2;
+                    else if (p.lse)
+                        p.lse[((int64_t)r.b * p.Hq + r.hq) * p.T + r.t] = lse2 * kLn2;
+                }
+            }
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                __syncwarp();
+                const int col = h * (D / 2) + c * 32;
+                uint32_t oa[32], ob[32];
+                ptx::tmem_ld32(tmem + lane_off + Lay::col_o(0) + (uint32_t)col, oa);
+                ptx::tmem_ld32(tmem + lane_off + Lay::col_o(1) + (uint32_t)col, ob);
+                ptx::tmem_wait_ld();
+                if (c + 1 == D / 64) {
+                    // O is in registers: the next tile's products may replace it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(o_read);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (!real || col + 8 * k >= p.c.D) continue;
+                    // (a half with no visible key has weight 0 and O_h = 0)
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = empty ? 0.f : fmaf(c0, u2f(oa[8 * k + e]), c1 * u2f(ob[8 * k + e]));
+                    if (direct) {
+                        *reinterpret_cast<uint4 *>(o_row + col + 8 * k) =
+                            make_uint4(ptx::pack16x2<kF16>(x[0], x[1]), ptx::pack16x2<kF16>(x[2], x[3]),
+                                       ptx::pack16x2<kF16>(x[4], x[5]), ptx::pack16x2<kF16>(x[6], x[7]));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part.o + at * p.c.D + col + 8 * k);
+                        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+                    }
+                }
+            }
+            __syncwarp();
+            walk.u.c += count - 1;
+            walk.left -= count;
+            if (walk.left > 0) line.advance(walk.u);
+        }
+    }
+    // ---- teardown ----------------------------------------------------------
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool kF16>
+cudaError_t launch(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
+{
+    // per call: the attribute belongs to the current device
+    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               TcLayout<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    paged_tc_kernel<D, kF16><<<ctas, kThreads, TcLayout<D>::kSmemBytes, stream>>>(tk, tv, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                            cudaStream_t stream)
+{
+    if (p.c.D <= 64) return p.f16 ? launch<64, true>(p, tk, tv, ctas, stream) : launch<64, false>(p, tk, tv, ctas, stream);
+    return p.f16 ? launch<128, true>(p, tk, tv, ctas, stream) : launch<128, false>(p, tk, tv, ctas, stream);
+}
+
+cudaError_t read_and_clear_status_paged(uint32_t *out)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_status_paged, sizeof(v));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_status_paged, &zero, sizeof(zero));
+        if (e != cudaSuccess) return e;
+    }
+    *out = v;
+    return cudaSuccess;
+}
+
+}  // namespace fa

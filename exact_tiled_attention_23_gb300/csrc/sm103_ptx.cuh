@@ -85,6 +85,18 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_
         : "memory");
 }
 
+// 4-D tiled load of one box into shared memory.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_t *bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)),
+          "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Tensor-memory allocation: the whole warp executes these.
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols)
