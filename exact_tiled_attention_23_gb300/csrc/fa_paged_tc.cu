@@ -15,10 +15,10 @@
 //
 //   * the roles run along the CTA's whole piece of the line without stopping
 //     at a tile's end: the rings, the score tile and the P tiles go on counting,
-//     Q has two buffers (warp 2 fetches the next tile's rows), and only O is
-//     handed over (o_final, o_read);
-//   * K and V come through the page table: every lane of warp 0 finds one box
-//     of a block (as many rows as divide a page, 8 to 128) and copies it.  A box
+//     the softmax warps fetch the next tile's Q once the last scores are done,
+//     and only O is handed over (o_final, o_read);
+//   * K and V come through the page table: the lanes of warps 0 (K) and 2 (V)
+//     each find one box of a block (as many rows as divide a page, 8 to 128).  A box
 //     past the tile's last key, or of a page outside the pool, is read past the
 //     tensor's end, which fills it with zeros;
 //   * a box that the sequence ends in brings whatever the page holds behind the
@@ -52,7 +52,7 @@ namespace {
 constexpr int BM = 128;                   // query rows per tile (= TMEM lanes)
 constexpr int BN = kBlockKeys;            // keys per block
 constexpr int kHalf = 64;                 // keys of a block per softmax warpgroup
-constexpr int kThreads = 384;             // warp 0 K/V copies, 1 PV, 2 Q rows, 3 S, 4-11 softmax
+constexpr int kThreads = 384;             // warp 0 K copies, 1 PV, 2 V copies, 3 S, 4-11 softmax
 constexpr int kSoftmaxWarp0 = 4;
 constexpr int kChunkBytes = 128 * 128;    // 128 rows x 64 columns of 16 bits
 constexpr uint32_t kTmemCols = 512;
@@ -65,16 +65,18 @@ template <int D>
 struct TcLayout {
     static constexpr int kChunks = D / 64;                      // 128-byte swizzle atoms per row
     static constexpr int kTileBytes = kChunks * kChunkBytes;    // a Q, K or V tile
-    static constexpr int kRing = D == 128 ? 2 : 4;              // K slots, and V slots
-    static constexpr int kQOff = 0;                             // two Q buffers
-    static constexpr int kKOff = 2 * kTileBytes;
-    static constexpr int kVOff = kKOff + kRing * kTileBytes;
-    static constexpr int kXchOff = kVOff + kRing * kTileBytes;  // (m, l, l_o) of both halves
+    // K slots and V slots: a tile takes ~1500 clk to arrive, and V's products
+    // follow the softmax, so V is requested further ahead.
+    static constexpr int kRingK = D == 128 ? 2 : 4, kRingV = D == 128 ? 3 : 4;
+    static constexpr int kQOff = 0;
+    static constexpr int kKOff = kTileBytes;
+    static constexpr int kVOff = kKOff + kRingK * kTileBytes;
+    static constexpr int kXchOff = kVOff + kRingV * kTileBytes;  // (m, l, l_o) of both halves
     static constexpr int kXchBytes = 2 * 3 * BM * 4;
     static constexpr int kBarOff = kXchOff + kXchBytes;
-    // q_full[2], q_empty[2], k_full/k_empty/v_full/v_empty[R], s_full, s_read,
+    // q_full, k_full/k_empty[RK], v_full/v_empty[RV], s_full, s_read,
     // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
-    static constexpr int kBars = 4 + 4 * kRing + 2 + 4 + 4 + 4;
+    static constexpr int kBars = 1 + 2 * (kRingK + kRingV) + 2 + 4 + 4 + 4;
     static constexpr int kScanOff = kBarOff + 512;
     static constexpr int kSmemBytes = kScanOff + 128 + 1024;    // + alignment slack
     __device__ static constexpr uint32_t col_o(int h) { return kColO + (uint32_t)(h * D); }
@@ -86,23 +88,23 @@ struct TcLayout {
     static_assert((kThreads / 32 + 2) * 8 <= 128, "scratch of the line's share");
 };
 
-// A role's way along the CTA's piece of the line.
+// A role's way along the CTA's piece of the line, tile by tile: what a block
+// needs beyond its number is found once per tile, because the issuing threads
+// run alone and every instruction between two products counts (a walk that
+// asked at every block, with a division, made the kernel 1.7 times slower).
 struct Walk {
     LineCursor u;
-    int left;          // blocks from here to the end of the piece, this one included
-    bool begins;       // this block is the first of its tile in this piece
-    __device__ __forceinline__ bool ends() const { return left == 1 || u.c + 1 == u.n; }
-    __device__ __forceinline__ void next(const Line<BN> &line)
+    int left;          // blocks from here to the end of the piece
+    // blocks of this tile in the piece
+    __device__ __forceinline__ int count() const { return min(u.n - u.c, left); }
+    // past `done` = count() blocks; false at the end of the piece
+    __device__ __forceinline__ bool next_tile(const Line<BN> &line, int done)
     {
-        begins = u.c + 1 == u.n;
+        left -= done;
+        if (left == 0) return false;
+        u.c += done - 1;
         line.advance(u);
-        --left;
-    }
-    // Rows of this block's V that hold what lies behind the sequence's last
-    // key: from the length to the end of the box that it falls into.
-    __device__ __forceinline__ bool has_rest(int box_rows) const
-    {
-        return u.len < (int64_t)(u.c + 1) * BN && u.len % box_rows != 0 && u.len >= (int64_t)u.c * BN;
+        return true;
     }
 };
 
@@ -111,19 +113,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
 {
     using Lay = TcLayout<D>;
-    constexpr int kChunks = Lay::kChunks, kTileBytes = Lay::kTileBytes, R = Lay::kRing;
+    constexpr int kChunks = Lay::kChunks, kTileBytes = Lay::kTileBytes, RK = Lay::kRingK, RV = Lay::kRingV;
     constexpr int kQOff = Lay::kQOff, kKOff = Lay::kKOff, kVOff = Lay::kVOff;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff);
-    uint64_t *q_full = bars + 0;               // [2], 32 arrivals: the lanes that copy a tile's rows
-    uint64_t *q_empty = q_full + 2;            // [2]: every S product of the tile done
-    uint64_t *k_full = q_empty + 2;            // [R]
-    uint64_t *k_empty = k_full + R;            // [R]
-    uint64_t *v_full = k_empty + R;            // [R]
-    uint64_t *v_empty = v_full + R;            // [R]
-    uint64_t *s_full = v_empty + R;            // S of a block complete
+    uint64_t *q_full = bars + 0;               // a tile's rows are in place (8 arrivals)
+    uint64_t *k_full = bars + 1;               // [RK]
+    uint64_t *k_empty = k_full + RK;           // [RK]
+    uint64_t *v_full = k_empty + RK;           // [RV]
+    uint64_t *v_empty = v_full + RV;           // [RV]
+    uint64_t *s_full = v_empty + RV;           // S of a block complete
     uint64_t *s_read = s_full + 1;             // all softmax warps hold it in registers (8 arrivals)
     uint64_t *p_full = s_read + 1;             // [half][P tile]: P_h stored (4 arrivals)
     uint64_t *pv_done = p_full + 4;            // [half][P tile]: O_h += P_h V done
@@ -144,15 +145,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int64_t g0;
     line.template share<kThreads>(reinterpret_cast<int64_t *>(smem + Lay::kScanOff), walk.u, g0, walk.left);
     if (walk.left == 0) return;
-    walk.begins = true;
     const int blocks = walk.left;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < Lay::kBars; ++i) {
             uint32_t count = 1;
-            if (&bars[i] == s_read || &bars[i] == o_read) count = 8;              // one arrival per softmax warp
+            if (&bars[i] == q_full || &bars[i] == s_read || &bars[i] == o_read) count = 8;   // one per softmax warp
             if (&bars[i] >= p_full && &bars[i] < p_full + 4) count = 4;           // the four warps of a half
-            if (&bars[i] >= q_full && &bars[i] < q_full + 2) count = 32;
             ptx::mbar_init(&bars[i], count);
         }
         *abort_word = 0;
@@ -170,92 +169,55 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // Rows `first`, `first + step`, ... of a tile's Q into buffer `buf`, in the
-    // 128-byte-swizzled layout; rows past the last and columns past D are zero.
-    auto copy_q = [&](const LineCursor &u, int buf, int thread, int threads) {
-        const int b = u.g / p.part.tiles, row0 = (u.g - b * p.part.tiles) * BM;
-        constexpr int kUnits = D / 8;
-        const uint32_t dst = ptx::smem_u32(smem + kQOff + buf * kTileBytes);
-#pragma unroll 4
-        for (int e = thread; e < BM * kUnits; e += threads) {
-            const int row = e / kUnits, unit = e % kUnits;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (row0 + row < line.R && unit * 8 < p.c.D) {
-                const RowPlace r = row_place(p, b, u.h, row0 + row);
-                w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
-            }
-            ptx::st_shared_v4(dst + (unit / 8) * kChunkBytes + row * 128 + (((unit % 8) ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
-        }
-        ptx::fence_proxy_async_smem();
-    };
-
-    if (warp == 0) {
-        // ================= K and V copies =================
-        // In the order the products read them: K_0, K_1, V_0, K_2, V_1, ...
-        // Lane i < boxes finds and copies box i of a block.
+    if (warp == 0 || warp == 2) {
+        // ================= K copies (warp 0), V copies (warp 2) =================
+        // Lane i < boxes finds box i of a block; lane 0 copies them all.  One
+        // warp each: a copy costs its issuing thread ~100 clk, and with pages
+        // of 16 keys a block takes 32.
         const int box = p.box_rows, boxes = BN / box;
         const uint32_t page_size = (uint32_t)p.c.page_size;
-        struct Box { int page, slot, h; };
-        auto find = [&](const LineCursor &u) -> Box {
-            Box r{p.c.num_pages, 0, u.h};                       // past the tensor's end: zeros
-            const int64_t key = (int64_t)u.c * BN + lane * box;
-            if (lane < boxes && key < u.keys) {
+        const CUtensorMap *tm = warp == 0 ? &tm_k : &tm_v;
+        uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
+        uint8_t *slots = smem + (warp == 0 ? kKOff : kVOff);
+        const int ring = warp == 0 ? RK : RV;
+        int issued = 0, slot = 0;
+        uint32_t phase = 1;                                     // of the slot's last release
+        for (int t = 0; t < blocks; ++t) {
+            int page = p.c.num_pages, at = 0;                   // past the tensor's end: zeros
+            const int64_t key = (int64_t)walk.u.c * BN + lane * box;
+            if (lane < boxes && key < walk.u.keys) {
                 const uint32_t which = (uint32_t)key / page_size;
-                const int page = p.c.table[(int64_t)(u.g / p.part.tiles) * p.c.table_stride + which];
-                if (page >= 0 && page < p.c.num_pages) r.page = page;
-                r.slot = (int)((uint32_t)key - which * page_size);
+                const int x = p.c.table[(int64_t)(walk.u.g / p.part.tiles) * p.c.table_stride + which];
+                if (x >= 0 && x < p.c.num_pages) page = x;
+                at = (int)((uint32_t)key - which * page_size);
             }
-            return r;
-        };
-        auto load = [&](const CUtensorMap *tm, int off, uint64_t *full, uint64_t *empty, int t, const Box &x) -> bool {
-            const int slot = t % R;
-            if (t >= R && !__all_sync(0xffffffffu, wait_bounded(&empty[slot], ((t - R) / R) & 1, limit, kSiteSlotEmpty, ab)))
-                return false;
+            const int h = walk.u.h;
+            if (t + 1 < blocks) line.advance(walk.u);
+            bool ok = true;
+            if (t >= ring && lane == 0) ok = wait_bounded(&empty[slot], phase, limit, kSiteSlotEmpty, ab);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
             if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], kTileBytes);
-            __syncwarp();
-            if (lane < boxes)
-                for (int c = 0; c < kChunks; ++c)
-                    ptx::tma_load_4d(smem + off + slot * kTileBytes + c * kChunkBytes + lane * box * 128, tm, &full[slot],
-                                     c * 64, x.slot, x.h, x.page);
-            return true;
-        };
-        Box now = find(walk.u), then = now;
-        bool ok = load(&tm_k, kKOff, k_full, k_empty, 0, now);
-        int k_issued = ok ? 1 : 0, v_issued = 0;
-        for (int t = 0; t < blocks && ok; ++t) {
-            if (t + 1 < blocks) {
-                walk.next(line);
-                then = find(walk.u);
-                ok = load(&tm_k, kKOff, k_full, k_empty, t + 1, then);
-                k_issued += ok;
+#pragma unroll 2
+            for (int i = 0; i < boxes; ++i) {
+                const int box_page = __shfl_sync(0xffffffffu, page, i), box_at = __shfl_sync(0xffffffffu, at, i);
+                if (lane == 0)
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        ptx::tma_load_4d(slots + slot * kTileBytes + c * kChunkBytes + i * box * 128, tm, &full[slot], c * 64,
+                                         box_at, h, box_page);
             }
-            if (ok) {
-                ok = load(&tm_v, kVOff, v_full, v_empty, t, now);
-                v_issued += ok;
+            issued = t + 1;
+            if (++slot == ring) {
+                slot = 0;
+                phase ^= 1;
             }
-            now = then;
         }
         // Drain: no copy may still be landing in shared memory at exit.
-        for (int t = k_issued > R ? k_issued - R : 0; t < k_issued; ++t)
-            wait_bounded(&k_full[t % R], (t / R) & 1, limit, kSiteDrain, ab, false);
-        for (int t = v_issued > R ? v_issued - R : 0; t < v_issued; ++t)
-            wait_bounded(&v_full[t % R], (t / R) & 1, limit, kSiteDrain, ab, false);
-    } else if (warp == 2) {
-        // ================= the next tiles' Q =================
-        // (the softmax warps fetch the first tile's)
-        for (int tile = 1;; ++tile) {
-            // to the first block of the next tile in this piece
-            const int skip = min(walk.u.n - walk.u.c, walk.left);
-            walk.left -= skip;
-            if (walk.left == 0) break;
-            walk.u.c += skip - 1;
-            line.advance(walk.u);
-            if (tile >= 2 && !__all_sync(0xffffffffu, wait_bounded(&q_empty[tile & 1], ((tile - 2) >> 1) & 1, limit,
-                                                                    kSiteSlotEmpty, ab)))
-                break;
-            copy_q(walk.u, tile & 1, lane, 32);
-            ptx::mbar_arrive(&q_full[tile & 1]);
-        }
+        if (lane == 0)
+            for (int t = issued > ring ? issued - ring : 0; t < issued; ++t)
+                wait_bounded(&full[t % ring], (t / ring) & 1, limit, kSiteDrain, ab, false);
+        __syncwarp();
     } else if (warp == 3) {
         // ================= S products =================
         // S of block t into the score tile, once the softmax warps hold block
@@ -265,28 +227,28 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const uint64_t q_desc = make_sdesc(ptx::smem_u32(smem + kQOff), 16, 1024);
             const uint64_t k_desc = make_sdesc(ptx::smem_u32(smem + kKOff), 16, 1024);
             constexpr uint64_t kTileStep = kTileBytes >> 4;
-            int tile = -1;
-            for (int t = 0; t < blocks; ++t) {
-                bool ok = true;
-                if (walk.begins) {
-                    ++tile;
-                    ok = wait_bounded(&q_full[tile & 1], (tile >> 1) & 1, limit, kSiteQFull, ab);
-                }
-                ok = ok && wait_bounded(&k_full[t % R], (t / R) & 1, limit, kSiteSlotFull, ab);
-                if (ok && t > 0) ok = wait_bounded(s_read, (t - 1) & 1, limit, kSiteSFull, ab);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint64_t qd = q_desc + (uint64_t)(tile & 1) * kTileStep;
-                const uint64_t kd = k_desc + (uint64_t)(t % R) * kTileStep;
+            int t = 0;
+            bool ok = true;
+            for (int tile = 0;; ++tile) {
+                const int count = walk.count(), end = t + count;
+                ok = wait_bounded(q_full, tile & 1, limit, kSiteQFull, ab);
+#pragma unroll 1
+                for (; ok && t < end; ++t) {
+                    ok = wait_bounded(&k_full[t % RK], (t / RK) & 1, limit, kSiteSlotFull, ab);
+                    if (ok && t > 0) ok = wait_bounded(s_read, (t - 1) & 1, limit, kSiteSFull, ab);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t kd = k_desc + (uint64_t)(t % RK) * kTileStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (uint64_t)(((k / 4) * kChunkBytes + (k % 4) * 32) >> 4);
-                    ptx::mma_ss(tmem + kColS, qd + off, kd + off, idesc, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = (uint64_t)(((k / 4) * kChunkBytes + (k % 4) * 32) >> 4);
+                        ptx::mma_ss(tmem + kColS, q_desc + off, kd + off, idesc, k > 0);
+                    }
+                    ptx::mma_commit(s_full);
+                    ptx::mma_commit(&k_empty[t % RK]);
                 }
-                ptx::mma_commit(s_full);
-                ptx::mma_commit(&k_empty[t % R]);
-                if (walk.ends()) ptx::mma_commit(&q_empty[tile & 1]);
-                if (t + 1 < blocks) walk.next(line);
+                if (!ok) break;
+                if (!walk.next_tile(line, count)) break;
             }
             ptx::mma_commit(mma_drain_s);
             wait_bounded(mma_drain_s, 0, limit, kSiteDrain, ab, false);
@@ -300,48 +262,56 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         constexpr uint32_t idesc = make_idesc(BM, D, 0, 1, kF16);
         const uint64_t v_desc = make_sdesc(ptx::smem_u32(smem + kVOff), kChunkBytes, 1024);
         constexpr uint64_t kTileStep = kTileBytes >> 4;
-        int tile = 0;
-        for (int t = 0; t < blocks; ++t) {
+        auto issue = [&](int t, bool first, bool v_ready) -> bool {
             const int buf = t & 1;
+            if (!v_ready && !wait_bounded(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab)) return false;
+            const uint64_t vd = v_desc + (uint64_t)(t % RV) * kTileStep;
+            for (int h = 0; h < 2; ++h) {
+                if (!wait_bounded(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab)) return false;
+                ptx::tc_fence_after();
+                const uint32_t to = tmem + Lay::col_o(h), tp = tmem + Lay::col_p(buf, h);
+#pragma unroll
+                for (int k = 0; k < kHalf / 16; ++k)
+                    ptx::mma_ts(to, tp + k * 8, vd + (uint64_t)(((4 * h + k) * 2048) >> 4), idesc, (!first || k > 0) ? 1u : 0u);
+                ptx::mma_commit(&pv_done[h * 2 + buf]);
+            }
+            ptx::mma_commit(&v_empty[t % RV]);
+            return true;
+        };
+        int t = 0;
+        for (int tile = 0;; ++tile) {
+            const int count = walk.count(), end = t + count;
+            // Rows of the last block's V that hold what lies behind the
+            // sequence's last key: from there to the end of the box it is in.
+            const int from = walk.u.len - (walk.u.c + count - 1) * BN;
+            const bool rest = from < BN && (from & (p.box_rows - 1)) != 0;      // (a box has a power of two rows)
+            const int to = rest ? (from | (p.box_rows - 1)) + 1 : from;
             bool ok = true;
-            if (lane == 0) ok = wait_bounded(&v_full[t % R], (t / R) & 1, limit, kSiteSlotFull, ab);
+            if (lane == 0) {
+                if (tile > 0) ok = wait_bounded(o_read, (tile - 1) & 1, limit, kSiteOFinal, ab);
+                const int t0 = t;
+#pragma unroll 1
+                for (; ok && t < end - (rest ? 1 : 0); ++t) ok = issue(t, t == t0, false);
+                if (rest) ok = ok && wait_bounded(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab);
+            }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            if (walk.has_rest(p.box_rows)) {
-                const int from = walk.u.len - walk.u.c * BN;
-                const int to = (from + p.box_rows - 1) / p.box_rows * p.box_rows;
-                const uint32_t v = ptx::smem_u32(smem + kVOff + (t % R) * kTileBytes);
-                __syncwarp();
+            if (rest) {
+                t = end - 1;
+                const uint32_t v = ptx::smem_u32(smem + kVOff + (t % RV) * kTileBytes);
                 for (int e = lane; e < (to - from) * kChunks * 8; e += 32) {
                     const int row = from + e / (kChunks * 8), unit = e % (kChunks * 8);
                     ptx::st_shared_v4(v + (unit / 8) * kChunkBytes + row * 128 + ((unit % 8) << 4), 0u, 0u, 0u, 0u);
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0) ok = issue(t, count == 1, true);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
             }
-            if (lane == 0) {
-                if (walk.begins && tile > 0) ok = wait_bounded(o_read, (tile - 1) & 1, limit, kSiteOFinal, ab);
-                const uint64_t vd = v_desc + (uint64_t)(t % R) * kTileStep;
-                for (int h = 0; h < 2 && ok; ++h) {
-                    ok = wait_bounded(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t to = tmem + Lay::col_o(h), tp = tmem + Lay::col_p(buf, h);
-#pragma unroll
-                    for (int k = 0; k < kHalf / 16; ++k)
-                        ptx::mma_ts(to, tp + k * 8, vd + (uint64_t)(((4 * h + k) * 2048) >> 4), idesc,
-                                    (!walk.begins || k > 0) ? 1u : 0u);
-                    ptx::mma_commit(&pv_done[h * 2 + buf]);
-                }
-                if (ok) {
-                    ptx::mma_commit(&v_empty[t % R]);
-                    if (walk.ends()) ptx::mma_commit(o_final);
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            tile += walk.ends();
-            if (t + 1 < blocks) walk.next(line);
+            t = end;
+            if (lane == 0) ptx::mma_commit(o_final);
+            if (!walk.next_tile(line, count)) break;
         }
         if (lane == 0) {
             ptx::mma_commit(mma_drain);
@@ -358,13 +328,37 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const uint32_t tS = tmem + lane_off + kColS + (uint32_t)(h * kHalf);
         const float sl2 = p.scale_log2;
 
+        // The rows of the walk's tile into the Q buffer, in the 128-byte-swizzled
+        // layout; rows past the last and columns past D are zero.  The products
+        // that read the buffer before are done.
+        auto copy_q = [&] {
+            const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
+            constexpr int kUnits = D / 8;
+            const uint32_t dst = ptx::smem_u32(smem + kQOff);
+#pragma unroll 4
+            for (int e = thread; e < BM * kUnits; e += 256) {
+                const int row = e / kUnits, unit = e % kUnits;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (row0 + row < line.R && unit * 8 < p.c.D) {
+                    const RowPlace r = row_place(p, b, walk.u.h, row0 + row);
+                    w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
+                }
+                ptx::st_shared_v4(dst + (unit / 8) * kChunkBytes + row * 128 + (((unit % 8) ^ (row & 7)) << 4), w.x, w.y, w.z,
+                                  w.w);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_full);
+        };
+
         // the first tile's Q, and whether any page of this piece is hidden
-        copy_q(walk.u, 0, thread, 256);
+        copy_q();
         bool hidden = false;
         {
             Walk s = walk;
-            while (s.left > 0) {
-                const int count = min(s.u.n - s.u.c, s.left);
+            int count;
+            do {
+                count = s.count();
                 const uint32_t page_size = (uint32_t)p.c.page_size;
                 const uint32_t from = (uint32_t)(s.u.c * BN) / page_size;
                 const uint32_t last = (uint32_t)min((int64_t)s.u.keys, (int64_t)(s.u.c + count) * BN) - 1u;
@@ -373,24 +367,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     const int page = table[i];
                     hidden = hidden || page < 0 || page >= p.c.num_pages;
                 }
-                s.u.c += count - 1;
-                s.left -= count;
-                if (s.left > 0) line.advance(s.u);
-            }
+            } while (s.next_tile(line, count));
         }
         if (hidden) *hidden_word = 1;
-        // all of Q is in place: one warp makes the arrivals
         ptx::bar_sync(1, 256);
-        if (warp == kSoftmaxWarp0) ptx::mbar_arrive(&q_full[0]);
         hidden = *hidden_word != 0;
 
         int t = 0;
         bool ok = true;
-        for (int tile = 0; t < blocks; ++tile) {
-            const int count = min(walk.u.n - walk.u.c, walk.left);
+        for (int tile = 0;; ++tile) {
+            const int count = walk.count();
             const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
             const int row = row0 + r_local;
             const int lim = min(walk.u.len, line.masked ? walk.u.len - p.T + row / p.G + 1 : walk.u.len);
+            // Blocks from t_mask on have keys that some row of the tile does
+            // not see; a tile's first row sees the fewest.
+            const int least = min(walk.u.len, line.masked ? walk.u.len - p.T + row0 / p.G + 1 : walk.u.len);
+            const int t_mask = t + max(0, least) / BN - walk.u.c;
             OnlineRow<D, kF16, kHalf> st;
             for (int j = 0; j < count; ++j, ++t) {
                 const int buf = t & 1;
@@ -405,6 +398,32 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 // waited for below only if it was not
                 const bool p_free = t < 2 || ptx::mbar_test(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1);
                 ptx::tc_fence_after();
+                // Hidden keys become -inf in TMEM, eight at a time and only in
+                // blocks that have some: selects on the 64 registers of the row
+                // would lie in the middle of the loop, whose instruction
+                // fetches cost more than this detour.
+                if (t >= t_mask || hidden) {
+                    const int key0 = (walk.u.c + j) * BN + h * kHalf;
+#pragma unroll 1
+                    for (int k = 0; k < kHalf; k += 8) {
+                        bool gone = false;                        // (a page holds a multiple of 8 keys)
+                        if (hidden && key0 + k < walk.u.keys) {
+                            const int page = p.c.table[(int64_t)b * p.c.table_stride +
+                                                       (uint32_t)(key0 + k) / (uint32_t)p.c.page_size];
+                            gone = page < 0 || page >= p.c.num_pages;
+                        }
+                        const int vis = gone ? 0 : lim - (key0 + k);         // columns i < vis are visible
+                        if (!__any_sync(0xffffffffu, vis < 8)) continue;
+                        uint32_t x[8];
+                        ptx::tmem_ld8(tS + k, x);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i >= vis) x[i] = f2u(-INFINITY);
+                        ptx::tmem_st8(tS + k, x);
+                    }
+                    ptx::tmem_wait_st();
+                }
                 uint32_t s_raw[2][32];
                 ptx::tmem_ld32(tS, s_raw[0]);
                 ptx::tmem_ld32(tS + 32, s_raw[1]);
@@ -413,31 +432,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(s_read);
 
-                const int64_t key0 = (int64_t)(walk.u.c + j) * BN + h * kHalf;
-                const int64_t vis = lim - key0;                   // columns k < vis are visible
-                if (vis < kHalf) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (c * 32 + k >= vis) s_raw[c][k] = f2u(-INFINITY);
-                }
-                if (hidden) {
-                    const int32_t *table = p.c.table + (int64_t)b * p.c.table_stride;
-                    uint64_t bad = 0;                             // one bit per key of this half
-                    for (int k = 0; k < kHalf; k += 8)            // a page holds a multiple of 8 keys
-                        if (key0 + k < walk.u.keys) {
-                            const int page = table[(uint32_t)(key0 + k) / (uint32_t)p.c.page_size];
-                            if (page < 0 || page >= p.c.num_pages) bad |= 0xffull << k;
-                        }
-                    if (bad) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if ((bad >> (c * 32 + k)) & 1) s_raw[c][k] = f2u(-INFINITY);
-                    }
-                }
                 bool hook_ok = true;
                 auto before_o = [&] {
                     if (j > 0) {
@@ -461,6 +455,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     break;
                 }
             }
+
+            // The scores of the tile are done: the next tile's Q, while the last
+            // products run.
+            const LineCursor was = walk.u;
+            const bool more = walk.next_tile(line, count);
+            if (ok && more) copy_q();
 
             // ---- join the halves: m = max(m_A, m_B), w_h = 2^(m_h - m),
             // O = (w_A O_A + w_B O_B) / (w_A l_oA + w_B l_oB)
@@ -495,14 +495,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const float lse2 = empty ? -INFINITY : m + log2f(l_all);
 
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
-            const bool direct = count == walk.u.n && !p.joined;
-            const int64_t tile_id = (int64_t)walk.u.g * p.c.Hkv + walk.u.h;
+            const bool direct = count == was.n && !p.joined;
+            const int64_t tile_id = (int64_t)was.g * p.c.Hkv + was.h;
             const int64_t at = ((int64_t)blockIdx.x + tile_id) * BM + r_local;
-            if (thread == 0 && walk.u.c == 0) p.part.first_chunk[tile_id] = g0 + (t - count);
+            if (thread == 0 && was.c == 0) p.part.first_chunk[tile_id] = g0 + (t - count);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {
-                const RowPlace r = row_place(p, b, walk.u.h, row);
+                const RowPlace r = row_place(p, b, was.h, row);
                 o_row = p.o + r.b * p.o_s[0] + r.hq * p.o_s[1] + r.t * p.o_s[2];
                 if (h == 0) {
                     if (!direct)
@@ -544,9 +544,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
             }
             __syncwarp();
-            walk.u.c += count - 1;
-            walk.left -= count;
-            if (walk.left > 0) line.advance(walk.u);
+            if (!more) break;
         }
     }
     // ---- teardown ----------------------------------------------------------
