@@ -229,14 +229,14 @@ def fa_kv_append(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, interleaved
                  stream) -> int:
     """New tokens into a paged cache; `cache` is an fa_paged_kv, K, V, Q and
     Q_out are fa_rows (Q and Q_out may be None)."""
-    return int(load().fa_kv_append(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, int(rot_dim),
-                                   int(bool(interleaved)), int(position_offset), int(bool(f16)), stream))
+    return (_lib or load()).fa_kv_append(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, bool(interleaved),
+                                         position_offset, bool(f16), stream)
 
 
 def fa_fwd_paged(Q, cache, O, LSE, B, Hq, T, causal, scale, f16, workspace, workspace_bytes, stream) -> int:
     """Forward over a paged cache; Q and O are fa_rows, `cache` an fa_paged_kv."""
-    return int(load().fa_fwd_paged(Q, cache, O, LSE, B, Hq, T, int(bool(causal)), float(scale),
-                                   int(bool(f16)), workspace, int(workspace_bytes), stream))
+    return (_lib or load()).fa_fwd_paged(Q, cache, O, LSE, B, Hq, T, bool(causal), scale, bool(f16), workspace,
+                                         workspace_bytes, stream)
 
 
 def fa_fwd_paged_workspace_bytes(cache, B, Hq, T) -> int:
@@ -246,9 +246,8 @@ def fa_fwd_paged_workspace_bytes(cache, B, Hq, T) -> int:
 def fa_fwd_shared_prefix(Q, cache, prefix_table, prefix_len, O, LSE, B, Hq, T, causal, scale, f16, workspace,
                          workspace_bytes, stream) -> int:
     """fa_fwd_paged behind a prefix that all sequences share."""
-    return int(load().fa_fwd_shared_prefix(Q, cache, prefix_table, int(prefix_len), O, LSE, B, Hq, T,
-                                           int(bool(causal)), float(scale), int(bool(f16)), workspace,
-                                           int(workspace_bytes), stream))
+    return (_lib or load()).fa_fwd_shared_prefix(Q, cache, prefix_table, prefix_len, O, LSE, B, Hq, T, bool(causal),
+                                                 scale, bool(f16), workspace, workspace_bytes, stream)
 
 
 def fa_fwd_shared_prefix_workspace_bytes(cache, prefix_len, B, Hq, T) -> int:
@@ -459,67 +458,85 @@ class PagedKV:
         self.k_cache, self.v_cache, self.block_table, self.seq_len = k_cache, v_cache, block_table, seq_len
         pages, Hkv, page_size, D = k_cache.shape
         self.batch, self.Hkv, self.D, self.dtype, self.device = B, Hkv, D, k_cache.dtype, k_cache.device
+        self._f16, self._index, self._workspace_bytes = k_cache.dtype == torch.float16, k_cache.get_device(), {}
         sp, sh, ss, _ = k_cache.stride()
         # the stride of a dimension of one entry is never followed
         self.c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
                              ss if page_size > 1 else 0, pages, page_size, Hkv, D, block_table.data_ptr(),
                              block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
 
+    def workspace_bytes(self, Hq: int, T: int, prefix_len: int = 0) -> int:
+        """Bytes of workspace that forward_paged() (forward_shared_prefix()
+        behind a prefix) needs for queries [B, Hq, T, D]."""
+        key = (Hq, T, prefix_len)
+        need = self._workspace_bytes.get(key)
+        if need is None:
+            import torch
+            with torch.cuda.device(self.device):
+                need = fa_fwd_shared_prefix_workspace_bytes(self.c, prefix_len, self.batch, Hq, T)
+            if len(self._workspace_bytes) > 4096:
+                self._workspace_bytes.clear()
+            self._workspace_bytes[key] = need
+        return need
 
-def _followable(x):
-    """Whether the paged kernels can read `x` through its strides."""
-    s = x.stride()
-    return s[3] == 1 and not ((s[0] | s[1] | s[2]) & 7) and not (x.data_ptr() & 15)
 
-
-def _paged_input(x, what, cache, H, T=None):
+# A generation step is a few microseconds of GPU time: these calls look at each
+# property of a tensor once.
+def _paged_input(x, what, cache, shape):
     """fa_rows of a [B, H, T, D] input, and the tensor it points into."""
-    shape = x.shape
-    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.D or (H is not None and shape[1] != H) or \
-            (T is not None and shape[2] != T):
-        raise ValueError(f"{what} must have shape [B, {H if H is not None else 'Hq'}, T, D] to match the cache")
-    if x.dtype != cache.dtype or x.device != cache.device:
+    if x.shape != shape:
+        raise ValueError(f"{what} must have shape {list(shape)} to match the cache, not {list(x.shape)}")
+    if x.dtype is not cache.dtype or x.get_device() != cache._index:
         raise ValueError(f"{what} must have the cache's dtype and device")
-    if not _followable(x):
-        x = x.clone(memory_format=_contiguous_format())
-    s = x.stride()
-    return fa_rows(x.data_ptr(), s[0], s[1], s[2]), x
+    sb, sh, sn, sd = x.stride()
+    ptr = x.data_ptr()
+    if sd != 1 or (sb | sh | sn) & 7 or ptr & 15:
+        import torch
+        x = x.clone(memory_format=torch.contiguous_format)
+        sb, sh, sn, _ = x.stride()
+        ptr = x.data_ptr()
+    return fa_rows(ptr, sb, sh, sn), x
 
 
-def _paged_output(out, what, like, cache):
+def _paged_output(out, what, like):
     """fa_rows of an output like the [B, H, T, D] tensor `like`, and the tensor."""
     if out is None:
         out = like.new_empty(like.shape)
-    elif out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+    elif out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
         raise ValueError(f"{what} must be a tensor like q")
-    elif not _followable(out):
+    sb, sh, sn, sd = out.stride()
+    ptr = out.data_ptr()
+    if sd != 1 or (sb | sh | sn) & 7 or ptr & 15:
         raise ValueError(f"{what} must have a contiguous last dimension, strides that are multiples of 8 and "
                          "16-byte alignment")
-    s = out.stride()
-    return fa_rows(out.data_ptr(), s[0], s[1], s[2]), out
+    return fa_rows(ptr, sb, sh, sn), out
 
 
-def _contiguous_format():
-    import torch
-    return torch.contiguous_format
-
-
-def _on_stream(fn, device, stream, args):
-    """fn(*args, stream pointer) with `device` current; torch's allocations and
-    copies go to `stream` too when one is given."""
+def _on_stream(fn, cache, stream, args):
+    """fn(*args, stream pointer) with the cache's device current; torch's
+    allocations and copies go to `stream` too when one is given."""
     import torch
 
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
-        with torch.cuda.device(device):
-            return fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        if torch.cuda.current_device() == cache._index:
+            return fn(*args, _current_raw_stream(cache._index))
+        with torch.cuda.device(cache.device):
+            return fn(*args, _current_raw_stream(cache._index))
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(stream or 0, device=device)
-    if stream.device != device:
+        stream = torch.cuda.ExternalStream(stream or 0, device=cache.device)
+    if stream.device != cache.device:
         raise ValueError("stream must belong to the cache's device")
     with torch.cuda.stream(stream):
         return fn(*args, stream.cuda_stream)
+
+
+def _current_raw_stream(index: int) -> int:
+    """The pointer of torch's current stream: its short way where torch has it
+    (2 us less than making a Stream object)."""
+    import torch
+
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short(index) if short is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, position_offset: int = 0,
@@ -536,30 +553,34 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
     position_offset: position of a sequence's first key.  Runs asynchronously
     on `stream` (default: torch's current stream).
     """
-    return _on_stream(_kv_append, cache.device, stream, (cache, k, v, q, inv_freq, interleaved, position_offset, q_out))
+    return _on_stream(_kv_append, cache, stream, (cache, k, v, q, inv_freq, interleaved, position_offset, q_out))
 
 
 def _kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out, stream):
-    import torch
-
-    T = k.shape[2] if k.dim() == 4 else None
-    ck, k = _paged_input(k, "k", cache, cache.Hkv)
-    cv, v = _paged_input(v, "v", cache, cache.Hkv, T)
+    B, Hkv, D = cache.batch, cache.Hkv, cache.D
+    if k.dim() != 4:
+        raise ValueError("k must have shape [B, Hkv, T, D]")
+    T = k.shape[2]
+    shape = (B, Hkv, T, D)
+    ck, k = _paged_input(k, "k", cache, shape)
+    cv, v = _paged_input(v, "v", cache, shape)
     Hq, cq, co = 0, None, None
     if q is not None:
-        cq, q = _paged_input(q, "q", cache, None, T)
+        if q.dim() != 4:
+            raise ValueError("q must have shape [B, Hq, T, D]")
         Hq = q.shape[1]
-        co, q_out = _paged_output(q_out, "q_out", q, cache)
+        cq, q = _paged_input(q, "q", cache, (B, Hq, T, D))
+        co, q_out = _paged_output(q_out, "q_out", q)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     rot, freq = 0, None
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != cache.device:
+        import torch
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != cache._index:
             raise ValueError("inv_freq must be a float32 tensor of one dimension on the cache's device")
         inv_freq = inv_freq.contiguous()
         rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    st = fa_kv_append(cache.c, ck, cv, cq, co, cache.batch, Hq, T, freq, rot, interleaved, position_offset,
-                      cache.dtype == torch.float16, stream)
+    st = fa_kv_append(cache.c, ck, cv, cq, co, B, Hq, T, freq, rot, interleaved, position_offset, cache._f16, stream)
     if st != FA_OK:
         raise FAError(st, "fa_kv_append")
     return q_out
@@ -574,10 +595,9 @@ def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None,
     that see no key get O = 0 and LSE = -inf.  The other arguments are
     forward()'s; q may have any strides, and out too (last dimension
     contiguous).  The workspace (a CUDA tensor of at least
-    fa_fwd_paged_workspace_bytes bytes) is allocated here when not given.
+    cache.workspace_bytes(Hq, T) bytes) is allocated here when not given.
     """
-    return _on_stream(_forward_paged, cache.device, stream,
-                      (q, cache, None, 0, causal, scale, out, lse, return_lse, workspace))
+    return _on_stream(_forward_paged, cache, stream, (q, cache, None, 0, causal, scale, out, lse, return_lse, workspace))
 
 
 def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool = True, scale=None, out=None,
@@ -587,47 +607,54 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     prefix_table: int32 CUDA tensor with the prefix's pages in order (of the
     same pool); the cache's block_table and seq_len give what follows it.  The
     prefix is read once for the whole batch.  The workspace takes
-    fa_fwd_shared_prefix_workspace_bytes bytes.
+    cache.workspace_bytes(Hq, T, prefix_len) bytes.
     """
-    return _on_stream(_forward_paged, cache.device, stream,
+    return _on_stream(_forward_paged, cache, stream,
                       (q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace))
 
 
 def _forward_paged(q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace, stream):
     import torch
 
-    cq, q = _paged_input(q, "q", cache, None)
-    B, Hq, T, D = q.shape
-    if Hq % max(1, cache.Hkv):
+    if q.dim() != 4:
+        raise ValueError("q must have shape [B, Hq, T, D]")
+    B, Hkv, (_, Hq, T, _) = cache.batch, cache.Hkv, q.shape
+    cq, q = _paged_input(q, "q", cache, (B, Hq, T, cache.D))
+    if Hkv == 0 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the cache's key heads")
     pages = None
     if prefix_table is not None:
-        if prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or prefix_table.device != cache.device:
+        if prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or \
+                prefix_table.get_device() != cache._index:
             raise ValueError("prefix_table must be an int32 tensor of one dimension on the cache's device")
         prefix_len = int(prefix_len)
         if prefix_len < 0 or prefix_len > prefix_table.numel() * cache.c.page_size:
             raise ValueError("prefix_len must lie in [0, what prefix_table's pages hold]")
         prefix_table = prefix_table.contiguous()
         pages = prefix_table.data_ptr()
-    co, out = _paged_output(out, "out", q, cache)
+    co, out = _paged_output(out, "out", q)
     if lse is not None:
-        if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != cache.device or \
+        if lse.shape != (B, Hq, T) or lse.dtype is not torch.float32 or lse.get_device() != cache._index or \
                 not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
     elif return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    need = fa_fwd_shared_prefix_workspace_bytes(cache.c, prefix_len, B, Hq, T)
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, lse.data_ptr() if lse is not None else None,
-                              B, Hq, T, causal, float("nan") if scale is None else float(scale),
-                              cache.dtype == torch.float16, workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), stream)
+        size = max(cache.workspace_bytes(Hq, T, prefix_len), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
+    else:
+        if workspace.get_device() != cache._index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        size = workspace.numel() * workspace.element_size()
+    st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, None if lse is None else lse.data_ptr(), B, Hq, T,
+                              causal, _DEFAULT_SCALE if scale is None else scale, cache._f16, workspace.data_ptr(),
+                              size, stream)
     if st != FA_OK:
-        raise FAError(st, "fa_fwd_shared_prefix" if prefix_table is not None else "fa_fwd_paged")
+        raise FAError(st, "fa_fwd_paged" if prefix_table is None else "fa_fwd_shared_prefix")
     return (out, lse) if return_lse else out
+
+
+_DEFAULT_SCALE = float("nan")
 
 
 # ------------------------------------------------------------- autograd

@@ -77,6 +77,7 @@ template <bool kF16, int kMode>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
 {
     extern __shared__ float2 cs[];                          // [rot / 2]
+    ptx::wait_for_primary();
     const int64_t b = blockIdx.x / p.T;
     const int t = (int)(blockIdx.x % p.T);
     const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
@@ -185,15 +186,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
 template <bool kF16>
 cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)((int64_t)p.B * p.T);
+    const dim3 grid((unsigned)((int64_t)p.B * p.T));
     const size_t smem = (size_t)(p.rot / 2) * sizeof(float2);
     if (p.interleaved || p.rot == 0)
-        append_kernel<kF16, kNeighbours><<<grid, kThreads, smem, stream>>>(p);
-    else if (p.rot % 16 == 0)
-        append_kernel<kF16, kHalves><<<grid, kThreads, smem, stream>>>(p);
-    else
-        append_kernel<kF16, kHalvesOdd><<<grid, kThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+        return launch_behind(append_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
+    if (p.rot % 16 == 0) return launch_behind(append_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
+    return launch_behind(append_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
 }
 
 }  // namespace

@@ -6,9 +6,31 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace fa {
+
+// Division of n < 2^31 by a number known on the host: with s = ceil(log2 d)
+// and mul = ceil(2^(31+s) / d) < 2^32, mul * d exceeds 2^(31+s) by less than
+// 2^s, so floor(n * mul / 2^(31+s)) = floor(n / d).
+struct FastDiv {
+    uint32_t mul, shift, by;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int quotient(int n) const
+    {
+        return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
+    }
+#endif
+};
+
+inline FastDiv make_fast_div(uint32_t d)
+{
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < d) ++s;
+    const uint64_t top = (uint64_t)1 << (31 + s);
+    return FastDiv{(uint32_t)((top + d - 1) / d), 31 + s, d};
+}
 
 // A sequence's keys and values through the page table.  `table` has one row
 // of `table_width` page numbers per sequence, `table_stride` entries apart.
@@ -20,6 +42,7 @@ struct PagedCache {
     const int32_t *seq_len;            // null: every sequence has fixed_len keys
     int table_width;
     int num_pages, page_size;
+    FastDiv by_page;                   // page_size
     int fixed_len;
     int Hkv, D;
 };
@@ -34,23 +57,27 @@ struct AppendParams {
     int B, T, Hq, rot, interleaved, f16;
 };
 
+// Where a tile's partial states are.
+struct TileSlots {
+    int first, count;
+};
+
 // Partial softmax states of row tiles, which the merge joins.  A tile is
 // `rows` stacked query rows of one (sequence, key head), in the order of
-// fa_paged_line.cuh.  Its states are in slots, each `rows` normalised fp32
-// outputs of D columns and `rows` base-2 log-sum-exps.
+// fa_paged_line.cuh.  Its states are in slots: normalised fp32 outputs, four
+// columns of all rows after four columns of all rows (a warp that holds one row
+// per lane stores and the merge loads whole lines), and base-2 log-sum-exps.
+// Tile i has the slots k + i of the CTAs k that had a share of its chunks.
+// (Along the line, k and i never fall and one of them grows from share to
+// share, so no two shares have one slot.)
 struct Partials {
-    float *o;              // [slots][rows][D]
+    float *o;              // [slots][D / 4][rows][4]
     float *lse;            // [slots][rows]
+    TileSlots *tile;       // [tiles in all], of tiles with at least one chunk
     int rows;              // stacked query rows per tile
     int tiles;             // row tiles per (sequence, key head)
     int stacked;           // 1: one list of tiles for all sequences (a shared prefix)
     int chunk;             // keys per chunk of the line
-    // Tile i has the slots k + i of the CTAs k that had a share of its chunks.
-    // They follow from the tile's first chunk and the chunks per CTA.  (Along
-    // the line, k and i never fall and one of them grows from share to share,
-    // so no two shares have one slot.)
-    int64_t *first_chunk;  // [tiles in all]
-    int64_t *per_cta;      // [1]
     int fixed_len;         // stacked: keys of the prefix
 };
 
@@ -62,8 +89,10 @@ struct PagedParams {
     int64_t o_s[3];
     float *lse;                        // [B, Hq, T] or null
     int B, T, Hq, G;                   // G = Hq / Hkv query heads share a key head
+    FastDiv by_g, by_gt;               // G, G * T
     int causal, f16;
     float scale_log2;
+    int second;                        // 1: may start beside the kernel before, and ends after it
     int joined;                        // 1: every tile leaves its state in a slot for the merge
     Partials part;
     int box_rows;                      // tensor-core kernel: key rows per copied box
@@ -71,7 +100,7 @@ struct PagedParams {
 };
 
 struct MergeParams {
-    Partials src[2];
+    Partials src[2];                   // the sequences' own keys, then the prefix
     int n_src;
     const int32_t *seq_len;
     int max_len;
@@ -79,21 +108,64 @@ struct MergeParams {
     int64_t o_s[3];
     float *lse;
     int B, T, Hq, G, D, causal, f16;
+    FastDiv by_g;
     int joined;                        // 0: a tile that one CTA finished is written already
 };
 
-// Keys per chunk of the line: the row kernel's, and the tensor-core kernel's.
-constexpr int kChunkKeys = 64;
+// Keys per block of the tensor-core kernel.
 constexpr int kBlockKeys = 128;
 
-// Query rows per tile, and CTAs per SM, of the row kernel.
+// The row kernel's query rows per tile, keys per chunk and CTAs per SM.
 int paged_rows_per_tile(int D, int64_t rows);
+int paged_rows_chunk(int D);
 int paged_rows_ctas_per_sm(int D);
+
+// The current device's number, and its multiprocessors (148 if unknown).
+int current_device();
+int sm_count_of(int device);
+
+// Raises a kernel's dynamic shared memory limit once per device.
+class SharedMemory {
+  public:
+    template <typename... P>
+    cudaError_t allow(void (*kernel)(P...), int bytes)
+    {
+        const int dev = current_device();
+        const bool known = dev >= 0 && dev < 64;
+        if (known && (done_.load(std::memory_order_acquire) >> dev) & 1) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && known) done_.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+        return e;
+    }
+
+  private:
+    std::atomic<uint64_t> done_{0};
+};
+
+// Launches `kernel` so that its launch may overlap the end of the kernel before
+// it on the stream; the kernel itself waits for that one's end (and its
+// writes) before it touches memory that one may write.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_paged_rows(const PagedParams &p, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                             cudaStream_t stream);
-cudaError_t launch_paged_merge(const MergeParams &p, cudaStream_t stream);
+// states: about how many partial states a row has
+cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaStream_t stream);
 
 }  // namespace fa

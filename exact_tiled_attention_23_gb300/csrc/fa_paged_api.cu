@@ -59,6 +59,7 @@ fa::PagedCache cache_of(const fa_paged_kv &c)
     r.seq_len = c.seq_len;
     r.num_pages = c.num_pages;
     r.page_size = c.page_size;
+    r.by_page = fa::make_fast_div((uint32_t)c.page_size);
     r.Hkv = c.Hkv;
     r.D = c.D;
     return r;
@@ -69,15 +70,6 @@ void strides_of(int64_t (&s)[3], const fa_rows &r)
     s[0] = r.stride_b;
     s[1] = r.stride_h;
     s[2] = r.stride_n;
-}
-
-int sm_count()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        sms = 148;
-    return sms;
 }
 
 size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -115,10 +107,10 @@ struct Plan {
         const int Hkv = c.Hkv, D = c.D;
         box = rows > kMostRows ? tc_box_rows(c) : 0;
         part.rows = box ? 128 : fa::paged_rows_per_tile(D, rows);
-        part.chunk = box ? fa::kBlockKeys : fa::kChunkKeys;
+        part.chunk = box ? fa::kBlockKeys : fa::paged_rows_chunk(D);
         const int64_t tiles = (rows + part.rows - 1) / part.rows;
         items = (int64_t)nseq * Hkv * tiles;
-        if (rows > INT32_MAX / 2 || (int64_t)Hkv * tiles > INT32_MAX || items > INT32_MAX) {
+        if (rows > INT32_MAX / 2 || Hkv > 65535 || (int64_t)Hkv * tiles > INT32_MAX || items > INT32_MAX) {
             ok = false;
             return;
         }
@@ -126,20 +118,22 @@ struct Plan {
         part.stacked = stacked;
         part.fixed_len = stacked ? (int)keys : 0;
         const int64_t chunks = items * ((keys + part.chunk - 1) / part.chunk);
-        ctas = (int64_t)sm_count() * (box ? 1 : fa::paged_rows_ctas_per_sm(D));
+        if (chunks + 4096 > INT32_MAX) {                    // places on the line are 32-bit numbers
+            ok = false;
+            return;
+        }
+        ctas = (int64_t)fa::sm_count_of(fa::current_device()) * (box ? 1 : fa::paged_rows_ctas_per_sm(D));
         if (ctas > chunks) ctas = chunks > 0 ? chunks : 1;
         const size_t slots = (size_t)(ctas + items);
-        bytes = 256 + round_up((size_t)items * 8) + round_up(slots * part.rows * 4) + round_up(slots * part.rows * D * 4);
+        bytes = round_up((size_t)items * sizeof(fa::TileSlots)) + round_up(slots * part.rows * 4) + round_up(slots * part.rows * D * 4);
     }
 
     // Places the piece at `at`; returns its end.
     uint8_t *place(uint8_t *at, int D)
     {
         const size_t slots = (size_t)(ctas + items);
-        part.per_cta = reinterpret_cast<int64_t *>(at);
-        at += 256;
-        part.first_chunk = reinterpret_cast<int64_t *>(at);
-        at += round_up((size_t)items * 8);
+        part.tile = reinterpret_cast<fa::TileSlots *>(at);
+        at += round_up((size_t)items * sizeof(fa::TileSlots));
         part.lse = reinterpret_cast<float *>(at);
         at += round_up(slots * part.rows * 4);
         part.o = reinterpret_cast<float *>(at);
@@ -212,6 +206,8 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     p.T = T;
     p.Hq = Hq;
     p.G = G;
+    p.by_g = fa::make_fast_div((uint32_t)G);
+    p.by_gt = fa::make_fast_div((uint32_t)(G * T));
     p.causal = causal ? 1 : 0;
     p.f16 = f16 ? 1 : 0;
     const bool given = scale > 0.f && !std::isinf(scale);
@@ -220,6 +216,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     fa::MergeParams m{};
+    m.src[m.n_src++] = own.part;
     if (prefix_len > 0) {
         fa::PagedParams f = p;
         f.c.table = prefix_table;
@@ -229,9 +226,9 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
         f.c.fixed_len = prefix_len;
         if (!launch_part(f, *c, front, cs)) return FA_ERR_CUDA;
         m.src[m.n_src++] = front.part;
+        p.second = 1;
     }
     if (!launch_part(p, *c, own, cs)) return FA_ERR_CUDA;
-    m.src[m.n_src++] = own.part;
     m.seq_len = c->seq_len;
     m.max_len = (int)own_keys;
     m.o = p.o;
@@ -241,14 +238,37 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     m.T = T;
     m.Hq = Hq;
     m.G = G;
+    m.by_g = p.by_g;
     m.D = D;
     m.causal = p.causal;
     m.f16 = p.f16;
     m.joined = p.joined;
-    return fa::launch_paged_merge(m, cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    const int64_t states = own.ctas / own.items + 1 + (prefix_len > 0 ? front.ctas / front.items + 1 : 0);
+    return fa::launch_paged_merge(m, (int)states, fa::sm_count_of(fa::current_device()), cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
+
+namespace fa {
+
+int current_device()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+int sm_count_of(int device)
+{
+    static std::atomic<int> known[64];
+    if (device < 0) return 148;
+    if (device < 64 && known[device].load(std::memory_order_relaxed) > 0) return known[device].load(std::memory_order_relaxed);
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0) return 148;
+    if (device < 64) known[device].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+}  // namespace fa
 
 extern "C" {
 

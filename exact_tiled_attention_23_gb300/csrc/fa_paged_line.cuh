@@ -19,11 +19,11 @@ __device__ __forceinline__ int keys_of_sequence(const PagedParams &p, int b)
 }
 
 // Keys that at least one row of row tile `rt` sees, of a sequence of `len`.
-__device__ __forceinline__ int keys_of_tile(int len, int rt, int rows, int R, int G, int T, bool causal)
+__device__ __forceinline__ int keys_of_tile(int len, int rt, int rows, int R, FastDiv by_g, int T, bool causal)
 {
     if (!causal) return len;
     const int last = min((rt + 1) * rows, R) - 1;
-    return max(0, min(len, len - T + last / G + 1));
+    return max(0, min(len, len - T + by_g.quotient(last) + 1));
 }
 
 __device__ __forceinline__ int chunks_of(int keys, int chunk) { return (int)(((int64_t)keys + chunk - 1) / chunk); }
@@ -52,10 +52,10 @@ struct Line {
 
     __device__ __forceinline__ void enter(LineCursor &u, int g) const
     {
-        const int b = g / p.part.tiles;
+        const int b = p.part.tiles == 1 ? g : g / p.part.tiles;
         u.g = g;
         u.len = keys_of_sequence(p, b);
-        u.keys = keys_of_tile(u.len, g - b * p.part.tiles, p.part.rows, R, p.G, p.T, masked);
+        u.keys = keys_of_tile(u.len, g - b * p.part.tiles, p.part.rows, R, p.by_g, p.T, masked);
         u.n = chunks_of(u.keys, kChunk);
     }
 
@@ -76,70 +76,79 @@ struct Line {
     }
 
     // This CTA's piece of the line: where it starts, its first chunk counted
-    // along the line and how many it has.  The whole CTA calls it; `scratch`
-    // holds kThreads / 32 + 2 numbers.  Thread i sums the chunks of a strip of
-    // groups, and the strips' prefix sums find the group to start in.
+    // along the line, how many it has, and how many a full piece has.  The
+    // whole CTA calls it; `scratch` holds kThreads / 32 + 2 numbers.  Thread i
+    // sums the chunks of a strip of groups, and the strips' prefix sums find the
+    // group to start in.  (The host keeps the line below 2^31 chunks.)
     template <int kThreads>
-    __device__ __forceinline__ void share(int64_t *scratch, LineCursor &at, int64_t &first, int &count) const
+    __device__ __forceinline__ void share(int *scratch, LineCursor &at, int &first, int &count, int &per) const
     {
         constexpr int kWarps = kThreads / 32;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        int64_t total, base = 0;
+        int total, base = 0;
         at.h = at.c = 0;
         if (groups == 1) {
             enter(at, 0);
-            total = (int64_t)at.n * p.c.Hkv;
+            total = at.n * p.c.Hkv;
+            per = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
         } else {
             const int strip = (groups + kThreads - 1) / kThreads;
             const int g0 = min(tid * strip, groups), g1 = min(g0 + strip, groups);
-            int64_t sum = 0;
+            int sum = 0;
             LineCursor u;
             for (int g = g0; g < g1; ++g) {
                 enter(u, g);
                 sum += u.n;
             }
-            int64_t scan = sum;
+            int scan = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, scan, d);
+                const int v = __shfl_up_sync(0xffffffffu, scan, d);
                 if (lane >= d) scan += v;
             }
             if (lane == 31) scratch[warp] = scan;
             __syncthreads();
-            int64_t all = 0;
+            int all = 0;
             for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) scan += scratch[w];
                 all += scratch[w];
             }
             total = all * p.c.Hkv;
-            const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-            const int64_t start = per * blockIdx.x;
-            if (start < total && (scan - sum) * p.c.Hkv <= start && start < scan * p.c.Hkv) {
-                int64_t before = scan - sum;
+            per = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
+            const unsigned start = (unsigned)per * blockIdx.x;
+            if (start < (unsigned)total && (unsigned)((scan - sum) * p.c.Hkv) <= start &&
+                start < (unsigned)(scan * p.c.Hkv)) {
+                int before = scan - sum;
                 int g = g0;
                 for (;; ++g) {
                     enter(u, g);
-                    if (start < (before + u.n) * p.c.Hkv) break;
+                    if (start < (unsigned)((before + u.n) * p.c.Hkv)) break;
                     before += u.n;
                 }
                 scratch[kWarps] = g;
                 scratch[kWarps + 1] = before * p.c.Hkv;
             }
             __syncthreads();
-            if (start < total) {
-                enter(at, (int)scratch[kWarps]);
+            if (start < (unsigned)total) {
+                enter(at, scratch[kWarps]);
                 base = scratch[kWarps + 1];
             }
         }
-        const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-        if (blockIdx.x == 0 && tid == 0) *p.part.per_cta = per;
-        first = per * blockIdx.x;
-        const int64_t end = first + per < total ? first + per : total;
-        count = end > first ? (int)(end - first) : 0;
+        const unsigned start = (unsigned)per * blockIdx.x;
+        count = start < (unsigned)total ? min(per, total - (int)start) : 0;
+        first = (int)start;
         if (count > 0) {
-            at.h = (int)((first - base) / at.n);
-            at.c = (int)((first - base) - (int64_t)at.h * at.n);
+            at.h = (first - base) / at.n;
+            at.c = (first - base) - at.h * at.n;
         }
+    }
+
+    // The CTA that has the first chunk of a tile says where its states will be.
+    __device__ __forceinline__ void record(const LineCursor &u, int first_chunk, int per) const
+    {
+        const int tile = u.g * p.c.Hkv + u.h;
+        const int last = (int)((unsigned)(first_chunk + u.n - 1) / (unsigned)per);
+        p.part.tile[tile] = TileSlots{(int)blockIdx.x + tile, last - (int)blockIdx.x + 1};
     }
 };
 
@@ -152,10 +161,10 @@ struct RowPlace {
 __device__ __forceinline__ RowPlace row_place(const PagedParams &p, int b, int h, int idx)
 {
     if (p.part.stacked) {
-        b = idx / (p.G * p.T);
-        idx -= b * p.G * p.T;
+        b = p.by_gt.quotient(idx);
+        idx -= b * (int)p.by_gt.by;
     }
-    const int t = idx / p.G;
+    const int t = p.by_g.quotient(idx);
     return RowPlace{b, h * p.G + idx - t * p.G, t};
 }
 

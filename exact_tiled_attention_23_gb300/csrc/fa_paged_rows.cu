@@ -38,18 +38,19 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStepKeys = 16;                      // keys of a warp per step
-static_assert(kChunkKeys == kWarps * kStepKeys, "one step of every warp per chunk");
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int DP, int MT>
 struct RowsLayout {
     static constexpr int kRows = 16 * MT;
+    // Keys of a warp per step: 8 KB of K and V at D <= 128.  (At D = 64 with 16
+    // keys the chain of a step, not memory, set the pace: eight warps an SM.)
+    static constexpr int kStepKeys = DP == 64 ? 32 : 16;
+    static constexpr int kChunk = kWarps * kStepKeys;
     static constexpr int kRowBytes = 2 * DP;
     static constexpr int kTileBytes = kStepKeys * kRowBytes;      // K or V of a step
     static constexpr int kStageBytes = 2 * kTileBytes;
-    // as many stages as 96 KB hold (two CTAs per SM), three at D = 256 (one CTA)
-    static constexpr int kStages = DP == 64 ? 6 : 3;
+    static constexpr int kStages = 3;              // 96 KB: two CTAs per SM (192 KB, one CTA, at D = 256)
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = kRows * kRowBytes;
     static constexpr int kStatOff = kRingOff + kWarps * kStages * kStageBytes;
@@ -57,7 +58,7 @@ struct RowsLayout {
     static constexpr int kMaskOff = kStatOff + kStatBytes;        // valid keys of every stage
     static constexpr int kScanOff = kMaskOff + kWarps * kStages * 4;
     static constexpr int kSmemBytes = kScanOff + 128;
-    static_assert((kWarps + 2) * 8 <= 128, "scratch of the line's share");
+    static_assert((kWarps + 2) * 4 <= 128, "scratch of the line's share");
     static_assert(kStageBytes >= 16 * DP * 4, "an output tile fits a stage");
     static_assert(kSmemBytes * (DP == 256 ? 1 : 2) + (DP == 256 ? 1 : 2) * 1024 <= 233472, "shared memory per SM");
 };
@@ -75,7 +76,8 @@ template <int DP, int MT, bool kF16>
 __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel(const PagedParams p)
 {
     using Lay = RowsLayout<DP, MT>;
-    constexpr int S = Lay::kStages, RM = Lay::kRows, RB = Lay::kRowBytes;
+    constexpr int S = Lay::kStages, RM = Lay::kRows, RB = Lay::kRowBytes, KS = Lay::kStepKeys;
+    constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : 0xffffu;
     constexpr int NT = DP / 8;                      // 8-column tiles of O
     constexpr int KT = DP / 16;                     // 16-column steps of a score
     extern __shared__ __align__(128) uint8_t smem[];
@@ -83,49 +85,56 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
     float *s_m = reinterpret_cast<float *>(smem + Lay::kStatOff);
     float *s_l = s_m + kWarps * RM;
     uint32_t *s_mask = reinterpret_cast<uint32_t *>(smem + Lay::kMaskOff);
-    int64_t *s_scan = reinterpret_cast<int64_t *>(smem + Lay::kScanOff);
+    int *s_scan = reinterpret_cast<int *>(smem + Lay::kScanOff);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Line<kChunkKeys> line(p);
+    if (!p.second) ptx::wait_for_primary();
+    ptx::launch_dependents();
+    const Line<Lay::kChunk> line(p);
     LineCursor at;
-    int64_t g0;
-    int steps;
-    line.share<kThreads>(s_scan, at, g0, steps);
-    if (steps == 0) return;
+    int g0, steps, per;
+    line.template share<kThreads>(s_scan, at, g0, steps, per);
+    if (steps == 0) {
+        if (p.second) ptx::wait_for_primary();
+        return;
+    }
     const int R = line.R;
 
     // ---- loads -----------------------------------------------------------
-    const int kr = lane & 15;                       // the key of the step whose address this lane finds
+    const int kr = lane % KS;                       // the key of the step whose address this lane finds
     LineCursor ld = at;
     int ld_left = steps;
-    // The page number of a step's key is fetched one step before its use.
-    int pg = -1, pg_slot = 0, pg_head = 0;
-    auto look_up = [&] {
-        pg = -1;
-        if (ld_left <= 0) return;
-        const int key = ld.c * kChunkKeys + warp * kStepKeys + kr;
-        pg_head = ld.h;
+    // Where a step's key is.  Its page number is fetched at least one step
+    // before its use.
+    struct Place {
+        int page, slot, h;
+    };
+    auto look_up = [&]() -> Place {
+        Place x{-1, 0, ld.h};
+        if (ld_left <= 0) return x;
+        const int key = ld.c * Lay::kChunk + warp * KS + kr;
         if (key < ld.keys) {
-            const uint32_t which = (uint32_t)key / (uint32_t)p.c.page_size;
-            pg_slot = key - (int)which * p.c.page_size;
-            pg = p.c.table[(int64_t)(ld.g / p.part.tiles) * p.c.table_stride + which];
+            const int which = p.c.by_page.quotient(key);
+            const int b = p.part.tiles == 1 ? ld.g : ld.g / p.part.tiles;
+            x.slot = key - which * p.c.page_size;
+            x.page = p.c.table[(int64_t)b * p.c.table_stride + which];
         }
         line.advance(ld);
         --ld_left;
+        return x;
     };
     const uint32_t ring = s_base + Lay::kRingOff + warp * S * Lay::kStageBytes;
-    auto load = [&](int stage) {
-        const bool ok = pg >= 0 && pg < p.c.num_pages;
-        const int64_t off = ok ? (int64_t)pg * p.c.s_page + (int64_t)pg_head * p.c.s_head + (int64_t)pg_slot * p.c.s_slot : 0;
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    auto load = [&](int stage, const Place &x) {
+        const bool ok = x.page >= 0 && x.page < p.c.num_pages;
+        const int64_t off = ok ? (int64_t)x.page * p.c.s_page + (int64_t)x.h * p.c.s_head + (int64_t)x.slot * p.c.s_slot : 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAll;
         if (lane == 0) s_mask[warp * S + stage] = mask;
-        look_up();
         constexpr int kLanes = DP / 8 < 32 ? DP / 8 : 32;      // lanes per row
         constexpr int kRowsPer = 32 / kLanes;
         const int unit = lane % kLanes;
         const uint32_t dst = ring + stage * Lay::kStageBytes;
 #pragma unroll
-        for (int i = 0; i < kStepKeys / kRowsPer; ++i) {
+        for (int i = 0; i < KS / kRowsPer; ++i) {
             const int row = i * kRowsPer + lane / kLanes;
             const int64_t o = __shfl_sync(0xffffffffu, off, row);
             const uint32_t bytes = ((mask >> row) & 1u) && unit * 8 < p.c.D ? 16u : 0u;
@@ -136,37 +145,62 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
         }
         ptx::cp_async_commit();
     };
-    look_up();
+    Place next;
+    {
+        Place x[S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) load(s);            // steps past the share load zeros
+        for (int s = 0; s < S; ++s) x[s] = look_up();
+        next = look_up();
+#pragma unroll
+        for (int s = 0; s < S; ++s) load(s, x[s]);  // steps past the share load zeros
+    }
+    auto load_next = [&](int stage) {
+        const Place x = next;
+        next = look_up();
+        load(stage, x);
+    };
 
     // ---- the share, tile by tile ------------------------------------------
     const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a tile
     const uint32_t q_smem = s_base + Lay::kQOff;
+    // Q of a tile: this thread's 16-byte units, loaded before the tile before
+    // is joined where there are registers for them.
+    constexpr int kQUnits = RM * (DP / 8) / kThreads;
+    constexpr bool kQEarly = MT == 1;
+    uint4 q_next[kQUnits];
+    auto load_q = [&](const LineCursor &u, int i) -> uint4 {
+        const int e = tid + i * kThreads, unit = e % (DP / 8);
+        const int b = p.part.tiles == 1 ? u.g : u.g / p.part.tiles;
+        const int row = (u.g - b * p.part.tiles) * RM + e / (DP / 8);
+        if (row >= R || unit * 8 >= p.c.D) return make_uint4(0u, 0u, 0u, 0u);   // rows past R, columns past D
+        const RowPlace r = row_place(p, b, u.h, row);
+        return *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
+    };
+    if constexpr (kQEarly) {
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) q_next[i] = load_q(at, i);
+    }
     int stage = 0, done = 0;
     while (done < steps) {
         const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the share
-        const int b = at.g / p.part.tiles, row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
-        const int64_t tile = (int64_t)at.g * p.c.Hkv + h;
+        const int b = p.part.tiles == 1 ? at.g : at.g / p.part.tiles;
+        const int row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
+        const int tile = at.g * p.c.Hkv + h;
         const bool whole = count == at.n;
-        if (at.c == 0 && tid == 0) p.part.first_chunk[tile] = g0 + done;
-        // Q rows of the tile; rows past R and columns past D are zero
-        for (int e = tid; e < RM * (DP / 8); e += kThreads) {
-            const int row = e / (DP / 8), unit = e % (DP / 8);
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (row0 + row < R && unit * 8 < p.c.D) {
-                const RowPlace r = row_place(p, b, h, row0 + row);
-                w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
-            }
-            ptx::st_shared_v4(q_smem + unit_at<RB>(row, unit), w.x, w.y, w.z, w.w);
+        if (at.c == 0 && tid == 0) line.record(at, g0 + done, per);
+#pragma unroll
+        for (int i = 0; i < kQUnits; ++i) {
+            const int e = tid + i * kThreads;
+            const uint4 w = kQEarly ? q_next[i] : load_q(at, i);
+            ptx::st_shared_v4(q_smem + unit_at<RB>(e / (DP / 8), e % (DP / 8)), w.x, w.y, w.z, w.w);
         }
         int lim[2 * MT];                            // keys that this lane's rows see
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) {
-            const int t = (row0 + i * 8 + qr) / p.G;
+            const int t = p.by_g.quotient(row0 + i * 8 + qr);
             lim[i] = line.masked ? at.len - p.T + t + 1 : at.len;
         }
-        const int lim_all = line.masked ? at.len - p.T + row0 / p.G + 1 : at.len;   // seen by every row
+        const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
         __syncthreads();
 
         float o[MT][NT][4], m[2 * MT], l[2 * MT];
@@ -185,52 +219,59 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
             __syncwarp();
             const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
             const uint32_t mask = s_mask[warp * S + stage];
-            const int key0 = (at.c + step) * kChunkKeys + warp * kStepKeys;
+            const int key0 = (at.c + step) * Lay::kChunk + warp * KS;
             if (mask) {
-                float s[MT][2][4];
+                float s[MT][KS / 8][4];
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KT; ++k) {
-                    // K rows 0-7 and 8-15, columns 16k .. +7 and +8 .. +15
-                    uint32_t kb[4];
-                    ptx::ldmatrix4(kb, kt + unit_at<RB>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                    uint32_t qa[MT][4];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        uint32_t qa[4];
-                        ptx::ldmatrix4(qa, q_smem + unit_at<RB>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
-                        ptx::mma_16816<kF16>(s[i][0], qa, kb[0], kb[1]);
-                        ptx::mma_16816<kF16>(s[i][1], qa, kb[2], kb[3]);
+                    for (int i = 0; i < MT; ++i)
+                        ptx::ldmatrix4(qa[i], q_smem + unit_at<RB>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j) {
+                        // K rows 16j .. +7 and +8 .. +15, columns 16k .. +7 and +8 .. +15
+                        uint32_t kb[4];
+                        ptx::ldmatrix4(kb, kt + unit_at<RB>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            ptx::mma_16816<kF16>(s[i][2 * j], qa[i], kb[0], kb[1]);
+                            ptx::mma_16816<kF16>(s[i][2 * j + 1], qa[i], kb[2], kb[3]);
+                        }
                     }
                 }
-                if (mask != 0xffffu || key0 + kStepKeys > lim_all) {
+                if (mask != kAll || key0 + KS > lim_all) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int key = n * 8 + 2 * qc + (e & 1);
                                 if (!((mask >> key) & 1u) || key0 + key >= lim[2 * i + (e >> 1)]) s[i][n][e] = -INFINITY;
                             }
                 }
-                uint32_t hi[MT][4], lo[MT][4];
+                uint32_t hi[MT][KS / 16][4], lo[MT][KS / 16][4];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float &mr = m[2 * i + r], &lr = l[2 * i + r];
-                        float mx = fmaxf(fmaxf(s[i][0][2 * r], s[i][0][2 * r + 1]), fmaxf(s[i][1][2 * r], s[i][1][2 * r + 1]));
+                        float mx = fmaxf(s[i][0][2 * r], s[i][0][2 * r + 1]);
+#pragma unroll
+                        for (int n = 1; n < KS / 8; ++n) mx = ptx::max3(mx, s[i][n][2 * r], s[i][n][2 * r + 1]);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         const float m_new = fmaxf(mr, mx * p.scale_log2);
                         const float ref = m_new == -INFINITY ? 0.f : m_new;
-                        const float alpha = ptx::ex2_approx(mr - ref);
                         if (__any_sync(0xffffffffu, m_new != mr)) {
+                            const float alpha = ptx::ex2_approx(mr - ref);
                             lr *= alpha;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
@@ -239,41 +280,50 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                             }
                         }
                         mr = m_new;
-                        float pv[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            pv[e] = ptx::ex2_approx(fmaf(s[i][e >> 1][2 * r + (e & 1)], p.scale_log2, -ref));
-                            lr += pv[e];
-                        }
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const uint32_t w = ptx::pack16x2<kF16>(pv[2 * n], pv[2 * n + 1]);
+                        for (int n = 0; n < KS / 8; ++n) {
+                            const float p0 = ptx::ex2_approx(fmaf(s[i][n][2 * r], p.scale_log2, -ref));
+                            const float p1 = ptx::ex2_approx(fmaf(s[i][n][2 * r + 1], p.scale_log2, -ref));
+                            lr += p0 + p1;
+                            const uint32_t w = ptx::pack16x2<kF16>(p0, p1);
                             float r0, r1;
                             ptx::unpack2(ptx::widen16x2<kF16>(w), r0, r1);
-                            hi[i][2 * n + r] = w;
-                            lo[i][2 * n + r] = ptx::pack16x2<kF16>(pv[2 * n] - r0, pv[2 * n + 1] - r1);
+                            hi[i][n / 2][2 * (n & 1) + r] = w;
+                            lo[i][n / 2][2 * (n & 1) + r] = ptx::pack16x2<kF16>(p0 - r0, p1 - r1);
                         }
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < KT; ++n) {
-                    // V rows 0-7 and 8-15 (the product's k), columns 16n .. +7 and +8 .. +15
-                    uint32_t vb[4];
-                    ptx::ldmatrix4_trans(vb, vt + unit_at<RB>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+                for (int j = 0; j < KS / 16; ++j)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        ptx::mma_16816<kF16>(o[i][2 * n], hi[i], vb[0], vb[1]);
-                        ptx::mma_16816<kF16>(o[i][2 * n + 1], hi[i], vb[2], vb[3]);
-                        ptx::mma_16816<kF16>(o[i][2 * n], lo[i], vb[0], vb[1]);
-                        ptx::mma_16816<kF16>(o[i][2 * n + 1], lo[i], vb[2], vb[3]);
+                    for (int n = 0; n < KT; ++n) {
+                        // V rows 16j .. +7 and +8 .. +15 (the product's k), columns 16n .. +7 and +8 .. +15
+                        uint32_t vb[4];
+                        ptx::ldmatrix4_trans(vb, vt + unit_at<RB>(16 * j + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            ptx::mma_16816<kF16>(o[i][2 * n], hi[i][j], vb[0], vb[1]);
+                            ptx::mma_16816<kF16>(o[i][2 * n + 1], hi[i][j], vb[2], vb[3]);
+                            ptx::mma_16816<kF16>(o[i][2 * n], lo[i][j], vb[0], vb[1]);
+                            ptx::mma_16816<kF16>(o[i][2 * n + 1], lo[i][j], vb[2], vb[3]);
+                        }
                     }
-                }
             }
             __syncwarp();
             last_stage = stage;
             stage = stage + 1 == S ? 0 : stage + 1;
             // the tile's last stage is refilled after the warps' states are joined
-            if (step + 1 < count) load(last_stage);
+            if (step + 1 < count) load_next(last_stage);
+        }
+
+        at.c += count - 1;
+        line.advance(at);
+        done += count;
+        if constexpr (kQEarly) {
+            if (done < steps) {
+#pragma unroll
+                for (int i = 0; i < kQUnits; ++i) q_next[i] = load_q(at, i);
+            }
         }
 
         // ---- join the warps' states -----------------------------------------
@@ -303,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                 }
             __syncthreads();
             for (int e = tid; e < 16 * DP / 4; e += kThreads) {
-                const int row = e / (DP / 4), col = (e % (DP / 4)) * 4;
+                // along the columns for rows of O, along the rows for a slot
+                const int row = direct ? e / (DP / 4) : e % 16, col = (direct ? e % (DP / 4) : e / 16) * 4;
                 const int tr = i * 16 + row;
                 float top = -INFINITY;
 #pragma unroll
@@ -338,31 +389,28 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                     if (p.lse && col == 0) p.lse[((int64_t)r.b * p.Hq + r.hq) * p.T + r.t] = lse2 * kLn2;
                 } else {
                     if (col < p.c.D)
-                        *reinterpret_cast<float4 *>(p.part.o + (slot * RM + tr) * p.c.D + col) =
+                        reinterpret_cast<float4 *>(p.part.o)[(slot * (p.c.D / 4) + col / 4) * RM + tr] =
                             make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (col == 0) p.part.lse[slot * RM + tr] = lse2;
                 }
             }
             __syncthreads();
         }
-        load(last_stage);
-        at.c += count - 1;
-        line.advance(at);
-        done += count;
+        load_next(last_stage);
     }
     ptx::cp_async_wait<0>();
+    // the merge starts when this kernel has ended, and needs the one before too
+    if (p.second) ptx::wait_for_primary();
 }
 
 template <int DP, int MT, bool kF16>
 cudaError_t launch_rows(const PagedParams &p, int ctas, cudaStream_t stream)
 {
-    // per call: the attribute belongs to the current device
-    const cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<DP, MT, kF16>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               RowsLayout<DP, MT>::kSmemBytes);
+    static SharedMemory allowed;
+    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, MT, kF16>, RowsLayout<DP, MT>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    paged_rows_kernel<DP, MT, kF16><<<ctas, kThreads, RowsLayout<DP, MT>::kSmemBytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_behind(paged_rows_kernel<DP, MT, kF16>, dim3((unsigned)ctas), kThreads, RowsLayout<DP, MT>::kSmemBytes,
+                         stream, p);
 }
 
 template <int DP, int MT>
@@ -372,85 +420,152 @@ cudaError_t launch_rows_f(const PagedParams &p, int ctas, cudaStream_t stream)
 }
 
 // ---------------------------------------------------------------- merge
-// One warp per query row: the largest LSE of the row's partial states, their
-// weights, and the weighted sum of their outputs, in the order of the slots.
-// Lane i holds columns 4 i .. 4 i + 3 (and 128 + 4 i .. at D = 256).
-template <bool kF16>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const MergeParams p)
+// The sum of a row's partial outputs, weighted by their LSEs against the
+// largest.  A CTA has kRows rows of one (sequence, key head), kCols threads for
+// four columns each, and kZ threads for each of those, which take every kZ-th
+// state and are joined in order: a launch of few rows with many states each
+// (one sequence of 131072 keys: 38) waited 10 us for one thread's chain of
+// loads.  The lanes of a load are neighbours in the slots.
+constexpr int kMergeThreads = 256;
+
+template <int kCols, int kZ, bool kF16>
+__global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const MergeParams p, const int groups)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)p.B * p.Hq * p.T) return;
-    const int t = (int)(row % p.T);
-    const int hq = (int)(row / p.T % p.Hq);
-    const int b = (int)(row / ((int64_t)p.T * p.Hq));
-    const int h = hq / p.G;
+    constexpr int kRows = kMergeThreads / (kCols * kZ);
+    const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kCols, z = threadIdx.x / (kRows * kCols);
+    const int b = blockIdx.x / (unsigned)groups;
+    const int R = p.G * p.T, Hkv = p.Hq / p.G, h = blockIdx.y;
+    const int idx = (blockIdx.x - b * groups) * kRows + row;
+    const bool real = idx < R;
+    const int t = p.by_g.quotient(real ? idx : 0), hq = h * p.G + (real ? idx : 0) - t * p.G;
+
+    // before the kernels that write the states have ended
     int len = p.seq_len[b];
     len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
     const bool padding = p.causal && len - p.T + t < 0;        // no token here
-
-    int64_t slot0[2];
-    int count[2], tr[2];
+    int keys[2], at[2], tile[2];
+#pragma unroll
     for (int s = 0; s < 2; ++s) {
-        slot0[s] = 0;
-        count[s] = tr[s] = 0;
-        if (s >= p.n_src || padding) continue;
         const Partials &src = p.src[s];
-        const int idx = t * p.G + hq % p.G + (src.stacked ? b * p.G * p.T : 0);
-        const int rt = idx / src.rows;
-        tr[s] = idx - rt * src.rows;
-        const int64_t tile = ((int64_t)(src.stacked ? 0 : b) * src.tiles + rt) * (p.Hq / p.G) + h;
-        const int chunks = chunks_of(
-            keys_of_tile(src.stacked ? src.fixed_len : len, rt, src.rows, p.G * p.T, p.G, p.T, p.causal && !src.stacked),
-            src.chunk);
-        if (chunks == 0) continue;
-        const int64_t per = *src.per_cta, c0 = src.first_chunk[tile];
-        const int64_t k0 = c0 / per, k1 = (c0 + chunks - 1) / per;
-        slot0[s] = k0 + tile;
-        count[s] = (int)(k1 - k0 + 1);
+        const int i = (real ? idx : 0) + (src.stacked ? b * R : 0);
+        const int rt = s < p.n_src ? i / src.rows : 0;
+        at[s] = i - rt * src.rows;
+        tile[s] = ((src.stacked ? 0 : b) * src.tiles + rt) * Hkv + h;
+        keys[s] = s >= p.n_src || padding || !real
+                      ? 0
+                      : src.stacked ? src.fixed_len
+                                    : keys_of_tile(len, rt, src.rows, R, p.by_g, p.T, p.causal != 0);
     }
-    // one CTA had the whole tile and wrote the row itself
-    if (!p.joined && count[0] == 1) return;
+    ptx::wait_for_primary();
 
-    float top = -INFINITY;
-    for (int s = 0; s < p.n_src; ++s)
-        for (int i = lane; i < count[s]; i += 32)
-            top = fmaxf(top, p.src[s].lse[(slot0[s] + i) * p.src[s].rows + tr[s]]);
+    TileSlots x[2];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float ref = top == -INFINITY ? 0.f : top;
+    for (int s = 0; s < 2; ++s) x[s] = keys[s] > 0 ? p.src[s].tile[tile[s]] : TileSlots{0, 0};
+    // not a row, or one CTA had the whole tile and wrote the row itself
+    const bool skip = !real || (!p.joined && x[0].count == 1);
+    if constexpr (kZ == 1)
+        if (skip) return;
 
-    float sum = 0.f, acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int s = 0; s < p.n_src; ++s) {
-        const Partials &src = p.src[s];
-        for (int i = 0; i < count[s]; ++i) {
-            const int64_t at = (slot0[s] + i) * src.rows + tr[s];
-            const float w = ptx::ex2_approx(src.lse[at] - ref);
-            sum += w;
+    // A batch of states at a time, their LSEs and outputs loaded together; the
+    // sums follow the largest LSE so far.
+    constexpr int kBatch = 4;
+    for (int c = col4; c < (p.D / 4 + kCols - 1) / kCols * kCols; c += kCols) {
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!skip && c < p.D / 4) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int col = c * 128 + lane * 4;
-                if (col >= p.D) continue;
-                const float4 v = *reinterpret_cast<const float4 *>(src.o + at * p.D + col);
-                acc[c][0] = fmaf(w, v.x, acc[c][0]);
-                acc[c][1] = fmaf(w, v.y, acc[c][1]);
-                acc[c][2] = fmaf(w, v.z, acc[c][2]);
-                acc[c][3] = fmaf(w, v.w, acc[c][3]);
+            for (int s = 0; s < 2; ++s) {
+                const Partials &src = p.src[s];
+                const float *lse = src.lse + (int64_t)x[s].first * src.rows + at[s];
+                const int64_t step = (int64_t)(p.D / 4) * src.rows;
+                const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.rows + at[s];
+                for (int i = z; i < x[s].count; i += kBatch * kZ) {
+                    float y[kBatch];
+                    float4 v[kBatch];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        y[j] = -INFINITY;
+                        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i + j * kZ < x[s].count) {
+                            y[j] = lse[(int64_t)(i + j * kZ) * src.rows];
+                            v[j] = o[(i + j * kZ) * step];
+                        }
+                    }
+                    float next = top;
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) next = fmaxf(next, y[j]);
+                    const float ref = next == -INFINITY ? 0.f : next;
+                    const float f = ptx::ex2_approx(top - ref);
+                    top = next;
+                    sum *= f;
+                    acc.x *= f;
+                    acc.y *= f;
+                    acc.z *= f;
+                    acc.w *= f;
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const float w = ptx::ex2_approx(y[j] - ref);
+                        sum += w;
+                        acc.x = fmaf(w, v[j].x, acc.x);
+                        acc.y = fmaf(w, v[j].y, acc.y);
+                        acc.z = fmaf(w, v[j].z, acc.z);
+                        acc.w = fmaf(w, v[j].w, acc.w);
+                    }
+                }
             }
         }
-    }
-    const bool empty = sum == 0.f;
-    const float inv = empty ? 0.f : 1.f / sum;
+        if constexpr (kZ > 1) {
+            __shared__ float2 s_stat[kMergeThreads];
+            __shared__ float4 s_acc[kMergeThreads];
+            s_stat[threadIdx.x] = make_float2(top, sum);
+            s_acc[threadIdx.x] = acc;
+            __syncthreads();
+            if (z == 0) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int col = c * 128 + lane * 4;
-        if (col >= p.D) continue;
-        *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + col) =
+                for (int j = 1; j < kZ; ++j) {
+                    const float2 st = s_stat[threadIdx.x + j * kRows * kCols];
+                    const float4 v = s_acc[threadIdx.x + j * kRows * kCols];
+                    const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.f : next;
+                    const float f = ptx::ex2_approx(top - ref), w = ptx::ex2_approx(st.x - ref);
+                    top = next;
+                    sum = sum * f + w * st.y;
+                    acc.x = acc.x * f + w * v.x;
+                    acc.y = acc.y * f + w * v.y;
+                    acc.z = acc.z * f + w * v.z;
+                    acc.w = acc.w * f + w * v.w;
+                }
+            }
+            __syncthreads();
+        }
+        if (z != 0 || skip || c >= p.D / 4) continue;
+        const bool empty = sum == 0.f;
+        const float inv = empty ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c) =
             empty ? make_uint2(0u, 0u)
-                  : make_uint2(ptx::pack16x2<kF16>(acc[c][0] * inv, acc[c][1] * inv),
-                               ptx::pack16x2<kF16>(acc[c][2] * inv, acc[c][3] * inv));
+                  : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
+        if (p.lse && c == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
-    if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <int kCols, int kZ>
+cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream)
+{
+    constexpr int kRows = kMergeThreads / (kCols * kZ);
+    const int groups = (p.G * p.T + kRows - 1) / kRows;
+    const dim3 grid((unsigned)(p.B * groups), (unsigned)(p.Hq / p.G));
+    return p.f16 ? launch_behind(paged_merge_kernel<kCols, kZ, true>, grid, kMergeThreads, 0, stream, p, groups)
+                 : launch_behind(paged_merge_kernel<kCols, kZ, false>, grid, kMergeThreads, 0, stream, p, groups);
+}
+
+template <int kCols>
+cudaError_t launch_merge_z(const MergeParams &p, int z, cudaStream_t stream)
+{
+    switch (z) {
+    case 1: return launch_merge<kCols, 1>(p, stream);
+    case 2: return launch_merge<kCols, 2>(p, stream);
+    case 4: return launch_merge<kCols, 4>(p, stream);
+    default: return launch_merge<kCols, 8>(p, stream);
+    }
 }
 
 }  // namespace
@@ -458,6 +573,8 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const MergeParams p)
 // 16 rows where they hold the tile or where D = 256 leaves no registers for
 // more, else 32.
 int paged_rows_per_tile(int D, int64_t rows) { return rows <= 16 || D > 128 ? 16 : 32; }
+
+int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 1>::kChunk : D <= 128 ? RowsLayout<128, 1>::kChunk : RowsLayout<256, 1>::kChunk; }
 
 int paged_rows_ctas_per_sm(int D) { return D > 128 ? 1 : 2; }
 
@@ -469,15 +586,18 @@ cudaError_t launch_paged_rows(const PagedParams &p, int ctas, cudaStream_t strea
     return p.part.rows == 16 ? launch_rows_f<64, 1>(p, ctas, stream) : launch_rows_f<64, 2>(p, ctas, stream);
 }
 
-cudaError_t launch_paged_merge(const MergeParams &p, cudaStream_t stream)
+cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)p.B * p.Hq * p.T;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (p.f16)
-        paged_merge_kernel<true><<<grid, 128, 0, stream>>>(p);
-    else
-        paged_merge_kernel<false><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    // Threads per column that share a row's states: as many as leave each two
+    // or more, while the launch stays within one wave of CTAs.
+    const int cols = p.D <= 64 ? 16 : 32;
+    int z = 1;
+    while (z < 8 && 4 * z <= states) {
+        const int rows = kMergeThreads / (cols * 2 * z);
+        if ((int64_t)p.B * ((p.G * p.T + rows - 1) / rows) * (p.Hq / p.G) > 4 * sms) break;
+        z *= 2;
+    }
+    return p.D <= 64 ? launch_merge_z<16>(p, z, stream) : launch_merge_z<32>(p, z, stream);
 }
 
 }  // namespace fa

@@ -85,7 +85,7 @@ struct TcLayout {
     static_assert(kColO + 2 * D <= kTmemCols, "TMEM columns");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(kBars * 8 + 16 <= 512, "barrier area");
-    static_assert((kThreads / 32 + 2) * 8 <= 128, "scratch of the line's share");
+    static_assert((kThreads / 32 + 2) * 4 <= 128, "scratch of the line's share");
 };
 
 // A role's way along the CTA's piece of the line, tile by tile: what a block
@@ -142,9 +142,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const int lane = threadIdx.x & 31;
     const Line<BN> line(p);
     Walk walk;
-    int64_t g0;
-    line.template share<kThreads>(reinterpret_cast<int64_t *>(smem + Lay::kScanOff), walk.u, g0, walk.left);
-    if (walk.left == 0) return;
+    int g0, per;
+    if (!p.second) ptx::wait_for_primary();
+    ptx::launch_dependents();
+    line.template share<kThreads>(reinterpret_cast<int *>(smem + Lay::kScanOff), walk.u, g0, walk.left, per);
+    if (walk.left == 0) {
+        if (p.second) ptx::wait_for_primary();
+        return;
+    }
     const int blocks = walk.left;
 
     if (threadIdx.x == 0) {
@@ -175,7 +180,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // warp each: a copy costs its issuing thread ~100 clk, and with pages
         // of 16 keys a block takes 32.
         const int box = p.box_rows, boxes = BN / box;
-        const uint32_t page_size = (uint32_t)p.c.page_size;
         const CUtensorMap *tm = warp == 0 ? &tm_k : &tm_v;
         uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
         uint8_t *slots = smem + (warp == 0 ? kKOff : kVOff);
@@ -186,10 +190,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             int page = p.c.num_pages, at = 0;                   // past the tensor's end: zeros
             const int64_t key = (int64_t)walk.u.c * BN + lane * box;
             if (lane < boxes && key < walk.u.keys) {
-                const uint32_t which = (uint32_t)key / page_size;
+                const int which = p.c.by_page.quotient((int)key);
                 const int x = p.c.table[(int64_t)(walk.u.g / p.part.tiles) * p.c.table_stride + which];
                 if (x >= 0 && x < p.c.num_pages) page = x;
-                at = (int)((uint32_t)key - which * page_size);
+                at = (int)key - which * p.c.page_size;
             }
             const int h = walk.u.h;
             if (t + 1 < blocks) line.advance(walk.u);
@@ -332,19 +336,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // layout; rows past the last and columns past D are zero.  The products
         // that read the buffer before are done.
         auto copy_q = [&] {
-            const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
-            constexpr int kUnits = D / 8;
-            const uint32_t dst = ptx::smem_u32(smem + kQOff);
-#pragma unroll 4
-            for (int e = thread; e < BM * kUnits; e += 256) {
-                const int row = e / kUnits, unit = e % kUnits;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (row0 + row < line.R && unit * 8 < p.c.D) {
-                    const RowPlace r = row_place(p, b, walk.u.h, row0 + row);
-                    w = *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
-                }
-                ptx::st_shared_v4(dst + (unit / 8) * kChunkBytes + row * 128 + (((unit % 8) ^ (row & 7)) << 4), w.x, w.y, w.z,
-                                  w.w);
+            // two threads per row, so that a row's place is found once
+            const int b = walk.u.g / p.part.tiles, row = thread >> 1, idx = (walk.u.g - b * p.part.tiles) * BM + row;
+            constexpr int kUnits = D / 16;                        // 16-byte units per thread
+            const int unit0 = (thread & 1) * kUnits;
+            uint4 w[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (idx < line.R) {
+                const RowPlace r = row_place(p, b, walk.u.h, idx);
+                const uint16_t *src = p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2];
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+                    if ((unit0 + i) * 8 < p.c.D) w[i] = *reinterpret_cast<const uint4 *>(src + (unit0 + i) * 8);
+            }
+            const uint32_t dst = ptx::smem_u32(smem + kQOff) + row * 128;
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                const int unit = unit0 + i;
+                ptx::st_shared_v4(dst + (unit / 8) * kChunkBytes + (((unit % 8) ^ (row & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
@@ -359,11 +369,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             int count;
             do {
                 count = s.count();
-                const uint32_t page_size = (uint32_t)p.c.page_size;
-                const uint32_t from = (uint32_t)(s.u.c * BN) / page_size;
-                const uint32_t last = (uint32_t)min((int64_t)s.u.keys, (int64_t)(s.u.c + count) * BN) - 1u;
+                const int from = p.c.by_page.quotient(s.u.c * BN);
+                const int last = p.c.by_page.quotient((int)min((int64_t)s.u.keys, (int64_t)(s.u.c + count) * BN) - 1);
                 const int32_t *table = p.c.table + (int64_t)(s.u.g / p.part.tiles) * p.c.table_stride;
-                for (uint32_t i = from + thread; i <= last / page_size; i += 256) {
+                for (int i = from + thread; i <= last; i += 256) {
                     const int page = table[i];
                     hidden = hidden || page < 0 || page >= p.c.num_pages;
                 }
@@ -379,10 +388,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int count = walk.count();
             const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
             const int row = row0 + r_local;
-            const int lim = min(walk.u.len, line.masked ? walk.u.len - p.T + row / p.G + 1 : walk.u.len);
+            const int lim = min(walk.u.len, line.masked ? walk.u.len - p.T + p.by_g.quotient(row) + 1 : walk.u.len);
             // Blocks from t_mask on have keys that some row of the tile does
             // not see; a tile's first row sees the fewest.
-            const int least = min(walk.u.len, line.masked ? walk.u.len - p.T + row0 / p.G + 1 : walk.u.len);
+            const int least = min(walk.u.len, line.masked ? walk.u.len - p.T + p.by_g.quotient(row0) + 1 : walk.u.len);
             const int t_mask = t + max(0, least) / BN - walk.u.c;
             OnlineRow<D, kF16, kHalf> st;
             for (int j = 0; j < count; ++j, ++t) {
@@ -408,8 +417,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     for (int k = 0; k < kHalf; k += 8) {
                         bool gone = false;                        // (a page holds a multiple of 8 keys)
                         if (hidden && key0 + k < walk.u.keys) {
-                            const int page = p.c.table[(int64_t)b * p.c.table_stride +
-                                                       (uint32_t)(key0 + k) / (uint32_t)p.c.page_size];
+                            const int page = p.c.table[(int64_t)b * p.c.table_stride + p.c.by_page.quotient(key0 + k)];
                             gone = page < 0 || page >= p.c.num_pages;
                         }
                         const int vis = gone ? 0 : lim - (key0 + k);         // columns i < vis are visible
@@ -496,9 +504,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
-            const int64_t tile_id = (int64_t)was.g * p.c.Hkv + was.h;
-            const int64_t at = ((int64_t)blockIdx.x + tile_id) * BM + r_local;
-            if (thread == 0 && was.c == 0) p.part.first_chunk[tile_id] = g0 + (t - count);
+            const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
+            if (thread == 0 && was.c == 0) line.record(was, g0 + (t - count), per);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {
@@ -506,7 +513,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 o_row = p.o + r.b * p.o_s[0] + r.hq * p.o_s[1] + r.t * p.o_s[2];
                 if (h == 0) {
                     if (!direct)
-                        p.part.lse[at] = lse2;
+                        p.part.lse[slot * BM + r_local] = lse2;
                     else if (p.lse)
                         p.lse[((int64_t)r.b * p.Hq + r.hq) * p.T + r.t] = lse2 * kLn2;
                 }
@@ -537,9 +544,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                             make_uint4(ptx::pack16x2<kF16>(x[0], x[1]), ptx::pack16x2<kF16>(x[2], x[3]),
                                        ptx::pack16x2<kF16>(x[4], x[5]), ptx::pack16x2<kF16>(x[6], x[7]));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part.o + at * p.c.D + col + 8 * k);
+                        float4 *dst = reinterpret_cast<float4 *>(p.part.o) +
+                                      (slot * (p.c.D / 4) + (col + 8 * k) / 4) * BM + r_local;
                         dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-                        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+                        dst[BM] = make_float4(x[4], x[5], x[6], x[7]);
                     }
                 }
             }
@@ -554,17 +562,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }
+    // the merge starts when this kernel has ended, and needs the one before too
+    if (p.second) ptx::wait_for_primary();
 }
 
 template <int D, bool kF16>
 cudaError_t launch(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
-    // per call: the attribute belongs to the current device
-    const cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               TcLayout<D>::kSmemBytes);
+    static SharedMemory allowed;
+    const cudaError_t e = allowed.allow(paged_tc_kernel<D, kF16>, TcLayout<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    paged_tc_kernel<D, kF16><<<ctas, kThreads, TcLayout<D>::kSmemBytes, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch_behind(paged_tc_kernel<D, kF16>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes, stream, tk, tv, p);
 }
 
 }  // namespace

@@ -366,6 +366,15 @@ __device__ __forceinline__ void st_shared_v4(uint32_t saddr, uint32_t a, uint32_
 }
 
 
+// ---------------------------------------------------------------- launches
+// Kernels launched to overlap this one's end may start once every CTA of this
+// grid has said so (or exited).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Wait until the kernel that this one was launched behind has ended and its
+// writes are visible (returns at once in an ordinary launch).
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- warp tiles
 // 16 bytes from global to shared memory; `bytes` < 16 fills the rest with zeros.
 __device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src, uint32_t bytes)
