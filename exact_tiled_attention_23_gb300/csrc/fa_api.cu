@@ -439,12 +439,13 @@ const char *fa_status_string(fa_status s)
 
 fa_status fa_device_status(void *stream)
 {
-    uint32_t v = 0, vb = 0, vd = 0, vh = 0, vp = 0;
+    uint32_t v = 0, vb = 0, vd = 0, vh = 0, vp = 0, vr = 0;
     if (fa::read_and_clear_status(static_cast<cudaStream_t>(stream), &v) != cudaSuccess ||
         fa::read_and_clear_status_bwd(&vb) != cudaSuccess || fa::read_and_clear_status_onetile(&vd) != cudaSuccess ||
-        fa::read_and_clear_status_halves(&vh) != cudaSuccess || fa::read_and_clear_status_paged(&vp) != cudaSuccess)
+        fa::read_and_clear_status_halves(&vh) != cudaSuccess || fa::read_and_clear_status_paged(&vp) != cudaSuccess ||
+        fa::read_and_clear_status_paged_rows(&vr) != cudaSuccess)
         return FA_ERR_CUDA;
-    v |= vb | vd | vh | vp;
+    v |= vb | vd | vh | vp | vr;
     if (v) {
         g_last_detail = v;
         if (v & fa::kStatusTimeout) return FA_ERR_TIMEOUT;

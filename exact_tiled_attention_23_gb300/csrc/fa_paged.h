@@ -67,19 +67,37 @@ struct TileSlots {
 // fa_paged_line.cuh.  Its states are in slots: normalised fp32 outputs, four
 // columns of all rows after four columns of all rows (a warp that holds one row
 // per lane stores and the merge loads whole lines), and base-2 log-sum-exps.
-// Tile i has the slots k + i of the CTAs k that had a share of its chunks.
+// Tile i has the slots k + i of the pieces k that have some of its chunks.
 // (Along the line, k and i never fall and one of them grows from share to
 // share, so no two shares have one slot.)
 struct Partials {
-    float *o;              // [slots][D / 4][rows][4]
-    float *lse;            // [slots][rows]
+    float *o;              // [slots][D / 4][slot_rows][4]
+    float *lse;            // [slots][slot_rows]
     TileSlots *tile;       // [tiles in all], of tiles with at least one chunk
     int rows;              // stacked query rows per tile
+    int slot_rows;         // rows of a slot: rows, or fewer where the only tile has fewer
     int tiles;             // row tiles per (sequence, key head)
     int stacked;           // 1: one list of tiles for all sequences (a shared prefix)
     int chunk;             // keys per chunk of the line
     int fixed_len;         // stacked: keys of the prefix
 };
+
+// A shared prefix on the tensor cores beside the sequences' own keys in the
+// row kernel: the first is bound by its chain of products and softmax, the
+// second by memory, so they run at the same time, each on some of the SMs, in
+// proportion to their work.  Both kernels work the split out from seq_len.
+struct Beside {
+    int on;
+    int sms, per_sm;                   // pieces of the row kernel per SM
+    int blocks;                        // 128-key blocks of the prefix's tiles
+    int chunk, tiles;                  // own keys per chunk; tiles per sequence (row tiles * Hkv)
+    const int32_t *seq_len;
+    int cap, B;                        // most keys of a sequence; sequences
+};
+
+// Own chunks (8 KB of keys and values at D = 64 and 128) that cost an SM as
+// much time as one block.
+constexpr int kBlockCost = 10;
 
 struct PagedParams {
     PagedCache c;
@@ -95,7 +113,8 @@ struct PagedParams {
     int second;                        // 1: may start beside the kernel before, and ends after it
     int joined;                        // 1: every tile leaves its state in a slot for the merge
     Partials part;
-    int box_rows;                      // tensor-core kernel: key rows per copied box
+    Beside beside;
+    int box_rows;                      // key rows per copied box (row kernel: 0 = 16-byte copies)
     uint64_t wait_limit_ns;
 };
 
@@ -115,10 +134,12 @@ struct MergeParams {
 // Keys per block of the tensor-core kernel.
 constexpr int kBlockKeys = 128;
 
-// The row kernel's query rows per tile, keys per chunk and CTAs per SM.
+// The row kernel's query rows per tile, keys per chunk, warps (each with a
+// piece of the line) per CTA, and CTAs per SM.
 int paged_rows_per_tile(int D, int64_t rows);
 int paged_rows_chunk(int D);
-int paged_rows_ctas_per_sm(int D);
+constexpr int kRowsWarps = 4;
+int paged_rows_ctas_per_sm(int D, int rows);
 
 // The current device's number, and its multiprocessors (148 if unknown).
 int current_device();
@@ -162,7 +183,9 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 }
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
-cudaError_t launch_paged_rows(const PagedParams &p, int ctas, cudaStream_t stream);
+// (tk, tv are read only where p.box_rows > 0)
+cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                              cudaStream_t stream);
 cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                             cudaStream_t stream);
 // states: about how many partial states a row has

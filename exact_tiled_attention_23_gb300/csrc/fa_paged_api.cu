@@ -7,6 +7,7 @@
 #include "fa_internal.h"
 #include "fa_paged.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -77,13 +78,12 @@ size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // Most stacked rows that the row kernel takes where the tensor-core kernel could.
 constexpr int64_t kMostRows = 32;
 
-// Key rows per box that the tensor-core kernel copies from this pool: the
-// largest power of two, 8 (the rows of a swizzle atom) to 128, that divides a
-// page.  0 where it cannot: other page sizes, D = 256 (its TMEM layout holds
-// two O tiles of at most 128 columns), strides past a tensor map's range.
-int tc_box_rows(const fa_paged_kv &c)
+// Key rows per TMA box of this pool: the largest power of two, 8 (the rows of a
+// swizzle atom) to 128, that divides a page.  0 where TMA cannot copy it: other
+// page sizes, strides past a tensor map's range.
+int box_rows_of(const fa_paged_kv &c)
 {
-    if (c.D > 128 || c.page_size % 8 != 0 || c.num_pages <= 0) return 0;
+    if (c.page_size % 8 != 0 || c.num_pages <= 0) return 0;
     const int64_t far = (int64_t)1 << 38;
     if (c.stride_page >= far || c.stride_head >= far || c.stride_slot >= far) return 0;
     int box = 8;
@@ -97,17 +97,21 @@ struct Plan {
     fa::Partials part{};
     int64_t items = 0;      // tiles in all
     int64_t ctas = 0;
+    int64_t pieces = 0;     // of the line: one per CTA, or per warp of the row kernel
     size_t bytes = 0;
     bool ok = true;
-    int box = 0;            // key rows per box of the tensor-core kernel, 0: the row kernel
+    bool tc = false;        // the tensor-core kernel (else the row kernel)
+    int box = 0;            // key rows per TMA box, 0: no TMA
 
     // rows: stacked query rows per (sequence, key head); keys: most keys of a sequence
     Plan(int nseq, const fa_paged_kv &c, int64_t rows, int64_t keys, bool stacked)
     {
         const int Hkv = c.Hkv, D = c.D;
-        box = rows > kMostRows ? tc_box_rows(c) : 0;
-        part.rows = box ? 128 : fa::paged_rows_per_tile(D, rows);
-        part.chunk = box ? fa::kBlockKeys : fa::paged_rows_chunk(D);
+        box = box_rows_of(c);
+        tc = box > 0 && D <= 128 && rows > kMostRows;    // (TMEM holds two O tiles of 128 columns at most)
+        if (!tc) box = std::min(box, fa::paged_rows_chunk(D));
+        part.rows = tc ? 128 : fa::paged_rows_per_tile(D, rows);
+        part.chunk = tc ? fa::kBlockKeys : fa::paged_rows_chunk(D);
         const int64_t tiles = (rows + part.rows - 1) / part.rows;
         items = (int64_t)nseq * Hkv * tiles;
         if (rows > INT32_MAX / 2 || Hkv > 65535 || (int64_t)Hkv * tiles > INT32_MAX || items > INT32_MAX) {
@@ -122,22 +126,25 @@ struct Plan {
             ok = false;
             return;
         }
-        ctas = (int64_t)fa::sm_count_of(fa::current_device()) * (box ? 1 : fa::paged_rows_ctas_per_sm(D));
-        if (ctas > chunks) ctas = chunks > 0 ? chunks : 1;
-        const size_t slots = (size_t)(ctas + items);
-        bytes = round_up((size_t)items * sizeof(fa::TileSlots)) + round_up(slots * part.rows * 4) + round_up(slots * part.rows * D * 4);
+        ctas = (int64_t)fa::sm_count_of(fa::current_device()) * (tc ? 1 : fa::paged_rows_ctas_per_sm(D, part.rows));
+        const int each = tc ? 1 : fa::kRowsWarps;
+        ctas = std::max<int64_t>(1, std::min(ctas, (chunks + each - 1) / each));
+        pieces = ctas * each;
+        part.slot_rows = (int)std::min<int64_t>(part.rows, tiles == 1 ? (tc ? 128 : rows) : part.rows);
+        const size_t slots = (size_t)(pieces + items);
+        bytes = round_up((size_t)items * sizeof(fa::TileSlots)) + round_up(slots * part.slot_rows * 4) + round_up(slots * part.slot_rows * D * 4);
     }
 
     // Places the piece at `at`; returns its end.
     uint8_t *place(uint8_t *at, int D)
     {
-        const size_t slots = (size_t)(ctas + items);
+        const size_t slots = (size_t)(pieces + items);
         part.tile = reinterpret_cast<fa::TileSlots *>(at);
         at += round_up((size_t)items * sizeof(fa::TileSlots));
         part.lse = reinterpret_cast<float *>(at);
-        at += round_up(slots * part.rows * 4);
+        at += round_up(slots * part.slot_rows * 4);
         part.o = reinterpret_cast<float *>(at);
-        return at + round_up(slots * part.rows * D * 4);
+        return at + round_up(slots * part.slot_rows * D * 4);
     }
 };
 
@@ -145,20 +152,21 @@ struct Plan {
 bool launch_part(fa::PagedParams p, const fa_paged_kv &c, const Plan &plan, cudaStream_t stream)
 {
     p.part = plan.part;
-    if (!plan.box) return fa::launch_paged_rows(p, (int)plan.ctas, stream) == cudaSuccess;
+    CUtensorMap tk{}, tv{};
+    p.box_rows = plan.box;
+    p.wait_limit_ns = fa::wait_budget_ns();
+    if (!plan.box) return fa::launch_paged_rows(p, tk, tv, (int)plan.ctas, stream) == cudaSuccess;
     // [D, slot, head, page]; the stride of a dimension of one entry is not followed
     const uint64_t row = (uint64_t)c.D * 2;
     const uint64_t dims[4] = {(uint64_t)c.D, (uint64_t)c.page_size, (uint64_t)c.Hkv, (uint64_t)c.num_pages};
     const uint64_t strides[3] = {(uint64_t)c.stride_slot * 2, c.Hkv > 1 ? (uint64_t)c.stride_head * 2 : row,
                                  c.num_pages > 1 ? (uint64_t)c.stride_page * 2 : row};
     const uint32_t box[4] = {64, (uint32_t)plan.box, 1, 1};
-    CUtensorMap tk, tv;
     if (!fa::encode_tiled16(&tk, c.k, 4, dims, strides, box, p.f16 != 0) ||
         !fa::encode_tiled16(&tv, c.v, 4, dims, strides, box, p.f16 != 0))
         return false;
-    p.box_rows = plan.box;
-    p.wait_limit_ns = fa::wait_budget_ns();
-    return fa::launch_paged_tc(p, tk, tv, (int)plan.ctas, stream) == cudaSuccess;
+    return (plan.tc ? fa::launch_paged_tc(p, tk, tv, (int)plan.ctas, stream)
+                    : fa::launch_paged_rows(p, tk, tv, (int)plan.ctas, stream)) == cudaSuccess;
 }
 
 // Sizes of a paged forward; `keys` is what a table row can hold.
@@ -218,6 +226,15 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     fa::MergeParams m{};
     m.src[m.n_src++] = own.part;
     if (prefix_len > 0) {
+        p.beside.on = front.tc && !own.tc;
+        p.beside.sms = fa::sm_count_of(fa::current_device());
+        p.beside.per_sm = fa::paged_rows_ctas_per_sm(D, own.part.rows) * fa::kRowsWarps;
+        p.beside.blocks = (int)(front.items * ((prefix_len + front.part.chunk - 1) / front.part.chunk));
+        p.beside.chunk = own.part.chunk;
+        p.beside.tiles = own.part.tiles * c->Hkv;
+        p.beside.seq_len = c->seq_len;
+        p.beside.cap = (int)own_keys;
+        p.beside.B = B;
         fa::PagedParams f = p;
         f.c.table = prefix_table;
         f.c.table_width = (int)((prefix_len + (int64_t)c->page_size - 1) / c->page_size);
@@ -243,7 +260,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     m.causal = p.causal;
     m.f16 = p.f16;
     m.joined = p.joined;
-    const int64_t states = own.ctas / own.items + 1 + (prefix_len > 0 ? front.ctas / front.items + 1 : 0);
+    const int64_t states = own.pieces / own.items + 1 + (prefix_len > 0 ? front.pieces / front.items + 1 : 0);
     return fa::launch_paged_merge(m, (int)states, fa::sm_count_of(fa::current_device()), cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -3,7 +3,7 @@
 // A group is one row tile of one sequence (its index is sequence * tiles + row
 // tile); each of the Hkv key heads has a tile of the group, with the same
 // number of chunks.  The line runs over groups, then key heads, then chunks;
-// every CTA takes an equal piece of it, whatever the sequences' lengths.
+// every CTA (or warp) takes an equal piece of it, whatever the sequences' lengths.
 #pragma once
 
 #include "fa_paged.h"
@@ -75,80 +75,92 @@ struct Line {
         } while (u.n == 0);
     }
 
-    // This CTA's piece of the line: where it starts, its first chunk counted
-    // along the line, how many it has, and how many a full piece has.  The
-    // whole CTA calls it; `scratch` holds kThreads / 32 + 2 numbers.  Thread i
-    // sums the chunks of a strip of groups, and the strips' prefix sums find the
-    // group to start in.  (The host keeps the line below 2^31 chunks.)
-    template <int kThreads>
-    __device__ __forceinline__ void share(int *scratch, LineCursor &at, int &first, int &count, int &per) const
+    __device__ __forceinline__ int chunks_of_group(int g) const
     {
-        constexpr int kWarps = kThreads / 32;
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        int total, base = 0;
-        at.h = at.c = 0;
-        if (groups == 1) {
-            enter(at, 0);
-            total = at.n * p.c.Hkv;
-            per = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
-        } else {
-            const int strip = (groups + kThreads - 1) / kThreads;
-            const int g0 = min(tid * strip, groups), g1 = min(g0 + strip, groups);
-            int sum = 0;
-            LineCursor u;
-            for (int g = g0; g < g1; ++g) {
-                enter(u, g);
-                sum += u.n;
-            }
-            int scan = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, scan, d);
-                if (lane >= d) scan += v;
-            }
-            if (lane == 31) scratch[warp] = scan;
-            __syncthreads();
-            int all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) scan += scratch[w];
-                all += scratch[w];
-            }
-            total = all * p.c.Hkv;
-            per = (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
-            const unsigned start = (unsigned)per * blockIdx.x;
-            if (start < (unsigned)total && (unsigned)((scan - sum) * p.c.Hkv) <= start &&
-                start < (unsigned)(scan * p.c.Hkv)) {
-                int before = scan - sum;
-                int g = g0;
-                for (;; ++g) {
-                    enter(u, g);
-                    if (start < (unsigned)((before + u.n) * p.c.Hkv)) break;
-                    before += u.n;
-                }
-                scratch[kWarps] = g;
-                scratch[kWarps + 1] = before * p.c.Hkv;
-            }
-            __syncthreads();
-            if (start < (unsigned)total) {
-                enter(at, scratch[kWarps]);
-                base = scratch[kWarps + 1];
-            }
-        }
-        const unsigned start = (unsigned)per * blockIdx.x;
-        count = start < (unsigned)total ? min(per, total - (int)start) : 0;
-        first = (int)start;
-        if (count > 0) {
-            at.h = (first - base) / at.n;
-            at.c = (first - base) - at.h * at.n;
-        }
+        LineCursor u;
+        enter(u, g);
+        return u.n;
     }
 
-    // The CTA that has the first chunk of a tile says where its states will be.
-    __device__ __forceinline__ void record(const LineCursor &u, int first_chunk, int per) const
+    // How many pieces a line of `total` chunks is cut into: `most`, or fewer
+    // where another kernel works beside.  (Whole warps call it, and share().)
+    __device__ __forceinline__ int pieces(int total, int most) const
+    {
+        const Beside &s = p.beside;
+        if (!s.on) return most;
+        int own = total;
+        if (p.part.stacked) {
+            own = 0;
+            for (int b = threadIdx.x % 32; b < s.B; b += 32) own += chunks_of(min(max(s.seq_len[b], 0), s.cap), s.chunk);
+            own = __reduce_add_sync(0xffffffffu, own) * s.tiles;
+        }
+        if (own == 0) return most;
+        const float part = (float)s.blocks * kBlockCost;
+        const int front = min(max((int)((float)s.sms * part / (part + (float)own) + 0.5f), 1), s.sms - 1);
+        return min(p.part.stacked ? front : (s.sms - front) * s.per_sm, most);
+    }
+
+    // Piece `piece` of the line: where it starts, its first chunk counted along
+    // the line, how many it has, and how many a full piece has.  Lane i sums the
+    // chunks of a strip of groups; the strips' prefix sums find the strip to
+    // start in, and its groups' the group.  Every warp does it for itself: no
+    // barrier, and little code to fetch.  (The host keeps the line below 2^31.)
+    __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &first, int &count, int &per) const
+    {
+        const int lane = threadIdx.x % 32;
+        const int strip = (groups + 31) / 32;
+        int sum = 0;
+#pragma unroll 4
+        for (int i = 0; i < strip; ++i) {
+            const int g = lane * strip + i;
+            sum += g < groups ? chunks_of_group(g) : 0;
+        }
+        int scan = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += v;
+        }
+        const int total = __shfl_sync(0xffffffffu, scan, 31) * p.c.Hkv;
+        const int cut = pieces(total, most);
+        per = (int)(((unsigned)total + cut - 1) / (unsigned)cut);
+        const unsigned start = (unsigned)per * (unsigned)piece;
+        first = (int)start;
+        count = piece < cut && start < (unsigned)total ? min(per, total - (int)start) : 0;
+        if (count == 0) return;
+        const int in = __ffs(__ballot_sync(0xffffffffu, start < (unsigned)(scan * p.c.Hkv))) - 1;
+        int before = __shfl_sync(0xffffffffu, scan - sum, in), g0 = in * strip;
+        if (strip > 1) {
+            for (;; g0 += 32) {
+                const int n = g0 + lane < min((in + 1) * strip, groups) ? chunks_of_group(g0 + lane) : 0;
+                int here = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, here, d);
+                    if (lane >= d) here += v;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, start < (unsigned)((before + here) * p.c.Hkv));
+                if (hit) {
+                    const int at_lane = __ffs(hit) - 1;
+                    before += __shfl_sync(0xffffffffu, here - n, at_lane);
+                    g0 += at_lane;
+                    break;
+                }
+                before += __shfl_sync(0xffffffffu, here, 31);
+            }
+        }
+        enter(at, g0);
+        const int left = first - before * p.c.Hkv;
+        at.h = left / at.n;
+        at.c = left - at.h * at.n;
+    }
+
+    // The piece that has the first chunk of a tile says where its states will be.
+    __device__ __forceinline__ void record(const LineCursor &u, int piece, int first_chunk, int per) const
     {
         const int tile = u.g * p.c.Hkv + u.h;
         const int last = (int)((unsigned)(first_chunk + u.n - 1) / (unsigned)per);
-        p.part.tile[tile] = TileSlots{(int)blockIdx.x + tile, last - (int)blockIdx.x + 1};
+        p.part.tile[tile] = TileSlots{piece + tile, last - piece + 1};
     }
 };
 

@@ -7,15 +7,18 @@
 // by memory: 4 D bytes and 4 D * rows operations per key.  What the layout is
 // for is to keep loads in flight:
 //
-//   * the keys of all tiles form one line of chunks of 64 keys, cut into equal
-//     shares, one per CTA, whatever the sequences' lengths.  A tile that two
-//     or more CTAs had a share of leaves a partial state (O_s, LSE_s) in a
-//     slot for each, and the merge joins them:
-//         m = max LSE_s,  w_s = 2^(LSE_s - m),  O = sum w_s O_s / sum w_s;
-//   * a warp takes 16 keys of a chunk and has its own ring of shared-memory
-//     stages, filled with 16-byte asynchronous copies from the addresses that
-//     the page table gives, one per key row, so that any page size and any
-//     page, head and slot strides do.  Warps meet only where a tile ends;
+//   * the keys of all tiles form one line of chunks (16 keys, 32 at D <= 64),
+//     cut into equal pieces, one per warp, whatever the sequences' lengths.  A
+//     tile that two or more warps had a share of leaves a partial state
+//     (O_s, LSE_s) in a slot for each, and the merge joins them:
+//         m = max LSE_s,  w_s = 2^(LSE_s - m),  O = sum w_s O_s / sum w_s.
+//     Warps never meet.  (With four warps on a tile, joined in shared memory at
+//     its end, the barriers and the code that runs once per tile, fetched anew
+//     each time, took a third of the time of tiles of 512 keys.)
+//   * a warp has its own ring of shared-memory stages.  Where pages hold a
+//     multiple of 8 keys, one lane copies boxes of 8 to 32 rows with TMA;
+//     elsewhere all lanes copy 16 bytes at a time.  Either way the addresses
+//     come from the page table, so any page, head and slot strides do;
 //   * scores and outputs come from 16x8x16 warp products.  The tcgen05 unit
 //     would have to multiply 128 rows whatever the tile holds, and its rate is
 //     not what bounds this kernel;
@@ -23,8 +26,9 @@
 //     of 2^-16 p (fp16: 2^-22), and V is multiplied by both: the products are
 //     not the bound, and the output keeps fp32's error until it is rounded.
 //
-// Keys at or past a sequence's length and keys of pages outside the pool are
-// never read; their shared-memory rows are zero and their scores -inf.
+// Keys at or past a sequence's length and keys of pages outside the pool get a
+// score of -inf, and their rows of V are zero in shared memory (0 * NaN is NaN).
+#include "fa_internal.h"
 #include "fa_paged.h"
 #include "fa_paged_line.cuh"
 #include "fa_tc_common.cuh"
@@ -34,85 +38,96 @@
 
 namespace fa {
 
+__device__ uint32_t g_status_paged_rows;
+
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kRowsWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int DP, int MT>
 struct RowsLayout {
     static constexpr int kRows = 16 * MT;
-    // Keys of a warp per step: 8 KB of K and V at D <= 128.  (At D = 64 with 16
-    // keys the chain of a step, not memory, set the pace: eight warps an SM.)
-    static constexpr int kStepKeys = DP == 64 ? 32 : 16;
-    static constexpr int kChunk = kWarps * kStepKeys;
-    static constexpr int kRowBytes = 2 * DP;
-    static constexpr int kTileBytes = kStepKeys * kRowBytes;      // K or V of a step
+    // Keys of a chunk, one step of a warp: 8 KB of K and V at D <= 128.
+    static constexpr int kChunk = DP == 64 ? 32 : 16;
+    static constexpr int kTileBytes = kChunk * DP * 2;            // K or V of a step
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = 3;              // 96 KB: two CTAs per SM (192 KB, one CTA, at D = 256)
-    static constexpr int kQOff = 0;
-    static constexpr int kRingOff = kRows * kRowBytes;
-    static constexpr int kStatOff = kRingOff + kWarps * kStages * kStageBytes;
-    static constexpr int kStatBytes = 2 * kWarps * kRows * 4;     // m and l of every warp
-    static constexpr int kMaskOff = kStatOff + kStatBytes;        // valid keys of every stage
-    static constexpr int kScanOff = kMaskOff + kWarps * kStages * 4;
-    static constexpr int kSmemBytes = kScanOff + 128;
-    static_assert((kWarps + 2) * 4 <= 128, "scratch of the line's share");
-    static_assert(kStageBytes >= 16 * DP * 4, "an output tile fits a stage");
-    static_assert(kSmemBytes * (DP == 256 ? 1 : 2) + (DP == 256 ? 1 : 2) * 1024 <= 233472, "shared memory per SM");
+    // Q in registers, or where O leaves too few, in shared memory per warp
+    static constexpr bool kQRegs = MT == 1 && DP <= 128;
+    static constexpr int kQBytes = kQRegs ? 0 : kRows * DP * 2;
+    // CTAs per SM and stages per warp: what registers and shared memory hold
+    static constexpr int kCtas = DP == 256 ? 1 : MT == 1 ? 3 : 2;
+    static constexpr int kStages = 2;
+    static constexpr int kRingOff = 0;
+    static constexpr int kQOff = kWarps * kStages * kStageBytes;
+    static constexpr int kMaskOff = kQOff + kWarps * kQBytes;     // visible keys of every stage
+    static constexpr int kBarOff = kMaskOff + kWarps * kStages * 4;
+    static constexpr int kAbortOff = kBarOff + kWarps * kStages * 8;
+    static constexpr int kSmemBytes = kAbortOff + kWarps * 4 + 1024;   // + alignment slack
+    static_assert(kBarOff % 8 == 0, "barriers");
+    static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
 
-// Byte offset of 16-byte unit `unit` of row `row` in a tile of rows of
-// `kRowBytes`: units are permuted by the row's low bits, so that the eight
-// rows of a matrix load touch all banks.
-template <int kRowBytes>
+// Byte offset of 16-byte unit `unit` of row `row` in a tile of `kTall` rows:
+// 64 columns of all rows after 64 columns of all rows, and within a row's 128
+// bytes the units permuted by the row's low bits (the layout that TMA's 128-byte
+// swizzle gives), so that the eight rows of a matrix load touch all banks.
+template <int kTall>
 __device__ __forceinline__ uint32_t unit_at(int row, int unit)
 {
-    return (uint32_t)(row * kRowBytes + ((unit ^ (row & 7)) << 4));
+    return (uint32_t)((unit >> 3) * (kTall * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
 }
 
-template <int DP, int MT, bool kF16>
-__global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel(const PagedParams p)
+template <int DP, int MT, bool kF16, bool kTma>
+__global__ void __launch_bounds__(kThreads, (RowsLayout<DP, MT>::kCtas))
+paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
 {
     using Lay = RowsLayout<DP, MT>;
-    constexpr int S = Lay::kStages, RM = Lay::kRows, RB = Lay::kRowBytes, KS = Lay::kStepKeys;
+    constexpr int S = Lay::kStages, RM = Lay::kRows, KS = Lay::kChunk;
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : 0xffffu;
     constexpr int NT = DP / 8;                      // 8-column tiles of O
     constexpr int KT = DP / 16;                     // 16-column steps of a score
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t s_base = ptx::smem_u32(smem);
-    float *s_m = reinterpret_cast<float *>(smem + Lay::kStatOff);
-    float *s_l = s_m + kWarps * RM;
-    uint32_t *s_mask = reinterpret_cast<uint32_t *>(smem + Lay::kMaskOff);
-    int *s_scan = reinterpret_cast<int *>(smem + Lay::kScanOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t *s_mask = reinterpret_cast<uint32_t *>(smem + Lay::kMaskOff) + warp * S;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Lay::kBarOff) + warp * S;
+    // the warp's own: a warp that gave up a wait stops nobody else
+    volatile int *abort_word = reinterpret_cast<int *>(smem + Lay::kAbortOff) + warp;
+    const Abort ab{abort_word, &g_status_paged_rows};
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if constexpr (kTma) {
+        if (lane == 0) {
+            for (int i = 0; i < S; ++i) ptx::mbar_init(&full[i], 1);
+            *abort_word = 0;
+            ptx::fence_mbarrier_init();
+        }
+        __syncwarp();
+    }
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    const Line<Lay::kChunk> line(p);
+    const Line<KS> line(p);
+    const int piece = (int)blockIdx.x * kWarps + warp;
     LineCursor at;
     int g0, steps, per;
-    line.template share<kThreads>(s_scan, at, g0, steps, per);
-    if (steps == 0) {
-        if (p.second) ptx::wait_for_primary();
-        return;
-    }
+    line.share(piece, (int)gridDim.x * kWarps, at, g0, steps, per);
     const int R = line.R;
 
     // ---- loads -----------------------------------------------------------
-    const int kr = lane % KS;                       // the key of the step whose address this lane finds
     LineCursor ld = at;
     int ld_left = steps;
-    // Where a step's key is.  Its page number is fetched at least one step
-    // before its use.
+    // Where this lane's key of a step is (lane % KS).  Its page number is
+    // fetched at least one step before its use.
     struct Place {
-        int page, slot, h;
+        int page, slot, h;      // page < 0: not a key that the tile sees; h < 0: past the piece
     };
     auto look_up = [&]() -> Place {
+        if (ld_left <= 0) return Place{-1, 0, -1};
         Place x{-1, 0, ld.h};
-        if (ld_left <= 0) return x;
-        const int key = ld.c * Lay::kChunk + warp * KS + kr;
+        const int key = ld.c * KS + lane % KS;
         if (key < ld.keys) {
             const int which = p.c.by_page.quotient(key);
             const int b = p.part.tiles == 1 ? ld.g : ld.g / p.part.tiles;
@@ -124,84 +139,106 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
         return x;
     };
     const uint32_t ring = s_base + Lay::kRingOff + warp * S * Lay::kStageBytes;
+    int issued = 0;             // steps copied
     auto load = [&](int stage, const Place &x) {
         const bool ok = x.page >= 0 && x.page < p.c.num_pages;
-        const int64_t off = ok ? (int64_t)x.page * p.c.s_page + (int64_t)x.h * p.c.s_head + (int64_t)x.slot * p.c.s_slot : 0;
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAll;
-        if (lane == 0) s_mask[warp * S + stage] = mask;
-        constexpr int kLanes = DP / 8 < 32 ? DP / 8 : 32;      // lanes per row
-        constexpr int kRowsPer = 32 / kLanes;
-        const int unit = lane % kLanes;
+        if (lane == 0) s_mask[stage] = mask;
         const uint32_t dst = ring + stage * Lay::kStageBytes;
+        if constexpr (kTma) {
+            if (x.h < 0) return;
+            ++issued;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[stage], Lay::kStageBytes);
+            const int page = ok ? x.page : p.c.num_pages;         // past the tensor's end: zeros
+#pragma unroll 1
+            for (int i = 0; i < KS; i += p.box_rows) {
+                const int box_page = __shfl_sync(0xffffffffu, page, i), box_slot = __shfl_sync(0xffffffffu, x.slot, i);
+                if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < KS / kRowsPer; ++i) {
-            const int row = i * kRowsPer + lane / kLanes;
-            const int64_t o = __shfl_sync(0xffffffffu, off, row);
-            const uint32_t bytes = ((mask >> row) & 1u) && unit * 8 < p.c.D ? 16u : 0u;
-            const int64_t src = bytes ? o + unit * 8 : 0;
-            const uint32_t to = dst + unit_at<RB>(row, unit);
-            ptx::cp_async16(to, p.c.k + src, bytes);
-            ptx::cp_async16(to + Lay::kTileBytes, p.c.v + src, bytes);
+                    for (int c = 0; c < DP / 64; ++c) {
+                        ptx::tma_load_4d(dst + (c * KS + i) * 128, &tm_k, &full[stage], c * 64, box_slot, x.h, box_page);
+                        ptx::tma_load_4d(dst + Lay::kTileBytes + (c * KS + i) * 128, &tm_v, &full[stage], c * 64, box_slot,
+                                         x.h, box_page);
+                    }
+                }
+            }
+        } else {
+            const int64_t off =
+                ok ? (int64_t)x.page * p.c.s_page + (int64_t)x.h * p.c.s_head + (int64_t)x.slot * p.c.s_slot : 0;
+            constexpr int kLanes = DP / 8 < 32 ? DP / 8 : 32;      // lanes per row
+            constexpr int kRowsPer = 32 / kLanes;
+            const int unit = lane % kLanes;
+#pragma unroll
+            for (int i = 0; i < KS / kRowsPer; ++i) {
+                const int row = i * kRowsPer + lane / kLanes;
+                const int64_t o = __shfl_sync(0xffffffffu, off, row);
+                const uint32_t bytes = ((mask >> row) & 1u) && unit * 8 < p.c.D ? 16u : 0u;
+                const int64_t src = bytes ? o + unit * 8 : 0;
+                const uint32_t to = dst + unit_at<KS>(row, unit);
+                ptx::cp_async16(to, p.c.k + src, bytes);
+                ptx::cp_async16(to + Lay::kTileBytes, p.c.v + src, bytes);
+            }
+            ptx::cp_async_commit();
         }
-        ptx::cp_async_commit();
     };
-    Place next;
-    {
-        Place x[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) x[s] = look_up();
-        next = look_up();
-#pragma unroll
-        for (int s = 0; s < S; ++s) load(s, x[s]);  // steps past the share load zeros
-    }
-    auto load_next = [&](int stage) {
+    Place next = look_up();
+#pragma unroll 1
+    for (int s = 0; s < S; ++s) {
         const Place x = next;
         next = look_up();
-        load(stage, x);
-    };
-
-    // ---- the share, tile by tile ------------------------------------------
-    const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a tile
-    const uint32_t q_smem = s_base + Lay::kQOff;
-    // Q of a tile: this thread's 16-byte units, loaded before the tile before
-    // is joined where there are registers for them.
-    constexpr int kQUnits = RM * (DP / 8) / kThreads;
-    constexpr bool kQEarly = MT == 1;
-    uint4 q_next[kQUnits];
-    auto load_q = [&](const LineCursor &u, int i) -> uint4 {
-        const int e = tid + i * kThreads, unit = e % (DP / 8);
-        const int b = p.part.tiles == 1 ? u.g : u.g / p.part.tiles;
-        const int row = (u.g - b * p.part.tiles) * RM + e / (DP / 8);
-        if (row >= R || unit * 8 >= p.c.D) return make_uint4(0u, 0u, 0u, 0u);   // rows past R, columns past D
-        const RowPlace r = row_place(p, b, u.h, row);
-        return *reinterpret_cast<const uint4 *>(p.q + r.b * p.q_s[0] + r.hq * p.q_s[1] + r.t * p.q_s[2] + unit * 8);
-    };
-    if constexpr (kQEarly) {
-#pragma unroll
-        for (int i = 0; i < kQUnits; ++i) q_next[i] = load_q(at, i);
+        load(s, x);
     }
+
+    // ---- the piece, tile by tile -------------------------------------------
+    const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a tile
+    const uint32_t q_smem = s_base + Lay::kQOff + warp * Lay::kQBytes;
     int stage = 0, done = 0;
+    uint32_t phase = 0;
+#pragma unroll 1
     while (done < steps) {
-        const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the share
+        const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the piece
         const int b = p.part.tiles == 1 ? at.g : at.g / p.part.tiles;
         const int row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
         const int tile = at.g * p.c.Hkv + h;
-        const bool whole = count == at.n;
-        if (at.c == 0 && tid == 0) line.record(at, g0 + done, per);
+        if (at.c == 0 && lane == 0) line.record(at, piece, g0 + done, per);
+
+        // Q: rows past R and columns past D are zero
+        uint32_t qf[Lay::kQRegs ? KT : 1][4];
+        if constexpr (Lay::kQRegs) {
 #pragma unroll
-        for (int i = 0; i < kQUnits; ++i) {
-            const int e = tid + i * kThreads;
-            const uint4 w = kQEarly ? q_next[i] : load_q(at, i);
-            ptx::st_shared_v4(q_smem + unit_at<RB>(e / (DP / 8), e % (DP / 8)), w.x, w.y, w.z, w.w);
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qf[k][e] = 0u;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (row0 + qr + 8 * r >= R) continue;
+                const RowPlace x = row_place(p, b, h, row0 + qr + 8 * r);
+                const uint16_t *src = p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + 2 * qc;
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (16 * k + 8 * e < p.c.D) qf[k][2 * e + r] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 * e);
+            }
+        } else {
+            __syncwarp();
+#pragma unroll 4
+            for (int e = lane; e < RM * (DP / 8); e += 32) {
+                const int row = e / (DP / 8), unit = e % (DP / 8);
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (row0 + row < R && unit * 8 < p.c.D) {
+                    const RowPlace x = row_place(p, b, h, row0 + row);
+                    w = *reinterpret_cast<const uint4 *>(p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + unit * 8);
+                }
+                ptx::st_shared_v4(q_smem + unit_at<RM>(row, unit), w.x, w.y, w.z, w.w);
+            }
+            __syncwarp();
         }
         int lim[2 * MT];                            // keys that this lane's rows see
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            const int t = p.by_g.quotient(row0 + i * 8 + qr);
-            lim[i] = line.masked ? at.len - p.T + t + 1 : at.len;
-        }
+        for (int i = 0; i < 2 * MT; ++i)
+            lim[i] = line.masked ? at.len - p.T + p.by_g.quotient(row0 + i * 8 + qr) + 1 : at.len;
         const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
-        __syncthreads();
 
         float o[MT][NT][4], m[2 * MT], l[2 * MT];
 #pragma unroll
@@ -213,13 +250,18 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
 
-        int last_stage = stage;
+#pragma unroll 1
         for (int step = 0; step < count; ++step) {
-            ptx::cp_async_wait<S - 1>();
+            // (a wait that gave up leaves the results undefined; the copies are
+            // waited for at the end)
+            if constexpr (kTma)
+                wait_bounded(&full[stage], phase, p.wait_limit_ns, kSiteSlotFull, ab);
+            else
+                ptx::cp_async_wait<S - 1>();
             __syncwarp();
             const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
-            const uint32_t mask = s_mask[warp * S + stage];
-            const int key0 = (at.c + step) * Lay::kChunk + warp * KS;
+            const uint32_t mask = s_mask[stage];
+            const int key0 = (at.c + step) * KS;
             if (mask) {
                 float s[MT][KS / 8][4];
 #pragma unroll
@@ -232,13 +274,19 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                 for (int k = 0; k < KT; ++k) {
                     uint32_t qa[MT][4];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        ptx::ldmatrix4(qa[i], q_smem + unit_at<RB>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
+                    for (int i = 0; i < MT; ++i) {
+                        if constexpr (Lay::kQRegs) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) qa[i][e] = qf[k][e];
+                        } else {
+                            ptx::ldmatrix4(qa[i], q_smem + unit_at<RM>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < KS / 16; ++j) {
                         // K rows 16j .. +7 and +8 .. +15, columns 16k .. +7 and +8 .. +15
                         uint32_t kb[4];
-                        ptx::ldmatrix4(kb, kt + unit_at<RB>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                        ptx::ldmatrix4(kb, kt + unit_at<KS>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             ptx::mma_16816<kF16>(s[i][2 * j], qa[i], kb[0], kb[1]);
@@ -247,6 +295,16 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                     }
                 }
                 if (mask != kAll || key0 + KS > lim_all) {
+                    if constexpr (kTma) {
+                        // a box brings what its page holds behind the last key
+                        if (mask != kAll) {
+#pragma unroll 1
+                            for (int e = lane; e < KS * (DP / 8); e += 32)
+                                if (!((mask >> (e % KS)) & 1u)) ptx::st_shared_v4(vt + unit_at<KS>(e % KS, e / KS), 0u, 0u, 0u, 0u);
+                            ptx::fence_proxy_async_smem();      // before the next copy into the stage
+                            __syncwarp();
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -268,9 +326,12 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                         for (int n = 1; n < KS / 8; ++n) mx = ptx::max3(mx, s[i][n][2 * r], s[i][n][2 * r + 1]);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float m_new = fmaxf(mr, mx * p.scale_log2);
-                        const float ref = m_new == -INFINITY ? 0.f : m_new;
-                        if (__any_sync(0xffffffffu, m_new != mr)) {
+                        // The reference follows the largest score only when that
+                        // is 2^8 above it: weights stay at most 256, and O is
+                        // rescaled rarely.
+                        mx *= p.scale_log2;
+                        if (__any_sync(0xffffffffu, mx > mr + 8.f)) {
+                            const float m_new = fmaxf(mr, mx), ref = m_new == -INFINITY ? 0.f : m_new;
                             const float alpha = ptx::ex2_approx(mr - ref);
                             lr *= alpha;
 #pragma unroll
@@ -278,8 +339,9 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                                 o[i][n][2 * r] *= alpha;
                                 o[i][n][2 * r + 1] *= alpha;
                             }
+                            mr = m_new;
                         }
-                        mr = m_new;
+                        const float ref = mr == -INFINITY ? 0.f : mr;
 #pragma unroll
                         for (int n = 0; n < KS / 8; ++n) {
                             const float p0 = ptx::ex2_approx(fmaf(s[i][n][2 * r], p.scale_log2, -ref));
@@ -299,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                     for (int n = 0; n < KT; ++n) {
                         // V rows 16j .. +7 and +8 .. +15 (the product's k), columns 16n .. +7 and +8 .. +15
                         uint32_t vb[4];
-                        ptx::ldmatrix4_trans(vb, vt + unit_at<RB>(16 * j + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+                        ptx::ldmatrix4_trans(vb, vt + unit_at<KS>(16 * j + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             ptx::mma_16816<kF16>(o[i][2 * n], hi[i][j], vb[0], vb[1]);
@@ -310,113 +372,84 @@ __global__ void __launch_bounds__(kThreads, DP == 256 ? 1 : 2) paged_rows_kernel
                     }
             }
             __syncwarp();
-            last_stage = stage;
-            stage = stage + 1 == S ? 0 : stage + 1;
-            // the tile's last stage is refilled after the warps' states are joined
-            if (step + 1 < count) load_next(last_stage);
+            const Place x = next;
+            next = look_up();
+            load(stage, x);                                   // steps past the piece load nothing
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
 
+        // ---- the tile's state -------------------------------------------------
+        const bool direct = count == at.n && !p.joined;
+        const int64_t slot = (int64_t)piece + tile;
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            float sum = l[i];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const int tr = i * 8 + qr;
+            if (row0 + tr >= R) continue;
+            // (a NaN among the scores reaches the output)
+            const bool empty = sum == 0.f;
+            const float inv = empty ? 0.f : 1.f / sum;
+            const float lse2 = empty ? -INFINITY : m[i] + log2f(sum);
+            if (direct) {
+                const RowPlace x = row_place(p, b, h, row0 + tr);
+                uint16_t *dst = p.o + x.b * p.o_s[0] + x.hq * p.o_s[1] + x.t * p.o_s[2] + 2 * qc;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (8 * n < p.c.D)
+                        *reinterpret_cast<uint32_t *>(dst + 8 * n) =
+                            empty ? 0u : ptx::pack16x2<kF16>(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
+                if (p.lse && qc == 0) p.lse[((int64_t)x.b * p.Hq + x.hq) * p.T + x.t] = lse2 * kLn2;
+            } else {
+                // columns 8n + 2 qc and the next: half of four columns
+                float2 *dst = reinterpret_cast<float2 *>(p.part.o) +
+                              ((slot * (p.c.D / 4) + qc / 2) * p.part.slot_rows + tr) * 2 + (qc & 1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (8 * n < p.c.D)
+                        dst[n * 4 * p.part.slot_rows] =
+                            empty ? make_float2(0.f, 0.f)
+                                  : make_float2(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
+                if (qc == 0) p.part.lse[slot * p.part.slot_rows + tr] = lse2;
+            }
+        }
+        __syncwarp();
         at.c += count - 1;
         line.advance(at);
         done += count;
-        if constexpr (kQEarly) {
-            if (done < steps) {
-#pragma unroll
-                for (int i = 0; i < kQUnits; ++i) q_next[i] = load_q(at, i);
-            }
-        }
-
-        // ---- join the warps' states -----------------------------------------
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (qc == 0) {
-                s_m[warp * RM + i * 8 + qr] = m[i];
-                s_l[warp * RM + i * 8 + qr] = l[i];
-            }
-        }
-        const bool direct = whole && !p.joined;
-        const int64_t slot = (int64_t)blockIdx.x + tile;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            // each warp puts a 16 x DP tile of O over its last stage, with the
-            // columns permuted by the row so that the stores spread over the banks
-            const uint32_t mine = ring + last_stage * Lay::kStageBytes;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = qr + 8 * r, col = (n * 8 + 2 * qc) ^ ((row & 7) << 3);
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mine + (uint32_t)(row * DP + col) * 4u),
-                                 "f"(o[i][n][2 * r]), "f"(o[i][n][2 * r + 1]) : "memory");
-                }
-            __syncthreads();
-            for (int e = tid; e < 16 * DP / 4; e += kThreads) {
-                // along the columns for rows of O, along the rows for a slot
-                const int row = direct ? e / (DP / 4) : e % 16, col = (direct ? e % (DP / 4) : e / 16) * 4;
-                const int tr = i * 16 + row;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * RM + tr]);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ptx::ex2_approx(s_m[w * RM + tr] - ref);
-                    sum = fmaf(f, s_l[w * RM + tr], sum);
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        smem + Lay::kRingOff + (w * S + last_stage) * Lay::kStageBytes +
-                        (size_t)(row * DP + (col ^ ((row & 7) << 3))) * 4);
-                    acc[0] = fmaf(f, v.x, acc[0]);
-                    acc[1] = fmaf(f, v.y, acc[1]);
-                    acc[2] = fmaf(f, v.z, acc[2]);
-                    acc[3] = fmaf(f, v.w, acc[3]);
-                }
-                // a NaN among the scores reaches the output
-                const bool empty = sum == 0.f;
-                const float inv = empty ? 0.f : 1.f / sum;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[c] = empty ? 0.f : acc[c] * inv;
-                const int idx = row0 + tr;
-                if (idx >= R) continue;
-                const float lse2 = empty ? -INFINITY : top + log2f(sum);
-                if (direct) {
-                    const RowPlace r = row_place(p, b, h, idx);
-                    if (col < p.c.D)
-                        *reinterpret_cast<uint2 *>(p.o + r.b * p.o_s[0] + r.hq * p.o_s[1] + r.t * p.o_s[2] + col) =
-                            make_uint2(ptx::pack16x2<kF16>(acc[0], acc[1]), ptx::pack16x2<kF16>(acc[2], acc[3]));
-                    if (p.lse && col == 0) p.lse[((int64_t)r.b * p.Hq + r.hq) * p.T + r.t] = lse2 * kLn2;
-                } else {
-                    if (col < p.c.D)
-                        reinterpret_cast<float4 *>(p.part.o)[(slot * (p.c.D / 4) + col / 4) * RM + tr] =
-                            make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    if (col == 0) p.part.lse[slot * RM + tr] = lse2;
-                }
-            }
-            __syncthreads();
-        }
-        load_next(last_stage);
     }
-    ptx::cp_async_wait<0>();
+    if constexpr (kTma) {
+        for (int i = max(0, issued - S); i < issued; ++i)
+            wait_bounded(&full[i % S], (i / S) & 1, p.wait_limit_ns, kSiteDrain, ab, false);
+    } else {
+        ptx::cp_async_wait<0>();
+    }
     // the merge starts when this kernel has ended, and needs the one before too
     if (p.second) ptx::wait_for_primary();
 }
 
-template <int DP, int MT, bool kF16>
-cudaError_t launch_rows(const PagedParams &p, int ctas, cudaStream_t stream)
+template <int DP, int MT, bool kF16, bool kTma>
+cudaError_t launch_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
     static SharedMemory allowed;
-    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, MT, kF16>, RowsLayout<DP, MT>::kSmemBytes);
+    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, MT, kF16, kTma>, RowsLayout<DP, MT>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_rows_kernel<DP, MT, kF16>, dim3((unsigned)ctas), kThreads, RowsLayout<DP, MT>::kSmemBytes,
-                         stream, p);
+    return launch_behind(paged_rows_kernel<DP, MT, kF16, kTma>, dim3((unsigned)ctas), kThreads,
+                         RowsLayout<DP, MT>::kSmemBytes, stream, tk, tv, p);
 }
 
 template <int DP, int MT>
-cudaError_t launch_rows_f(const PagedParams &p, int ctas, cudaStream_t stream)
+cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
-    return p.f16 ? launch_rows<DP, MT, true>(p, ctas, stream) : launch_rows<DP, MT, false>(p, ctas, stream);
+    if (p.box_rows)
+        return p.f16 ? launch_rows<DP, MT, true, true>(p, tk, tv, ctas, stream)
+                     : launch_rows<DP, MT, false, true>(p, tk, tv, ctas, stream);
+    return p.f16 ? launch_rows<DP, MT, true, false>(p, tk, tv, ctas, stream)
+                 : launch_rows<DP, MT, false, false>(p, tk, tv, ctas, stream);
 }
 
 // ---------------------------------------------------------------- merge
@@ -476,9 +509,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const Partials &src = p.src[s];
-                const float *lse = src.lse + (int64_t)x[s].first * src.rows + at[s];
-                const int64_t step = (int64_t)(p.D / 4) * src.rows;
-                const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.rows + at[s];
+                const float *lse = src.lse + (int64_t)x[s].first * src.slot_rows + at[s];
+                const int64_t step = (int64_t)(p.D / 4) * src.slot_rows;
+                const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.slot_rows + at[s];
                 for (int i = z; i < x[s].count; i += kBatch * kZ) {
                     float y[kBatch];
                     float4 v[kBatch];
@@ -487,7 +520,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
                         y[j] = -INFINITY;
                         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (i + j * kZ < x[s].count) {
-                            y[j] = lse[(int64_t)(i + j * kZ) * src.rows];
+                            y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
                             v[j] = o[(i + j * kZ) * step];
                         }
                     }
@@ -574,16 +607,35 @@ cudaError_t launch_merge_z(const MergeParams &p, int z, cudaStream_t stream)
 // more, else 32.
 int paged_rows_per_tile(int D, int64_t rows) { return rows <= 16 || D > 128 ? 16 : 32; }
 
-int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 1>::kChunk : D <= 128 ? RowsLayout<128, 1>::kChunk : RowsLayout<256, 1>::kChunk; }
+int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 1>::kChunk : RowsLayout<128, 1>::kChunk; }
 
-int paged_rows_ctas_per_sm(int D) { return D > 128 ? 1 : 2; }
-
-cudaError_t launch_paged_rows(const PagedParams &p, int ctas, cudaStream_t stream)
+int paged_rows_ctas_per_sm(int D, int rows)
 {
-    if (p.c.D > 128) return launch_rows_f<256, 1>(p, ctas, stream);
+    return D > 128 ? RowsLayout<256, 1>::kCtas : rows == 16 ? RowsLayout<128, 1>::kCtas : RowsLayout<128, 2>::kCtas;
+}
+
+cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                              cudaStream_t stream)
+{
+    if (p.c.D > 128) return launch_rows_f<256, 1>(p, tk, tv, ctas, stream);
     if (p.c.D > 64)
-        return p.part.rows == 16 ? launch_rows_f<128, 1>(p, ctas, stream) : launch_rows_f<128, 2>(p, ctas, stream);
-    return p.part.rows == 16 ? launch_rows_f<64, 1>(p, ctas, stream) : launch_rows_f<64, 2>(p, ctas, stream);
+        return p.part.rows == 16 ? launch_rows_f<128, 1>(p, tk, tv, ctas, stream)
+                                 : launch_rows_f<128, 2>(p, tk, tv, ctas, stream);
+    return p.part.rows == 16 ? launch_rows_f<64, 1>(p, tk, tv, ctas, stream) : launch_rows_f<64, 2>(p, tk, tv, ctas, stream);
+}
+
+cudaError_t read_and_clear_status_paged_rows(uint32_t *out)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_status_paged_rows, sizeof(v));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_status_paged_rows, &zero, sizeof(zero));
+        if (e != cudaSuccess) return e;
+    }
+    *out = v;
+    return cudaSuccess;
 }
 
 cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaStream_t stream)

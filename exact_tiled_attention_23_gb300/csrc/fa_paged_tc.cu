@@ -77,15 +77,13 @@ struct TcLayout {
     // q_full, k_full/k_empty[RK], v_full/v_empty[RV], s_full, s_read,
     // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
     static constexpr int kBars = 1 + 2 * (kRingK + kRingV) + 2 + 4 + 4 + 4;
-    static constexpr int kScanOff = kBarOff + 512;
-    static constexpr int kSmemBytes = kScanOff + 128 + 1024;    // + alignment slack
+    static constexpr int kSmemBytes = kBarOff + 512 + 1024;    // + alignment slack
     __device__ static constexpr uint32_t col_o(int h) { return kColO + (uint32_t)(h * D); }
     __device__ static constexpr uint32_t col_p(int buf, int h) { return kColP + (uint32_t)(buf * 64 + h * 32); }
     static_assert(D == 64 || D == 128, "head dim");
     static_assert(kColO + 2 * D <= kTmemCols, "TMEM columns");
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(kBars * 8 + 16 <= 512, "barrier area");
-    static_assert((kThreads / 32 + 2) * 4 <= 128, "scratch of the line's share");
 };
 
 // A role's way along the CTA's piece of the line, tile by tile: what a block
@@ -145,7 +143,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int g0, per;
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    line.template share<kThreads>(reinterpret_cast<int *>(smem + Lay::kScanOff), walk.u, g0, walk.left, per);
+    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, g0, walk.left, per);
     if (walk.left == 0) {
         if (p.second) ptx::wait_for_primary();
         return;
@@ -182,7 +180,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int box = p.box_rows, boxes = BN / box;
         const CUtensorMap *tm = warp == 0 ? &tm_k : &tm_v;
         uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
-        uint8_t *slots = smem + (warp == 0 ? kKOff : kVOff);
+        const uint32_t slots = ptx::smem_u32(smem + (warp == 0 ? kKOff : kVOff));
         const int ring = warp == 0 ? RK : RV;
         int issued = 0, slot = 0;
         uint32_t phase = 1;                                     // of the slot's last release
@@ -505,7 +503,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
             const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
-            if (thread == 0 && was.c == 0) line.record(was, g0 + (t - count), per);
+            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, g0 + (t - count), per);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {

@@ -85,14 +85,14 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_
         : "memory");
 }
 
-// 4-D tiled load of one box into shared memory.
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_t *bar,
+// 4-D tiled load of one box into shared memory (`dst`: its shared address).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint64_t *bar,
                                             int32_t x, int32_t y, int32_t z, int32_t w)
 {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5, %6}], [%2];"
-        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)),
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)),
           "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
