@@ -435,6 +435,9 @@ class PagedKV:
     block_table: int32 [B, W], the pages of each sequence in order.  seq_len:
     int32 [B], keys per sequence.  The caller updates the contents of both in
     place; the object checks the tensors once and keeps them alive.
+
+    Calls on the default stream, which run one after another, share a workspace
+    of up to 32 MB that the object keeps.
     """
 
     def __init__(self, k_cache, v_cache, block_table, seq_len):
@@ -459,6 +462,7 @@ class PagedKV:
         pages, Hkv, page_size, D = k_cache.shape
         self.batch, self.Hkv, self.D, self.dtype, self.device = B, Hkv, D, k_cache.dtype, k_cache.device
         self._f16, self._index, self._workspace_bytes = k_cache.dtype == torch.float16, k_cache.get_device(), {}
+        self._lock, self._workspace = threading.Lock(), None
         sp, sh, ss, _ = k_cache.stride()
         # the stride of a dimension of one entry is never followed
         self.c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
@@ -501,7 +505,8 @@ def _paged_input(x, what, cache, shape):
 def _paged_output(out, what, like):
     """fa_rows of an output like the [B, H, T, D] tensor `like`, and the tensor."""
     if out is None:
-        out = like.new_empty(like.shape)
+        import torch
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
     elif out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
         raise ValueError(f"{what} must be a tensor like q")
     sb, sh, sn, sd = out.stride()
@@ -640,7 +645,21 @@ def _forward_paged(q, cache, prefix_table, prefix_len, causal, scale, out, lse, 
     elif return_lse:
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
     if workspace is None:
-        size = max(cache.workspace_bytes(Hq, T, prefix_len), 16)
+        size = cache.workspace_bytes(Hq, T, prefix_len)
+        if stream == 0 and size <= _KEPT_WORKSPACE:
+            # Only the default stream: another stream's calls, or a graph
+            # captured on one, may run beside these.  The lock keeps two host
+            # threads' launches apart.
+            with cache._lock:
+                workspace = cache._workspace
+                if workspace is None or workspace.numel() < size:
+                    cache._workspace = workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
+                st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, None if lse is None else lse.data_ptr(),
+                                          B, Hq, T, causal, _DEFAULT_SCALE if scale is None else scale, cache._f16,
+                                          workspace.data_ptr(), size, 0)
+            if st != FA_OK:
+                raise FAError(st, "fa_fwd_paged" if prefix_table is None else "fa_fwd_shared_prefix")
+            return (out, lse) if return_lse else out
         workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
     else:
         if workspace.get_device() != cache._index or not workspace.is_contiguous():
@@ -654,6 +673,7 @@ def _forward_paged(q, cache, prefix_table, prefix_len, causal, scale, out, lse, 
     return (out, lse) if return_lse else out
 
 
+_KEPT_WORKSPACE = 32 << 20
 _DEFAULT_SCALE = float("nan")
 
 

@@ -127,8 +127,10 @@ struct Plan {
             return;
         }
         ctas = (int64_t)fa::sm_count_of(fa::current_device()) * (tc ? 1 : fa::paged_rows_ctas_per_sm(D, part.rows));
-        const int each = tc ? 1 : fa::kRowsWarps;
-        ctas = std::max<int64_t>(1, std::min(ctas, (chunks + each - 1) / each));
+        // at least two chunks per warp: they arrive together, and half as many
+        // states are joined
+        const int each = tc ? 1 : fa::kRowsWarps, least = tc ? 1 : 2 * each;
+        ctas = std::max<int64_t>(1, std::min(ctas, (chunks + least - 1) / least));
         pieces = ctas * each;
         part.slot_rows = (int)std::min<int64_t>(part.rows, tiles == 1 ? (tc ? 128 : rows) : part.rows);
         const size_t slots = (size_t)(pieces + items);

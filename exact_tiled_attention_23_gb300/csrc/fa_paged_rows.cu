@@ -456,9 +456,9 @@ cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUt
 // The sum of a row's partial outputs, weighted by their LSEs against the
 // largest.  A CTA has kRows rows of one (sequence, key head), kCols threads for
 // four columns each, and kZ threads for each of those, which take every kZ-th
-// state and are joined in order: a launch of few rows with many states each
-// (one sequence of 131072 keys: 38) waited 10 us for one thread's chain of
-// loads.  The lanes of a load are neighbours in the slots.
+// state and are joined in order: one thread's chain of loads through the 228
+// states of a row (one sequence of 131072 keys) took 18 us.  The lanes of a load
+// are neighbours in the slots.
 constexpr int kMergeThreads = 256;
 
 template <int kCols, int kZ, bool kF16>
@@ -502,82 +502,84 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
     // A batch of states at a time, their LSEs and outputs loaded together; the
     // sums follow the largest LSE so far.
     constexpr int kBatch = 4;
-    for (int c = col4; c < (p.D / 4 + kCols - 1) / kCols * kCols; c += kCols) {
-        float top = -INFINITY, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!skip && c < p.D / 4) {
+    const int c = blockIdx.z * kCols + col4;
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!skip && c < p.D / 4) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Partials &src = p.src[s];
-                const float *lse = src.lse + (int64_t)x[s].first * src.slot_rows + at[s];
-                const int64_t step = (int64_t)(p.D / 4) * src.slot_rows;
-                const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.slot_rows + at[s];
-                for (int i = z; i < x[s].count; i += kBatch * kZ) {
-                    float y[kBatch];
-                    float4 v[kBatch];
+        for (int s = 0; s < 2; ++s) {
+            const Partials &src = p.src[s];
+            const float *lse = src.lse + (int64_t)x[s].first * src.slot_rows + at[s];
+            const int64_t step = (int64_t)(p.D / 4) * src.slot_rows;
+            const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.slot_rows + at[s];
+            for (int i = z; i < x[s].count; i += kBatch * kZ) {
+                float y[kBatch];
+                float4 v[kBatch];
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        y[j] = -INFINITY;
-                        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (i + j * kZ < x[s].count) {
-                            y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
-                            v[j] = o[(i + j * kZ) * step];
-                        }
+                for (int j = 0; j < kBatch; ++j) {
+                    y[j] = -INFINITY;
+                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i + j * kZ < x[s].count) {
+                        y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
+                        v[j] = o[(i + j * kZ) * step];
                     }
-                    float next = top;
+                }
+                float next = top;
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) next = fmaxf(next, y[j]);
-                    const float ref = next == -INFINITY ? 0.f : next;
-                    const float f = ptx::ex2_approx(top - ref);
-                    top = next;
-                    sum *= f;
-                    acc.x *= f;
-                    acc.y *= f;
-                    acc.z *= f;
-                    acc.w *= f;
+                for (int j = 0; j < kBatch; ++j) next = fmaxf(next, y[j]);
+                const float ref = next == -INFINITY ? 0.f : next;
+                const float f = ptx::ex2_approx(top - ref);
+                top = next;
+                sum *= f;
+                acc.x *= f;
+                acc.y *= f;
+                acc.z *= f;
+                acc.w *= f;
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const float w = ptx::ex2_approx(y[j] - ref);
-                        sum += w;
-                        acc.x = fmaf(w, v[j].x, acc.x);
-                        acc.y = fmaf(w, v[j].y, acc.y);
-                        acc.z = fmaf(w, v[j].z, acc.z);
-                        acc.w = fmaf(w, v[j].w, acc.w);
-                    }
+                for (int j = 0; j < kBatch; ++j) {
+                    const float w = ptx::ex2_approx(y[j] - ref);
+                    sum += w;
+                    acc.x = fmaf(w, v[j].x, acc.x);
+                    acc.y = fmaf(w, v[j].y, acc.y);
+                    acc.z = fmaf(w, v[j].z, acc.z);
+                    acc.w = fmaf(w, v[j].w, acc.w);
                 }
             }
         }
-        if constexpr (kZ > 1) {
-            __shared__ float2 s_stat[kMergeThreads];
-            __shared__ float4 s_acc[kMergeThreads];
-            s_stat[threadIdx.x] = make_float2(top, sum);
-            s_acc[threadIdx.x] = acc;
-            __syncthreads();
-            if (z == 0) {
-#pragma unroll
-                for (int j = 1; j < kZ; ++j) {
-                    const float2 st = s_stat[threadIdx.x + j * kRows * kCols];
-                    const float4 v = s_acc[threadIdx.x + j * kRows * kCols];
-                    const float next = fmaxf(top, st.x), ref = next == -INFINITY ? 0.f : next;
-                    const float f = ptx::ex2_approx(top - ref), w = ptx::ex2_approx(st.x - ref);
-                    top = next;
-                    sum = sum * f + w * st.y;
-                    acc.x = acc.x * f + w * v.x;
-                    acc.y = acc.y * f + w * v.y;
-                    acc.z = acc.z * f + w * v.z;
-                    acc.w = acc.w * f + w * v.w;
-                }
-            }
-            __syncthreads();
-        }
-        if (z != 0 || skip || c >= p.D / 4) continue;
-        const bool empty = sum == 0.f;
-        const float inv = empty ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c) =
-            empty ? make_uint2(0u, 0u)
-                  : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
-        if (p.lse && c == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
+    if constexpr (kZ > 1) {
+        __shared__ float2 s_stat[kMergeThreads];
+        __shared__ float4 s_acc[kMergeThreads];
+        s_stat[threadIdx.x] = make_float2(top, sum);
+        s_acc[threadIdx.x] = acc;
+        __syncthreads();
+        if (z != 0) return;
+        float2 st[kZ];
+#pragma unroll
+        for (int j = 0; j < kZ; ++j) st[j] = s_stat[threadIdx.x + j * kRows * kCols];
+#pragma unroll
+        for (int j = 1; j < kZ; ++j) top = fmaxf(top, st[j].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kZ; ++j) {
+            const float w = ptx::ex2_approx(st[j].x - ref);
+            const float4 v = s_acc[threadIdx.x + j * kRows * kCols];
+            sum = fmaf(w, st[j].y, sum);
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+    }
+    if (skip || c >= p.D / 4) return;
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c) =
+        empty ? make_uint2(0u, 0u)
+              : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
+    if (p.lse && c == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int kCols, int kZ>
@@ -585,7 +587,7 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream)
 {
     constexpr int kRows = kMergeThreads / (kCols * kZ);
     const int groups = (p.G * p.T + kRows - 1) / kRows;
-    const dim3 grid((unsigned)(p.B * groups), (unsigned)(p.Hq / p.G));
+    const dim3 grid((unsigned)(p.B * groups), (unsigned)(p.Hq / p.G), (unsigned)((p.D / 4 + kCols - 1) / kCols));
     return p.f16 ? launch_behind(paged_merge_kernel<kCols, kZ, true>, grid, kMergeThreads, 0, stream, p, groups)
                  : launch_behind(paged_merge_kernel<kCols, kZ, false>, grid, kMergeThreads, 0, stream, p, groups);
 }
@@ -641,14 +643,15 @@ cudaError_t read_and_clear_status_paged_rows(uint32_t *out)
 cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaStream_t stream)
 {
     // Threads per column that share a row's states: as many as leave each two
-    // or more, while the launch stays within one wave of CTAs.
+    // or more, while the launch stays within a wave of CTAs.
     const int cols = p.D <= 64 ? 16 : 32;
+    const auto ctas = [&](int z, int c) {
+        const int rows = kMergeThreads / (c * z);
+        return (int64_t)p.B * ((p.G * p.T + rows - 1) / rows) * (p.Hq / p.G) * ((p.D / 4 + c - 1) / c);
+    };
+    if (states >= 32 && ctas(32, 8) <= 4 * sms) return launch_merge<8, 32>(p, stream);
     int z = 1;
-    while (z < 8 && 4 * z <= states) {
-        const int rows = kMergeThreads / (cols * 2 * z);
-        if ((int64_t)p.B * ((p.G * p.T + rows - 1) / rows) * (p.Hq / p.G) > 4 * sms) break;
-        z *= 2;
-    }
+    while (z < 8 && 4 * z <= states && ctas(2 * z, cols) <= 4 * sms) z *= 2;
     return p.D <= 64 ? launch_merge_z<16>(p, z, stream) : launch_merge_z<32>(p, z, stream);
 }
 

@@ -67,13 +67,11 @@ struct TcLayout {
     static constexpr int kTileBytes = kChunks * kChunkBytes;    // a Q, K or V tile
     // K slots and V slots: a tile takes ~1500 clk to arrive, and V's products
     // follow the softmax, so V is requested further ahead.
-    static constexpr int kRingK = D == 128 ? 2 : 4, kRingV = D == 128 ? 3 : 4;
+    static constexpr int kRingK = D == 128 ? 3 : 4, kRingV = D == 128 ? 3 : 4;
     static constexpr int kQOff = 0;
     static constexpr int kKOff = kTileBytes;
     static constexpr int kVOff = kKOff + kRingK * kTileBytes;
-    static constexpr int kXchOff = kVOff + kRingV * kTileBytes;  // (m, l, l_o) of both halves
-    static constexpr int kXchBytes = 2 * 3 * BM * 4;
-    static constexpr int kBarOff = kXchOff + kXchBytes;
+    static constexpr int kBarOff = kVOff + kRingV * kTileBytes;
     // q_full, k_full/k_empty[RK], v_full/v_empty[RV], s_full, s_read,
     // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
     static constexpr int kBars = 1 + 2 * (kRingK + kRingV) + 2 + 4 + 4 + 4;
@@ -477,18 +475,27 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             have = ptx::bar_and(1, 256, have);
             if (!have) break;
             ptx::tc_fence_after();
-            float *xch = reinterpret_cast<float *>(smem + Lay::kXchOff);   // [half][3][BM]
-            xch[(h * 3 + 0) * BM + r_local] = st.m_ref;
-            xch[(h * 3 + 1) * BM + r_local] = st.l;
-            xch[(h * 3 + 2) * BM + r_local] = st.l_o;
+            // (m, l, l_o) of the other half through the first columns of P tile
+            // 0, which no product reads before these warps store the next P.
+            uint32_t mine[4] = {f2u(st.m_ref), f2u(st.l), f2u(st.l_o), 0u}, its[4];
+            ptx::tmem_st4(tmem + lane_off + kColP + (uint32_t)(h * 4), mine);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
             ptx::bar_sync(2, 256);
+            ptx::tc_fence_after();
+            ptx::tmem_ld4(tmem + lane_off + kColP + (uint32_t)((1 - h) * 4), its);
+            ptx::tmem_wait_ld();
             float mh[2], lh[2], loh[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mh[e] = xch[(e * 3 + 0) * BM + r_local];
-                lh[e] = xch[(e * 3 + 1) * BM + r_local];
-                loh[e] = xch[(e * 3 + 2) * BM + r_local];
+                mh[e] = u2f(e == h ? mine[0] : its[0]);
+                lh[e] = u2f(e == h ? mine[1] : its[1]);
+                loh[e] = u2f(e == h ? mine[2] : its[2]);
             }
+            // both halves have read before either stores the next tile's P
+            ptx::tc_fence_before();
+            ptx::bar_sync(2, 256);
+            ptx::tc_fence_after();
             const bool on[2] = {lh[0] != 0.f, lh[1] != 0.f};      // a NaN stays on and reaches the output
             const float m = fmaxf(on[0] ? mh[0] : -INFINITY, on[1] ? mh[1] : -INFINITY);
             float w[2];
