@@ -89,7 +89,7 @@ struct Partials {
 struct Beside {
     int on;
     int sms, per_sm;                   // pieces of the row kernel per SM
-    int blocks;                        // 128-key blocks of the prefix's tiles
+    int blocks, front_tiles;           // the prefix's tiles, and their 128-key blocks
     int chunk, tiles;                  // own keys per chunk; tiles per sequence (row tiles * Hkv)
     const int32_t *seq_len;
     int cap, B;                        // most keys of a sequence; sequences

@@ -127,10 +127,8 @@ struct Plan {
             return;
         }
         ctas = (int64_t)fa::sm_count_of(fa::current_device()) * (tc ? 1 : fa::paged_rows_ctas_per_sm(D, part.rows));
-        // at least two chunks per warp: they arrive together, and half as many
-        // states are joined
-        const int each = tc ? 1 : fa::kRowsWarps, least = tc ? 1 : 2 * each;
-        ctas = std::max<int64_t>(1, std::min(ctas, (chunks + least - 1) / least));
+        const int each = tc ? 1 : fa::kRowsWarps;
+        ctas = std::max<int64_t>(1, std::min(ctas, (chunks + each - 1) / each));
         pieces = ctas * each;
         part.slot_rows = (int)std::min<int64_t>(part.rows, tiles == 1 ? (tc ? 128 : rows) : part.rows);
         const size_t slots = (size_t)(pieces + items);
@@ -231,6 +229,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
         p.beside.on = front.tc && !own.tc;
         p.beside.sms = fa::sm_count_of(fa::current_device());
         p.beside.per_sm = fa::paged_rows_ctas_per_sm(D, own.part.rows) * fa::kRowsWarps;
+        p.beside.front_tiles = (int)front.items;
         p.beside.blocks = (int)(front.items * ((prefix_len + front.part.chunk - 1) / front.part.chunk));
         p.beside.chunk = own.part.chunk;
         p.beside.tiles = own.part.tiles * c->Hkv;

@@ -200,7 +200,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int b = p.part.tiles == 1 ? at.g : at.g / p.part.tiles;
         const int row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
         const int tile = at.g * p.c.Hkv + h;
-        if (at.c == 0 && lane == 0) line.record(at, piece, g0 + done, per);
+        if (at.c == 0 && lane == 0) line.record(at, piece, g0, g0 + done, per);
 
         // Q: rows past R and columns past D are zero
         uint32_t qf[Lay::kQRegs ? KT : 1][4];

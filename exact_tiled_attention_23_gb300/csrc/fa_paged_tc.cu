@@ -510,7 +510,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
             const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
-            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, g0 + (t - count), per);
+            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, g0, g0 + (t - count), per);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {
