@@ -461,87 +461,57 @@ class PagedKV:
         self.k_cache, self.v_cache, self.block_table, self.seq_len = k_cache, v_cache, block_table, seq_len
         pages, Hkv, page_size, D = k_cache.shape
         self.batch, self.Hkv, self.D, self.dtype, self.device = B, Hkv, D, k_cache.dtype, k_cache.device
-        self._f16, self._index, self._workspace_bytes = k_cache.dtype == torch.float16, k_cache.get_device(), {}
-        self._lock, self._workspace = threading.Lock(), None
         sp, sh, ss, _ = k_cache.stride()
         # the stride of a dimension of one entry is never followed
         self.c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
                              ss if page_size > 1 else 0, pages, page_size, Hkv, D, block_table.data_ptr(),
                              block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
+        self._native = _binding().cache(ctypes.addressof(self.c), B, k_cache.dtype == torch.float16,
+                                        k_cache.get_device())
 
     def workspace_bytes(self, Hq: int, T: int, prefix_len: int = 0) -> int:
         """Bytes of workspace that forward_paged() (forward_shared_prefix()
         behind a prefix) needs for queries [B, Hq, T, D]."""
-        key = (Hq, T, prefix_len)
-        need = self._workspace_bytes.get(key)
-        if need is None:
-            import torch
-            with torch.cuda.device(self.device):
-                need = fa_fwd_shared_prefix_workspace_bytes(self.c, prefix_len, self.batch, Hq, T)
-            if len(self._workspace_bytes) > 4096:
-                self._workspace_bytes.clear()
-            self._workspace_bytes[key] = need
-        return need
-
-
-# A generation step is a few microseconds of GPU time: these calls look at each
-# property of a tensor once.
-def _paged_input(x, what, cache, shape):
-    """fa_rows of a [B, H, T, D] input, and the tensor it points into."""
-    if x.shape != shape:
-        raise ValueError(f"{what} must have shape {list(shape)} to match the cache, not {list(x.shape)}")
-    if x.dtype is not cache.dtype or x.get_device() != cache._index:
-        raise ValueError(f"{what} must have the cache's dtype and device")
-    sb, sh, sn, sd = x.stride()
-    ptr = x.data_ptr()
-    if sd != 1 or (sb | sh | sn) & 7 or ptr & 15:
         import torch
-        x = x.clone(memory_format=torch.contiguous_format)
-        sb, sh, sn, _ = x.stride()
-        ptr = x.data_ptr()
-    return fa_rows(ptr, sb, sh, sn), x
+
+        with torch.cuda.device(self.device):
+            return fa_fwd_shared_prefix_workspace_bytes(self.c, prefix_len, self.batch, Hq, T)
 
 
-def _paged_output(out, what, like):
-    """fa_rows of an output like the [B, H, T, D] tensor `like`, and the tensor."""
-    if out is None:
-        import torch
-        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    elif out.shape != like.shape or out.dtype is not like.dtype or out.device != like.device:
-        raise ValueError(f"{what} must be a tensor like q")
-    sb, sh, sn, sd = out.stride()
-    ptr = out.data_ptr()
-    if sd != 1 or (sb | sh | sn) & 7 or ptr & 15:
-        raise ValueError(f"{what} must have a contiguous last dimension, strides that are multiples of 8 and "
-                         "16-byte alignment")
-    return fa_rows(ptr, sb, sh, sn), out
+_BINDING = None
 
 
-def _on_stream(fn, cache, stream, args):
-    """fn(*args, stream pointer) with the cache's device current; torch's
-    allocations and copies go to `stream` too when one is given."""
+def _binding():
+    """lib/fa_torch.so, which passes torch tensors to the paged-cache entry points."""
+    global _BINDING
+    if _BINDING is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (the module uses its libraries)
+
+        lib, path = load(), _build.BINDING_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"the torch binding is not built ({path}); run exact_tiled_attention_23_gb300.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("fa_torch", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_torch", loader))
+        loader.exec_module(module)
+        module.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.fa_kv_append, lib.fa_fwd_shared_prefix, lib.fa_fwd_shared_prefix_workspace_bytes)))
+        _BINDING = module
+    return _BINDING
+
+
+def _stream_context(cache, stream):
+    """torch's context for `stream` (a stream of the cache's device, or its
+    pointer): allocations and copies go there too."""
     import torch
 
-    if stream is None:
-        if torch.cuda.current_device() == cache._index:
-            return fn(*args, _current_raw_stream(cache._index))
-        with torch.cuda.device(cache.device):
-            return fn(*args, _current_raw_stream(cache._index))
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(stream or 0, device=cache.device)
     if stream.device != cache.device:
         raise ValueError("stream must belong to the cache's device")
-    with torch.cuda.stream(stream):
-        return fn(*args, stream.cuda_stream)
-
-
-def _current_raw_stream(index: int) -> int:
-    """The pointer of torch's current stream: its short way where torch has it
-    (2 us less than making a Stream object)."""
-    import torch
-
-    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return short(index) if short is not None else torch.cuda.current_stream(index).cuda_stream
+    return torch.cuda.stream(stream)
 
 
 def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, position_offset: int = 0,
@@ -556,39 +526,15 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
     position, one per pair (2 * numel <= D elements of a head turn), or None
     for no rotation; pairs are (p, p + numel), or neighbours if interleaved.
     position_offset: position of a sequence's first key.  Runs asynchronously
-    on `stream` (default: torch's current stream).
+    on `stream` (default: torch's current stream of the cache's device).
     """
-    return _on_stream(_kv_append, cache, stream, (cache, k, v, q, inv_freq, interleaved, position_offset, q_out))
-
-
-def _kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out, stream):
-    B, Hkv, D = cache.batch, cache.Hkv, cache.D
-    if k.dim() != 4:
-        raise ValueError("k must have shape [B, Hkv, T, D]")
-    T = k.shape[2]
-    shape = (B, Hkv, T, D)
-    ck, k = _paged_input(k, "k", cache, shape)
-    cv, v = _paged_input(v, "v", cache, shape)
-    Hq, cq, co = 0, None, None
-    if q is not None:
-        if q.dim() != 4:
-            raise ValueError("q must have shape [B, Hq, T, D]")
-        Hq = q.shape[1]
-        cq, q = _paged_input(q, "q", cache, (B, Hq, T, D))
-        co, q_out = _paged_output(q_out, "q_out", q)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    rot, freq = 0, None
-    if inv_freq is not None:
-        import torch
-        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != cache._index:
-            raise ValueError("inv_freq must be a float32 tensor of one dimension on the cache's device")
-        inv_freq = inv_freq.contiguous()
-        rot, freq = 2 * inv_freq.numel(), inv_freq.data_ptr()
-    st = fa_kv_append(cache.c, ck, cv, cq, co, B, Hq, T, freq, rot, interleaved, position_offset, cache._f16, stream)
-    if st != FA_OK:
-        raise FAError(st, "fa_kv_append")
-    return q_out
+    if stream is not None:
+        with _stream_context(cache, stream):
+            return kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out)
+    r = _BINDING.kv_append(cache._native, k, v, q, inv_freq, interleaved, position_offset, q_out)
+    if type(r) is int:
+        raise FAError(r, "fa_kv_append")
+    return r
 
 
 def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None, return_lse: bool = True,
@@ -602,7 +548,13 @@ def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None,
     contiguous).  The workspace (a CUDA tensor of at least
     cache.workspace_bytes(Hq, T) bytes) is allocated here when not given.
     """
-    return _on_stream(_forward_paged, cache, stream, (q, cache, None, 0, causal, scale, out, lse, return_lse, workspace))
+    if stream is not None:
+        with _stream_context(cache, stream):
+            return forward_paged(q, cache, causal, scale, out, lse, return_lse, workspace)
+    r = _BINDING.forward(cache._native, q, None, 0, causal, scale, out, lse, return_lse, workspace)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_paged")
+    return r
 
 
 def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool = True, scale=None, out=None,
@@ -614,67 +566,13 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     prefix is read once for the whole batch.  The workspace takes
     cache.workspace_bytes(Hq, T, prefix_len) bytes.
     """
-    return _on_stream(_forward_paged, cache, stream,
-                      (q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace))
-
-
-def _forward_paged(q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace, stream):
-    import torch
-
-    if q.dim() != 4:
-        raise ValueError("q must have shape [B, Hq, T, D]")
-    B, Hkv, (_, Hq, T, _) = cache.batch, cache.Hkv, q.shape
-    cq, q = _paged_input(q, "q", cache, (B, Hq, T, cache.D))
-    if Hkv == 0 or Hq % Hkv:
-        raise ValueError("the query heads must be a multiple of the cache's key heads")
-    pages = None
-    if prefix_table is not None:
-        if prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or \
-                prefix_table.get_device() != cache._index:
-            raise ValueError("prefix_table must be an int32 tensor of one dimension on the cache's device")
-        prefix_len = int(prefix_len)
-        if prefix_len < 0 or prefix_len > prefix_table.numel() * cache.c.page_size:
-            raise ValueError("prefix_len must lie in [0, what prefix_table's pages hold]")
-        prefix_table = prefix_table.contiguous()
-        pages = prefix_table.data_ptr()
-    co, out = _paged_output(out, "out", q)
-    if lse is not None:
-        if lse.shape != (B, Hq, T) or lse.dtype is not torch.float32 or lse.get_device() != cache._index or \
-                not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous float32 tensor [B, Hq, T] on the cache's device")
-    elif return_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
-    if workspace is None:
-        size = cache.workspace_bytes(Hq, T, prefix_len)
-        if stream == 0 and size <= _KEPT_WORKSPACE:
-            # Only the default stream: another stream's calls, or a graph
-            # captured on one, may run beside these.  The lock keeps two host
-            # threads' launches apart.
-            with cache._lock:
-                workspace = cache._workspace
-                if workspace is None or workspace.numel() < size:
-                    cache._workspace = workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
-                st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, None if lse is None else lse.data_ptr(),
-                                          B, Hq, T, causal, _DEFAULT_SCALE if scale is None else scale, cache._f16,
-                                          workspace.data_ptr(), size, 0)
-            if st != FA_OK:
-                raise FAError(st, "fa_fwd_paged" if prefix_table is None else "fa_fwd_shared_prefix")
-            return (out, lse) if return_lse else out
-        workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
-    else:
-        if workspace.get_device() != cache._index or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        size = workspace.numel() * workspace.element_size()
-    st = fa_fwd_shared_prefix(cq, cache.c, pages, prefix_len, co, None if lse is None else lse.data_ptr(), B, Hq, T,
-                              causal, _DEFAULT_SCALE if scale is None else scale, cache._f16, workspace.data_ptr(),
-                              size, stream)
-    if st != FA_OK:
-        raise FAError(st, "fa_fwd_paged" if prefix_table is None else "fa_fwd_shared_prefix")
-    return (out, lse) if return_lse else out
-
-
-_KEPT_WORKSPACE = 32 << 20
-_DEFAULT_SCALE = float("nan")
+    if stream is not None:
+        with _stream_context(cache, stream):
+            return forward_shared_prefix(q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace)
+    r = _BINDING.forward(cache._native, q, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_shared_prefix")
+    return r
 
 
 # ------------------------------------------------------------- autograd

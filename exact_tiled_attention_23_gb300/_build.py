@@ -1,16 +1,20 @@
 """Build the attention library (libfa.so) in-tree with nvcc for sm_103a.
 
 Each .cu under csrc/ is compiled in parallel to an object under _build/, then
-linked into lib/libfa.so.  Nothing is installed anywhere else.  A rebuild is
-skipped when the library is newer than every source and header.
+linked into lib/libfa.so.  Beside them the C++ compiler builds lib/fa_torch.so,
+which passes torch tensors to the paged-cache entry points (skipped where torch
+cannot be imported: the C ABI does not need it).  Nothing is installed anywhere
+else.  A rebuild is skipped when both are newer than every source and header.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "fa_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -41,14 +47,37 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+        + glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SOURCE, os.path.abspath(__file__)]
+
+
+def _have_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    built = [LIB_PATH] + ([BINDING_PATH] if _have_torch() else [])
+    if not all(os.path.exists(f) for f in built):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(f) for f in built)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _build_binding() -> None:
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(at, "include"),
+           "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), "-I" + INCLUDE, BINDING_SOURCE, "-o", tmp,
+           "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -70,8 +99,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout, r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(sources()))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
+        binding = ex.submit(_build_binding) if _have_torch() else None
         objs = list(ex.map(compile_one, sources()))
+        if binding is not None:
+            binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     r = subprocess.run([exe, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
