@@ -89,7 +89,7 @@ struct Partials {
 struct Beside {
     int on;
     int sms, per_sm;                   // pieces of the row kernel per SM
-    int blocks, front_tiles;           // the prefix's tiles, and their 128-key blocks
+    int blocks;                        // 128-key blocks of the prefix's tiles
     int chunk, tiles;                  // own keys per chunk; tiles per sequence (row tiles * Hkv)
     const int32_t *seq_len;
     int cap, B;                        // most keys of a sequence; sequences
@@ -98,6 +98,16 @@ struct Beside {
 // Own chunks (8 KB of keys and values at D = 64 and 128) that cost an SM as
 // much time as one block.
 constexpr int kBlockCost = 10;
+
+// SMs for the prefix beside `own` chunks of the sequences' own keys.
+#ifdef __CUDACC__
+__device__ __forceinline__ int beside_front(const Beside &s, int own)
+{
+    const float part = (float)s.blocks * kBlockCost;
+    const int front = (int)((float)s.sms * part / (part + (float)own) + 0.5f);
+    return front < 1 ? 1 : front < s.sms ? front : s.sms - 1;
+}
+#endif
 
 struct PagedParams {
     PagedCache c;
@@ -138,7 +148,7 @@ constexpr int kBlockKeys = 128;
 // piece of the line) per CTA, and CTAs per SM.
 int paged_rows_per_tile(int D, int64_t rows);
 int paged_rows_chunk(int D);
-constexpr int kRowsWarps = 4;
+constexpr int kRowsWarps = 2;
 int paged_rows_ctas_per_sm(int D, int rows);
 
 // The current device's number, and its multiprocessors (148 if unknown).

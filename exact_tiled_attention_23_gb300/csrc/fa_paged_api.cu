@@ -229,7 +229,6 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
         p.beside.on = front.tc && !own.tc;
         p.beside.sms = fa::sm_count_of(fa::current_device());
         p.beside.per_sm = fa::paged_rows_ctas_per_sm(D, own.part.rows) * fa::kRowsWarps;
-        p.beside.front_tiles = (int)front.items;
         p.beside.blocks = (int)(front.items * ((prefix_len + front.part.chunk - 1) / front.part.chunk));
         p.beside.chunk = own.part.chunk;
         p.beside.tiles = own.part.tiles * c->Hkv;

@@ -95,11 +95,7 @@ struct Line {
             own = __reduce_add_sync(0xffffffffu, own) * s.tiles;
         }
         if (own == 0) return most;
-        const float part = (float)s.blocks * kBlockCost;
-        int front = min(max((int)((float)s.sms * part / (part + (float)own) + 0.5f), 1), s.sms - 1);
-        // whole numbers of pieces per tile of the prefix, where they come near
-        const int each = max(1, (front + s.front_tiles / 2) / s.front_tiles);
-        if (each * s.front_tiles < s.sms) front = each * s.front_tiles;
+        const int front = beside_front(s, own);
         return min(p.part.stacked ? front : (s.sms - front) * s.per_sm, most);
     }
 
@@ -108,27 +104,9 @@ struct Line {
     // chunks of a strip of groups; the strips' prefix sums find the strip to
     // start in, and its groups' the group.  Every warp does it for itself: no
     // barrier, and little code to fetch.  (The host keeps the line below 2^31.)
-    // The tiles of a prefix have one length; with at least one piece for each,
-    // no piece crosses from one to the next (which costs the tensor-core kernel
-    // 4 to 10 us).
     __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &first, int &count, int &per) const
     {
         const int lane = threadIdx.x % 32;
-        if (p.part.stacked) {
-            const int tiles = groups * p.c.Hkv;
-            enter(at, 0);
-            const int cut = pieces(at.n * tiles, most);
-            if (cut >= tiles) {
-                const int each = cut / tiles, tile = piece / each, part = piece - tile * each;
-                per = (at.n + each - 1) / each;
-                at.c = part * per;
-                at.g = tile / p.c.Hkv;
-                at.h = tile - at.g * p.c.Hkv;
-                first = tile * at.n + at.c;
-                count = tile < tiles ? max(0, min(per, at.n - at.c)) : 0;
-                return;
-            }
-        }
         const int strip = (groups + 31) / 32;
         int sum = 0;
 #pragma unroll 4

@@ -46,18 +46,21 @@ constexpr int kWarps = kRowsWarps;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int DP, int MT>
+template <int DP, int RM>
 struct RowsLayout {
-    static constexpr int kRows = 16 * MT;
+    // Up to 8 rows are the products' columns (keys and columns of V their rows:
+    // half the products, weights and registers of 16 rows), more are their rows.
+    static constexpr bool kColumns = RM == 8;
+    static constexpr int MT = kColumns ? 1 : RM / 16;             // 16-row tiles of Q
     // Keys of a chunk, one step of a warp: 8 KB of K and V at D <= 128.
     static constexpr int kChunk = DP == 64 ? 32 : 16;
     static constexpr int kTileBytes = kChunk * DP * 2;            // K or V of a step
     static constexpr int kStageBytes = 2 * kTileBytes;
     // Q in registers, or where O leaves too few, in shared memory per warp
-    static constexpr bool kQRegs = MT == 1 && DP <= 128;
-    static constexpr int kQBytes = kQRegs ? 0 : kRows * DP * 2;
-    // CTAs per SM and stages per warp: what registers and shared memory hold
-    static constexpr int kCtas = DP == 256 ? 1 : MT == 1 ? 3 : 2;
+    static constexpr bool kQRegs = kColumns || (RM == 16 && DP <= 128);
+    static constexpr int kQBytes = kQRegs ? 0 : RM * DP * 2;
+    // CTAs per SM: what registers and shared memory hold
+    static constexpr int kCtas = DP == 256 ? (RM == 8 ? 3 : 2) : RM == 32 ? 4 : 6;
     static constexpr int kStages = 2;
     static constexpr int kRingOff = 0;
     static constexpr int kQOff = kWarps * kStages * kStageBytes;
@@ -65,6 +68,7 @@ struct RowsLayout {
     static constexpr int kBarOff = kMaskOff + kWarps * kStages * 4;
     static constexpr int kAbortOff = kBarOff + kWarps * kStages * 8;
     static constexpr int kSmemBytes = kAbortOff + kWarps * 4 + 1024;   // + alignment slack
+    static_assert(RM == 8 || RM == 16 || (RM == 32 && DP <= 128), "rows");
     static_assert(kBarOff % 8 == 0, "barriers");
     static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
@@ -79,12 +83,12 @@ __device__ __forceinline__ uint32_t unit_at(int row, int unit)
     return (uint32_t)((unit >> 3) * (kTall * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
 }
 
-template <int DP, int MT, bool kF16, bool kTma>
-__global__ void __launch_bounds__(kThreads, (RowsLayout<DP, MT>::kCtas))
+template <int DP, int RM, bool kF16, bool kTma>
+__global__ void __launch_bounds__(kThreads, (RowsLayout<DP, RM>::kCtas))
 paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
 {
-    using Lay = RowsLayout<DP, MT>;
-    constexpr int S = Lay::kStages, RM = Lay::kRows, KS = Lay::kChunk;
+    using Lay = RowsLayout<DP, RM>;
+    constexpr int S = Lay::kStages, MT = Lay::MT, KS = Lay::kChunk;
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : 0xffffu;
     constexpr int NT = DP / 8;                      // 8-column tiles of O
     constexpr int KT = DP / 16;                     // 16-column steps of a score
@@ -100,10 +104,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const Abort ab{abort_word, &g_status_paged_rows};
 
     if constexpr (kTma) {
+        // (set-up that reads no memory overlaps the end of the kernel before)
         if (lane == 0) {
             for (int i = 0; i < S; ++i) ptx::mbar_init(&full[i], 1);
             *abort_word = 0;
             ptx::fence_mbarrier_init();
+            ptx::tma_prefetch_desc(&tm_k);
+            ptx::tma_prefetch_desc(&tm_v);
         }
         __syncwarp();
     }
@@ -190,10 +197,40 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
 
     // ---- the piece, tile by tile -------------------------------------------
-    const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a tile
+    const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a product
     const uint32_t q_smem = s_base + Lay::kQOff + warp * Lay::kQBytes;
     int stage = 0, done = 0;
     uint32_t phase = 0;
+    // Waits for a step's keys; returns which of them are visible.  (A wait that
+    // gave up leaves the results undefined; its copies are waited for at the end.)
+    auto landed = [&]() -> uint32_t {
+        if constexpr (kTma)
+            wait_bounded(&full[stage], phase, p.wait_limit_ns, kSiteSlotFull, ab);
+        else
+            ptx::cp_async_wait<S - 1>();
+        __syncwarp();
+        return s_mask[stage];
+    };
+    // A box brings what its page holds behind the last key.
+    auto clear_rest = [&](uint32_t mask, uint32_t vt) {
+        if (!kTma || mask == kAll) return;
+#pragma unroll 1
+        for (int e = lane; e < KS * (DP / 8); e += 32)
+            if (!((mask >> (e % KS)) & 1u)) ptx::st_shared_v4(vt + unit_at<KS>(e % KS, e / KS), 0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();              // before the next copy into the stage
+        __syncwarp();
+    };
+    // The step is done: its stage takes the next one (past the piece, nothing).
+    auto refill = [&] {
+        __syncwarp();
+        const Place x = next;
+        next = look_up();
+        load(stage, x);
+        if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
 #pragma unroll 1
     while (done < steps) {
         const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the piece
@@ -202,219 +239,357 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int tile = at.g * p.c.Hkv + h;
         if (at.c == 0 && lane == 0) line.record(at, piece, g0, g0 + done, per);
 
-        // Q: rows past R and columns past D are zero
-        uint32_t qf[Lay::kQRegs ? KT : 1][4];
-        if constexpr (Lay::kQRegs) {
+        const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
+
+        if constexpr (Lay::kColumns) {
+            // Q: this lane's row qr, columns 2 qc, +1 of every 8
+            uint32_t qb[KT][2];
 #pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) qf[k][e] = 0u;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (row0 + qr + 8 * r >= R) continue;
-                const RowPlace x = row_place(p, b, h, row0 + qr + 8 * r);
+            for (int k = 0; k < KT; ++k) qb[k][0] = qb[k][1] = 0u;
+            if (row0 + qr < R) {
+                const RowPlace x = row_place(p, b, h, row0 + qr);
                 const uint16_t *src = p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + 2 * qc;
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (16 * k + 8 * e < p.c.D) qf[k][2 * e + r] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 * e);
+                        if (16 * k + 8 * e < p.c.D) qb[k][e] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 * e);
+            }
+            int lim[2];                             // keys that rows 2 qc and 2 qc + 1 see
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                lim[r] = line.masked ? at.len - p.T + p.by_g.quotient(row0 + 2 * qc + r) + 1 : at.len;
+            // o[n]: columns 16 n + qr (and + 8) of rows 2 qc and 2 qc + 1
+            float o[KT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < KT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+
+#pragma unroll 1
+            for (int step = 0; step < count; ++step) {
+                const uint32_t mask = landed();
+                const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
+                const int key0 = (at.c + step) * KS;
+                if (mask) {
+                    // scores of keys 16 j + qr (and + 8) and the two rows
+                    float s[KS / 16][4];
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int j = 0; j < KS / 16; ++j) {
+                            uint32_t ka[4];
+                            ptx::ldmatrix4(ka, kt + unit_at<KS>(16 * j + (lane & 15), 2 * k + (lane >> 4)));
+                            ptx::mma_16816<kF16>(s[j], ka, qb[k][0], qb[k][1]);
+                        }
+                    if (mask != kAll || key0 + KS > lim_all) {
+                        clear_rest(mask, vt);
+#pragma unroll
+                        for (int j = 0; j < KS / 16; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int key = 16 * j + qr + 8 * (e >> 1);
+                                if (!((mask >> key) & 1u) || key0 + key >= lim[e & 1]) s[j][e] = -INFINITY;
+                            }
+                    }
+                    float ref[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float mx = fmaxf(s[0][r], s[0][r + 2]);
+#pragma unroll
+                        for (int j = 1; j < KS / 16; ++j) mx = ptx::max3(mx, s[j][r], s[j][r + 2]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        mx *= p.scale_log2;
+                        // (as below: the reference follows only rises of 2^8)
+                        if (__any_sync(0xffffffffu, mx > m[r] + 8.f)) {
+                            const float m_new = fmaxf(m[r], mx);
+                            const float alpha = ptx::ex2_approx(m[r] - (m_new == -INFINITY ? 0.f : m_new));
+                            l[r] *= alpha;
+#pragma unroll
+                            for (int n = 0; n < KT; ++n) {
+                                o[n][r] *= alpha;
+                                o[n][r + 2] *= alpha;
+                            }
+                            m[r] = m_new;
+                        }
+                        ref[r] = m[r] == -INFINITY ? 0.f : m[r];
+                    }
+                    uint32_t hi[KS / 16][2], lo[KS / 16][2];
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float p0 = ptx::ex2_approx(fmaf(s[j][2 * e], p.scale_log2, -ref[0]));
+                            const float p1 = ptx::ex2_approx(fmaf(s[j][2 * e + 1], p.scale_log2, -ref[1]));
+                            l[0] += p0;
+                            l[1] += p1;
+                            const uint32_t w = ptx::pack16x2<kF16>(p0, p1);
+                            float r0, r1;
+                            ptx::unpack2(ptx::widen16x2<kF16>(w), r0, r1);
+                            // keys of a lane's weights become those of a product's lane
+                            hi[j][e] = ptx::transpose8(w);
+                            lo[j][e] = ptx::transpose8(ptx::pack16x2<kF16>(p0 - r0, p1 - r1));
+                        }
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j)
+#pragma unroll
+                        for (int n = 0; n < KT; ++n) {
+                            // columns 16 n .. of V as rows, keys 16 j .. as the product's k
+                            uint32_t va[4];
+                            ptx::ldmatrix4_trans(va, vt + unit_at<KS>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * n + ((lane >> 3) & 1)));
+                            ptx::mma_16816<kF16>(o[n], va, hi[j][0], hi[j][1]);
+                            ptx::mma_16816<kF16>(o[n], va, lo[j][0], lo[j][1]);
+                        }
+                }
+                refill();
+            }
+
+            // ---- the tile's state ----
+            const bool direct = count == at.n && !p.joined;
+            const int64_t slot = (int64_t)piece + tile;
+            bool empty[2];
+            float inv[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float sum = l[r];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                // (a NaN among the scores reaches the output)
+                empty[r] = sum == 0.f;
+                inv[r] = empty[r] ? 0.f : 1.f / sum;
+                const int tr = 2 * qc + r;
+                if (qr == 0 && row0 + tr < R) {
+                    const float lse2 = empty[r] ? -INFINITY : m[r] + log2f(sum);
+                    if (!direct) {
+                        p.part.lse[slot * p.part.slot_rows + tr] = lse2;
+                    } else if (p.lse) {
+                        const RowPlace x = row_place(p, b, h, row0 + tr);
+                        p.lse[((int64_t)x.b * p.Hq + x.hq) * p.T + x.t] = lse2 * kLn2;
+                    }
+                }
+            }
+            if (direct) {
+                // back to a row's neighbouring columns per lane
+                const bool mine = row0 + qr < R;
+                const RowPlace x = row_place(p, b, h, mine ? row0 + qr : row0);
+                uint16_t *dst = p.o + x.b * p.o_s[0] + x.hq * p.o_s[1] + x.t * p.o_s[2] + 2 * qc;
+#pragma unroll
+                for (int n = 0; n < KT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = ptx::transpose8(ptx::pack16x2<kF16>(empty[0] ? 0.f : o[n][2 * e] * inv[0],
+                                                                               empty[1] ? 0.f : o[n][2 * e + 1] * inv[1]));
+                        if (mine && 16 * n + 8 * e < p.c.D) *reinterpret_cast<uint32_t *>(dst + 16 * n + 8 * e) = w;
+                    }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (row0 + 2 * qc + r >= R) continue;
+                    float *dst = p.part.o + ((slot * (p.c.D / 4) + qr / 4) * p.part.slot_rows + 2 * qc + r) * 4 + qr % 4;
+#pragma unroll
+                    for (int n = 0; n < KT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (16 * n + 8 * e < p.c.D)
+                                dst[(4 * n + 2 * e) * 4 * p.part.slot_rows] = empty[r] ? 0.f : o[n][2 * e + r] * inv[r];
+                }
             }
         } else {
-            __syncwarp();
+            // Q: rows past R and columns past D are zero
+            uint32_t qf[Lay::kQRegs ? KT : 1][4];
+            if constexpr (Lay::kQRegs) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qf[k][e] = 0u;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (row0 + qr + 8 * r >= R) continue;
+                    const RowPlace x = row_place(p, b, h, row0 + qr + 8 * r);
+                    const uint16_t *src = p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + 2 * qc;
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (16 * k + 8 * e < p.c.D) qf[k][2 * e + r] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8 * e);
+                }
+            } else {
+                __syncwarp();
 #pragma unroll 4
-            for (int e = lane; e < RM * (DP / 8); e += 32) {
-                const int row = e / (DP / 8), unit = e % (DP / 8);
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (row0 + row < R && unit * 8 < p.c.D) {
-                    const RowPlace x = row_place(p, b, h, row0 + row);
-                    w = *reinterpret_cast<const uint4 *>(p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + unit * 8);
+                for (int e = lane; e < RM * (DP / 8); e += 32) {
+                    const int row = e / (DP / 8), unit = e % (DP / 8);
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (row0 + row < R && unit * 8 < p.c.D) {
+                        const RowPlace x = row_place(p, b, h, row0 + row);
+                        w = *reinterpret_cast<const uint4 *>(p.q + x.b * p.q_s[0] + x.hq * p.q_s[1] + x.t * p.q_s[2] + unit * 8);
+                    }
+                    ptx::st_shared_v4(q_smem + unit_at<RM>(row, unit), w.x, w.y, w.z, w.w);
                 }
-                ptx::st_shared_v4(q_smem + unit_at<RM>(row, unit), w.x, w.y, w.z, w.w);
+                __syncwarp();
             }
-            __syncwarp();
-        }
-        int lim[2 * MT];                            // keys that this lane's rows see
+            int lim[2 * MT];                            // keys that this lane's rows see
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i)
-            lim[i] = line.masked ? at.len - p.T + p.by_g.quotient(row0 + i * 8 + qr) + 1 : at.len;
-        const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
+            for (int i = 0; i < 2 * MT; ++i)
+                lim[i] = line.masked ? at.len - p.T + p.by_g.quotient(row0 + i * 8 + qr) + 1 : at.len;
 
-        float o[MT][NT][4], m[2 * MT], l[2 * MT];
+            float o[MT][NT][4], m[2 * MT], l[2 * MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+            for (int i = 0; i < 2 * MT; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
 
 #pragma unroll 1
-        for (int step = 0; step < count; ++step) {
-            // (a wait that gave up leaves the results undefined; the copies are
-            // waited for at the end)
-            if constexpr (kTma)
-                wait_bounded(&full[stage], phase, p.wait_limit_ns, kSiteSlotFull, ab);
-            else
-                ptx::cp_async_wait<S - 1>();
-            __syncwarp();
-            const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
-            const uint32_t mask = s_mask[stage];
-            const int key0 = (at.c + step) * KS;
-            if (mask) {
-                float s[MT][KS / 8][4];
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int n = 0; n < KS / 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    uint32_t qa[MT][4];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        if constexpr (Lay::kQRegs) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) qa[i][e] = qf[k][e];
-                        } else {
-                            ptx::ldmatrix4(qa[i], q_smem + unit_at<RM>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < KS / 16; ++j) {
-                        // K rows 16j .. +7 and +8 .. +15, columns 16k .. +7 and +8 .. +15
-                        uint32_t kb[4];
-                        ptx::ldmatrix4(kb, kt + unit_at<KS>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            ptx::mma_16816<kF16>(s[i][2 * j], qa[i], kb[0], kb[1]);
-                            ptx::mma_16816<kF16>(s[i][2 * j + 1], qa[i], kb[2], kb[3]);
-                        }
-                    }
-                }
-                if (mask != kAll || key0 + KS > lim_all) {
-                    if constexpr (kTma) {
-                        // a box brings what its page holds behind the last key
-                        if (mask != kAll) {
-#pragma unroll 1
-                            for (int e = lane; e < KS * (DP / 8); e += 32)
-                                if (!((mask >> (e % KS)) & 1u)) ptx::st_shared_v4(vt + unit_at<KS>(e % KS, e / KS), 0u, 0u, 0u, 0u);
-                            ptx::fence_proxy_async_smem();      // before the next copy into the stage
-                            __syncwarp();
-                        }
-                    }
+            for (int step = 0; step < count; ++step) {
+                const uint32_t mask = landed();
+                const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
+                const int key0 = (at.c + step) * KS;
+                if (mask) {
+                    float s[MT][KS / 8][4];
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int key = n * 8 + 2 * qc + (e & 1);
-                                if (!((mask >> key) & 1u) || key0 + key >= lim[2 * i + (e >> 1)]) s[i][n][e] = -INFINITY;
-                            }
-                }
-                uint32_t hi[MT][KS / 16][4], lo[MT][KS / 16][4];
+                            for (int e = 0; e < 4; ++e) s[i][n][e] = 0.f;
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float &mr = m[2 * i + r], &lr = l[2 * i + r];
-                        float mx = fmaxf(s[i][0][2 * r], s[i][0][2 * r + 1]);
-#pragma unroll
-                        for (int n = 1; n < KS / 8; ++n) mx = ptx::max3(mx, s[i][n][2 * r], s[i][n][2 * r + 1]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        // The reference follows the largest score only when that
-                        // is 2^8 above it: weights stay at most 256, and O is
-                        // rescaled rarely.
-                        mx *= p.scale_log2;
-                        if (__any_sync(0xffffffffu, mx > mr + 8.f)) {
-                            const float m_new = fmaxf(mr, mx), ref = m_new == -INFINITY ? 0.f : m_new;
-                            const float alpha = ptx::ex2_approx(mr - ref);
-                            lr *= alpha;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                o[i][n][2 * r] *= alpha;
-                                o[i][n][2 * r + 1] *= alpha;
-                            }
-                            mr = m_new;
-                        }
-                        const float ref = mr == -INFINITY ? 0.f : mr;
-#pragma unroll
-                        for (int n = 0; n < KS / 8; ++n) {
-                            const float p0 = ptx::ex2_approx(fmaf(s[i][n][2 * r], p.scale_log2, -ref));
-                            const float p1 = ptx::ex2_approx(fmaf(s[i][n][2 * r + 1], p.scale_log2, -ref));
-                            lr += p0 + p1;
-                            const uint32_t w = ptx::pack16x2<kF16>(p0, p1);
-                            float r0, r1;
-                            ptx::unpack2(ptx::widen16x2<kF16>(w), r0, r1);
-                            hi[i][n / 2][2 * (n & 1) + r] = w;
-                            lo[i][n / 2][2 * (n & 1) + r] = ptx::pack16x2<kF16>(p0 - r0, p1 - r1);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < KS / 16; ++j)
-#pragma unroll
-                    for (int n = 0; n < KT; ++n) {
-                        // V rows 16j .. +7 and +8 .. +15 (the product's k), columns 16n .. +7 and +8 .. +15
-                        uint32_t vb[4];
-                        ptx::ldmatrix4_trans(vb, vt + unit_at<KS>(16 * j + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+                    for (int k = 0; k < KT; ++k) {
+                        uint32_t qa[MT][4];
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            ptx::mma_16816<kF16>(o[i][2 * n], hi[i][j], vb[0], vb[1]);
-                            ptx::mma_16816<kF16>(o[i][2 * n + 1], hi[i][j], vb[2], vb[3]);
-                            ptx::mma_16816<kF16>(o[i][2 * n], lo[i][j], vb[0], vb[1]);
-                            ptx::mma_16816<kF16>(o[i][2 * n + 1], lo[i][j], vb[2], vb[3]);
+                            if constexpr (Lay::kQRegs) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) qa[i][e] = qf[k][e];
+                            } else {
+                                ptx::ldmatrix4(qa[i], q_smem + unit_at<RM>(i * 16 + (lane & 15), 2 * k + (lane >> 4)));
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < KS / 16; ++j) {
+                            // K rows 16j .. +7 and +8 .. +15, columns 16k .. +7 and +8 .. +15
+                            uint32_t kb[4];
+                            ptx::ldmatrix4(kb, kt + unit_at<KS>(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                ptx::mma_16816<kF16>(s[i][2 * j], qa[i], kb[0], kb[1]);
+                                ptx::mma_16816<kF16>(s[i][2 * j + 1], qa[i], kb[2], kb[3]);
+                            }
                         }
                     }
+                    if (mask != kAll || key0 + KS > lim_all) {
+                        clear_rest(mask, vt);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int n = 0; n < KS / 8; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int key = n * 8 + 2 * qc + (e & 1);
+                                    if (!((mask >> key) & 1u) || key0 + key >= lim[2 * i + (e >> 1)]) s[i][n][e] = -INFINITY;
+                                }
+                    }
+                    uint32_t hi[MT][KS / 16][4], lo[MT][KS / 16][4];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float &mr = m[2 * i + r], &lr = l[2 * i + r];
+                            float mx = fmaxf(s[i][0][2 * r], s[i][0][2 * r + 1]);
+#pragma unroll
+                            for (int n = 1; n < KS / 8; ++n) mx = ptx::max3(mx, s[i][n][2 * r], s[i][n][2 * r + 1]);
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                            // The reference follows the largest score only when that
+                            // is 2^8 above it: weights stay at most 256, and O is
+                            // rescaled rarely.
+                            mx *= p.scale_log2;
+                            if (__any_sync(0xffffffffu, mx > mr + 8.f)) {
+                                const float m_new = fmaxf(mr, mx), ref = m_new == -INFINITY ? 0.f : m_new;
+                                const float alpha = ptx::ex2_approx(mr - ref);
+                                lr *= alpha;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    o[i][n][2 * r] *= alpha;
+                                    o[i][n][2 * r + 1] *= alpha;
+                                }
+                                mr = m_new;
+                            }
+                            const float ref = mr == -INFINITY ? 0.f : mr;
+#pragma unroll
+                            for (int n = 0; n < KS / 8; ++n) {
+                                const float p0 = ptx::ex2_approx(fmaf(s[i][n][2 * r], p.scale_log2, -ref));
+                                const float p1 = ptx::ex2_approx(fmaf(s[i][n][2 * r + 1], p.scale_log2, -ref));
+                                lr += p0 + p1;
+                                const uint32_t w = ptx::pack16x2<kF16>(p0, p1);
+                                float r0, r1;
+                                ptx::unpack2(ptx::widen16x2<kF16>(w), r0, r1);
+                                hi[i][n / 2][2 * (n & 1) + r] = w;
+                                lo[i][n / 2][2 * (n & 1) + r] = ptx::pack16x2<kF16>(p0 - r0, p1 - r1);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < KS / 16; ++j)
+#pragma unroll
+                        for (int n = 0; n < KT; ++n) {
+                            // V rows 16j .. +7 and +8 .. +15 (the product's k), columns 16n .. +7 and +8 .. +15
+                            uint32_t vb[4];
+                            ptx::ldmatrix4_trans(vb, vt + unit_at<KS>(16 * j + (lane & 7) + (((lane >> 3) & 1) << 3), 2 * n + (lane >> 4)));
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                ptx::mma_16816<kF16>(o[i][2 * n], hi[i][j], vb[0], vb[1]);
+                                ptx::mma_16816<kF16>(o[i][2 * n + 1], hi[i][j], vb[2], vb[3]);
+                                ptx::mma_16816<kF16>(o[i][2 * n], lo[i][j], vb[0], vb[1]);
+                                ptx::mma_16816<kF16>(o[i][2 * n + 1], lo[i][j], vb[2], vb[3]);
+                            }
+                        }
+                }
+                refill();
             }
-            __syncwarp();
-            const Place x = next;
-            next = look_up();
-            load(stage, x);                                   // steps past the piece load nothing
-            if (++stage == S) {
-                stage = 0;
-                phase ^= 1;
-            }
-        }
 
-        // ---- the tile's state -------------------------------------------------
-        const bool direct = count == at.n && !p.joined;
-        const int64_t slot = (int64_t)piece + tile;
+            // ---- the tile's state -------------------------------------------------
+            const bool direct = count == at.n && !p.joined;
+            const int64_t slot = (int64_t)piece + tile;
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-            float sum = l[i];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int tr = i * 8 + qr;
-            if (row0 + tr >= R) continue;
-            // (a NaN among the scores reaches the output)
-            const bool empty = sum == 0.f;
-            const float inv = empty ? 0.f : 1.f / sum;
-            const float lse2 = empty ? -INFINITY : m[i] + log2f(sum);
-            if (direct) {
-                const RowPlace x = row_place(p, b, h, row0 + tr);
-                uint16_t *dst = p.o + x.b * p.o_s[0] + x.hq * p.o_s[1] + x.t * p.o_s[2] + 2 * qc;
+            for (int i = 0; i < 2 * MT; ++i) {
+                float sum = l[i];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int tr = i * 8 + qr;
+                if (row0 + tr >= R) continue;
+                // (a NaN among the scores reaches the output)
+                const bool empty = sum == 0.f;
+                const float inv = empty ? 0.f : 1.f / sum;
+                const float lse2 = empty ? -INFINITY : m[i] + log2f(sum);
+                if (direct) {
+                    const RowPlace x = row_place(p, b, h, row0 + tr);
+                    uint16_t *dst = p.o + x.b * p.o_s[0] + x.hq * p.o_s[1] + x.t * p.o_s[2] + 2 * qc;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (8 * n < p.c.D)
-                        *reinterpret_cast<uint32_t *>(dst + 8 * n) =
-                            empty ? 0u : ptx::pack16x2<kF16>(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
-                if (p.lse && qc == 0) p.lse[((int64_t)x.b * p.Hq + x.hq) * p.T + x.t] = lse2 * kLn2;
-            } else {
-                // columns 8n + 2 qc and the next: half of four columns
-                float2 *dst = reinterpret_cast<float2 *>(p.part.o) +
-                              ((slot * (p.c.D / 4) + qc / 2) * p.part.slot_rows + tr) * 2 + (qc & 1);
+                    for (int n = 0; n < NT; ++n)
+                        if (8 * n < p.c.D)
+                            *reinterpret_cast<uint32_t *>(dst + 8 * n) =
+                                empty ? 0u : ptx::pack16x2<kF16>(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
+                    if (p.lse && qc == 0) p.lse[((int64_t)x.b * p.Hq + x.hq) * p.T + x.t] = lse2 * kLn2;
+                } else {
+                    // columns 8n + 2 qc and the next: half of four columns
+                    float2 *dst = reinterpret_cast<float2 *>(p.part.o) +
+                                  ((slot * (p.c.D / 4) + qc / 2) * p.part.slot_rows + tr) * 2 + (qc & 1);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (8 * n < p.c.D)
-                        dst[n * 4 * p.part.slot_rows] =
-                            empty ? make_float2(0.f, 0.f)
-                                  : make_float2(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
-                if (qc == 0) p.part.lse[slot * p.part.slot_rows + tr] = lse2;
+                    for (int n = 0; n < NT; ++n)
+                        if (8 * n < p.c.D)
+                            dst[n * 4 * p.part.slot_rows] =
+                                empty ? make_float2(0.f, 0.f)
+                                      : make_float2(o[i / 2][n][2 * (i & 1)] * inv, o[i / 2][n][2 * (i & 1) + 1] * inv);
+                    if (qc == 0) p.part.lse[slot * p.part.slot_rows + tr] = lse2;
+                }
             }
         }
         __syncwarp();
@@ -432,24 +607,24 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (p.second) ptx::wait_for_primary();
 }
 
-template <int DP, int MT, bool kF16, bool kTma>
+template <int DP, int RM, bool kF16, bool kTma>
 cudaError_t launch_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
     static SharedMemory allowed;
-    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, MT, kF16, kTma>, RowsLayout<DP, MT>::kSmemBytes);
+    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, RM, kF16, kTma>, RowsLayout<DP, RM>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_rows_kernel<DP, MT, kF16, kTma>, dim3((unsigned)ctas), kThreads,
-                         RowsLayout<DP, MT>::kSmemBytes, stream, tk, tv, p);
+    return launch_behind(paged_rows_kernel<DP, RM, kF16, kTma>, dim3((unsigned)ctas), kThreads,
+                         RowsLayout<DP, RM>::kSmemBytes, stream, tk, tv, p);
 }
 
-template <int DP, int MT>
+template <int DP, int RM>
 cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
     if (p.box_rows)
-        return p.f16 ? launch_rows<DP, MT, true, true>(p, tk, tv, ctas, stream)
-                     : launch_rows<DP, MT, false, true>(p, tk, tv, ctas, stream);
-    return p.f16 ? launch_rows<DP, MT, true, false>(p, tk, tv, ctas, stream)
-                 : launch_rows<DP, MT, false, false>(p, tk, tv, ctas, stream);
+        return p.f16 ? launch_rows<DP, RM, true, true>(p, tk, tv, ctas, stream)
+                     : launch_rows<DP, RM, false, true>(p, tk, tv, ctas, stream);
+    return p.f16 ? launch_rows<DP, RM, true, false>(p, tk, tv, ctas, stream)
+                 : launch_rows<DP, RM, false, false>(p, tk, tv, ctas, stream);
 }
 
 // ---------------------------------------------------------------- merge
@@ -605,25 +780,31 @@ cudaError_t launch_merge_z(const MergeParams &p, int z, cudaStream_t stream)
 
 }  // namespace
 
-// 16 rows where they hold the tile or where D = 256 leaves no registers for
-// more, else 32.
-int paged_rows_per_tile(int D, int64_t rows) { return rows <= 16 || D > 128 ? 16 : 32; }
+// 8 or 16 rows where they hold the tile, 16 where D = 256 leaves no registers
+// for more, else 32.
+int paged_rows_per_tile(int D, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
 
-int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 1>::kChunk : RowsLayout<128, 1>::kChunk; }
+int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 16>::kChunk : RowsLayout<128, 16>::kChunk; }
 
 int paged_rows_ctas_per_sm(int D, int rows)
 {
-    return D > 128 ? RowsLayout<256, 1>::kCtas : rows == 16 ? RowsLayout<128, 1>::kCtas : RowsLayout<128, 2>::kCtas;
+    if (D > 128) return rows == 8 ? RowsLayout<256, 8>::kCtas : RowsLayout<256, 16>::kCtas;
+    return rows == 32 ? RowsLayout<128, 32>::kCtas : RowsLayout<128, 16>::kCtas;
 }
 
 cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                               cudaStream_t stream)
 {
-    if (p.c.D > 128) return launch_rows_f<256, 1>(p, tk, tv, ctas, stream);
+    if (p.c.D > 128)
+        return p.part.rows == 8 ? launch_rows_f<256, 8>(p, tk, tv, ctas, stream)
+                                : launch_rows_f<256, 16>(p, tk, tv, ctas, stream);
     if (p.c.D > 64)
-        return p.part.rows == 16 ? launch_rows_f<128, 1>(p, tk, tv, ctas, stream)
-                                 : launch_rows_f<128, 2>(p, tk, tv, ctas, stream);
-    return p.part.rows == 16 ? launch_rows_f<64, 1>(p, tk, tv, ctas, stream) : launch_rows_f<64, 2>(p, tk, tv, ctas, stream);
+        return p.part.rows == 8    ? launch_rows_f<128, 8>(p, tk, tv, ctas, stream)
+               : p.part.rows == 16 ? launch_rows_f<128, 16>(p, tk, tv, ctas, stream)
+                                   : launch_rows_f<128, 32>(p, tk, tv, ctas, stream);
+    return p.part.rows == 8    ? launch_rows_f<64, 8>(p, tk, tv, ctas, stream)
+           : p.part.rows == 16 ? launch_rows_f<64, 16>(p, tk, tv, ctas, stream)
+                               : launch_rows_f<64, 32>(p, tk, tv, ctas, stream);
 }
 
 cudaError_t read_and_clear_status_paged_rows(uint32_t *out)

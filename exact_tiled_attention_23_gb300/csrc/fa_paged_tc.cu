@@ -136,18 +136,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const Line<BN> line(p);
-    Walk walk;
-    int g0, per;
-    if (!p.second) ptx::wait_for_primary();
-    ptx::launch_dependents();
-    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, g0, walk.left, per);
-    if (walk.left == 0) {
-        if (p.second) ptx::wait_for_primary();
-        return;
-    }
-    const int blocks = walk.left;
-
+    // Set-up that reads no memory overlaps the end of the kernel before.
     if (threadIdx.x == 0) {
         for (int i = 0; i < Lay::kBars; ++i) {
             uint32_t count = 1;
@@ -161,6 +150,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         ptx::tma_prefetch_desc(&tm_k);
         ptx::tma_prefetch_desc(&tm_v);
     }
+    if (!p.second) ptx::wait_for_primary();
+    ptx::launch_dependents();
+    const Line<BN> line(p);
+    Walk walk;
+    int g0, per;
+    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, g0, walk.left, per);
+    if (walk.left == 0) {
+        if (p.second) ptx::wait_for_primary();
+        return;
+    }
+    const int blocks = walk.left;
     if (warp == 1) {
         ptx::tmem_alloc(tmem_slot, kTmemCols);
         ptx::tmem_relinquish();

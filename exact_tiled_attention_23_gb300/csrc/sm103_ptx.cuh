@@ -417,6 +417,14 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t saddr
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
 }
 
+// An 8x8 tile of 16-bit values, a row's pairs in the lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t w)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+    return r;
+}
+
 // d += a b over a 16x8x16 tile, one warp, fp32 accumulators.
 template <bool kF16>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
