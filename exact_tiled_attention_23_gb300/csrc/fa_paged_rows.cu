@@ -637,7 +637,7 @@ cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUt
 constexpr int kMergeThreads = 256;
 
 template <int kCols, int kZ, bool kF16>
-__global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const MergeParams p, const int groups)
+__global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 6 : 4) paged_merge_kernel(const MergeParams p, const int groups)
 {
     constexpr int kRows = kMergeThreads / (kCols * kZ);
     const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kCols, z = threadIdx.x / (kRows * kCols);
@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
 
     // A batch of states at a time, their LSEs and outputs loaded together; the
     // sums follow the largest LSE so far.
-    constexpr int kBatch = 4;
+    // (kZ = 1 is for many rows of few states: more CTAs an SM, smaller batches)
+    constexpr int kBatch = kZ == 1 ? 2 : 4;
     const int c = blockIdx.z * kCols + col4;
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

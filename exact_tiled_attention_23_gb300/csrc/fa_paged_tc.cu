@@ -84,6 +84,21 @@ struct TcLayout {
     static_assert(kBars * 8 + 16 <= 512, "barrier area");
 };
 
+// wait_bounded with everything past its first test out of line.  The loops below
+// are bound by the fetch of their instructions; with the tests of the clock at
+// every wait inside them, pieces of a prompt ran 6 % slower.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort ab,
+                                       bool follow_abort)
+{
+    return wait_bounded(bar, parity, limit_ns, site, ab, follow_abort);
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort ab,
+                                         bool follow_abort = true)
+{
+    return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, ab, follow_abort);
+}
+
 // A role's way along the CTA's piece of the line, tile by tile: what a block
 // needs beyond its number is found once per tile, because the issuing threads
 // run alone and every instruction between two products counts (a walk that
@@ -194,7 +209,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int h = walk.u.h;
             if (t + 1 < blocks) line.advance(walk.u);
             bool ok = true;
-            if (t >= ring && lane == 0) ok = wait_bounded(&empty[slot], phase, limit, kSiteSlotEmpty, ab);
+            if (t >= ring && lane == 0) ok = wait_for(&empty[slot], phase, limit, kSiteSlotEmpty, ab);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) ptx::mbar_arrive_expect_tx(&full[slot], kTileBytes);
@@ -216,7 +231,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // Drain: no copy may still be landing in shared memory at exit.
         if (lane == 0)
             for (int t = issued > ring ? issued - ring : 0; t < issued; ++t)
-                wait_bounded(&full[t % ring], (t / ring) & 1, limit, kSiteDrain, ab, false);
+                wait_for(&full[t % ring], (t / ring) & 1, limit, kSiteDrain, ab, false);
         __syncwarp();
     } else if (warp == 3) {
         // ================= S products =================
@@ -231,11 +246,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             bool ok = true;
             for (int tile = 0;; ++tile) {
                 const int count = walk.count(), end = t + count;
-                ok = wait_bounded(q_full, tile & 1, limit, kSiteQFull, ab);
+                ok = wait_for(q_full, tile & 1, limit, kSiteQFull, ab);
 #pragma unroll 1
                 for (; ok && t < end; ++t) {
-                    ok = wait_bounded(&k_full[t % RK], (t / RK) & 1, limit, kSiteSlotFull, ab);
-                    if (ok && t > 0) ok = wait_bounded(s_read, (t - 1) & 1, limit, kSiteSFull, ab);
+                    ok = wait_for(&k_full[t % RK], (t / RK) & 1, limit, kSiteSlotFull, ab);
+                    if (ok && t > 0) ok = wait_for(s_read, (t - 1) & 1, limit, kSiteSFull, ab);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint64_t kd = k_desc + (uint64_t)(t % RK) * kTileStep;
@@ -251,7 +266,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 if (!walk.next_tile(line, count)) break;
             }
             ptx::mma_commit(mma_drain_s);
-            wait_bounded(mma_drain_s, 0, limit, kSiteDrain, ab, false);
+            wait_for(mma_drain_s, 0, limit, kSiteDrain, ab, false);
         }
     } else if (warp == 1) {
         // ================= PV products =================
@@ -264,10 +279,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         constexpr uint64_t kTileStep = kTileBytes >> 4;
         auto issue = [&](int t, bool first, bool v_ready) -> bool {
             const int buf = t & 1;
-            if (!v_ready && !wait_bounded(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab)) return false;
+            if (!v_ready && !wait_for(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab)) return false;
             const uint64_t vd = v_desc + (uint64_t)(t % RV) * kTileStep;
             for (int h = 0; h < 2; ++h) {
-                if (!wait_bounded(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab)) return false;
+                if (!wait_for(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab)) return false;
                 ptx::tc_fence_after();
                 const uint32_t to = tmem + Lay::col_o(h), tp = tmem + Lay::col_p(buf, h);
 #pragma unroll
@@ -288,11 +303,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             const int to = rest ? (from | (p.box_rows - 1)) + 1 : from;
             bool ok = true;
             if (lane == 0) {
-                if (tile > 0) ok = wait_bounded(o_read, (tile - 1) & 1, limit, kSiteOFinal, ab);
+                if (tile > 0) ok = wait_for(o_read, (tile - 1) & 1, limit, kSiteOFinal, ab);
                 const int t0 = t;
 #pragma unroll 1
                 for (; ok && t < end - (rest ? 1 : 0); ++t) ok = issue(t, t == t0, false);
-                if (rest) ok = ok && wait_bounded(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab);
+                if (rest) ok = ok && wait_for(&v_full[t % RV], (t / RV) & 1, limit, kSiteSlotFull, ab);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
@@ -315,7 +330,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         if (lane == 0) {
             ptx::mma_commit(mma_drain);
-            wait_bounded(mma_drain, 0, limit, kSiteDrain, ab, false);
+            wait_for(mma_drain, 0, limit, kSiteDrain, ab, false);
         }
         __syncwarp();
     } else {
@@ -394,7 +409,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 const int buf = t & 1;
                 const uint32_t tP = tmem + lane_off + Lay::col_p(buf, h);
                 const uint32_t tO = tmem + lane_off + Lay::col_o(h);
-                const bool got = wait_bounded(s_full, t & 1, limit, kSiteSFull, ab);
+                const bool got = wait_for(s_full, t & 1, limit, kSiteSFull, ab);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
@@ -439,18 +454,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 bool hook_ok = true;
                 auto before_o = [&] {
                     if (j > 0) {
-                        hook_ok = wait_bounded(&pv_done[h * 2 + ((t - 1) & 1)], ((t - 1) >> 1) & 1, limit, kSiteOFinal, ab) &&
+                        hook_ok = wait_for(&pv_done[h * 2 + ((t - 1) & 1)], ((t - 1) >> 1) & 1, limit, kSiteOFinal, ab) &&
                                   hook_ok;
                         ptx::tc_fence_after();
                     }
                 };
                 auto before_p = [&] {
                     if (!__all_sync(0xffffffffu, p_free)) {
-                        hook_ok = wait_bounded(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1, limit, kSiteOFinal, ab) && hook_ok;
+                        hook_ok = wait_for(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1, limit, kSiteOFinal, ab) && hook_ok;
                         ptx::tc_fence_after();
                     }
                 };
-                st.template block<1>(s_raw, sl2, j > 0, tP, tO, before_o, before_p);
+                // OnlineRow::block as a loop of at most two turns: one copy of its code
+                float sum, sum_o;
+                bool raise = __any_sync(0xffffffffu, st.m_ref == -INFINITY);
+#pragma unroll 1
+                for (int turn = 0; turn < 2; ++turn) {
+                    if (raise) st.raise(s_raw, sl2, j > 0, tO, before_o);
+                    st.template exp_pass<1>(s_raw, sl2, tP, sum, sum_o, before_p);
+                    raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kLazyLimitF16 : kLazyLimit)));
+                    ptx::tmem_wait_st();      // the first turn's P stores land before new ones
+                    if (!raise) break;
+                }
+                st.l += sum;
+                st.l_o += sum_o;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&p_full[h * 2 + buf]);
@@ -469,7 +496,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // ---- join the halves: m = max(m_A, m_B), w_h = 2^(m_h - m),
             // O = (w_A O_A + w_B O_B) / (w_A l_oA + w_B l_oB)
             bool have = ok;
-            if (have) have = wait_bounded(o_final, tile & 1, limit, kSiteOFinal, ab);
+            if (have) have = wait_for(o_final, tile & 1, limit, kSiteOFinal, ab);
             // all eight warps agree, so that the named barriers are reached by
             // all of them or by none; the last tile's exchange is read, too
             have = ptx::bar_and(1, 256, have);
