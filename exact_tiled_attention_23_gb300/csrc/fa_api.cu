@@ -30,6 +30,13 @@ EncodeTiledFn encode_fn()
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<EncodeTiledFn>(ptr);
     });
+    // The encoder needs a current context, which a thread that has made no
+    // runtime call yet does not have.
+    static thread_local bool bound = false;
+    if (!bound) {
+        int dev = 0;
+        bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    }
     return fn;
 }
 

@@ -71,6 +71,7 @@ struct TileSlots {
 // (Along the line, k and i never fall and one of them grows from share to
 // share, so no two shares have one slot.)
 struct Partials {
+    int slots;
     float *o;              // [slots][D / 4][slot_rows][4]
     float *lse;            // [slots][slot_rows]
     TileSlots *tile;       // [tiles in all], of tiles with at least one chunk

@@ -28,6 +28,10 @@ bool rows_ok(const fa_rows *r, int B, int H, int T, int D, bool output)
     return (B <= 1 || r->stride_b >= D) && (H <= 1 || r->stride_h >= D) && (T <= 1 || r->stride_n >= D);
 }
 
+// Most keys of a sequence: places in it, up to the end of a block past the last
+// key, are 32-bit numbers.
+constexpr int64_t kMostKeys = INT32_MAX - 4095;
+
 fa_status check_cache(const fa_paged_kv *c, int B)
 {
     if (!c) return FA_ERR_INVALID_ARG;
@@ -41,8 +45,7 @@ fa_status check_cache(const fa_paged_kv *c, int B)
     if (!c->seq_len || !aligned(c->seq_len, 4)) return FA_ERR_INVALID_ARG;
     if (c->table_width > 0 && (!c->table || !aligned(c->table, 4))) return FA_ERR_INVALID_ARG;
     if (B > 1 && c->table_stride < c->table_width) return FA_ERR_INVALID_ARG;
-    // positions inside a sequence are 32-bit numbers
-    if ((int64_t)c->table_width * c->page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if ((int64_t)c->table_width * c->page_size > kMostKeys) return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
@@ -132,6 +135,11 @@ struct Plan {
         pieces = ctas * each;
         part.slot_rows = (int)std::min<int64_t>(part.rows, tiles == 1 ? (tc ? 128 : rows) : part.rows);
         const size_t slots = (size_t)(pieces + items);
+        if (slots > INT32_MAX) {
+            ok = false;
+            return;
+        }
+        part.slots = (int)slots;
         bytes = round_up((size_t)items * sizeof(fa::TileSlots)) + round_up(slots * part.slot_rows * 4) + round_up(slots * part.slot_rows * D * 4);
     }
 
@@ -193,7 +201,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     if (LSE && !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
     if (prefix_len > 0 && (!prefix_table || !aligned(prefix_table, 4))) return FA_ERR_INVALID_ARG;
     const int64_t own_keys = (int64_t)c->table_width * c->page_size;
-    if (own_keys + prefix_len > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (own_keys + prefix_len > kMostKeys) return FA_ERR_INVALID_ARG;
     const int G = Hq / c->Hkv;
     Plan own(B, *c, (int64_t)G * T, own_keys, false);
     Plan front(1, *c, (int64_t)G * T * B, prefix_len, true);
@@ -346,7 +354,7 @@ size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix
     if (check_sizes(cache, B, Hq, T) != FA_OK || prefix_len < 0 || (int64_t)B * Hq * T == 0) return 0;
     const int G = Hq / cache->Hkv;
     const Plan own(B, *cache, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, false);
-    if (!own.ok) return 0;
+    if (!own.ok || (int64_t)cache->table_width * cache->page_size + prefix_len > kMostKeys) return 0;
     if (prefix_len == 0) return own.bytes;
     const Plan front(1, *cache, (int64_t)G * T * B, prefix_len, true);
     return front.ok ? own.bytes + front.bytes : 0;

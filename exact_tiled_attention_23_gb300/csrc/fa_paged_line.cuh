@@ -130,8 +130,9 @@ struct Line {
         const int in = __ffs(__ballot_sync(0xffffffffu, start < (unsigned)(scan * p.c.Hkv))) - 1;
         int before = __shfl_sync(0xffffffffu, scan - sum, in), g0 = in * strip;
         if (strip > 1) {
+            const int end = min((in + 1) * strip, groups);
             for (;; g0 += 32) {
-                const int n = g0 + lane < min((in + 1) * strip, groups) ? chunks_of_group(g0 + lane) : 0;
+                const int n = g0 + lane < end ? chunks_of_group(g0 + lane) : 0;
                 int here = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
@@ -139,6 +140,11 @@ struct Line {
                     if (lane >= d) here += v;
                 }
                 const unsigned hit = __ballot_sync(0xffffffffu, start < (unsigned)((before + here) * p.c.Hkv));
+                // (a second read of lengths that are being changed may find none)
+                if (g0 + 32 >= end && !hit) {
+                    count = 0;
+                    return;
+                }
                 if (hit) {
                     const int at_lane = __ffs(hit) - 1;
                     before += __shfl_sync(0xffffffffu, here - n, at_lane);
@@ -149,9 +155,13 @@ struct Line {
             }
         }
         enter(at, g0);
+        if (at.n == 0) {
+            count = 0;
+            return;
+        }
         const int left = first - before * p.c.Hkv;
-        at.h = left / at.n;
-        at.c = left - at.h * at.n;
+        at.h = min(left / at.n, p.c.Hkv - 1);
+        at.c = min(left - at.h * at.n, at.n - 1);
     }
 
     // The piece that has the first chunk of a tile says where its states will be.

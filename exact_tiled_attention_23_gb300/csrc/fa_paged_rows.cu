@@ -201,14 +201,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t q_smem = s_base + Lay::kQOff + warp * Lay::kQBytes;
     int stage = 0, done = 0;
     uint32_t phase = 0;
-    // Waits for a step's keys; returns which of them are visible.  (A wait that
-    // gave up leaves the results undefined; its copies are waited for at the end.)
+    // Waits for a step's keys; returns which of them are visible.  After a wait
+    // that gave up (the results are undefined then) the warp computes nothing
+    // and, above all, copies nothing more: its stages still have copies in
+    // flight, and an arrival on a barrier whose phase they hold open is invalid.
+    bool gave_up = false;
     auto landed = [&]() -> uint32_t {
-        if constexpr (kTma)
-            wait_bounded(&full[stage], phase, p.wait_limit_ns, kSiteSlotFull, ab);
-        else
+        if constexpr (kTma) {
+            if (!gave_up)
+                gave_up = !__all_sync(0xffffffffu, wait_bounded(&full[stage], phase, p.wait_limit_ns, kSiteSlotFull, ab));
+            if (gave_up) return 0u;
+        } else {
             ptx::cp_async_wait<S - 1>();
-        __syncwarp();
+            __syncwarp();
+        }
         return s_mask[stage];
     };
     // A box brings what its page holds behind the last key.
@@ -223,6 +229,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // The step is done: its stage takes the next one (past the piece, nothing).
     auto refill = [&] {
         __syncwarp();
+        if (gave_up) return;
         const Place x = next;
         next = look_up();
         load(stage, x);
@@ -598,6 +605,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         done += count;
     }
     if constexpr (kTma) {
+        // Drain: no copy may still be landing in shared memory at exit.
         for (int i = max(0, issued - S); i < issued; ++i)
             wait_bounded(&full[i % S], (i / S) & 1, p.wait_limit_ns, kSiteDrain, ab, false);
     } else {
@@ -668,7 +676,12 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 6 : 4) paged_merge_ke
 
     TileSlots x[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) x[s] = keys[s] > 0 ? p.src[s].tile[tile[s]] : TileSlots{0, 0};
+    for (int s = 0; s < 2; ++s) {
+        x[s] = keys[s] > 0 ? p.src[s].tile[tile[s]] : TileSlots{0, 0};
+        // no read past the workspace, whatever a kernel that gave up has left
+        x[s].first = min(max(x[s].first, 0), p.src[s].slots);
+        x[s].count = min(x[s].count, p.src[s].slots - x[s].first);
+    }
     // not a row, or one CTA had the whole tile and wrote the row itself
     const bool skip = !real || (!p.joined && x[0].count == 1);
     if constexpr (kZ == 1)

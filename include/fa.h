@@ -349,7 +349,7 @@ typedef struct fa_paged_kv {
     int Hkv, D;                  /* key heads; head dimension: a multiple of 8 up to 128, or 256 */
     const int32_t *table;        /* [B, table_width] page numbers, rows table_stride entries apart */
     int64_t table_stride;
-    int table_width;             /* table_width * page_size < 2^31 */
+    int table_width;             /* table_width * page_size <= 2^31 - 4096 (with a prefix: the sum) */
     const int32_t *seq_len;      /* [B] keys per sequence, the call's own tokens included */
 } fa_paged_kv;
 
