@@ -674,13 +674,15 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 6 : 4) paged_merge_ke
     }
     ptx::wait_for_primary();
 
+    // (read before it is known whether the tile has any keys: one wait less)
     TileSlots x[2];
 #pragma unroll
+    for (int s = 0; s < 2; ++s) x[s] = s < p.n_src ? p.src[s].tile[tile[s]] : TileSlots{0, 0};
+#pragma unroll
     for (int s = 0; s < 2; ++s) {
-        x[s] = keys[s] > 0 ? p.src[s].tile[tile[s]] : TileSlots{0, 0};
         // no read past the workspace, whatever a kernel that gave up has left
         x[s].first = min(max(x[s].first, 0), p.src[s].slots);
-        x[s].count = min(x[s].count, p.src[s].slots - x[s].first);
+        x[s].count = keys[s] > 0 ? min(x[s].count, p.src[s].slots - x[s].first) : 0;
     }
     // not a row, or one CTA had the whole tile and wrote the row itself
     const bool skip = !real || (!p.joined && x[0].count == 1);
