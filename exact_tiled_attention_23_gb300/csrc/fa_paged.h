@@ -125,6 +125,9 @@ struct PagedParams {
     int joined;                        // 1: every tile leaves its state in a slot for the merge
     Partials part;
     Beside beside;
+    int team;                          // CTAs that share a tile (teams only: 1, 2, 4 or 8)
+    const int32_t *prefix_table;       // teams only: keys before the own ones
+    int prefix_len;
     int box_rows;                      // key rows per copied box (row kernel: 0 = 16-byte copies)
     uint64_t wait_limit_ns;
 };
@@ -150,6 +153,7 @@ constexpr int kBlockKeys = 128;
 int paged_rows_per_tile(int D, int64_t rows);
 int paged_rows_chunk(int D);
 constexpr int kRowsWarps = 2;
+constexpr int kTeamWarps = 8;             // of a CTA that works in a team
 int paged_rows_ctas_per_sm(int D, int rows);
 
 // The current device's number, and its multiprocessors (148 if unknown).
@@ -178,24 +182,36 @@ class SharedMemory {
 // it on the stream; the kernel itself waits for that one's end (and its
 // writes) before it touches memory that one may write.
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+cudaError_t launch_clusters(void (*kernel)(P...), int cluster, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                            A... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+{
+    return launch_clusters(kernel, 1, grid, threads, smem, stream, args...);
 }
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 // (tk, tv are read only where p.box_rows > 0)
 cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
+                              cudaStream_t stream);
+cudaError_t launch_paged_team(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                               cudaStream_t stream);
 cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                             cudaStream_t stream);

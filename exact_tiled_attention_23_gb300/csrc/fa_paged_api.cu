@@ -156,6 +156,24 @@ struct Plan {
     }
 };
 
+// CTAs of a team per tile, 0 where teams do not pay.  A team's tile has up to 8
+// rows, so that its states fit the stages.  Every warp has at most four chunks
+// of the longest sequence that the table allows, two if there are CTAs for that,
+// and all teams are on the GPU at once.
+int team_size(const fa_paged_kv &c, const Plan &own, int prefix_len, int64_t own_keys, int sms)
+{
+    if (c.D > 128 || own.part.rows != 8 || own.part.tiles != 1) return 0;
+    const int chunk = fa::paged_rows_chunk(c.D);
+    const int64_t chunks = (prefix_len + (int64_t)chunk - 1) / chunk + (own_keys + chunk - 1) / chunk;
+    int team = 0;
+    for (int t = 1; t <= 8 && own.items * t <= sms; t *= 2) {
+        const int64_t each = (chunks + t * fa::kTeamWarps - 1) / (t * fa::kTeamWarps);
+        if (each <= 4) team = t;
+        if (each <= 1) break;
+    }
+    return team;
+}
+
 // One part's kernel.
 bool launch_part(fa::PagedParams p, const fa_paged_kv &c, const Plan &plan, cudaStream_t stream)
 {
@@ -163,7 +181,9 @@ bool launch_part(fa::PagedParams p, const fa_paged_kv &c, const Plan &plan, cuda
     CUtensorMap tk{}, tv{};
     p.box_rows = plan.box;
     p.wait_limit_ns = fa::wait_budget_ns();
-    if (!plan.box) return fa::launch_paged_rows(p, tk, tv, (int)plan.ctas, stream) == cudaSuccess;
+    if (!plan.box)
+        return (p.team ? fa::launch_paged_team(p, tk, tv, (int)plan.items * p.team, stream)
+                       : fa::launch_paged_rows(p, tk, tv, (int)plan.ctas, stream)) == cudaSuccess;
     // [D, slot, head, page]; the stride of a dimension of one entry is not followed
     const uint64_t row = (uint64_t)c.D * 2;
     const uint64_t dims[4] = {(uint64_t)c.D, (uint64_t)c.page_size, (uint64_t)c.Hkv, (uint64_t)c.num_pages};
@@ -173,6 +193,7 @@ bool launch_part(fa::PagedParams p, const fa_paged_kv &c, const Plan &plan, cuda
     if (!fa::encode_tiled16(&tk, c.k, 4, dims, strides, box, p.f16 != 0) ||
         !fa::encode_tiled16(&tv, c.v, 4, dims, strides, box, p.f16 != 0))
         return false;
+    if (p.team) return fa::launch_paged_team(p, tk, tv, (int)plan.items * p.team, stream) == cudaSuccess;
     return (plan.tc ? fa::launch_paged_tc(p, tk, tv, (int)plan.ctas, stream)
                     : fa::launch_paged_rows(p, tk, tv, (int)plan.ctas, stream)) == cudaSuccess;
 }
@@ -231,6 +252,12 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     p.joined = prefix_len > 0;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    p.team = team_size(*c, own, prefix_len, own_keys, fa::sm_count_of(fa::current_device()));
+    if (p.team) {
+        p.prefix_table = prefix_table;
+        p.prefix_len = prefix_len;
+        return launch_part(p, *c, own, cs) ? FA_OK : FA_ERR_CUDA;
+    }
     fa::MergeParams m{};
     m.src[m.n_src++] = own.part;
     if (prefix_len > 0) {

@@ -42,12 +42,13 @@ __device__ uint32_t g_status_paged_rows;
 
 namespace {
 
-constexpr int kWarps = kRowsWarps;
-constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int DP, int RM>
+// kTeam: all warps of a cluster work on one tile and join it in shared memory
+// (below); else every warp has a piece of the line.
+template <int DP, int RM, bool kTeam>
 struct RowsLayout {
+    static constexpr int kWarps = kTeam ? kTeamWarps : kRowsWarps;
     // Up to 8 rows are the products' columns (keys and columns of V their rows:
     // half the products, weights and registers of 16 rows), more are their rows.
     static constexpr bool kColumns = RM == 8;
@@ -60,16 +61,18 @@ struct RowsLayout {
     static constexpr bool kQRegs = kColumns || (RM == 16 && DP <= 128);
     static constexpr int kQBytes = kQRegs ? 0 : RM * DP * 2;
     // CTAs per SM: what registers and shared memory hold
-    static constexpr int kCtas = DP == 256 ? (RM == 8 ? 3 : 2) : RM == 32 ? 4 : 6;
+    static constexpr int kCtas = kTeam ? 1 : DP == 256 ? (RM == 8 ? 3 : 2) : RM == 32 ? 4 : 6;
     static constexpr int kStages = 2;
     static constexpr int kRingOff = 0;
     static constexpr int kQOff = kWarps * kStages * kStageBytes;
     static constexpr int kMaskOff = kQOff + kWarps * kQBytes;     // visible keys of every stage
     static constexpr int kBarOff = kMaskOff + kWarps * kStages * 4;
     static constexpr int kAbortOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kSmemBytes = kAbortOff + kWarps * 4 + 1024;   // + alignment slack
+    static constexpr int kStatOff = kAbortOff + kWarps * 4;       // team: (m, l) of every warp's rows
+    static constexpr int kSmemBytes = kStatOff + (kTeam ? kWarps * RM * 8 : 0) + 1024;   // + alignment slack
     static_assert(RM == 8 || RM == 16 || (RM == 32 && DP <= 128), "rows");
-    static_assert(kBarOff % 8 == 0, "barriers");
+    static_assert(kBarOff % 8 == 0 && kStatOff % 8 == 0, "barriers, states");
+    static_assert(!kTeam || (RM == 8 && DP <= 128 && RM * DP * 4 <= kStageBytes), "a team's states fit its stages");
     static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
 
@@ -83,11 +86,83 @@ __device__ __forceinline__ uint32_t unit_at(int row, int unit)
     return (uint32_t)((unit >> 3) * (kTall * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
 }
 
-template <int DP, int RM, bool kF16, bool kTma>
-__global__ void __launch_bounds__(kThreads, (RowsLayout<DP, RM>::kCtas))
+// The join of a team's tile: `ring` and `stat` are the shared addresses, alike in
+// every CTA of the cluster, of the warps' outputs (`pitch` apart) and of their
+// (m, l).  CTA r takes every p.team-th group of four columns of a row; p.team
+// neighbouring threads take the states of one CTA each and exchange sums.
+template <int DP, bool kF16>
+__device__ __forceinline__ void join_team(const PagedParams &p, uint32_t ring, int pitch, uint32_t stat, int b, int h, int len)
+{
+    constexpr int RM = 8;
+    __syncwarp();
+    ptx::cluster_sync();
+    const int rank = (int)blockIdx.x % p.team, z = (int)threadIdx.x % p.team, first = (int)threadIdx.x / p.team;
+    const int units = p.c.D / 4 * RM / p.team, R = p.G * p.T;
+    const uint32_t its_ring = ptx::cluster_address(ring, z), its_stat = ptx::cluster_address(stat, z);
+#pragma unroll 1
+    for (int u0 = 0; u0 < units; u0 += 32 * kTeamWarps / p.team) {
+        const int unit = (u0 + first) * p.team + rank, row = unit % RM, c4 = unit / RM;
+        const bool mine = u0 + first < units && row < R;
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine) {
+            float2 st[kTeamWarps];
+            float4 v[kTeamWarps];
+#pragma unroll
+            for (int w = 0; w < kTeamWarps; ++w) {
+                st[w] = ptx::ld_cluster2(its_stat + (uint32_t)(w * RM + row) * 8u);
+                v[w] = ptx::ld_cluster4(its_ring + (uint32_t)(w * pitch) + (uint32_t)(c4 * RM + row) * 16u);
+            }
+#pragma unroll
+            for (int w = 0; w < kTeamWarps; ++w) top = fmaxf(top, st[w].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int w = 0; w < kTeamWarps; ++w) {
+                const float f = ptx::ex2_approx(st[w].x - ref);
+                sum = fmaf(f, st[w].y, sum);
+                acc.x = fmaf(f, v[w].x, acc.x);
+                acc.y = fmaf(f, v[w].y, acc.y);
+                acc.z = fmaf(f, v[w].z, acc.z);
+                acc.w = fmaf(f, v[w].w, acc.w);
+            }
+        }
+#pragma unroll 1
+        for (int d = 1; d < p.team; d <<= 1) {
+            const float top2 = __shfl_xor_sync(0xffffffffu, top, d), next = fmaxf(top, top2);
+            const float ref = next == -INFINITY ? 0.f : next;
+            const float f = ptx::ex2_approx(top - ref), f2 = ptx::ex2_approx(top2 - ref);
+            const auto both = [&](float x) { return fmaf(f, x, f2 * __shfl_xor_sync(0xffffffffu, x, d)); };
+            sum = both(sum);
+            acc = make_float4(both(acc.x), both(acc.y), both(acc.z), both(acc.w));
+            top = next;
+        }
+        if (!mine || z != 0) continue;
+        const int t = p.by_g.quotient(row), hq = h * p.G + row - t * p.G;
+        // (a row without a token sees nothing, not even a prefix)
+        const bool empty = sum == 0.f || (p.causal && len - p.T + t < 0);
+        const float inv = empty ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c4) =
+            empty ? make_uint2(0u, 0u)
+                  : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
+        if (p.lse && c4 == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    // no CTA ends while another reads its states
+    __syncwarp();
+    ptx::cluster_sync();
+}
+
+// Teams.  Where there is little work, two launches and the way through memory
+// between them are most of its time.  Then a cluster of up to eight CTAs takes a
+// tile: every warp some of its chunks, and the states are joined through the
+// cluster's shared memory.  One sequence of 1000 keys: 8.2 -> 6.3 us.  A shared
+// prefix, whose keys come first, is read by every tile: from the L2, and the
+// rows are too few for the tensor cores.
+template <int DP, int RM, bool kF16, bool kTma, bool kTeam>
+__global__ void __launch_bounds__((32 * RowsLayout<DP, RM, kTeam>::kWarps), (RowsLayout<DP, RM, kTeam>::kCtas))
 paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
 {
-    using Lay = RowsLayout<DP, RM>;
+    using Lay = RowsLayout<DP, RM, kTeam>;
+    constexpr int kWarps = Lay::kWarps;
     constexpr int S = Lay::kStages, MT = Lay::MT, KS = Lay::kChunk;
     constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : 0xffffu;
     constexpr int NT = DP / 8;                      // 8-column tiles of O
@@ -120,7 +195,21 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int piece = (int)blockIdx.x * kWarps + warp;
     LineCursor at;
     int g0, steps, per;
-    line.share(piece, (int)gridDim.x * kWarps, at, g0, steps, per);
+    int front = 0;              // team: chunks of the prefix, before the own ones
+    if constexpr (kTeam) {
+        const int tile = (int)blockIdx.x / p.team, g = tile / p.c.Hkv;
+        line.enter(at, g);
+        at.h = tile - g * p.c.Hkv;
+        front = chunks_of(p.prefix_len, KS);
+        at.n += front;
+        const int warps = p.team * kWarps, mine = ((int)blockIdx.x - tile * p.team) * kWarps + warp;
+        per = (at.n + warps - 1) / warps;
+        at.c = min(mine * per, at.n);
+        steps = min(per, at.n - at.c);
+        g0 = 0;
+    } else {
+        line.share(piece, (int)gridDim.x * kWarps, at, g0, steps, per);
+    }
     const int R = line.R;
 
     // ---- loads -----------------------------------------------------------
@@ -134,14 +223,24 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     auto look_up = [&]() -> Place {
         if (ld_left <= 0) return Place{-1, 0, -1};
         Place x{-1, 0, ld.h};
-        const int key = ld.c * KS + lane % KS;
-        if (key < ld.keys) {
+        const int key = (ld.c - front) * KS + lane % KS;
+        if (kTeam && ld.c < front) {
+            const int k = ld.c * KS + lane % KS;
+            if (k < p.prefix_len) {
+                const int which = p.c.by_page.quotient(k);
+                x.slot = k - which * p.c.page_size;
+                x.page = p.prefix_table[which];
+            }
+        } else if (key < ld.keys) {
             const int which = p.c.by_page.quotient(key);
             const int b = p.part.tiles == 1 ? ld.g : ld.g / p.part.tiles;
             x.slot = key - which * p.c.page_size;
             x.page = p.c.table[(int64_t)b * p.c.table_stride + which];
         }
-        line.advance(ld);
+        if constexpr (kTeam)
+            ++ld.c;
+        else
+            line.advance(ld);
         --ld_left;
         return x;
     };
@@ -238,13 +337,22 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             phase ^= 1;
         }
     };
+    // No copy may still be landing in shared memory at exit.
+    auto drain = [&] {
+        if constexpr (kTma) {
+            for (int i = max(0, issued - S); i < issued; ++i)
+                wait_bounded(&full[i % S], (i / S) & 1, p.wait_limit_ns, kSiteDrain, ab, false);
+        } else {
+            ptx::cp_async_wait<0>();
+        }
+    };
 #pragma unroll 1
-    while (done < steps) {
+    while (kTeam || done < steps) {
         const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the piece
         const int b = p.part.tiles == 1 ? at.g : at.g / p.part.tiles;
         const int row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
         const int tile = at.g * p.c.Hkv + h;
-        if (at.c == 0 && lane == 0) line.record(at, piece, g0, g0 + done, per);
+        if (!kTeam && at.c == 0 && lane == 0) line.record(at, piece, g0, g0 + done, per);
 
         const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
 
@@ -277,7 +385,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             for (int step = 0; step < count; ++step) {
                 const uint32_t mask = landed();
                 const uint32_t kt = ring + stage * Lay::kStageBytes, vt = kt + Lay::kTileBytes;
-                const int key0 = (at.c + step) * KS;
+                // (the prefix's keys come before every row's limit)
+                const int key0 = at.c + step < front ? INT32_MIN / 2 : (at.c + step - front) * KS;
                 if (mask) {
                     // scores of keys 16 j + qr (and + 8) and the two rows
                     float s[KS / 16][4];
@@ -354,6 +463,29 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         }
                 }
                 refill();
+            }
+
+            if constexpr (kTeam) {
+                drain();
+                __syncwarp();
+                // O over the warp's first stage: four columns of all rows after
+                // four columns of all rows
+                float *mine = reinterpret_cast<float *>(smem + Lay::kRingOff + warp * S * Lay::kStageBytes);
+                float2 *stat = reinterpret_cast<float2 *>(smem + Lay::kStatOff) + warp * RM;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float sum = l[r];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    if (qr == 0) stat[2 * qc + r] = make_float2(m[r], sum);
+#pragma unroll
+                    for (int n = 0; n < KT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            mine[((4 * n + 2 * e + qr / 4) * RM + 2 * qc + r) * 4 + qr % 4] = o[n][2 * e + r];
+                }
+                join_team<DP, kF16>(p, s_base + Lay::kRingOff, S * Lay::kStageBytes, s_base + Lay::kStatOff, b, h, at.len);
+                return;
             }
 
             // ---- the tile's state ----
@@ -604,25 +736,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         line.advance(at);
         done += count;
     }
-    if constexpr (kTma) {
-        // Drain: no copy may still be landing in shared memory at exit.
-        for (int i = max(0, issued - S); i < issued; ++i)
-            wait_bounded(&full[i % S], (i / S) & 1, p.wait_limit_ns, kSiteDrain, ab, false);
-    } else {
-        ptx::cp_async_wait<0>();
-    }
+    drain();
     // the merge starts when this kernel has ended, and needs the one before too
     if (p.second) ptx::wait_for_primary();
 }
 
-template <int DP, int RM, bool kF16, bool kTma>
+template <int DP, int RM, bool kF16, bool kTma, bool kTeam = false>
 cudaError_t launch_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
+    using Lay = RowsLayout<DP, RM, kTeam>;
     static SharedMemory allowed;
-    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, RM, kF16, kTma>, RowsLayout<DP, RM>::kSmemBytes);
+    const cudaError_t e = allowed.allow(paged_rows_kernel<DP, RM, kF16, kTma, kTeam>, Lay::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_rows_kernel<DP, RM, kF16, kTma>, dim3((unsigned)ctas), kThreads,
-                         RowsLayout<DP, RM>::kSmemBytes, stream, tk, tv, p);
+    return launch_clusters(paged_rows_kernel<DP, RM, kF16, kTma, kTeam>, kTeam ? p.team : 1, dim3((unsigned)ctas),
+                           32 * Lay::kWarps, Lay::kSmemBytes, stream, tk, tv, p);
 }
 
 template <int DP, int RM>
@@ -800,12 +927,12 @@ cudaError_t launch_merge_z(const MergeParams &p, int z, cudaStream_t stream)
 // for more, else 32.
 int paged_rows_per_tile(int D, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32; }
 
-int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 16>::kChunk : RowsLayout<128, 16>::kChunk; }
+int paged_rows_chunk(int D) { return D <= 64 ? RowsLayout<64, 16, false>::kChunk : RowsLayout<128, 16, false>::kChunk; }
 
 int paged_rows_ctas_per_sm(int D, int rows)
 {
-    if (D > 128) return rows == 8 ? RowsLayout<256, 8>::kCtas : RowsLayout<256, 16>::kCtas;
-    return rows == 32 ? RowsLayout<128, 32>::kCtas : RowsLayout<128, 16>::kCtas;
+    if (D > 128) return rows == 8 ? RowsLayout<256, 8, false>::kCtas : RowsLayout<256, 16, false>::kCtas;
+    return rows == 32 ? RowsLayout<128, 32, false>::kCtas : RowsLayout<128, 16, false>::kCtas;
 }
 
 cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
@@ -821,6 +948,21 @@ cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const
     return p.part.rows == 8    ? launch_rows_f<64, 8>(p, tk, tv, ctas, stream)
            : p.part.rows == 16 ? launch_rows_f<64, 16>(p, tk, tv, ctas, stream)
                                : launch_rows_f<64, 32>(p, tk, tv, ctas, stream);
+}
+
+template <int DP>
+cudaError_t launch_team(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
+{
+    if (p.box_rows)
+        return p.f16 ? launch_rows<DP, 8, true, true, true>(p, tk, tv, ctas, stream)
+                     : launch_rows<DP, 8, false, true, true>(p, tk, tv, ctas, stream);
+    return p.f16 ? launch_rows<DP, 8, true, false, true>(p, tk, tv, ctas, stream)
+                 : launch_rows<DP, 8, false, false, true>(p, tk, tv, ctas, stream);
+}
+
+cudaError_t launch_paged_team(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
+{
+    return p.c.D > 64 ? launch_team<128>(p, tk, tv, ctas, stream) : launch_team<64>(p, tk, tv, ctas, stream);
 }
 
 cudaError_t read_and_clear_status_paged_rows(uint32_t *out)

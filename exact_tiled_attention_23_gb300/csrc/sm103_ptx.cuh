@@ -388,6 +388,37 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 // writes are visible (returns at once in an ordinary launch).
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ---------------------------------------------------------------- clusters
+// Every thread of every CTA of the cluster; shared memory written before is
+// visible to all of them after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The shared address `saddr` of CTA `rank` of the cluster, for ld_cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, int rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- warp tiles
 // 16 bytes from global to shared memory; `bytes` < 16 fills the rest with zeros.
 __device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src, uint32_t bytes)
