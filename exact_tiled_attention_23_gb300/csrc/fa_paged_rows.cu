@@ -68,10 +68,12 @@ struct RowsLayout {
     static constexpr int kMaskOff = kQOff + kWarps * kQBytes;     // visible keys of every stage
     static constexpr int kBarOff = kMaskOff + kWarps * kStages * 4;
     static constexpr int kAbortOff = kBarOff + kWarps * kStages * 8;
-    static constexpr int kStatOff = kAbortOff + kWarps * 4;       // team: (m, l) of every warp's rows
-    static constexpr int kSmemBytes = kStatOff + (kTeam ? kWarps * RM * 8 : 0) + 1024;   // + alignment slack
+    // team: (m, l) of every warp's rows, and 24 bytes for each row and four columns
+    static constexpr int kStatOff = kAbortOff + kWarps * 4;
+    static constexpr int kMailOff = kStatOff + kWarps * RM * 8;
+    static constexpr int kSmemBytes = (kTeam ? kMailOff + RM * DP / 4 * 24 : kStatOff) + 1024;   // + alignment slack
     static_assert(RM == 8 || RM == 16 || (RM == 32 && DP <= 128), "rows");
-    static_assert(kBarOff % 8 == 0 && kStatOff % 8 == 0, "barriers, states");
+    static_assert(kBarOff % 8 == 0 && (!kTeam || kMailOff % 16 == 0), "barriers, states");
     static_assert(!kTeam || (RM == 8 && DP <= 128 && RM * DP * 4 <= kStageBytes), "a team's states fit its stages");
     static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory per SM");
 };
@@ -86,69 +88,92 @@ __device__ __forceinline__ uint32_t unit_at(int row, int unit)
     return (uint32_t)((unit >> 3) * (kTall * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
 }
 
-// The join of a team's tile: `ring` and `stat` are the shared addresses, alike in
-// every CTA of the cluster, of the warps' outputs (`pitch` apart) and of their
-// (m, l).  CTA r takes every p.team-th group of four columns of a row; p.team
-// neighbouring threads take the states of one CTA each and exchange sums.
-template <int DP, bool kF16>
-__device__ __forceinline__ void join_team(const PagedParams &p, uint32_t ring, int pitch, uint32_t stat, int b, int h, int len)
+// A state of a row and four of its columns: m, l and O, not yet divided by l.
+struct Four {
+    float top, sum;
+    float4 acc;
+};
+
+// The join of `kMany` of them.
+template <int kMany>
+__device__ __forceinline__ Four join(const float2 (&stat)[kMany], const float4 (&o)[kMany])
 {
-    constexpr int RM = 8;
-    __syncwarp();
-    ptx::cluster_sync();
-    const int rank = (int)blockIdx.x % p.team, z = (int)threadIdx.x % p.team, first = (int)threadIdx.x / p.team;
-    const int units = p.c.D / 4 * RM / p.team, R = p.G * p.T;
-    const uint32_t its_ring = ptx::cluster_address(ring, z), its_stat = ptx::cluster_address(stat, z);
-#pragma unroll 1
-    for (int u0 = 0; u0 < units; u0 += 32 * kTeamWarps / p.team) {
-        const int unit = (u0 + first) * p.team + rank, row = unit % RM, c4 = unit / RM;
-        const bool mine = u0 + first < units && row < R;
-        float top = -INFINITY, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mine) {
-            float2 st[kTeamWarps];
-            float4 v[kTeamWarps];
+    Four x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-            for (int w = 0; w < kTeamWarps; ++w) {
-                st[w] = ptx::ld_cluster2(its_stat + (uint32_t)(w * RM + row) * 8u);
-                v[w] = ptx::ld_cluster4(its_ring + (uint32_t)(w * pitch) + (uint32_t)(c4 * RM + row) * 16u);
-            }
+    for (int i = 0; i < kMany; ++i) x.top = fmaxf(x.top, stat[i].x);
+    const float ref = x.top == -INFINITY ? 0.f : x.top;
 #pragma unroll
-            for (int w = 0; w < kTeamWarps; ++w) top = fmaxf(top, st[w].x);
-            const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int w = 0; w < kTeamWarps; ++w) {
-                const float f = ptx::ex2_approx(st[w].x - ref);
-                sum = fmaf(f, st[w].y, sum);
-                acc.x = fmaf(f, v[w].x, acc.x);
-                acc.y = fmaf(f, v[w].y, acc.y);
-                acc.z = fmaf(f, v[w].z, acc.z);
-                acc.w = fmaf(f, v[w].w, acc.w);
-            }
-        }
-#pragma unroll 1
-        for (int d = 1; d < p.team; d <<= 1) {
-            const float top2 = __shfl_xor_sync(0xffffffffu, top, d), next = fmaxf(top, top2);
-            const float ref = next == -INFINITY ? 0.f : next;
-            const float f = ptx::ex2_approx(top - ref), f2 = ptx::ex2_approx(top2 - ref);
-            const auto both = [&](float x) { return fmaf(f, x, f2 * __shfl_xor_sync(0xffffffffu, x, d)); };
-            sum = both(sum);
-            acc = make_float4(both(acc.x), both(acc.y), both(acc.z), both(acc.w));
-            top = next;
-        }
-        if (!mine || z != 0) continue;
-        const int t = p.by_g.quotient(row), hq = h * p.G + row - t * p.G;
-        // (a row without a token sees nothing, not even a prefix)
-        const bool empty = sum == 0.f || (p.causal && len - p.T + t < 0);
-        const float inv = empty ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c4) =
-            empty ? make_uint2(0u, 0u)
-                  : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
-        if (p.lse && c4 == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+    for (int i = 0; i < kMany; ++i) {
+        const float f = ptx::ex2_approx(stat[i].x - ref);
+        x.sum = fmaf(f, stat[i].y, x.sum);
+        x.acc.x = fmaf(f, o[i].x, x.acc.x);
+        x.acc.y = fmaf(f, o[i].y, x.acc.y);
+        x.acc.z = fmaf(f, o[i].z, x.acc.z);
+        x.acc.w = fmaf(f, o[i].w, x.acc.w);
     }
-    // no CTA ends while another reads its states
+    return x;
+}
+
+// The join of a team's tile, after the warps have left their states: O `pitch`
+// bytes apart from `ring` on, (m, l) from `stat` on.  A thread joins the CTA's
+// states of a row and four columns and sends the result to the CTA that finishes
+// them, every p.team-th four columns; `mail` has a place for each of the team.
+// (Reading all warps' states across the cluster instead: 2.5 us more.)
+template <int DP, bool kF16>
+__device__ __forceinline__ void join_team(const PagedParams &p, const uint8_t *ring, int pitch, const float2 *stat,
+                                          float4 *mail, int b, int h, int len)
+{
+    constexpr int RM = 8, kUnits = RM * DP / 4;
+    static_assert(kUnits <= 32 * kTeamWarps, "a thread per row and four columns");
+    float2 *mail_stat = reinterpret_cast<float2 *>(mail + kUnits);
+    const int rank = (int)blockIdx.x % p.team, unit = threadIdx.x, units = RM * p.c.D / 4;
+    __syncthreads();
+    Four x{};
+    if (unit < units) {
+        float2 st[kTeamWarps];
+        float4 o[kTeamWarps];
+#pragma unroll
+        for (int w = 0; w < kTeamWarps; ++w) {
+            st[w] = stat[w * RM + unit % RM];
+            o[w] = *reinterpret_cast<const float4 *>(ring + w * pitch + unit * 16);
+        }
+        x = join<kTeamWarps>(st, o);
+    }
     __syncwarp();
-    ptx::cluster_sync();
+    ptx::cluster_wait();                            // the team's CTAs have all started
+    if (unit < units) {
+        const int c4 = unit / RM, to = c4 % p.team;
+        const int place = (c4 / p.team * p.team + rank) * RM + unit % RM;
+        ptx::st_cluster4(ptx::cluster_address(ptx::smem_u32(mail + place), to), x.acc);
+        ptx::st_cluster2(ptx::cluster_address(ptx::smem_u32(mail_stat + place), to), make_float2(x.top, x.sum));
+    }
+    __syncwarp();
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    const int row = unit % RM, mine = unit / RM, c4 = mine * p.team + rank;
+    if (c4 >= p.c.D / 4 || row >= p.G * p.T) return;
+    float2 st[8];
+    float4 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        st[i] = make_float2(-INFINITY, 0.f);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < p.team) {
+            const int place = (mine * p.team + i) * RM + row;
+            st[i] = mail_stat[place];
+            o[i] = mail[place];
+        }
+    }
+    x = join<8>(st, o);
+    const int t = p.by_g.quotient(row), hq = h * p.G + row - t * p.G;
+    // (a row without a token sees nothing, not even a prefix)
+    const bool empty = x.sum == 0.f || (p.causal && len - p.T + t < 0);
+    const float inv = empty ? 0.f : 1.f / x.sum;
+    *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c4) =
+        empty ? make_uint2(0u, 0u)
+              : make_uint2(ptx::pack16x2<kF16>(x.acc.x * inv, x.acc.y * inv),
+                           ptx::pack16x2<kF16>(x.acc.z * inv, x.acc.w * inv));
+    if (p.lse && c4 == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (x.top + log2f(x.sum)) * kLn2;
 }
 
 // Teams.  Where there is little work, two launches and the way through memory
@@ -189,6 +214,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         __syncwarp();
     }
+    if constexpr (kTeam) ptx::cluster_arrive();
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
     const Line<KS> line(p);
@@ -318,12 +344,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     };
     // A box brings what its page holds behind the last key.
     auto clear_rest = [&](uint32_t mask, uint32_t vt) {
-        if (!kTma || mask == kAll) return;
+        if constexpr (kTma) {
+            if (mask == kAll) return;
 #pragma unroll 1
-        for (int e = lane; e < KS * (DP / 8); e += 32)
-            if (!((mask >> (e % KS)) & 1u)) ptx::st_shared_v4(vt + unit_at<KS>(e % KS, e / KS), 0u, 0u, 0u, 0u);
-        ptx::fence_proxy_async_smem();              // before the next copy into the stage
-        __syncwarp();
+            for (int e = lane; e < KS * (DP / 8); e += 32)
+                if (!((mask >> (e % KS)) & 1u)) ptx::st_shared_v4(vt + unit_at<KS>(e % KS, e / KS), 0u, 0u, 0u, 0u);
+            ptx::fence_proxy_async_smem();          // before the next copy into the stage
+            __syncwarp();
+        }
     };
     // The step is done: its stage takes the next one (past the piece, nothing).
     auto refill = [&] {
@@ -484,7 +512,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         for (int e = 0; e < 2; ++e)
                             mine[((4 * n + 2 * e + qr / 4) * RM + 2 * qc + r) * 4 + qr % 4] = o[n][2 * e + r];
                 }
-                join_team<DP, kF16>(p, s_base + Lay::kRingOff, S * Lay::kStageBytes, s_base + Lay::kStatOff, b, h, at.len);
+                join_team<DP, kF16>(p, smem + Lay::kRingOff, S * Lay::kStageBytes,
+                                    reinterpret_cast<const float2 *>(smem + Lay::kStatOff),
+                                    reinterpret_cast<float4 *>(smem + Lay::kMailOff), b, h, at.len);
                 return;
             }
 

@@ -389,14 +389,12 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- clusters
-// Every thread of every CTA of the cluster; shared memory written before is
-// visible to all of them after.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// A barrier of all threads of all CTAs of a cluster, in two halves: shared memory
+// written before the arrival is visible to all of them after the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The shared address `saddr` of CTA `rank` of the cluster, for ld_cluster.
+// The shared address `saddr` of CTA `rank` of the cluster, for st_cluster.
 __device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, int rank)
 {
     uint32_t r;
@@ -404,19 +402,15 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t saddr, int rank)
     return r;
 }
 
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr)
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v)
 {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" :: "r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
+                 :: "r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 // ---------------------------------------------------------------- warp tiles
