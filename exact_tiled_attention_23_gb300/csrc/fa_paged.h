@@ -154,6 +154,7 @@ int paged_rows_per_tile(int D, int64_t rows);
 int paged_rows_chunk(int D);
 constexpr int kRowsWarps = 2;
 constexpr int kTeamWarps = 8;             // of a CTA that works in a team
+constexpr int kMostTeam = 8;              // CTAs of a team (the largest cluster that any GPU takes)
 int paged_rows_ctas_per_sm(int D, int rows);
 
 // The current device's number, and its multiprocessors (148 if unknown).
@@ -213,6 +214,9 @@ cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const
                               cudaStream_t stream);
 cudaError_t launch_paged_team(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                               cudaStream_t stream);
+// Teams of `team` CTAs that fit the device together (a cluster does not cross a
+// group of SMs, so that fewer than SMs / team do); 0 if it cannot be known.
+int paged_teams_at_once(int device, int team);
 cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                             cudaStream_t stream);
 // states: about how many partial states a row has

@@ -157,18 +157,23 @@ struct Plan {
 };
 
 // CTAs of a team per tile, 0 where teams do not pay.  A team's tile has up to 8
-// rows, so that its states fit the stages.  Every warp has at most four chunks
-// of the longest sequence that the table allows, two if there are CTAs for that,
-// and all teams are on the GPU at once.
-int team_size(const fa_paged_kv &c, const Plan &own, int prefix_len, int64_t own_keys, int sms)
+// rows, so that its states fit the stages.  All teams are on the GPU at once
+// (16 teams of 8 where 15 fit: 10.1 us, as teams of 4: 6.3), and a warp has at
+// most eight chunks of the longest sequence that the table allows.  With 8 of
+// 128 tiles of 1024 keys: 12.0 us, cut as a line 18.4, and where one sequence
+// alone is that long 11.2 and 10.2, since a line spreads it over the GPU; with 16
+// of 2048 keys 24.3 and 29.9, but 18.9 and 13.6.
+int team_size(const fa_paged_kv &c, const Plan &own, int prefix_len, int64_t own_keys)
 {
+    constexpr int kMostChunks = 8;
     if (c.D > 128 || own.part.rows != 8 || own.part.tiles != 1) return 0;
-    const int chunk = fa::paged_rows_chunk(c.D);
+    const int chunk = fa::paged_rows_chunk(c.D), device = fa::current_device();
+    if (own.items > fa::sm_count_of(device)) return 0;
     const int64_t chunks = (prefix_len + (int64_t)chunk - 1) / chunk + (own_keys + chunk - 1) / chunk;
     int team = 0;
-    for (int t = 1; t <= 8 && own.items * t <= sms; t *= 2) {
+    for (int t = 1; t <= fa::kMostTeam && own.items <= fa::paged_teams_at_once(device, t); t *= 2) {
         const int64_t each = (chunks + t * fa::kTeamWarps - 1) / (t * fa::kTeamWarps);
-        if (each <= 4) team = t;
+        if (each <= kMostChunks) team = t;
         if (each <= 1) break;
     }
     return team;
@@ -252,7 +257,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     p.joined = prefix_len > 0;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    p.team = team_size(*c, own, prefix_len, own_keys, fa::sm_count_of(fa::current_device()));
+    p.team = team_size(*c, own, prefix_len, own_keys);
     if (p.team) {
         p.prefix_table = prefix_table;
         p.prefix_len = prefix_len;
