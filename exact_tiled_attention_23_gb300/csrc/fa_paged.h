@@ -141,7 +141,7 @@ struct MergeParams {
     int64_t o_s[3];
     float *lse;
     int B, T, Hq, G, D, causal, f16;
-    FastDiv by_g;
+    FastDiv by_g, by_r;                // by G, by G T
     int joined;                        // 0: a tile that one CTA finished is written already
 };
 

@@ -296,6 +296,7 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     m.Hq = Hq;
     m.G = G;
     m.by_g = p.by_g;
+    m.by_r = p.by_gt;
     m.D = D;
     m.causal = p.causal;
     m.f16 = p.f16;

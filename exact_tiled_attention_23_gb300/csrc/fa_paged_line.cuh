@@ -10,12 +10,16 @@
 
 namespace fa {
 
+// seq_len[b] as it counts: within what the table can hold.
+__device__ __forceinline__ int clamped_length(const PagedParams &p, int n)
+{
+    const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
+    return n < 0 ? 0 : (n > cap ? (int)cap : n);
+}
+
 __device__ __forceinline__ int keys_of_sequence(const PagedParams &p, int b)
 {
-    if (!p.c.seq_len) return p.c.fixed_len;
-    const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
-    const int n = p.c.seq_len[b];
-    return n < 0 ? 0 : (n > cap ? (int)cap : n);
+    return p.c.seq_len ? clamped_length(p, p.c.seq_len[b]) : p.c.fixed_len;
 }
 
 // Keys that at least one row of row tile `rt` sees, of a sequence of `len`.
@@ -75,11 +79,24 @@ struct Line {
         } while (u.n == 0);
     }
 
-    __device__ __forceinline__ int chunks_of_group(int g) const
+    // Chunks of the groups base + 32 i + lane; their lengths are loaded together.
+    static constexpr int kHeld = 8;
+    __device__ __forceinline__ void chunks_of_groups(int base, int (&n)[kHeld]) const
     {
-        LineCursor u;
-        enter(u, g);
-        return u.n;
+        int b[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int g = base + 32 * i + (int)threadIdx.x % 32;
+            b[i] = g >= groups ? -1 : p.part.tiles == 1 ? g : g / p.part.tiles;
+            n[i] = b[i] >= 0 && p.c.seq_len ? p.c.seq_len[b[i]] : p.c.fixed_len;
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int g = base + 32 * i + (int)threadIdx.x % 32;
+            const int len = p.c.seq_len ? clamped_length(p, n[i]) : n[i];
+            n[i] = b[i] < 0 ? 0
+                            : chunks_of(keys_of_tile(len, g - b[i] * p.part.tiles, p.part.rows, R, p.by_g, p.T, masked), kChunk);
+        }
     }
 
     // How many pieces a line of `total` chunks is cut into: `most`, or fewer
@@ -100,61 +117,57 @@ struct Line {
     }
 
     // Piece `piece` of the line: where it starts, its first chunk counted along
-    // the line, how many it has, and how many a full piece has.  Lane i sums the
-    // chunks of a strip of groups; the strips' prefix sums find the strip to
-    // start in, and its groups' the group.  Every warp does it for itself: no
-    // barrier, and little code to fetch.  (The host keeps the line below 2^31.)
+    // the line, how many it has, and how many a full piece has.  The lanes sum
+    // the groups' chunks, 256 groups at a time; then the row of 32 groups to
+    // start in is found from the rows' sums, and the group from that row's prefix
+    // sums.  Every warp does it for itself: no barrier, and little code to fetch.
+    // (The host keeps the line below 2^31.)
     __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &first, int &count, int &per) const
     {
         const int lane = threadIdx.x % 32;
-        const int strip = (groups + 31) / 32;
-        int sum = 0;
-#pragma unroll 4
-        for (int i = 0; i < strip; ++i) {
-            const int g = lane * strip + i;
-            sum += g < groups ? chunks_of_group(g) : 0;
-        }
-        int scan = sum;
+        int n[kHeld], sum = 0;
+#pragma unroll 1
+        for (int base = 0; base < groups; base += 32 * kHeld) {
+            chunks_of_groups(base, n);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += v;
+            for (int i = 0; i < kHeld; ++i) sum += n[i];
         }
-        const int total = __shfl_sync(0xffffffffu, scan, 31) * p.c.Hkv;
+        const int total = __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv;
         const int cut = pieces(total, most);
         per = (int)(((unsigned)total + cut - 1) / (unsigned)cut);
         const unsigned start = (unsigned)per * (unsigned)piece;
         first = (int)start;
         count = piece < cut && start < (unsigned)total ? min(per, total - (int)start) : 0;
         if (count == 0) return;
-        const int in = __ffs(__ballot_sync(0xffffffffu, start < (unsigned)(scan * p.c.Hkv))) - 1;
-        int before = __shfl_sync(0xffffffffu, scan - sum, in), g0 = in * strip;
-        if (strip > 1) {
-            const int end = min((in + 1) * strip, groups);
-            for (;; g0 += 32) {
-                const int n = g0 + lane < end ? chunks_of_group(g0 + lane) : 0;
-                int here = n;
+        const int target = (int)(start / (unsigned)p.c.Hkv);      // of the chunks of one key head
+        int before = 0, here = 0, row = -1;
+#pragma unroll 1
+        for (int base = 0; base < groups && row < 0; base += 32 * kHeld) {
+            if (groups > 32 * kHeld) chunks_of_groups(base, n);
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, here, d);
-                    if (lane >= d) here += v;
+            for (int i = 0; i < kHeld; ++i) {
+                const int all = __reduce_add_sync(0xffffffffu, n[i]);
+                if (row < 0 && target < before + all) {
+                    row = base + 32 * i;
+                    here = n[i];
                 }
-                const unsigned hit = __ballot_sync(0xffffffffu, start < (unsigned)((before + here) * p.c.Hkv));
-                // (a second read of lengths that are being changed may find none)
-                if (g0 + 32 >= end && !hit) {
-                    count = 0;
-                    return;
-                }
-                if (hit) {
-                    const int at_lane = __ffs(hit) - 1;
-                    before += __shfl_sync(0xffffffffu, here - n, at_lane);
-                    g0 += at_lane;
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, here, 31);
+                if (row < 0) before += all;
             }
         }
-        enter(at, g0);
+        // (a second read of lengths that are being changed may find none)
+        if (row < 0) {
+            count = 0;
+            return;
+        }
+        const int mine = here;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, here, d);
+            if (lane >= d) here += v;
+        }
+        const int at_lane = __ffs(__ballot_sync(0xffffffffu, target < before + here)) - 1;
+        before += __shfl_sync(0xffffffffu, here - mine, at_lane);
+        enter(at, row + at_lane);
         if (at.n == 0) {
             count = 0;
             return;

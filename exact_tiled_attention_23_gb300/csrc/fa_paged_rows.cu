@@ -808,10 +808,13 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 6 : 4) paged_merge_ke
 {
     constexpr int kRows = kMergeThreads / (kCols * kZ);
     const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kCols, z = threadIdx.x / (kRows * kCols);
-    const int b = blockIdx.x / (unsigned)groups;
     const int R = p.G * p.T, Hkv = p.Hq / p.G, h = blockIdx.y;
-    const int idx = (blockIdx.x - b * groups) * kRows + row;
-    const bool real = idx < R;
+    // a sequence's rows take `groups` CTAs, or, if 0, a CTA has those of several
+    const int several = groups ? 1 : kRows / R, sub = groups ? 0 : p.by_r.quotient(row);
+    const int at_b = groups ? blockIdx.x / (unsigned)groups : blockIdx.x * several + sub;
+    const int idx = groups ? (blockIdx.x - at_b * groups) * kRows + row : row - sub * R;
+    const bool real = idx < R && sub < several && at_b < p.B;
+    const int b = real ? at_b : 0;
     const int t = p.by_g.quotient(real ? idx : 0), hq = h * p.G + (real ? idx : 0) - t * p.G;
 
     // before the kernels that write the states have ended
@@ -936,8 +939,9 @@ template <int kCols, int kZ>
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream)
 {
     constexpr int kRows = kMergeThreads / (kCols * kZ);
-    const int groups = (p.G * p.T + kRows - 1) / kRows;
-    const dim3 grid((unsigned)(p.B * groups), (unsigned)(p.Hq / p.G), (unsigned)((p.D / 4 + kCols - 1) / kCols));
+    const int R = p.G * p.T, groups = 2 * R <= kRows ? 0 : (R + kRows - 1) / kRows;
+    const int blocks = groups ? p.B * groups : (p.B + kRows / R - 1) / (kRows / R);
+    const dim3 grid((unsigned)blocks, (unsigned)(p.Hq / p.G), (unsigned)((p.D / 4 + kCols - 1) / kCols));
     return p.f16 ? launch_behind(paged_merge_kernel<kCols, kZ, true>, grid, kMergeThreads, 0, stream, p, groups)
                  : launch_behind(paged_merge_kernel<kCols, kZ, false>, grid, kMergeThreads, 0, stream, p, groups);
 }
@@ -1046,7 +1050,9 @@ cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaSt
     const int cols = p.D <= 64 ? 16 : 32;
     const auto ctas = [&](int z, int c) {
         const int rows = kMergeThreads / (c * z);
-        return (int64_t)p.B * ((p.G * p.T + rows - 1) / rows) * (p.Hq / p.G) * ((p.D / 4 + c - 1) / c);
+        const int64_t R = p.G * p.T;
+        return (2 * R <= rows ? (p.B + rows / R - 1) / (rows / R) : p.B * ((R + rows - 1) / rows)) * (p.Hq / p.G) *
+               ((p.D / 4 + c - 1) / c);
     };
     if (states >= 32 && ctas(32, 8) <= 4 * sms) return launch_merge<8, 32>(p, stream);
     int z = 1;
