@@ -96,13 +96,17 @@ struct Beside {
     int cap, B;                        // most keys of a sequence; sequences
 };
 
-// Own chunks (8 KB of keys and values at D = 64 and 128) that cost an SM as
-// much time as one block.
+// Units (fa_paged_line.cuh) of the row kernel's line: a tile costs about as much as
+// a chunk beside its keys (256 sequences of 1 to 511 keys: 64 -> 57 us).
+constexpr int kRowsUnit = 1, kRowsTile = 1;
+
+// Such units (a chunk has 8 KB of keys and values at D = 64 and 128) that cost an
+// SM as much time as one block.
 constexpr int kBlockCost = 10;
 
-// SMs for the prefix beside `own` chunks of the sequences' own keys.
+// SMs for the prefix beside `own` units of the sequences' own keys.
 #ifdef __CUDACC__
-__device__ __forceinline__ int beside_front(const Beside &s, int own)
+__device__ __forceinline__ int beside_front(const Beside &s, unsigned own)
 {
     const float part = (float)s.blocks * kBlockCost;
     const int front = (int)((float)s.sms * part / (part + (float)own) + 0.5f);

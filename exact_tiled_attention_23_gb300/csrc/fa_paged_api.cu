@@ -125,7 +125,9 @@ struct Plan {
         part.stacked = stacked;
         part.fixed_len = stacked ? (int)keys : 0;
         const int64_t chunks = items * ((keys + part.chunk - 1) / part.chunk);
-        if (chunks + 4096 > INT32_MAX) {                    // places on the line are 32-bit numbers
+        // places on the line are 32-bit numbers
+        const int64_t most = tc ? INT32_MAX : UINT32_MAX / (fa::kRowsUnit + fa::kRowsTile);
+        if (chunks + 4096 > most) {
             ok = false;
             return;
         }

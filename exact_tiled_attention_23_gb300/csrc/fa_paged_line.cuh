@@ -40,7 +40,10 @@ struct LineCursor {
     int len;       // keys of the sequence
 };
 
-template <int kChunk>
+// Pieces are equal in units: a chunk is kUnit of them, and a tile's first chunk
+// kTile more, for what a tile costs beside its keys.  A chunk belongs to the piece
+// in which it begins.
+template <int kChunk, int kUnit, int kTile>
 struct Line {
     const PagedParams &p;
     int R;         // stacked rows per (sequence, key head)
@@ -79,9 +82,18 @@ struct Line {
         } while (u.n == 0);
     }
 
-    // Chunks of the groups base + 32 i + lane; their lengths are loaded together.
+    static __device__ __forceinline__ int units_of(int chunks) { return chunks ? chunks * kUnit + kTile : 0; }
+    // Where a tile's chunk c begins.
+    static __device__ __forceinline__ int start_of(int c) { return c ? c * kUnit + kTile : 0; }
+    // How many chunks from `c` on begin within `units` (of chunk c's start).
+    static __device__ __forceinline__ int chunks_within(int c, int units)
+    {
+        return (max(0, units - (c ? 0 : kTile + kUnit)) + kUnit - 1) / kUnit + (c ? 0 : 1);
+    }
+
+    // Units of a tile of the groups base + 32 i + lane; their lengths are loaded together.
     static constexpr int kHeld = 8;
-    __device__ __forceinline__ void chunks_of_groups(int base, int (&n)[kHeld]) const
+    __device__ __forceinline__ void units_of_groups(int base, int (&n)[kHeld]) const
     {
         int b[kHeld];
 #pragma unroll
@@ -94,21 +106,24 @@ struct Line {
         for (int i = 0; i < kHeld; ++i) {
             const int g = base + 32 * i + (int)threadIdx.x % 32;
             const int len = p.c.seq_len ? clamped_length(p, n[i]) : n[i];
-            n[i] = b[i] < 0 ? 0
-                            : chunks_of(keys_of_tile(len, g - b[i] * p.part.tiles, p.part.rows, R, p.by_g, p.T, masked), kChunk);
+            const int keys = b[i] < 0 ? 0 : keys_of_tile(len, g - b[i] * p.part.tiles, p.part.rows, R, p.by_g, p.T, masked);
+            n[i] = units_of(chunks_of(keys, kChunk));
         }
     }
 
-    // How many pieces a line of `total` chunks is cut into: `most`, or fewer
+    // How many pieces a line of `total` units is cut into: `most`, or fewer
     // where another kernel works beside.  (Whole warps call it, and share().)
-    __device__ __forceinline__ int pieces(int total, int most) const
+    __device__ __forceinline__ int pieces(unsigned total, int most) const
     {
         const Beside &s = p.beside;
         if (!s.on) return most;
-        int own = total;
+        unsigned own = total;
         if (p.part.stacked) {
             own = 0;
-            for (int b = threadIdx.x % 32; b < s.B; b += 32) own += chunks_of(min(max(s.seq_len[b], 0), s.cap), s.chunk);
+            for (int b = threadIdx.x % 32; b < s.B; b += 32) {
+                const int n = chunks_of(min(max(s.seq_len[b], 0), s.cap), s.chunk);
+                own += n ? n * kRowsUnit + kRowsTile : 0;
+            }
             own = __reduce_add_sync(0xffffffffu, own) * s.tiles;
         }
         if (own == 0) return most;
@@ -116,75 +131,81 @@ struct Line {
         return min(p.part.stacked ? front : (s.sms - front) * s.per_sm, most);
     }
 
-    // Piece `piece` of the line: where it starts, its first chunk counted along
-    // the line, how many it has, and how many a full piece has.  The lanes sum
-    // the groups' chunks, 256 groups at a time; then the row of 32 groups to
-    // start in is found from the rows' sums, and the group from that row's prefix
-    // sums.  Every warp does it for itself: no barrier, and little code to fetch.
-    // (The host keeps the line below 2^31.)
-    __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &first, int &count, int &per) const
+    // Piece `piece` of the line: its first chunk, how many units there are from
+    // that chunk's start to the piece's end (none: no chunk is the piece's), how
+    // many before it, and how many in a full piece.  The lanes sum the groups'
+    // units, 256 groups at a time; then the row of 32 groups to start in is found
+    // from the rows' sums, and the group from that row's prefix sums.  Every warp
+    // does it for itself: no barrier, and little code to fetch.  (The host keeps
+    // the line below 2^32 units.)
+    __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &before, int &units, int &per) const
     {
         const int lane = threadIdx.x % 32;
-        int n[kHeld], sum = 0;
+        int n[kHeld];
+        unsigned sum = 0;
 #pragma unroll 1
         for (int base = 0; base < groups; base += 32 * kHeld) {
-            chunks_of_groups(base, n);
+            units_of_groups(base, n);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) sum += n[i];
         }
-        const int total = __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv;
+        const unsigned total = __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv;
         const int cut = pieces(total, most);
-        per = (int)(((unsigned)total + cut - 1) / (unsigned)cut);
+        // (a full piece has the start of a chunk)
+        per = max((int)((total + cut - 1) / (unsigned)cut), kUnit + kTile);
         const unsigned start = (unsigned)per * (unsigned)piece;
-        first = (int)start;
-        count = piece < cut && start < (unsigned)total ? min(per, total - (int)start) : 0;
-        if (count == 0) return;
-        const int target = (int)(start / (unsigned)p.c.Hkv);      // of the chunks of one key head
-        int before = 0, here = 0, row = -1;
+        before = units = 0;
+        if (piece >= cut || start / (unsigned)per != (unsigned)piece || start >= total) return;
+        const int size = (int)min((unsigned)per, total - start);
+        const unsigned target = start / (unsigned)p.c.Hkv;      // of the units of one key head
+        unsigned sums = 0;                                       // units of the groups in front
+        int here = 0, row = -1;
 #pragma unroll 1
         for (int base = 0; base < groups && row < 0; base += 32 * kHeld) {
-            if (groups > 32 * kHeld) chunks_of_groups(base, n);
+            if (groups > 32 * kHeld) units_of_groups(base, n);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-                const int all = __reduce_add_sync(0xffffffffu, n[i]);
-                if (row < 0 && target < before + all) {
+                const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)n[i]);
+                if (row < 0 && target - sums < all) {
                     row = base + 32 * i;
                     here = n[i];
                 }
-                if (row < 0) before += all;
+                if (row < 0) sums += all;
             }
         }
         // (a second read of lengths that are being changed may find none)
-        if (row < 0) {
-            count = 0;
-            return;
-        }
+        if (row < 0) return;
         const int mine = here;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, here, d);
             if (lane >= d) here += v;
         }
-        const int at_lane = __ffs(__ballot_sync(0xffffffffu, target < before + here)) - 1;
-        before += __shfl_sync(0xffffffffu, here - mine, at_lane);
+        const int at_lane = __ffs(__ballot_sync(0xffffffffu, target - sums < (unsigned)here)) - 1;
+        sums += __shfl_sync(0xffffffffu, here - mine, at_lane);
         enter(at, row + at_lane);
-        if (at.n == 0) {
-            count = 0;
-            return;
+        if (at.n == 0) return;
+        const int span = units_of(at.n), left = (int)(start - sums * p.c.Hkv);
+        at.h = min(left / span, p.c.Hkv - 1);
+        const int x = min(left - at.h * span, span - 1);
+        at.c = x == 0 ? 0 : max(1, (x - kTile + kUnit - 1) / kUnit);
+        if (at.c < at.n) {
+            before = start_of(at.c) - x;
+        } else {                                                 // in the tile's last chunk: the next tile
+            before = span - x;
+            at.c = at.n - 1;
+            advance(at);
+            if (at.n == 0) return;
         }
-        const int left = first - before * p.c.Hkv;
-        at.h = min(left / at.n, p.c.Hkv - 1);
-        at.c = min(left - at.h * at.n, at.n - 1);
+        units = max(0, size - before);
     }
 
-    // The piece that has the first chunk of a tile says where its states will be.
-    // (`first`: the piece's own first chunk)
-    __device__ __forceinline__ void record(const LineCursor &u, int piece, int first, int first_chunk, int per) const
+    // The piece that has the first chunk of a tile says where its states will be;
+    // `before`: units of the piece in front of the tile.
+    __device__ __forceinline__ void record(const LineCursor &u, int piece, int before, int per) const
     {
         const int tile = u.g * p.c.Hkv + u.h;
-        // from the piece's start the tile's chunks fill pieces of `per`
-        const int before = (int)((unsigned)first_chunk - (unsigned)first);
-        p.part.tile[tile] = TileSlots{piece + tile, (before + u.n + per - 1) / per};
+        p.part.tile[tile] = TileSlots{piece + tile, (before + start_of(u.n - 1)) / per + 1};
     }
 };
 

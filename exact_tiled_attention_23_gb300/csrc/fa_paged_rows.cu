@@ -219,10 +219,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if constexpr (kTeam) ptx::cluster_arrive();
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    const Line<KS> line(p);
+    const Line<KS, kRowsUnit, kRowsTile> line(p);
     const int piece = (int)blockIdx.x * kWarps + warp;
     LineCursor at;
-    int g0, steps, per;
+    // of the piece: units, those in front of `at`; a full piece's.  Team: chunks.
+    int units, used, per;
     int front = 0;              // team: chunks of the prefix, before the own ones
     if constexpr (kTeam) {
         const int tile = (int)blockIdx.x / p.team, g = tile / p.c.Hkv;
@@ -233,16 +234,17 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int warps = p.team * kWarps, mine = ((int)blockIdx.x - tile * p.team) * kWarps + warp;
         per = (at.n + warps - 1) / warps;
         at.c = min(mine * per, at.n);
-        steps = min(per, at.n - at.c);
-        g0 = 0;
+        units = min(per, at.n - at.c);
+        used = 0;
     } else {
-        line.share(piece, (int)gridDim.x * kWarps, at, g0, steps, per);
+        line.share(piece, (int)gridDim.x * kWarps, at, used, units, per);
+        units += used;
     }
     const int R = line.R;
 
     // ---- loads -----------------------------------------------------------
     LineCursor ld = at;
-    int ld_left = steps;
+    int ld_left = units - used;
     // Where this lane's key of a step is (lane % KS).  Its page number is
     // fetched at least one step before its use.
     struct Place {
@@ -265,14 +267,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             x.slot = key - which * p.c.page_size;
             x.page = p.c.table[(int64_t)b * p.c.table_stride + which];
         }
-        if constexpr (kTeam)
+        if constexpr (kTeam) {
             ++ld.c;
-        else
+            --ld_left;
+        } else {
+            ld_left -= ld.c ? kRowsUnit : kRowsUnit + kRowsTile;
             line.advance(ld);
-        --ld_left;
+        }
         return x;
     };
     const uint32_t ring = s_base + Lay::kRingOff + warp * S * Lay::kStageBytes;
+    // Keys that one tile alone reads need not stay in the L2, where a prefix that
+    // other CTAs read again and again has its keys (256 sequences behind a prefix
+    // of 4097 keys: 82 -> 69 us).
+    const uint64_t policy = kTma ? ptx::l2_policy(!kTeam && p.part.tiles == 1) : 0;
     int issued = 0;             // steps copied
     auto load = [&](int stage, const Place &x) {
         const bool ok = x.page >= 0 && x.page < p.c.num_pages;
@@ -290,9 +298,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 if (lane == 0) {
 #pragma unroll
                     for (int c = 0; c < DP / 64; ++c) {
-                        ptx::tma_load_4d(dst + (c * KS + i) * 128, &tm_k, &full[stage], c * 64, box_slot, x.h, box_page);
-                        ptx::tma_load_4d(dst + Lay::kTileBytes + (c * KS + i) * 128, &tm_v, &full[stage], c * 64, box_slot,
-                                         x.h, box_page);
+                        ptx::tma_load_4d_hint(dst + (c * KS + i) * 128, &tm_k, &full[stage], c * 64, box_slot, x.h,
+                                              box_page, policy);
+                        ptx::tma_load_4d_hint(dst + Lay::kTileBytes + (c * KS + i) * 128, &tm_v, &full[stage], c * 64,
+                                              box_slot, x.h, box_page, policy);
                     }
                 }
             }
@@ -326,7 +335,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ---- the piece, tile by tile -------------------------------------------
     const int qr = lane >> 2, qc = lane & 3;        // this lane's rows (qr, qr + 8) and columns (2 qc, +1) of a product
     const uint32_t q_smem = s_base + Lay::kQOff + warp * Lay::kQBytes;
-    int stage = 0, done = 0;
+    int stage = 0;
     uint32_t phase = 0;
     // Waits for a step's keys; returns which of them are visible.  After a wait
     // that gave up (the results are undefined then) the warp computes nothing
@@ -377,12 +386,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
     };
 #pragma unroll 1
-    while (kTeam || done < steps) {
-        const int count = min(at.n - at.c, steps - done);      // chunks of this tile in the piece
+    while (kTeam || used < units) {
+        const int rest = units - used;
+        const int count = kTeam ? rest : min(at.n - at.c, line.chunks_within(at.c, rest));      // chunks of this tile in the piece
         const int b = p.part.tiles == 1 ? at.g : at.g / p.part.tiles;
         const int row0 = (at.g - b * p.part.tiles) * RM, h = at.h;
         const int tile = at.g * p.c.Hkv + h;
-        if (!kTeam && at.c == 0 && lane == 0) line.record(at, piece, g0, g0 + done, per);
+        if (!kTeam && at.c == 0 && lane == 0) line.record(at, piece, used, per);
 
         const int lim_all = line.masked ? at.len - p.T + p.by_g.quotient(row0) + 1 : at.len;   // seen by every row
 
@@ -764,9 +774,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
         }
         __syncwarp();
+        used += line.start_of(at.c + count) - line.start_of(at.c);
         at.c += count - 1;
         line.advance(at);
-        done += count;
     }
     drain();
     // the merge starts when this kernel has ended, and needs the one before too

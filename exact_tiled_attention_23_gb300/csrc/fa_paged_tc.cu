@@ -99,6 +99,8 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_
     return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, ab, follow_abort);
 }
 
+using BlockLine = Line<BN, 1, 0>;
+
 // A role's way along the CTA's piece of the line, tile by tile: what a block
 // needs beyond its number is found once per tile, because the issuing threads
 // run alone and every instruction between two products counts (a walk that
@@ -109,7 +111,7 @@ struct Walk {
     // blocks of this tile in the piece
     __device__ __forceinline__ int count() const { return min(u.n - u.c, left); }
     // past `done` = count() blocks; false at the end of the piece
-    __device__ __forceinline__ bool next_tile(const Line<BN> &line, int done)
+    __device__ __forceinline__ bool next_tile(const BlockLine &line, int done)
     {
         left -= done;
         if (left == 0) return false;
@@ -167,10 +169,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    const Line<BN> line(p);
+    const BlockLine line(p);
     Walk walk;
-    int g0, per;
-    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, g0, walk.left, per);
+    int before, per;
+    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, before, walk.left, per);
     if (walk.left == 0) {
         if (p.second) ptx::wait_for_primary();
         return;
@@ -537,7 +539,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
             const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
-            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, g0, g0 + (t - count), per);
+            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, t - count, per);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {

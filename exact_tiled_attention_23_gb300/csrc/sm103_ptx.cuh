@@ -97,6 +97,26 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
+// How long the L2 keeps what a copy reads: L2::evict_first or the ordinary way.
+__device__ __forceinline__ uint64_t l2_policy(bool evict_first)
+{
+    uint64_t first, normal;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+    return evict_first ? first : normal;
+}
+
+__device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const void *tmap, uint64_t *bar,
+                                                 int32_t x, int32_t y, int32_t z, int32_t w, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)),
+          "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Tensor-memory allocation: the whole warp executes these.
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols)
