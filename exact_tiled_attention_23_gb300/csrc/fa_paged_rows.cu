@@ -814,7 +814,7 @@ cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUt
 constexpr int kMergeThreads = 256;
 
 template <int kCols, int kZ, bool kF16>
-__global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 6 : 4) paged_merge_kernel(const MergeParams p, const int groups)
+__global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_kernel(const MergeParams p, const int groups)
 {
     constexpr int kRows = kMergeThreads / (kCols * kZ);
     const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kCols, z = threadIdx.x / (kRows * kCols);

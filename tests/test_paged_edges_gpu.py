@@ -249,3 +249,35 @@ def test_a_wait_that_runs_out_reports_a_timeout(T):
     assert run.returncode == 0, run.stderr[-2000:]
     got = json.loads(run.stdout.strip().splitlines()[-1])
     assert got == {"status": fa.FA_ERR_TIMEOUT, "sum": float(1 << 20), "after": fa.FA_OK}
+
+
+FIRST_IN_A_GRAPH = r"""
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import torch
+import exact_tiled_attention_23_gb300 as fa
+from test_paged_gpu import BF16, Pool
+
+for T, width, prefix in ((1, None, 0), (1, None, 100), (1, 1300, 0), (40, None, 0), (40, None, 300)):
+    pool = Pool([200, 30], 2, 64, 16, BF16, seed=51, prefix=prefix, width=width)
+    cache, q, table = pool.gpu(), pool.queries(4, T).cuda(), pool.prefix_table.cuda()
+    x = torch.randn((2, 2, 1, 64), device="cuda").to(BF16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fa.kv_append(cache, x, x)
+        o, lse = fa.forward_shared_prefix(q, cache, table, prefix) if prefix else fa.forward_paged(q, cache)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = fa.forward_shared_prefix(q, cache, table, prefix) if prefix else fa.forward_paged(q, cache)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]), (T, width, prefix)
+assert fa.fa_device_status(None) == fa.FA_OK
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """What the library asks the driver for once per process may be asked during a capture."""
+    run = subprocess.run([sys.executable, "-c", FIRST_IN_A_GRAPH, ROOT], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stderr[-2000:]
