@@ -12,6 +12,12 @@
 // bits: inv_freq[p] / 2pi as a fixed-point number F of 2^-64 turns, and n * F
 // modulo 2^64 drops whole turns exactly.  F is good to 2^-61 of itself, so the
 // angle is good to 2^-30 turns at n = 2^31, and its fp32 form decides.
+//
+// Bound by memory: every value is read once and written once, whole 16-byte units
+// at a time.  One CTA per token, so that a token's angles are computed once for all
+// heads.  Two prompts of 8192 tokens, 32 query and 8 key heads, D = 128: 403 MB in
+// 62 us, 6.5 TB/s (a copy: 6.8).  One token: 3 us, a launch and four waits in turn
+// (length, page, values, stores).
 #include "fa_paged.h"
 #include "sm103_ptx.cuh"
 

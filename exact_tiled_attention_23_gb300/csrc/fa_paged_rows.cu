@@ -1,20 +1,23 @@
 // fa_paged_rows.cu -- attention of few query rows over a paged cache, and the
 // merge of partial softmax states.
 //
-// A tile is up to 16 or 32 stacked query rows of one (sequence, key head): the
+// A tile is up to 8, 16 or 32 stacked query rows of one (sequence, key head): the
 // Hq / Hkv query heads that share the key head, times the query tokens.  Every
 // key and value is read once for the whole tile, so a decoding step is bound
 // by memory: 4 D bytes and 4 D * rows operations per key.  What the layout is
 // for is to keep loads in flight:
 //
 //   * the keys of all tiles form one line of chunks (16 keys, 32 at D <= 64),
-//     cut into equal pieces, one per warp, whatever the sequences' lengths.  A
+//     cut into equal pieces, one per warp, whatever the sequences' lengths (a
+//     tile weighs as much as one chunk more, for what it costs to begin it).  A
 //     tile that two or more warps had a share of leaves a partial state
 //     (O_s, LSE_s) in a slot for each, and the merge joins them:
 //         m = max LSE_s,  w_s = 2^(LSE_s - m),  O = sum w_s O_s / sum w_s.
 //     Warps never meet.  (With four warps on a tile, joined in shared memory at
 //     its end, the barriers and the code that runs once per tile, fetched anew
-//     each time, took a third of the time of tiles of 512 keys.)
+//     each time, took a third of the time of tiles of 512 keys.)  Where the work
+//     is so little that the merge would be most of it, a cluster of CTAs takes a
+//     tile instead and joins it by itself ("Teams" below);
 //   * a warp has its own ring of shared-memory stages.  Where pages hold a
 //     multiple of 8 keys, one lane copies boxes of 8 to 32 rows with TMA;
 //     elsewhere all lanes copy 16 bytes at a time.  Either way the addresses
@@ -25,6 +28,12 @@
 //   * each weight p is split into two 16-bit numbers, p = hi + lo with an error
 //     of 2^-16 p (fp16: 2^-22), and V is multiplied by both: the products are
 //     not the bound, and the output keeps fp32's error until it is rounded.
+//
+// Measured (D = 128, 8 key heads of 4 queries, bf16): a token of 64 sequences of
+// up to 8191 keys, 1.07 GB, 165 us, 6.5 TB/s (a copy: 6.8); of one sequence of
+// 131072 keys, 537 MB, 92 us, 5.8 TB/s.  A quarter of the issue slots are used and
+// 13 % of the products' rate: what is left is 3 us until the first keys land and
+// 5 us from the last keys to the end of the merge.
 //
 // Keys at or past a sequence's length and keys of pages outside the pool get a
 // score of -inf, and their rows of V are zero in shared memory (0 * NaN is NaN).

@@ -27,6 +27,12 @@
 //   * keys of pages outside the pool are hidden: a scan of the CTA's pages, done
 //     while the first copies fly, decides whether the blocks have to ask.
 //
+// Measured: 1024 tokens over 16384 keys, 32 query and 8 key heads, D = 128, bf16,
+// 2.7e11 operations, 208 us with the merge, 1.28 PFLOP/s (a large matrix product:
+// 1.88); ~1680 clk per block, as in the split-row kernel, bound by the softmax and
+// the hand-offs around it (tensor pipe 52 % busy).  Short calls pay ~10 us until
+// the pipeline runs, most of it instruction fetch.
+//
 // P is rounded to 16 bits for the second product and O divided by the sum of
 // the rounded weights, as in fa_fwd: the tensor cores take 16-bit operands, and
 // a second product for the rounding's rest would cost a third of the rate.
