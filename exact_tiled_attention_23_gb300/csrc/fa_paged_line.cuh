@@ -92,7 +92,7 @@ struct Line {
     }
 
     // Units of a tile of the groups base + 32 i + lane; their lengths are loaded together.
-    static constexpr int kHeld = 8;
+    static constexpr int kHeld = 2;
     __device__ __forceinline__ void units_of_groups(int base, int (&n)[kHeld]) const
     {
         int b[kHeld];
@@ -134,10 +134,11 @@ struct Line {
     // Piece `piece` of the line: its first chunk, how many units there are from
     // that chunk's start to the piece's end (none: no chunk is the piece's), how
     // many before it, and how many in a full piece.  The lanes sum the groups'
-    // units, 256 groups at a time; then the row of 32 groups to start in is found
-    // from the rows' sums, and the group from that row's prefix sums.  Every warp
-    // does it for itself: no barrier, and little code to fetch.  (The host keeps
-    // the line below 2^32 units.)
+    // units, 64 groups at a time (256: more code to fetch, 54 us where 64 take 53
+    // behind a shared prefix; 32: 256 sequences 53.6 where 64 take 52.7); then
+    // the row of 32 groups to start in is found from the rows' sums, and the group
+    // from that row's prefix sums.  Every warp does it for itself: no barrier, and
+    // little code to fetch.  (The host keeps the line below 2^32 units.)
     __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &before, int &units, int &per) const
     {
         const int lane = threadIdx.x % 32;
