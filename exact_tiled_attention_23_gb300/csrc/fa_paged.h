@@ -96,15 +96,17 @@ struct Beside {
     int cap, B;                        // most keys of a sequence; sequences
 };
 
-// Units (fa_paged_line.cuh) of the row kernel's line: a tile costs about as much as
-// a chunk beside its keys (256 sequences of 1 to 511 keys: 64 -> 57 us).
-constexpr int kRowsUnit = 1, kRowsTile = 1;
+// What a tile costs beside its keys, in chunks of the row kernel (256 sequences of
+// 1 to 511 keys: 64 -> 57 us) and in blocks of the tensor-core kernel (64 sequences
+// behind a prefix of 16384 keys: 1 block 54.8 us, 3 53.8, 5 51.3, 8 51.3; 256 behind
+// 4097: 68.2, 65.2, 66.2, 69.0).
+constexpr int kRowsTile = 1, kBlocksTile = 5;
 
-// Such units (a chunk has 8 KB of keys and values at D = 64 and 128) that cost an
-// SM as much time as one block.
+// Own chunks and tiles (a chunk has 8 KB of keys and values at D = 64 and 128)
+// that cost an SM as much time as one block.
 constexpr int kBlockCost = 10;
 
-// SMs for the prefix beside `own` units of the sequences' own keys.
+// SMs for the prefix beside `own` chunks and tiles of the sequences' own keys.
 #ifdef __CUDACC__
 __device__ __forceinline__ int beside_front(const Beside &s, unsigned own)
 {

@@ -126,8 +126,7 @@ struct Plan {
         part.fixed_len = stacked ? (int)keys : 0;
         const int64_t chunks = items * ((keys + part.chunk - 1) / part.chunk);
         // places on the line are 32-bit numbers
-        const int64_t most = tc ? INT32_MAX : UINT32_MAX / (fa::kRowsUnit + fa::kRowsTile);
-        if (chunks + 4096 > most) {
+        if (chunks + 4096 > (tc ? UINT32_MAX / (1 + fa::kBlocksTile) : UINT32_MAX / (1 + fa::kRowsTile))) {
             ok = false;
             return;
         }

@@ -40,15 +40,16 @@ struct LineCursor {
     int len;       // keys of the sequence
 };
 
-// Pieces are equal in units: a chunk is kUnit of them, and a tile's first chunk
-// kTile more, for what a tile costs beside its keys.  A chunk belongs to the piece
-// in which it begins.
-template <int kChunk, int kUnit, int kTile>
+// Pieces are equal in units: a chunk is one, and where pieces are long a tile's
+// first chunk counts kTile more, for what a tile costs beside its keys.  A chunk
+// belongs to the piece in which it begins.
+template <int kChunk, int kTile>
 struct Line {
     const PagedParams &p;
     int R;         // stacked rows per (sequence, key head)
     int groups;
     bool masked;   // rows see different keys
+    int weight = 0;                // kTile or 0, set by share()
 
     __device__ __forceinline__ explicit Line(const PagedParams &q) : p(q)
     {
@@ -82,18 +83,16 @@ struct Line {
         } while (u.n == 0);
     }
 
-    static __device__ __forceinline__ int units_of(int chunks) { return chunks ? chunks * kUnit + kTile : 0; }
+    __device__ __forceinline__ int units_of(int chunks) const { return chunks ? chunks + weight : 0; }
     // Where a tile's chunk c begins.
-    static __device__ __forceinline__ int start_of(int c) { return c ? c * kUnit + kTile : 0; }
-    // How many chunks from `c` on begin within `units` (of chunk c's start).
-    static __device__ __forceinline__ int chunks_within(int c, int units)
-    {
-        return (max(0, units - (c ? 0 : kTile + kUnit)) + kUnit - 1) / kUnit + (c ? 0 : 1);
-    }
+    __device__ __forceinline__ int start_of(int c) const { return c ? c + weight : 0; }
+    // How many chunks from `c` on begin within `units` (> 0) of chunk c's start.
+    __device__ __forceinline__ int chunks_within(int c, int units) const { return c ? units : max(1, units - weight); }
 
-    // Units of a tile of the groups base + 32 i + lane; their lengths are loaded together.
+    // Chunks of a tile of the groups base + 32 i + lane; their lengths are loaded
+    // together.
     static constexpr int kHeld = 2;
-    __device__ __forceinline__ void units_of_groups(int base, int (&n)[kHeld]) const
+    __device__ __forceinline__ void chunks_of_groups(int base, int (&n)[kHeld]) const
     {
         int b[kHeld];
 #pragma unroll
@@ -107,22 +106,22 @@ struct Line {
             const int g = base + 32 * i + (int)threadIdx.x % 32;
             const int len = p.c.seq_len ? clamped_length(p, n[i]) : n[i];
             const int keys = b[i] < 0 ? 0 : keys_of_tile(len, g - b[i] * p.part.tiles, p.part.rows, R, p.by_g, p.T, masked);
-            n[i] = units_of(chunks_of(keys, kChunk));
+            n[i] = chunks_of(keys, kChunk);
         }
     }
 
-    // How many pieces a line of `total` units is cut into: `most`, or fewer
-    // where another kernel works beside.  (Whole warps call it, and share().)
-    __device__ __forceinline__ int pieces(unsigned total, int most) const
+    // How many pieces a line is cut into: `most`, or fewer where another kernel
+    // works beside.  `own`: its chunks and tiles.  (Whole warps call it, and
+    // share().)
+    __device__ __forceinline__ int pieces(unsigned own, int most) const
     {
         const Beside &s = p.beside;
         if (!s.on) return most;
-        unsigned own = total;
         if (p.part.stacked) {
             own = 0;
             for (int b = threadIdx.x % 32; b < s.B; b += 32) {
                 const int n = chunks_of(min(max(s.seq_len[b], 0), s.cap), s.chunk);
-                own += n ? n * kRowsUnit + kRowsTile : 0;
+                own += n ? n + 1 : 0;
             }
             own = __reduce_add_sync(0xffffffffu, own) * s.tiles;
         }
@@ -134,42 +133,49 @@ struct Line {
     // Piece `piece` of the line: its first chunk, how many units there are from
     // that chunk's start to the piece's end (none: no chunk is the piece's), how
     // many before it, and how many in a full piece.  The lanes sum the groups'
-    // units, 64 groups at a time (256: more code to fetch, 54 us where 64 take 53
+    // chunks, 64 groups at a time (256: more code to fetch, 54 us where 64 take 53
     // behind a shared prefix; 32: 256 sequences 53.6 where 64 take 52.7); then
     // the row of 32 groups to start in is found from the rows' sums, and the group
     // from that row's prefix sums.  Every warp does it for itself: no barrier, and
     // little code to fetch.  (The host keeps the line below 2^32 units.)
-    __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &before, int &units, int &per) const
+    __device__ __forceinline__ void share(int piece, int most, LineCursor &at, int &before, int &units, int &per)
     {
         const int lane = threadIdx.x % 32;
         int n[kHeld];
-        unsigned sum = 0;
+        unsigned chunks = 0, tiles = 0;
 #pragma unroll 1
         for (int base = 0; base < groups; base += 32 * kHeld) {
-            units_of_groups(base, n);
+            chunks_of_groups(base, n);
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) sum += n[i];
+            for (int i = 0; i < kHeld; ++i) {
+                chunks += n[i];
+                tiles += n[i] > 0;
+            }
         }
-        const unsigned total = __reduce_add_sync(0xffffffffu, sum) * p.c.Hkv;
-        const int cut = pieces(total, most);
-        // (a full piece has the start of a chunk)
-        per = max((int)((total + cut - 1) / (unsigned)cut), kUnit + kTile);
+        chunks = __reduce_add_sync(0xffffffffu, chunks) * p.c.Hkv;
+        tiles = __reduce_add_sync(0xffffffffu, tiles) * p.c.Hkv;
+        const int cut = pieces(chunks + tiles, most);
+        // (short pieces: equal in chunks)
+        weight = chunks / (unsigned)cut >= 2 * kTile ? kTile : 0;
+        const unsigned total = chunks + tiles * weight;
+        // (a full piece is longer than kTile, so that a chunk begins in it)
+        per = (int)((total + cut - 1) / (unsigned)cut);
         const unsigned start = (unsigned)per * (unsigned)piece;
         before = units = 0;
-        if (piece >= cut || start / (unsigned)per != (unsigned)piece || start >= total) return;
+        if (piece >= cut || start >= total) return;
         const int size = (int)min((unsigned)per, total - start);
         const unsigned target = start / (unsigned)p.c.Hkv;      // of the units of one key head
         unsigned sums = 0;                                       // units of the groups in front
         int here = 0, row = -1;
 #pragma unroll 1
         for (int base = 0; base < groups && row < 0; base += 32 * kHeld) {
-            if (groups > 32 * kHeld) units_of_groups(base, n);
+            if (groups > 32 * kHeld) chunks_of_groups(base, n);
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) {
-                const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)n[i]);
+                const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)units_of(n[i]));
                 if (row < 0 && target - sums < all) {
                     row = base + 32 * i;
-                    here = n[i];
+                    here = units_of(n[i]);
                 }
                 if (row < 0) sums += all;
             }
@@ -189,7 +195,7 @@ struct Line {
         const int span = units_of(at.n), left = (int)(start - sums * p.c.Hkv);
         at.h = min(left / span, p.c.Hkv - 1);
         const int x = min(left - at.h * span, span - 1);
-        at.c = x == 0 ? 0 : max(1, (x - kTile + kUnit - 1) / kUnit);
+        at.c = x == 0 ? 0 : max(1, x - weight);
         if (at.c < at.n) {
             before = start_of(at.c) - x;
         } else {                                                 // in the tile's last chunk: the next tile

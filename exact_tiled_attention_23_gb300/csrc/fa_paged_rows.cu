@@ -228,7 +228,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if constexpr (kTeam) ptx::cluster_arrive();
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    const Line<KS, kRowsUnit, kRowsTile> line(p);
+    Line<KS, kRowsTile> line(p);
     const int piece = (int)blockIdx.x * kWarps + warp;
     LineCursor at;
     // of the piece: units, those in front of `at`; a full piece's.  Team: chunks.
@@ -280,7 +280,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             ++ld.c;
             --ld_left;
         } else {
-            ld_left -= ld.c ? kRowsUnit : kRowsUnit + kRowsTile;
+            ld_left -= ld.c ? 1 : 1 + line.weight;
             line.advance(ld);
         }
         return x;

@@ -105,7 +105,7 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_
     return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, ab, follow_abort);
 }
 
-using BlockLine = Line<BN, 1, 0>;
+using BlockLine = Line<BN, kBlocksTile>;
 
 // A role's way along the CTA's piece of the line, tile by tile: what a block
 // needs beyond its number is found once per tile, because the issuing threads
@@ -175,10 +175,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
-    const BlockLine line(p);
+    BlockLine line(p);
     Walk walk;
-    int before, per;
-    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, before, walk.left, per);
+    int used, units, per;                      // units of the piece: before `walk`, from there on; a full piece's
+    line.share((int)blockIdx.x, (int)gridDim.x, walk.u, used, units, per);
+    walk.left = 0;
+    {
+        LineCursor u = walk.u;
+        for (int rest = units; rest > 0;) {
+            const int n = min(u.n - u.c, line.chunks_within(u.c, rest));
+            walk.left += n;
+            rest -= line.start_of(u.c + n) - line.start_of(u.c);
+            u.c += n - 1;
+            line.advance(u);
+            if (u.n == 0) break;
+        }
+    }
     if (walk.left == 0) {
         if (p.second) ptx::wait_for_primary();
         return;
@@ -545,7 +557,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
             const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
-            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, t - count, per);
+            if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, used, per);
+            used += line.start_of(was.c + count) - line.start_of(was.c);
             uint16_t *o_row = nullptr;
             const bool real = row < line.R;
             if (real) {

@@ -231,7 +231,13 @@ k = torch.randn((8192, 8, 16, 128), device="cuda", dtype=torch.bfloat16)
 table = torch.randperm(8192, device="cuda").to(torch.int32).view(32, 256)
 cache = fa.PagedKV(k, k.clone(), table, torch.full((32,), 4096, dtype=torch.int32, device="cuda"))
 q = torch.randn((32, 32, T, 128), device="cuda", dtype=torch.bfloat16)
-fa.forward_paged(q, cache)
+a, b = (torch.empty(1 << 29, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+torch.cuda.synchronize()
+with torch.cuda.stream(torch.cuda.Stream()):
+    for _ in range(60):
+        b.copy_(a)
+for _ in range(100):
+    fa.forward_paged(q, cache)
 torch.cuda.synchronize()
 status = fa.fa_device_status(None)
 total = torch.ones(1 << 20, device="cuda").sum().item()
@@ -241,9 +247,10 @@ print(json.dumps({"status": status, "sum": total, "after": fa.fa_device_status(N
 
 @pytest.mark.parametrize("T", [1, 40], ids=["rows", "tensor_cores"])
 def test_a_wait_that_runs_out_reports_a_timeout(T):
-    """A budget of 0.2 us, which the copies of a whole GPU's warps that all start
-    at once (29 MB from device memory) cannot meet: the kernel ends by itself,
-    and the context still runs work."""
+    """A budget of 0.2 us.  A probe of a barrier may itself be suspended for some
+    microseconds, so what runs out is a wait well above that: 100 calls, whose
+    copies (29 MB at once from device memory) compete with another stream's.
+    The kernels end by themselves, and the context still runs work."""
     run = subprocess.run([sys.executable, "-c", CHILD, str(T), ROOT], env=dict(os.environ, FA_WAIT_LIMIT_MS="0.0002"),
                          capture_output=True, text=True, timeout=120)
     assert run.returncode == 0, run.stderr[-2000:]
