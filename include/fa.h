@@ -410,8 +410,10 @@ fa_status fa_kv_append(const fa_paged_kv *cache, const fa_rows *K, const fa_rows
  *              not matter, and calls that may overlap need separate ones.
  * Queries that see no key get O = +0.0 and LSE = -inf.  Results do not depend
  * on timing: partial states are joined in a fixed order.  Returns as fa_fwd,
- * and FA_ERR_INVALID_ARG for a missing, misaligned or too small workspace or
- * an Hq that is no multiple of Hkv.
+ * and FA_ERR_INVALID_ARG for a missing, misaligned or too small workspace, an
+ * Hq that is no multiple of Hkv, or sizes past what 32 bits count: tables that
+ * allow up to 2^29 chunks of keys in all (16 keys, 32 at D <= 64, 128 where more
+ * than 32 rows share keys; per sequence, key head and tile of rows) are taken.
  */
 fa_status fa_fwd_paged(const fa_rows *Q, const fa_paged_kv *cache, const fa_rows *O, float *LSE, int B, int Hq, int T,
                        int causal, float scale, int f16, void *workspace, size_t workspace_bytes, void *stream);

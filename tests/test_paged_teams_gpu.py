@@ -124,3 +124,20 @@ def test_teams_in_graphs_follow_lengths(prefix):
         want = step(want_cache)
         torch.cuda.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("D,T", [(64, 1), (256, 1), (64, 40)])
+def test_tables_without_pages(D, T):
+    """Sequences that own no pages at all: nothing to see but a prefix."""
+    pool = Pool([0, 0], 2, D, 16, BF16, seed=44, prefix=70)
+    cache = fa.PagedKV(pool.k.cuda(), pool.v.cuda(), torch.empty((2, 0), dtype=torch.int32, device="cuda"),
+                       torch.tensor([0, 5], dtype=torch.int32, device="cuda"))       # 5 counts as 0
+    q = pool.queries(4, T).cuda()
+    o, lse = fa.forward_paged(q, cache, causal=False)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = fa.forward_shared_prefix(q, cache, pool.prefix_table.cuda(), 70)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    got = fa.forward_shared_prefix(q, cache, pool.prefix_table.cuda(), 70, causal=False)
+    torch.cuda.synchronize()
+    want = run_paged(pool, 4, T, causal=False, prefix=70, q=q.cpu())
+    assert torch.equal(got[0], want[2]) and torch.equal(got[1], want[3])
