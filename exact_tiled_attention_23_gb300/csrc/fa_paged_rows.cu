@@ -815,18 +815,22 @@ cudaError_t launch_rows_f(const PagedParams &p, const CUtensorMap &tk, const CUt
 
 // ---------------------------------------------------------------- merge
 // The sum of a row's partial outputs, weighted by their LSEs against the
-// largest.  A CTA has kRows rows of one (sequence, key head), kCols threads for
-// four columns each, and kZ threads for each of those, which take every kZ-th
-// state and are joined in order: one thread's chain of loads through the 228
-// states of a row (one sequence of 131072 keys) took 18 us.  The lanes of a load
-// are neighbours in the slots.
+// largest.  A CTA has kRows rows of a key head and 4 kCols of their columns, and
+// kZ threads for each four columns, which take every kZ-th state and are joined in
+// order: one thread's chain of loads through the 228 states of a row (one sequence
+// of 131072 keys) took 18 us.  Where kZ = 1 there are many rows of few states: a
+// thread has four columns twice, so that fewer CTAs wait for a place.  The lanes of
+// a load are neighbours in the slots.
 constexpr int kMergeThreads = 256;
 
+constexpr int merge_wide(int z) { return z == 1 ? 2 : 1; }
+constexpr int merge_rows(int cols, int z) { return kMergeThreads * merge_wide(z) / (cols * z); }
+
 template <int kCols, int kZ, bool kF16>
-__global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_kernel(const MergeParams p, const int groups)
+__global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const MergeParams p, const int groups)
 {
-    constexpr int kRows = kMergeThreads / (kCols * kZ);
-    const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kCols, z = threadIdx.x / (kRows * kCols);
+    constexpr int kRows = merge_rows(kCols, kZ), kWide = merge_wide(kZ), kPart = kCols / kWide;
+    const int row = threadIdx.x % kRows, col4 = threadIdx.x / kRows % kPart, z = threadIdx.x / (kRows * kPart);
     const int R = p.G * p.T, Hkv = p.Hq / p.G, h = blockIdx.y;
     // a sequence's rows take `groups` CTAs, or, if 0, a CTA has those of several
     const int several = groups ? 1 : kRows / R, sub = groups ? 0 : p.by_r.quotient(row);
@@ -872,11 +876,12 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_ke
 
     // A batch of states at a time, their LSEs and outputs loaded together; the
     // sums follow the largest LSE so far.
-    // (kZ = 1 is for many rows of few states: more CTAs an SM, smaller batches)
     constexpr int kBatch = kZ == 1 ? 2 : 4;
-    const int c = blockIdx.z * kCols + col4;
+    const int c = blockIdx.z * kCols + col4;        // and every kPart-th
     float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[kWide];
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!skip && c < p.D / 4) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -886,14 +891,16 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_ke
             const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.slot_rows + at[s];
             for (int i = z; i < x[s].count; i += kBatch * kZ) {
                 float y[kBatch];
-                float4 v[kBatch];
+                float4 v[kBatch][kWide];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     y[j] = -INFINITY;
-                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i + j * kZ < x[s].count) {
-                        y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
-                        v[j] = o[(i + j * kZ) * step];
+                    const bool is = i + j * kZ < x[s].count;
+                    if (is) y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
+#pragma unroll
+                    for (int e = 0; e < kWide; ++e) {
+                        v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (is && c + e * kPart < p.D / 4) v[j][e] = o[(i + j * kZ) * step + e * kPart * src.slot_rows];
                     }
                 }
                 float next = top;
@@ -903,18 +910,24 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_ke
                 const float f = ptx::ex2_approx(top - ref);
                 top = next;
                 sum *= f;
-                acc.x *= f;
-                acc.y *= f;
-                acc.z *= f;
-                acc.w *= f;
+#pragma unroll
+                for (int e = 0; e < kWide; ++e) {
+                    acc[e].x *= f;
+                    acc[e].y *= f;
+                    acc[e].z *= f;
+                    acc[e].w *= f;
+                }
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const float w = ptx::ex2_approx(y[j] - ref);
                     sum += w;
-                    acc.x = fmaf(w, v[j].x, acc.x);
-                    acc.y = fmaf(w, v[j].y, acc.y);
-                    acc.z = fmaf(w, v[j].z, acc.z);
-                    acc.w = fmaf(w, v[j].w, acc.w);
+#pragma unroll
+                    for (int e = 0; e < kWide; ++e) {
+                        acc[e].x = fmaf(w, v[j][e].x, acc[e].x);
+                        acc[e].y = fmaf(w, v[j][e].y, acc[e].y);
+                        acc[e].z = fmaf(w, v[j][e].z, acc[e].z);
+                        acc[e].w = fmaf(w, v[j][e].w, acc[e].w);
+                    }
                 }
             }
         }
@@ -923,7 +936,7 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_ke
         __shared__ float2 s_stat[kMergeThreads];
         __shared__ float4 s_acc[kMergeThreads];
         s_stat[threadIdx.x] = make_float2(top, sum);
-        s_acc[threadIdx.x] = acc;
+        s_acc[threadIdx.x] = acc[0];
         __syncthreads();
         if (z != 0) return;
         float2 st[kZ];
@@ -933,31 +946,36 @@ __global__ void __launch_bounds__(kMergeThreads, kZ == 1 ? 5 : 4) paged_merge_ke
         for (int j = 1; j < kZ; ++j) top = fmaxf(top, st[j].x);
         const float ref = top == -INFINITY ? 0.f : top;
         sum = 0.f;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < kZ; ++j) {
             const float w = ptx::ex2_approx(st[j].x - ref);
             const float4 v = s_acc[threadIdx.x + j * kRows * kCols];
             sum = fmaf(w, st[j].y, sum);
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+            acc[0].x = fmaf(w, v.x, acc[0].x);
+            acc[0].y = fmaf(w, v.y, acc[0].y);
+            acc[0].z = fmaf(w, v.z, acc[0].z);
+            acc[0].w = fmaf(w, v.w, acc[0].w);
         }
     }
     if (skip || c >= p.D / 4) return;
     const bool empty = sum == 0.f;
     const float inv = empty ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2] + 4 * c) =
-        empty ? make_uint2(0u, 0u)
-              : make_uint2(ptx::pack16x2<kF16>(acc.x * inv, acc.y * inv), ptx::pack16x2<kF16>(acc.z * inv, acc.w * inv));
+    uint16_t *dst = p.o + b * p.o_s[0] + hq * p.o_s[1] + t * p.o_s[2];
+#pragma unroll
+    for (int e = 0; e < kWide; ++e)
+        if (c + e * kPart < p.D / 4)
+            *reinterpret_cast<uint2 *>(dst + 4 * (c + e * kPart)) =
+                empty ? make_uint2(0u, 0u)
+                      : make_uint2(ptx::pack16x2<kF16>(acc[e].x * inv, acc[e].y * inv),
+                                   ptx::pack16x2<kF16>(acc[e].z * inv, acc[e].w * inv));
     if (p.lse && c == 0) p.lse[((int64_t)b * p.Hq + hq) * p.T + t] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int kCols, int kZ>
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream)
 {
-    constexpr int kRows = kMergeThreads / (kCols * kZ);
+    constexpr int kRows = merge_rows(kCols, kZ);
     const int R = p.G * p.T, groups = 2 * R <= kRows ? 0 : (R + kRows - 1) / kRows;
     const int blocks = groups ? p.B * groups : (p.B + kRows / R - 1) / (kRows / R);
     const dim3 grid((unsigned)blocks, (unsigned)(p.Hq / p.G), (unsigned)((p.D / 4 + kCols - 1) / kCols));
@@ -1068,7 +1086,7 @@ cudaError_t launch_paged_merge(const MergeParams &p, int states, int sms, cudaSt
     // or more, while the launch stays within a wave of CTAs.
     const int cols = p.D <= 64 ? 16 : 32;
     const auto ctas = [&](int z, int c) {
-        const int rows = kMergeThreads / (c * z);
+        const int rows = merge_rows(c, z);
         const int64_t R = p.G * p.T;
         return (2 * R <= rows ? (p.B + rows / R - 1) / (rows / R) : p.B * ((R + rows - 1) / rows)) * (p.Hq / p.G) *
                ((p.D / 4 + c - 1) / c);
