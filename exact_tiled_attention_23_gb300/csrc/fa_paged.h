@@ -103,8 +103,10 @@ struct Beside {
 constexpr int kRowsTile = 1, kBlocksTile = 5;
 
 // Own chunks and tiles (a chunk has 8 KB of keys and values at D = 64 and 128)
-// that cost an SM as much time as one block.
-constexpr int kBlockCost = 10;
+// that cost an SM as much time as one block.  Geometric mean of ten shapes (32 to
+// 256 sequences of 100 to 4000 keys at most, prefixes of 1000 to 30000): 8: 47.2 us,
+// 10: 45.0, 12: 44.1, 14: 44.3, 16: 45.6.
+constexpr int kBlockCost = 12;
 
 // SMs for the prefix beside `own` chunks and tiles of the sequences' own keys.
 #ifdef __CUDACC__
