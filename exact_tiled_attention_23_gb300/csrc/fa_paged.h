@@ -104,9 +104,10 @@ constexpr int kRowsTile = 1, kBlocksTile = 5;
 
 // Own chunks and tiles (a chunk has 8 KB of keys and values at D = 64 and 128)
 // that cost an SM as much time as one block.  Geometric mean of ten shapes (32 to
-// 256 sequences of 100 to 4000 keys at most, prefixes of 1000 to 30000): 8: 47.2 us,
-// 10: 45.0, 12: 44.1, 14: 44.3, 16: 45.6.
-constexpr int kBlockCost = 12;
+// 256 sequences of 100 to 4000 keys at most, prefixes of 1000 to 30000), with cold
+// caches and warm: 8: 60.0 and 47.2 us, 10: 58.6 and 45.0, 12: 58.9 and 44.1, 13:
+// 59.6 and 44.6.
+constexpr int kBlockCost = 10;
 
 // SMs for the prefix beside `own` chunks and tiles of the sequences' own keys.
 #ifdef __CUDACC__
