@@ -1059,8 +1059,10 @@ int paged_teams_at_once(int device, int team)
         cfg.numAttrs = 1;
         int clusters = 0;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess)
-            return 0;
+            cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();               // the line serves every call
+            clusters = 0;
+        }
         n.store(1 + clusters, std::memory_order_relaxed);
     }
     return n.load(std::memory_order_relaxed) - 1;
