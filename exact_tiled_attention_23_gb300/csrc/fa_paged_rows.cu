@@ -26,8 +26,9 @@
 //     would have to multiply 128 rows whatever the tile holds, and its rate is
 //     not what bounds this kernel;
 //   * each weight p is split into two 16-bit numbers, p = hi + lo with an error
-//     of 2^-16 p (fp16: 2^-22), and V is multiplied by both: the products are
-//     not the bound, and the output keeps fp32's error until it is rounded.
+//     of 2^-16 p (fp16: 2^-22 p, or 2^-37 of the row's largest weight where that
+//     is more, see kLift), and V is multiplied by both: the products are not the
+//     bound.
 //
 // Measured (D = 128, 8 key heads of 4 queries, bf16): a token of 64 sequences of
 // up to 8191 keys, 1.07 GB, 165 us, 6.5 TB/s (a copy: 6.8); of one sequence of
@@ -53,6 +54,16 @@ __device__ uint32_t g_status_paged_rows;
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// A row's weights are p = 2^(s - m).  m is raised, and O rescaled, only where a
+// score lies 2^(kLift + kRise) above it, to 2^kLift below the largest one then.
+// bf16 has the exponents of fp32.  fp16 numbers are multiples of 2^-24, so hi +
+// lo may be off by 2^-25 whatever p is: weights of up to 2^15 put that 2^-37 or
+// more below the row's largest.  (At m = the largest, a first key that draws the
+// attention lost the others: 8192 keys that share 0.5 % of the weight came out 2.6 %
+// off.)
+template <bool kF16> constexpr float kLift = kF16 ? 12.f : 0.f;
+template <bool kF16> constexpr float kRise = kF16 ? 3.f : 8.f;
 
 // kTeam: all warps of a cluster work on one tile and join it in shared memory
 // (below); else every warp has a piece of the line.
@@ -470,9 +481,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                         mx *= p.scale_log2;
-                        // (as below: the reference follows only rises of 2^8)
-                        if (__any_sync(0xffffffffu, mx > m[r] + 8.f)) {
-                            const float m_new = fmaxf(m[r], mx);
+                        if (__any_sync(0xffffffffu, mx > m[r] + (kLift<kF16> + kRise<kF16>))) {
+                            const float m_new = fmaxf(m[r], mx - kLift<kF16>);
                             const float alpha = ptx::ex2_approx(m[r] - (m_new == -INFINITY ? 0.f : m_new));
                             l[r] *= alpha;
 #pragma unroll
@@ -697,12 +707,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             for (int n = 1; n < KS / 8; ++n) mx = ptx::max3(mx, s[i][n][2 * r], s[i][n][2 * r + 1]);
                             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                            // The reference follows the largest score only when that
-                            // is 2^8 above it: weights stay at most 256, and O is
-                            // rescaled rarely.
                             mx *= p.scale_log2;
-                            if (__any_sync(0xffffffffu, mx > mr + 8.f)) {
-                                const float m_new = fmaxf(mr, mx), ref = m_new == -INFINITY ? 0.f : m_new;
+                            if (__any_sync(0xffffffffu, mx > mr + (kLift<kF16> + kRise<kF16>))) {
+                                const float m_new = fmaxf(mr, mx - kLift<kF16>), ref = m_new == -INFINITY ? 0.f : m_new;
                                 const float alpha = ptx::ex2_approx(mr - ref);
                                 lr *= alpha;
 #pragma unroll
