@@ -44,12 +44,14 @@ constexpr float kLazyLimitF16 = 32768.f;
 
 // D: number of fp32 O columns in TMEM for this row; kF16: P is fp16 (else
 // bf16); kCols: scores per key block (128, or 64 when two threads share a row
-// and each keeps its own m_ref, l, l_o and O).
-template <int D, bool kF16, int kCols = 128>
+// and each keeps its own m_ref, l, l_o and O); kLift: powers of 2 that m_ref is
+// set below the largest score, for fp16 P, whose smallest step is 2^-24.
+template <int D, bool kF16, int kCols = 128, int kLift = 0>
 struct OnlineRow {
     static_assert(kCols == 64 || kCols == 128, "scores per block");
+    static_assert(!kF16 || (kCols << kLift) <= 32768, "a block's sum of weights below the limit");
     static constexpr int kC = kCols / 32;      // 32-score chunks
-    float m_ref = -INFINITY;   // reference max of scale*log2e*S: a lower bound of the running max
+    float m_ref = -INFINITY;   // reference of scale*log2e*S: kLift below a lower bound of the running max
     float l = 0.f;             // running sum of p against m_ref (fp32 p): the LSE
     float l_o = 0.f;           // running sum of the 16-bit rounded P: O's normaliser
 
@@ -75,7 +77,9 @@ struct OnlineRow {
         for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], u2f(s[kC - 1][24 + a]));
         const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
                                fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_new = fmaxf(m_ref, mx * sl2);
+        float top = mx * sl2;
+        if constexpr (kLift > 0) top -= (float)kLift;
+        const float m_new = fmaxf(m_ref, top);
         const float alpha = (m_ref == -INFINITY) ? 0.f : ptx::ex2_approx(m_ref - m_new);
         if (o_live && __any_sync(0xffffffffu, alpha != 1.f)) {
             before_o_touch();

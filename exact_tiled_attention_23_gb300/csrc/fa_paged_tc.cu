@@ -66,6 +66,11 @@ constexpr uint32_t kColS = 0;             // S [0,128)
 constexpr uint32_t kColP = 128;           // P tiles [128,192), [192,256)
 constexpr uint32_t kColO = 256;           // O_A and O_B, D columns each
 constexpr float kLn2 = 0.69314718055994530942f;
+// fp16 weights are multiples of 2^-24.  Against a reference 2^7 below the largest
+// score a weight is off by 2^-32 of the row's largest (against the largest itself,
+// by 2^-25: 8192 keys with 0.5 % of the weight came out 1.3 % off), and 64 weights
+// as large as that still stay below the limit of a block's sum.
+constexpr int kLiftF16 = 7;
 
 template <int D>
 struct TcLayout {
@@ -424,7 +429,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // not see; a tile's first row sees the fewest.
             const int least = min(walk.u.len, line.masked ? walk.u.len - p.T + p.by_g.quotient(row0) + 1 : walk.u.len);
             const int t_mask = t + max(0, least) / BN - walk.u.c;
-            OnlineRow<D, kF16, kHalf> st;
+            OnlineRow<D, kF16, kHalf, kF16 ? kLiftF16 : 0> st;
             for (int j = 0; j < count; ++j, ++t) {
                 const int buf = t & 1;
                 const uint32_t tP = tmem + lane_off + Lay::col_p(buf, h);

@@ -13,8 +13,9 @@ pytestmark = pytest.mark.gpu
 
 BF16, F16 = torch.bfloat16, torch.float16
 
-# fp16: a row's largest weight is at least 2^LIFT in the row kernel's units
-LIFT = 12
+# fp16: a row's largest weight is at least 2^LIFT in the row kernel's units, and
+# 2^LIFT_TILES in the tensor-core kernel's
+LIFT, LIFT_TILES = 12, 7
 
 # sequences, keys of each (all share their pages), how far the first key lies
 # above the others in powers of 2, query tokens, D, page
@@ -68,3 +69,14 @@ def check(B, n, gap, T, D, page, dtype, one_number, lift):
 @pytest.mark.parametrize("B,n,gap,T,D,page", ROWS)
 def test_rows_keep_small_weights(B, n, gap, T, D, page, dtype):
     check(B, n, gap, T, D, page, dtype, False, LIFT)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B,n,gap,T,D,page", [
+    (256, 8192, 20.5, 40, 64, 16),         # a CTA has whole tiles
+    (256, 8192, 23.6, 40, 128, 16),
+    (128, 8192, 23.6, 32, 96, 64),
+    (1, 131072, 24.4, 40, 128, 16),        # a tile is cut among all CTAs
+])
+def test_tiles_keep_small_weights(B, n, gap, T, D, page, dtype):
+    check(B, n, gap, T, D, page, dtype, True, LIFT_TILES)
