@@ -426,6 +426,18 @@ def backward(q, k, v, o, do, lse, causal: bool = True, scale=None, kv_len=None, 
 
 
 # ---------------------------------------------------------- paged cache
+def _fixed(name, doc):
+    """A property of PagedKV whose value does not change.  (`cache.seq_len += 1`
+    updates the tensor in place and then assigns the same one.)"""
+    def get(self):
+        return self.__dict__["_" + name]
+
+    def put(self, value):
+        if value is not get(self):
+            raise AttributeError(f"PagedKV.{name} cannot be replaced: update its contents in place or make a new PagedKV")
+    return property(get, put, doc=doc)
+
+
 class PagedKV:
     """A paged key/value cache: a pool of pages and the pages of each sequence.
 
@@ -434,7 +446,10 @@ class PagedKV:
     [pages, page_size, Hkv, D] pool is passed as its transpose(1, 2)).
     block_table: int32 [B, W], the pages of each sequence in order.  seq_len:
     int32 [B], keys per sequence.  The caller updates the contents of both in
-    place; the object checks the tensors once and keeps them alive.
+    place (cache.seq_len += 1); the object checks the tensors once and keeps
+    them alive.  Another tensor in the place of one of them needs a new PagedKV:
+    assigning one raises, and so does a call after a tensor has been given other
+    memory (resize_, .data).
 
     Calls on the default stream, which run one after another, share a workspace
     of up to 32 MB that the object keeps.
@@ -458,16 +473,30 @@ class PagedKV:
             raise ValueError("seq_len must be a contiguous int32 tensor with B entries")
         if not k_cache.is_cuda or any(x.device != k_cache.device for x in (v_cache, block_table, seq_len)):
             raise ValueError("the caches, block_table and seq_len must be CUDA tensors of one device")
-        self.k_cache, self.v_cache, self.block_table, self.seq_len = k_cache, v_cache, block_table, seq_len
+        self._k_cache, self._v_cache, self._block_table, self._seq_len = k_cache, v_cache, block_table, seq_len
         pages, Hkv, page_size, D = k_cache.shape
-        self.batch, self.Hkv, self.D, self.dtype, self.device = B, Hkv, D, k_cache.dtype, k_cache.device
+        self._batch, self._Hkv, self._D, self._dtype, self._device = B, Hkv, D, k_cache.dtype, k_cache.device
         sp, sh, ss, _ = k_cache.stride()
         # the stride of a dimension of one entry is never followed
-        self.c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
-                             ss if page_size > 1 else 0, pages, page_size, Hkv, D, block_table.data_ptr(),
-                             block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
-        self._native = _binding().cache(ctypes.addressof(self.c), B, k_cache.dtype == torch.float16,
-                                        k_cache.get_device())
+        self._c = fa_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), sp if pages > 1 else 0, sh if Hkv > 1 else 0,
+                              ss if page_size > 1 else 0, pages, page_size, Hkv, D, block_table.data_ptr(),
+                              block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
+        self._native = _binding().cache(ctypes.addressof(self._c), k_cache, v_cache, block_table, seq_len)
+
+    k_cache = _fixed("k_cache", "The pool of keys.")
+    v_cache = _fixed("v_cache", "The pool of values.")
+    block_table = _fixed("block_table", "The pages of each sequence.")
+    seq_len = _fixed("seq_len", "Keys per sequence.")
+    batch = _fixed("batch", "Sequences.")
+    Hkv = _fixed("Hkv", "Key heads.")
+    D = _fixed("D", "Head dimension.")
+    dtype = _fixed("dtype", "Of the pools.")
+    device = _fixed("device", "Of all tensors.")
+
+    @property
+    def c(self):
+        """The cache as the C entry points take it (a copy)."""
+        return fa_paged_kv.from_buffer_copy(self._c)
 
     def workspace_bytes(self, Hq: int, T: int, prefix_len: int = 0) -> int:
         """Bytes of workspace that forward_paged() (forward_shared_prefix()
@@ -475,7 +504,7 @@ class PagedKV:
         import torch
 
         with torch.cuda.device(self.device):
-            return fa_fwd_shared_prefix_workspace_bytes(self.c, prefix_len, self.batch, Hq, T)
+            return fa_fwd_shared_prefix_workspace_bytes(self._c, prefix_len, self.batch, Hq, T)
 
 
 _BINDING = None

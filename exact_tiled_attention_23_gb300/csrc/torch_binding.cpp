@@ -43,8 +43,17 @@ struct Cache {
     int64_t B;
     at::ScalarType dtype;
     c10::DeviceIndex device;
+    at::Tensor k, v, table, seq_len;       // what c points to
     std::mutex mutex;        // keeps the launches of two host threads' calls apart
     at::Tensor workspace;
+
+    // Whether the tensors still have the memory that c points to (resize_() and
+    // assignments to .data give a tensor another).
+    bool in_place() const
+    {
+        return k.const_data_ptr() == c.k && v.const_data_ptr() == c.v && table.const_data_ptr() == c.table &&
+               seq_len.const_data_ptr() == c.seq_len;
+    }
 };
 
 constexpr const char *kCapsule = "fa_torch.cache";
@@ -128,20 +137,36 @@ bool vector(PyObject *object, const char *text, at::ScalarType type, const Cache
     return true;
 }
 
-Cache *cache_of(PyObject *capsule) { return static_cast<Cache *>(PyCapsule_GetPointer(capsule, kCapsule)); }
+Cache *cache_of(PyObject *capsule)
+{
+    Cache *cache = static_cast<Cache *>(PyCapsule_GetPointer(capsule, kCapsule));
+    if (cache && !cache->in_place()) {
+        value_error("a tensor of the cache has other memory than when the PagedKV was made: make a new one");
+        return nullptr;
+    }
+    return cache;
+}
 
-// cache(address of an fa_paged_kv, B, f16, device index) -> capsule
+// cache(address of an fa_paged_kv, k, v, table, seq_len), the four tensors that
+// it points to -> capsule, which keeps them
 PyObject *new_cache(PyObject *, PyObject *args)
 {
+    HANDLE_TH_ERRORS
     unsigned long long address;
-    long long B;
-    int f16, device;
-    if (!PyArg_ParseTuple(args, "KLpi", &address, &B, &f16, &device)) return nullptr;
-    Cache *cache = new Cache{*reinterpret_cast<const fa_paged_kv *>(address), B,
-                             f16 ? at::ScalarType::Half : at::ScalarType::BFloat16, (c10::DeviceIndex)device, {}, {}};
+    PyObject *x[4];
+    if (!PyArg_ParseTuple(args, "KOOOO", &address, &x[0], &x[1], &x[2], &x[3])) return nullptr;
+    for (PyObject *o : x)
+        if (!THPVariable_Check(o)) {
+            PyErr_SetString(PyExc_TypeError, "the caches, block_table and seq_len must be tensors");
+            return nullptr;
+        }
+    const at::Tensor &k = THPVariable_Unpack(x[0]), &seq_len = THPVariable_Unpack(x[3]);
+    Cache *cache = new Cache{*reinterpret_cast<const fa_paged_kv *>(address), seq_len.numel(), k.scalar_type(),
+                             k.get_device(), k, THPVariable_Unpack(x[1]), THPVariable_Unpack(x[2]), seq_len, {}, {}};
     PyObject *capsule = PyCapsule_New(cache, kCapsule, free_cache);
     if (!capsule) delete cache;
     return capsule;
+    END_HANDLE_TH_ERRORS
 }
 
 // kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out) ->
