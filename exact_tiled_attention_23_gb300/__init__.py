@@ -554,8 +554,9 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
     counts the new tokens.  inv_freq: float32 CUDA tensor of the angles per
     position, one per pair (2 * numel <= D elements of a head turn), or None
     for no rotation; pairs are (p, p + numel), or neighbours if interleaved.
-    position_offset: position of a sequence's first key.  Runs asynchronously
-    on `stream` (default: torch's current stream of the cache's device).
+    position_offset: position of a sequence's first key.  q_out: where to put
+    the queries, q itself for in place.  Runs asynchronously on `stream`
+    (default: torch's current stream of the cache's device).
     """
     if stream is not None:
         with _stream_context(cache, stream):

@@ -151,40 +151,55 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
                 *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
             }
         }
-    } else {
+    } else if constexpr (kMode == kNeighbours) {
         for (int e = threadIdx.x; e < (k_heads + q_heads) * units; e += kThreads) {
             const int head = e / units, u = e % units;
-            const uint16_t *src = source(head);
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + u * 8);
+            const uint4 w = *reinterpret_cast<const uint4 *>(source(head) + u * 8);
             uint4 out = w;
             if (u * 8 < p.rot) {
                 float x[8], r[8];
                 widen8<kF16>(w, x);
-                if constexpr (kMode == kNeighbours) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool in = u * 8 + 2 * j < p.rot;
-                        const float2 a = in ? cs[u * 4 + j] : make_float2(1.f, 0.f);
-                        r[2 * j] = in ? x[2 * j] * a.x - x[2 * j + 1] * a.y : x[2 * j];
-                        r[2 * j + 1] = in ? x[2 * j + 1] * a.x + x[2 * j] * a.y : x[2 * j + 1];
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int d = u * 8 + j;
-                        r[j] = x[j];
-                        if (d < half) {
-                            const float y = widen1<kF16>(src[d + half]);
-                            r[j] = x[j] * cs[d].x - y * cs[d].y;
-                        } else if (d < p.rot) {
-                            const float y = widen1<kF16>(src[d - half]);
-                            r[j] = x[j] * cs[d - half].x + y * cs[d - half].y;
-                        }
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = u * 8 + 2 * j < p.rot;
+                    const float2 a = in ? cs[u * 4 + j] : make_float2(1.f, 0.f);
+                    r[2 * j] = in ? x[2 * j] * a.x - x[2 * j + 1] * a.y : x[2 * j];
+                    r[2 * j + 1] = in ? x[2 * j + 1] * a.x + x[2 * j] * a.y : x[2 * j + 1];
                 }
                 out = narrow8<kF16>(r);
             }
             *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
+        }
+    } else {
+        // The halves of a pair are other threads' elements, which q_out = q
+        // overwrites: whole heads at a time, all read before any is written.
+        const int per = kThreads / units, mine = threadIdx.x / units, u = threadIdx.x % units;
+        for (int first = 0; first < k_heads + q_heads; first += per) {
+            const int head = first + mine;
+            const bool on = mine < per && head < k_heads + q_heads;
+            uint4 out = make_uint4(0u, 0u, 0u, 0u);
+            if (on) {
+                const uint16_t *src = source(head);
+                out = *reinterpret_cast<const uint4 *>(src + u * 8);
+                if (u * 8 < p.rot) {
+                    float r[8];
+                    widen8<kF16>(out, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int d = u * 8 + j;
+                        if (d < half) {
+                            const float y = widen1<kF16>(src[d + half]);
+                            r[j] = r[j] * cs[d].x - y * cs[d].y;
+                        } else if (d < p.rot) {
+                            const float y = widen1<kF16>(src[d - half]);
+                            r[j] = r[j] * cs[d - half].x + y * cs[d - half].y;
+                        }
+                    }
+                    out = narrow8<kF16>(r);
+                }
+            }
+            __syncthreads();
+            if (on) *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
         }
     }
 }

@@ -76,6 +76,13 @@ void strides_of(int64_t (&s)[3], const fa_rows &r)
     s[2] = r.stride_n;
 }
 
+// Whether rows of one address are the same rows.
+bool same_rows(const fa_rows &x, const fa_rows &y, int B, int H, int T)
+{
+    return x.ptr == y.ptr && (B == 1 || x.stride_b == y.stride_b) && (H == 1 || x.stride_h == y.stride_h) &&
+           (T == 1 || x.stride_n == y.stride_n);
+}
+
 size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Most stacked rows that the row kernel takes where the tensor-core kernel could.
@@ -347,6 +354,8 @@ fa_status fa_kv_append(const fa_paged_kv *cache, const fa_rows *K, const fa_rows
     if (!rows_ok(K, B, cache->Hkv, T, D, false) || !rows_ok(V, B, cache->Hkv, T, D, false)) return FA_ERR_INVALID_ARG;
     const bool queries = Q && Hq > 0;
     if (queries && (!rows_ok(Q, B, Hq, T, D, false) || !rows_ok(Q_out, B, Hq, T, D, true))) return FA_ERR_INVALID_ARG;
+    if (queries && Q_out->ptr == Q->ptr && !same_rows(*Q, *Q_out, B, Hq, T)) return FA_ERR_INVALID_ARG;
+    if (queries && (Q_out->ptr == K->ptr || Q_out->ptr == V->ptr)) return FA_ERR_INVALID_ARG;
     if ((int64_t)(queries ? Hq : 0) + cache->Hkv > INT32_MAX / D) return FA_ERR_INVALID_ARG;
 
     fa::AppendParams p{};

@@ -378,7 +378,8 @@ typedef struct fa_rows {
  *
  *   K, V             [B, Hkv, T, D] new keys and values.
  *   Q, Q_out         [B, Hq, T, D] queries and where to put them rotated, or
- *                    Q = NULL for none.  Q_out may not overlap an input.
+ *                    Q = NULL for none.  Q_out may be Q (same address and
+ *                    strides) and may not overlap an input otherwise.
  *   inv_freq         float [rot_dim / 2] device array, each in [-65536, 65536]
  *                    (others give NaN).  NULL with rot_dim = 0: no rotation.
  *   rot_dim          even, 0 <= rot_dim <= D.
