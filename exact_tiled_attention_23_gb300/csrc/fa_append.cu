@@ -10,8 +10,10 @@
 // A far position times a frequency loses its angle in fp32 (a product of 10^5
 // is good to 2^-7 radians), so the angle is kept as a fraction of a turn in 64
 // bits: inv_freq[p] / 2pi as a fixed-point number F of 2^-64 turns, and n * F
-// modulo 2^64 drops whole turns exactly.  F is good to 2^-61 of itself, so the
-// angle is good to 2^-30 turns at n = 2^31, and its fp32 form decides.
+// modulo 2^64 drops whole turns exactly.  F comes from 128 bits of 1 / 2pi, so it
+// is off by less than its last bit for every frequency up to 2^16, and the angle
+// by n 2^-64 turns: 2^-33 at n = 2^31, where the fp32 form's 2^-26 decides, and
+// 2^-24 at the farthest position, 2^40 + 2^31.
 //
 // Bound by memory: every value is read once and written once, whole 16-byte units
 // at a time.  One CTA per token, so that a token's angles are computed once for all
@@ -27,8 +29,8 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// 2^64 / (2 pi): the bits of 1 / (2 pi) after the binary point.
-constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;
+// 2^128 / (2 pi): the bits of 1 / (2 pi) after the binary point.
+constexpr uint64_t kInvTwoPiHi = 0x28be60db9391054aull, kInvTwoPiLo = 0x7f09d5f47d4d3770ull;
 
 // cos and sin of n * f radians, for |f| <= 65536.
 __device__ __forceinline__ float2 turn(int64_t n, float f)
@@ -39,7 +41,9 @@ __device__ __forceinline__ float2 turn(int64_t n, float f)
     const int e = (int)(bits >> 23);                       // a = m * 2^(e - 150)
     const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : 0u;
     const int shift = 150 - e;                             // >= 6 for a <= 2^16
-    const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+    // bits 64 .. 191 of m * (2^128 / 2 pi)
+    const uint64_t part = m * kInvTwoPiHi, lo = part + __umul64hi(m, kInvTwoPiLo);
+    const uint64_t hi = __umul64hi(m, kInvTwoPiHi) + (lo < part ? 1 : 0);
     const uint64_t F = shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : shift < 128 ? hi >> (shift - 64) : 0ull;
     const uint64_t frac = (uint64_t)n * F;                 // modulo one turn
     // to [-1/2, 1/2) turns; sincospif takes half turns

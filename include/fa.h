@@ -373,8 +373,9 @@ typedef struct fa_rows {
  *
  * The first rot_dim elements of a head turn in pairs: pair p, of elements p
  * and p + rot_dim / 2 (2p and 2p + 1 if interleaved), by the angle n *
- * inv_freq[p].  The angle is kept modulo one turn in 64-bit fixed point, so
- * far positions lose nothing; values are fp32 until they are rounded once.
+ * inv_freq[p].  The angle is kept modulo one turn in 64-bit fixed point, good
+ * to n 2^-64 turns (2^-24 at the farthest position); its sine and cosine and the
+ * products are fp32 until they are rounded once.
  *
  *   K, V             [B, Hkv, T, D] new keys and values.
  *   Q, Q_out         [B, Hq, T, D] queries and where to put them rotated, or
