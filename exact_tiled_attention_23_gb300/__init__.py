@@ -554,7 +554,9 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
     counts the new tokens.  inv_freq: float32 CUDA tensor of the angles per
     position, one per pair (2 * numel <= D elements of a head turn), or None
     for no rotation; pairs are (p, p + numel), or neighbours if interleaved.
-    position_offset: position of a sequence's first key.  q_out: where to put
+    position_offset: position of a sequence's first key; behind a shared prefix
+    (forward_shared_prefix()) this is the prefix's length, since seq_len counts
+    only the keys that follow it.  q_out: where to put
     the queries, q itself for in place.  Runs asynchronously on `stream`
     (default: torch's current stream of the cache's device).
     """
@@ -592,8 +594,9 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     """forward_paged() for sequences that begin with the same prefix_len keys.
 
     prefix_table: int32 CUDA tensor with the prefix's pages in order (of the
-    same pool); the cache's block_table and seq_len give what follows it.  The
-    prefix is read once for the whole batch.  The workspace takes
+    same pool); the cache's block_table and seq_len give what follows it, so the
+    queries and the own keys are turned by kv_append() with position_offset =
+    prefix_len.  The prefix is read once for the whole batch.  The workspace takes
     cache.workspace_bytes(Hq, T, prefix_len) bytes.
     """
     if stream is not None:

@@ -384,8 +384,8 @@ typedef struct fa_rows {
  *   inv_freq         float [rot_dim / 2] device array, each in [-65536, 65536]
  *                    (others give NaN).  NULL with rot_dim = 0: no rotation.
  *   rot_dim          even, 0 <= rot_dim <= D.
- *   position_offset  position of a sequence's first key, 0 .. 2^40 (the length
- *                    of a shared prefix, say).
+ *   position_offset  position of a sequence's first key, 0 .. 2^40: behind a
+ *                    shared prefix its length, which seq_len does not count.
  *   f16              elements are IEEE half (else bf16).
  *
  * Two tokens of one call that land on the same slot (tables that share a page
