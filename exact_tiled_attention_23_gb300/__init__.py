@@ -595,7 +595,7 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     """forward_paged() for sequences that begin with the same prefix_len keys.
 
     prefix_table: int32 CUDA tensor with the prefix's pages in order (of the
-    same pool); the cache's block_table and seq_len give what follows it, so the
+    same pool), or None where prefix_len is 0; the cache's block_table and seq_len give what follows it, so the
     queries and the own keys are turned by kv_append() with position_offset =
     prefix_len.  The prefix is read once for the whole batch.  The workspace takes
     cache.workspace_bytes(Hq, T, prefix_len) bytes.

@@ -243,16 +243,14 @@ PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         value_error("sizes must fit 32 bits");
         return nullptr;
     }
-    long long prefix = 0;
-    if (a[2] != Py_None) {
-        if (!vector(a[2], "prefix_table must be an int32 tensor of one dimension on the cache's device", at::kInt, *cache, pages))
-            return nullptr;
-        prefix = PyLong_AsLongLong(a[3]);
-        if (prefix == -1 && PyErr_Occurred()) return nullptr;
-        if (prefix < 0 || prefix > pages.numel() * cache->c.page_size || prefix > INT32_MAX) {
-            value_error("prefix_len must lie in [0, what prefix_table's pages hold]");
-            return nullptr;
-        }
+    if (a[2] != Py_None &&
+        !vector(a[2], "prefix_table must be an int32 tensor of one dimension on the cache's device", at::kInt, *cache, pages))
+        return nullptr;
+    const long long prefix = PyLong_AsLongLong(a[3]);
+    if (prefix == -1 && PyErr_Occurred()) return nullptr;
+    if (prefix < 0 || prefix > (pages.defined() ? pages.numel() * cache->c.page_size : 0) || prefix > INT32_MAX) {
+        value_error("prefix_len must lie in [0, what prefix_table's pages hold]");
+        return nullptr;
     }
     const int causal = PyObject_IsTrue(a[4]), return_lse = PyObject_IsTrue(a[8]);
     const double scale = a[5] == Py_None ? NAN : PyFloat_AsDouble(a[5]);

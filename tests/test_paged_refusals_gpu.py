@@ -1,0 +1,29 @@
+"""Calls of the paged-cache operators that have to be refused, or answered with nothing."""
+import pytest
+import torch
+
+import exact_tiled_attention_23_gb300 as fa
+from test_paged_gpu import BF16, Pool
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fa.build()
+    fa.load()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_prefix_without_its_pages_is_refused(T):
+    pool = Pool([50, 3], 2, 64, 16, BF16, seed=1, prefix=40)
+    cache, q = pool.gpu(), pool.queries(4, T).cuda()
+    with pytest.raises(ValueError, match="prefix_len must lie"):
+        fa.forward_shared_prefix(q, cache, None, 40)
+    with pytest.raises(ValueError, match="prefix_len must lie"):
+        fa.forward_shared_prefix(q, cache, pool.prefix_table[:0].cuda(), 1)
+    # no prefix at all: forward_paged()
+    want = fa.forward_paged(q, cache)
+    for none in (None, pool.prefix_table[:0].cuda(), pool.prefix_table.cuda()):
+        got = fa.forward_shared_prefix(q, cache, none, 0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
