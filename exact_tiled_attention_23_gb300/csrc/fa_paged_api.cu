@@ -42,8 +42,8 @@ fa_status check_cache(const fa_paged_kv *c, int B)
     if ((c->num_pages > 1 && c->stride_page < c->D) || (c->Hkv > 1 && c->stride_head < c->D) ||
         (c->page_size > 1 && c->stride_slot < c->D))
         return FA_ERR_INVALID_ARG;
-    if (!c->seq_len || !aligned(c->seq_len, 4)) return FA_ERR_INVALID_ARG;
-    if (c->table_width > 0 && (!c->table || !aligned(c->table, 4))) return FA_ERR_INVALID_ARG;
+    if ((B > 0 && !c->seq_len) || !aligned(c->seq_len, 4)) return FA_ERR_INVALID_ARG;
+    if ((B > 0 && c->table_width > 0 && !c->table) || !aligned(c->table, 4)) return FA_ERR_INVALID_ARG;
     if (B > 1 && c->table_stride < c->table_width) return FA_ERR_INVALID_ARG;
     if ((int64_t)c->table_width * c->page_size > kMostKeys) return FA_ERR_INVALID_ARG;
     return FA_OK;

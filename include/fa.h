@@ -350,7 +350,8 @@ typedef struct fa_paged_kv {
     const int32_t *table;        /* [B, table_width] page numbers, rows table_stride entries apart */
     int64_t table_stride;
     int table_width;             /* table_width * page_size <= 2^31 - 4096 (with a prefix: the sum) */
-    const int32_t *seq_len;      /* [B] keys per sequence, the call's own tokens included */
+    const int32_t *seq_len;      /* [B] keys per sequence, the call's own tokens included
+                                  * (seq_len and table may be NULL where B is 0) */
 } fa_paged_kv;
 
 /* A [B, H, N, D] array of 16-bit elements whose last dimension is contiguous:

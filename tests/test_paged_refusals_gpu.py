@@ -27,3 +27,17 @@ def test_a_prefix_without_its_pages_is_refused(T):
     for none in (None, pool.prefix_table[:0].cuda(), pool.prefix_table.cuda()):
         got = fa.forward_shared_prefix(q, cache, none, 0)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_batch_of_no_sequences():
+    pool = Pool([50, 3], 2, 64, 16, BF16, seed=2, prefix=40)
+    full = pool.gpu()
+    cache = fa.PagedKV(full.k_cache, full.v_cache, torch.empty((0, 7), dtype=torch.int32, device="cuda"),
+                       torch.empty(0, dtype=torch.int32, device="cuda"))
+    kept = full.k_cache.clone()
+    q, kv = (torch.empty((0, h, 3, 64), dtype=BF16, device="cuda") for h in (4, 2))
+    for o, lse in (fa.forward_paged(q, cache), fa.forward_shared_prefix(q, cache, pool.prefix_table.cuda(), 40)):
+        assert o.shape == (0, 4, 3, 64) and lse.shape == (0, 4, 3)
+    assert fa.kv_append(cache, kv, kv, q=q).shape == q.shape
+    torch.cuda.synchronize()
+    assert torch.equal(full.k_cache.view(torch.int16), kept.view(torch.int16))
