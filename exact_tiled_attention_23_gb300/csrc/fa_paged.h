@@ -57,7 +57,7 @@ struct AppendParams {
     int B, T, Hq, rot, interleaved, f16;
 };
 
-// Where a tile's partial states are.
+// Where a tile's partial states are: from which slot on, and how many.
 struct TileSlots {
     int first, count;
 };
@@ -69,9 +69,14 @@ struct TileSlots {
 // per lane stores and the merge loads whole lines), and base-2 log-sum-exps.
 // Tile i has the slots k + i of the pieces k that have some of its chunks.
 // (Along the line, k and i never fall and one of them grows from share to
-// share, so no two shares have one slot.)
+// share, so no two shares have one slot.)  Where there are more tiles than
+// pieces and a tile within one piece leaves no state, `pairs` is 1 and a piece
+// has two slots: 2k for the tile that continues in it, 2k + 1 for the one that
+// begins in it and ends in another.  (16 sequences of 4096 tokens, 32 heads of
+// 128: 20 MB, where a slot for every tile took 1.09 GB.)
 struct Partials {
     int slots;
+    int pairs;
     float *o;              // [slots][D / 4][slot_rows][4]
     float *lse;            // [slots][slot_rows]
     TileSlots *tile;       // [tiles in all], of tiles with at least one chunk
@@ -81,6 +86,20 @@ struct Partials {
     int stacked;           // 1: one list of tiles for all sequences (a shared prefix)
     int chunk;             // keys per chunk of the line
     int fixed_len;         // stacked: keys of the prefix
+#ifdef __CUDACC__
+    // What a tile's record says of piece `piece`, its first; the slot of its
+    // state from a piece (continued: from a chunk past its first on); and the
+    // slot of its state number i.
+    __device__ __forceinline__ int first_of(int piece, int at_tile) const { return pairs ? 2 * piece : piece + at_tile; }
+    __device__ __forceinline__ int slot_of(int piece, int at_tile, bool continued) const
+    {
+        return pairs ? 2 * piece + (continued ? 0 : 1) : piece + at_tile;
+    }
+    __device__ __forceinline__ int slot_at(int first, int i) const
+    {
+        return pairs ? first + 2 * i + (i == 0 ? 1 : 0) : first + i;
+    }
+#endif
 };
 
 // A shared prefix on the tensor cores beside the sequences' own keys in the

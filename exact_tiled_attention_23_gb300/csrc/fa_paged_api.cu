@@ -113,8 +113,9 @@ struct Plan {
     bool tc = false;        // the tensor-core kernel (else the row kernel)
     int box = 0;            // key rows per TMA box, 0: no TMA
 
-    // rows: stacked query rows per (sequence, key head); keys: most keys of a sequence
-    Plan(int nseq, const fa_paged_kv &c, int64_t rows, int64_t keys, bool stacked)
+    // rows: stacked query rows per (sequence, key head); keys: most keys of a
+    // sequence; joined: every tile leaves a state
+    Plan(int nseq, const fa_paged_kv &c, int64_t rows, int64_t keys, bool stacked, bool joined)
     {
         const int Hkv = c.Hkv, D = c.D;
         box = box_rows_of(c);
@@ -142,7 +143,8 @@ struct Plan {
         ctas = std::max<int64_t>(1, std::min(ctas, (chunks + each - 1) / each));
         pieces = ctas * each;
         part.slot_rows = (int)std::min<int64_t>(part.rows, tiles == 1 ? (tc ? 128 : rows) : part.rows);
-        const size_t slots = (size_t)(pieces + items);
+        part.pairs = !joined && items > pieces;
+        const size_t slots = (size_t)(part.pairs ? 2 * pieces : pieces + items);
         if (slots > INT32_MAX) {
             ok = false;
             return;
@@ -154,7 +156,7 @@ struct Plan {
     // Places the piece at `at`; returns its end.
     uint8_t *place(uint8_t *at, int D)
     {
-        const size_t slots = (size_t)(pieces + items);
+        const size_t slots = (size_t)part.slots;
         part.tile = reinterpret_cast<fa::TileSlots *>(at);
         at += round_up((size_t)items * sizeof(fa::TileSlots));
         part.lse = reinterpret_cast<float *>(at);
@@ -237,8 +239,8 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
     const int64_t own_keys = (int64_t)c->table_width * c->page_size;
     if (own_keys + prefix_len > kMostKeys) return FA_ERR_INVALID_ARG;
     const int G = Hq / c->Hkv;
-    Plan own(B, *c, (int64_t)G * T, own_keys, false);
-    Plan front(1, *c, (int64_t)G * T * B, prefix_len, true);
+    Plan own(B, *c, (int64_t)G * T, own_keys, false, prefix_len > 0);
+    Plan front(1, *c, (int64_t)G * T * B, prefix_len, true, true);
     if (!own.ok || (prefix_len > 0 && !front.ok)) return FA_ERR_INVALID_ARG;
     const size_t need = own.bytes + (prefix_len > 0 ? front.bytes : 0);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return FA_ERR_INVALID_ARG;
@@ -396,10 +398,10 @@ size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix
 {
     if (check_sizes(cache, B, Hq, T) != FA_OK || prefix_len < 0 || (int64_t)B * Hq * T == 0) return 0;
     const int G = Hq / cache->Hkv;
-    const Plan own(B, *cache, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, false);
+    const Plan own(B, *cache, (int64_t)G * T, (int64_t)cache->table_width * cache->page_size, false, prefix_len > 0);
     if (!own.ok || (int64_t)cache->table_width * cache->page_size + prefix_len > kMostKeys) return 0;
     if (prefix_len == 0) return own.bytes;
-    const Plan front(1, *cache, (int64_t)G * T * B, prefix_len, true);
+    const Plan front(1, *cache, (int64_t)G * T * B, prefix_len, true, true);
     return front.ok ? own.bytes + front.bytes : 0;
 }
 

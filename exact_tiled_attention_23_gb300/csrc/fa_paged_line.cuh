@@ -212,7 +212,7 @@ struct Line {
     __device__ __forceinline__ void record(const LineCursor &u, int piece, int before, int per) const
     {
         const int tile = u.g * p.c.Hkv + u.h;
-        p.part.tile[tile] = TileSlots{piece + tile, (before + start_of(u.n - 1)) / per + 1};
+        p.part.tile[tile] = TileSlots{p.part.first_of(piece, tile), (before + start_of(u.n - 1)) / per + 1};
     }
 };
 

@@ -551,7 +551,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
             // ---- the tile's state ----
             const bool direct = count == at.n && !p.joined;
-            const int64_t slot = (int64_t)piece + tile;
+            const int64_t slot = p.part.slot_of(piece, tile, at.c > 0);
             bool empty[2];
             float inv[2];
 #pragma unroll
@@ -754,7 +754,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
             // ---- the tile's state -------------------------------------------------
             const bool direct = count == at.n && !p.joined;
-            const int64_t slot = (int64_t)piece + tile;
+            const int64_t slot = p.part.slot_of(piece, tile, at.c > 0);
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
                 float sum = l[i];
@@ -874,7 +874,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
     for (int s = 0; s < 2; ++s) {
         // no read past the workspace, whatever a kernel that gave up has left
         x[s].first = min(max(x[s].first, 0), p.src[s].slots);
-        x[s].count = keys[s] > 0 ? min(x[s].count, p.src[s].slots - x[s].first) : 0;
+        x[s].count = keys[s] > 0 ? min(x[s].count, (p.src[s].slots - x[s].first) >> p.src[s].pairs) : 0;
     }
     // not a row, or one CTA had the whole tile and wrote the row itself
     const bool skip = !real || (!p.joined && x[0].count == 1);
@@ -893,9 +893,9 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const Partials &src = p.src[s];
-            const float *lse = src.lse + (int64_t)x[s].first * src.slot_rows + at[s];
+            const float *lse = src.lse + at[s];
             const int64_t step = (int64_t)(p.D / 4) * src.slot_rows;
-            const float4 *o = reinterpret_cast<const float4 *>(src.o) + x[s].first * step + (int64_t)c * src.slot_rows + at[s];
+            const float4 *o = reinterpret_cast<const float4 *>(src.o) + (int64_t)c * src.slot_rows + at[s];
             for (int i = z; i < x[s].count; i += kBatch * kZ) {
                 float y[kBatch];
                 float4 v[kBatch][kWide];
@@ -903,11 +903,12 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge_kernel(const Mer
                 for (int j = 0; j < kBatch; ++j) {
                     y[j] = -INFINITY;
                     const bool is = i + j * kZ < x[s].count;
-                    if (is) y[j] = lse[(int64_t)(i + j * kZ) * src.slot_rows];
+                    const int64_t slot = src.slot_at(x[s].first, i + j * kZ);
+                    if (is) y[j] = lse[slot * src.slot_rows];
 #pragma unroll
                     for (int e = 0; e < kWide; ++e) {
                         v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (is && c + e * kPart < p.D / 4) v[j][e] = o[(i + j * kZ) * step + e * kPart * src.slot_rows];
+                        if (is && c + e * kPart < p.D / 4) v[j][e] = o[slot * step + e * kPart * src.slot_rows];
                     }
                 }
                 float next = top;

@@ -561,7 +561,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
             // This thread writes columns [h*D/2, (h+1)*D/2) of its row.
             const bool direct = count == was.n && !p.joined;
-            const int64_t slot = (int64_t)blockIdx.x + was.g * p.c.Hkv + was.h;
+            const int64_t slot = p.part.slot_of((int)blockIdx.x, was.g * p.c.Hkv + was.h, was.c > 0);
             if (thread == 0 && was.c == 0) line.record(was, (int)blockIdx.x, used, per);
             used += line.start_of(was.c + count) - line.start_of(was.c);
             uint16_t *o_row = nullptr;
