@@ -116,9 +116,10 @@ struct Beside {
 };
 
 // What a tile costs beside its keys, in chunks of the row kernel (256 sequences of
-// 1 to 511 keys: 64 -> 57 us) and in blocks of the tensor-core kernel (64 sequences
-// behind a prefix of 16384 keys: 1 block 54.8 us, 3 53.8, 5 51.3, 8 51.3; 256 behind
-// 4097: 68.2, 65.2, 66.2, 69.0).
+// 1 to 511 keys: 64 -> 57 us) and in blocks of the tensor-core kernel (geometric
+// means in us of ten batches behind prefixes, the shapes at kBlockCost, and of six
+// batches of 16 to 1024 tokens over 1000 to 16384 keys: 1 block 48.1 and 112, 3
+// blocks 47.4 and 82.0, 5 blocks 46.8 and 79.0, 8 blocks 46.8 and 81.3).
 constexpr int kRowsTile = 1, kBlocksTile = 5;
 
 // Own chunks and tiles (a chunk has 8 KB of keys and values at D = 64 and 128)

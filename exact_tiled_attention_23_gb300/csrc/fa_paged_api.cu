@@ -86,6 +86,11 @@ bool same_rows(const fa_rows &x, const fa_rows &y, int B, int H, int T)
 size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Most stacked rows that the row kernel takes where the tensor-core kernel could.
+// Row kernel against tensor cores in us, geometric means of seven batches (1 to 64
+// sequences of 500 to 65536 keys, 1 or 8 key heads of 4 queries, bf16): D = 64: 16
+// rows 18 and 26, 32 rows 26.2 and 26.3, 36 rows 38 and 27; D = 128: 16 rows 32 and
+// 30, 20 to 32 rows 50 to 56 and 30 to 31, 36 rows 78 and 32.  At D = 128 and 17 to
+// 32 rows it is the weights of two 16-bit numbers that the row kernel is for.
 constexpr int64_t kMostRows = 32;
 
 // Key rows per TMA box of this pool: the largest power of two, 8 (the rows of a

@@ -297,9 +297,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         return x;
     };
     const uint32_t ring = s_base + Lay::kRingOff + warp * S * Lay::kStageBytes;
-    // Keys that one tile alone reads need not stay in the L2, where a prefix that
-    // other CTAs read again and again has its keys (256 sequences behind a prefix
-    // of 4097 keys: 82 -> 69 us).
+    // A sequence with one row tile has its keys read once, by that tile, unless
+    // another sequence's table has the same pages.  They leave the L2 first, and a
+    // prefix that other CTAs read again and again keeps its place (256 sequences
+    // behind a prefix of 4097 keys: 77 -> 66 us; 64 sequences of up to 8191 keys of
+    // their own: 169 -> 165).  Pages that tables share do not lose by it: 64
+    // sequences with 4096 keys in common, 89.6 -> 89.3, 16 with 32768, 166.6 ->
+    // 165.6, 256 with 1024, 95.8 -> 95.4.
     const uint64_t policy = kTma ? ptx::l2_policy(!kTeam && p.part.tiles == 1) : 0;
     int issued = 0;             // steps copied
     auto load = [&](int stage, const Place &x) {
