@@ -90,10 +90,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     ptx::wait_for_primary();
     const int64_t b = blockIdx.x / p.T;
     const int t = (int)(blockIdx.x % p.T);
-    const int64_t cap = (int64_t)p.c.table_width * p.c.page_size;
-    int64_t len = p.c.seq_len[b];
-    len = len < 0 ? 0 : (len > cap ? cap : len);
-    const int64_t i = len - p.T + t;
+    const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
     const int half = p.rot / 2, D = p.c.D, Hkv = p.c.Hkv;
     const int units = D / 8;
 
@@ -105,7 +102,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
         return;
     }
     const uint32_t at = (uint32_t)i, size = (uint32_t)p.c.page_size;
-    const int page = p.c.table[b * p.c.table_stride + at / size];
+    int page = -1;
+    if (at / size < (uint32_t)p.c.table_width) page = p.c.table[b * p.c.table_stride + at / size];
     const bool stored = page >= 0 && page < p.c.num_pages;   // otherwise the key and value are dropped
     const int64_t row = stored ? page * p.c.s_page + (int64_t)(at % size) * p.c.s_slot : 0;
     for (int j = threadIdx.x; j < half; j += kThreads) cs[j] = turn(p.offset + i, p.inv_freq[j]);

@@ -370,7 +370,9 @@ typedef struct fa_rows {
  * seq_len already counts the new tokens: token t of sequence b is its key i =
  * seq_len[b] - T + t, at position n = position_offset + i.  Tokens with i < 0
  * do not exist (a shorter row of a padded batch is aligned at its end): they
- * are not stored, and their query is set to zero.
+ * are not stored, and their query is set to zero.  Tokens that the table has no
+ * room for, i >= table_width * page_size, are not stored either (seq_len is not
+ * clamped here, so that no earlier key is overwritten); their query is turned.
  *
  * The first rot_dim elements of a head turn in pairs: pair p, of elements p
  * and p + rot_dim / 2 (2p and 2p + 1 if interleaved), by the angle n *

@@ -41,3 +41,26 @@ def test_a_batch_of_no_sequences():
     assert fa.kv_append(cache, kv, kv, q=q).shape == q.shape
     torch.cuda.synchronize()
     assert torch.equal(full.k_cache.view(torch.int16), kept.view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_tokens_past_the_table_overwrite_nothing(T):
+    """A table of 32 keys: what does not fit is dropped, and its query is turned by its position."""
+    D, page, before = 64, 16, [30, 31, 32, 40]
+    pool = Pool([32, 32, 32, 32], 2, D, page, BF16, seed=3)
+    cache = pool.gpu()
+    freq = (1000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).float().cuda()
+    q, k, v = (torch.randn((4, h, T, D), generator=pool.g).to(BF16).cuda() for h in (4, 2, 2))
+    cache.seq_len.copy_(torch.tensor(before, dtype=torch.int32) + T)
+    old_k, old_v = cache.k_cache.clone(), cache.v_cache.clone()
+    got = fa.kv_append(cache, k, v, q=q, inv_freq=freq)
+    # the same tokens in a table that has room
+    wide = Pool([64] * 4, 2, D, page, BF16, seed=4).gpu()
+    wide.seq_len.copy_(cache.seq_len)
+    assert torch.equal(got, fa.kv_append(wide, k, v, q=q, inv_freq=freq))
+    for new, old, there in ((cache.k_cache, old_k, wide.k_cache), (cache.v_cache, old_v, wide.v_cache)):
+        for b, n in enumerate(before):
+            for i in range(32):
+                page_at = int(cache.block_table[b, i // page]), slice(None), i % page
+                want = there[int(wide.block_table[b, i // page]), :, i % page] if n <= i < n + T else old[page_at]
+                assert torch.equal(new[page_at], want), (b, i)
