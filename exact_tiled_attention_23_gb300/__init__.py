@@ -520,9 +520,12 @@ def _binding():
         import torch  # noqa: F401  (the module uses its libraries)
 
         lib, path = load(), _build.BINDING_PATH
-        if not os.path.exists(path) or not _build.binding_up_to_date():
-            raise RuntimeError(f"the torch binding is not built for this torch and these sources ({path}); "
-                               "run exact_tiled_attention_23_gb300.build() first")
+        if not os.path.exists(path):
+            raise RuntimeError(f"the torch binding is not built ({path}); run exact_tiled_attention_23_gb300.build() first")
+        built, here = _build.binding_built_for(), _build.binding_target()
+        if built is not None and built != here:
+            raise RuntimeError(f"the torch binding was built for {built}, not for {here}; "
+                               "run exact_tiled_attention_23_gb300.build() again")
         loader = importlib.machinery.ExtensionFileLoader("fa_torch", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_torch", loader))
         loader.exec_module(module)

@@ -61,21 +61,34 @@ def _newer(built: str, inputs: list[str]) -> bool:
     return os.path.exists(built) and all(os.path.getmtime(f) <= os.path.getmtime(built) for f in inputs)
 
 
-def binding_target() -> list[str] | None:
-    """What the binding has to be built for: torch's version and place, its CUDA
-    and this Python's ABI.  None without a torch for CUDA.  (torch is not imported:
-    that takes seconds.)"""
+def _torch_place() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else None
+
+
+def binding_target() -> list[str] | None:
+    """What the binding has to be built for: torch's version, its CUDA and this
+    Python's ABI.  None without a torch for CUDA.  (torch is not imported: that
+    takes seconds.)"""
+    at = _torch_place()
+    if at is None:
         return None
-    at = list(spec.submodule_search_locations)[0]
     try:
         v = runpy.run_path(os.path.join(at, "version.py"))
     except OSError:
         return None
     if not v.get("cuda"):
         return None
-    return [str(v["__version__"]), at, v["cuda"], str(sysconfig.get_config_var("SOABI"))]
+    return [str(v["__version__"]), v["cuda"], str(sysconfig.get_config_var("SOABI"))]
+
+
+def binding_built_for() -> list[str] | None:
+    """What the binding that is there was built for (None: it does not say)."""
+    try:
+        with open(BINDING_STAMP) as f:
+            return json.load(f)
+    except (OSError, ValueError):
+        return None
 
 
 def library_up_to_date() -> bool:
@@ -88,13 +101,8 @@ def binding_up_to_date() -> bool:
     target = binding_target()
     if target is None:
         return True
-    if not _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]):
-        return False
-    try:
-        with open(BINDING_STAMP) as f:
-            return json.load(f) == target
-    except (OSError, ValueError):
-        return False
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]
+    return _newer(BINDING_PATH, inputs) and binding_built_for() == target
 
 
 def up_to_date() -> bool:
@@ -104,7 +112,7 @@ def up_to_date() -> bool:
 def _build_binding(target: list[str]) -> None:
     import torch
 
-    at = target[1]
+    at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",

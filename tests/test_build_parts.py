@@ -19,10 +19,11 @@ def tree(tmp_path, monkeypatch):
                        ("BINDING_PATH", tmp_path / "lib" / "fa_torch.so"), ("BINDING_STAMP", tmp_path / "lib" / "fa_torch.json")):
         monkeypatch.setattr(_build, name, str(path))
     monkeypatch.setattr(_build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
-    state = types.SimpleNamespace(ran=[], gcc_fails=False, target=["9.9", str(tmp_path / "torch"), "13.0", "abi"])
+    state = types.SimpleNamespace(ran=[], gcc_fails=False, target=["9.9", "13.0", "abi"])
     monkeypatch.setattr(_build, "binding_target", lambda: state.target)
     fake = types.ModuleType("torch")
     fake._C = types.SimpleNamespace(_GLIBCXX_USE_CXX11_ABI=True)
+    fake.__file__ = str(tmp_path / "torch" / "__init__.py")
     monkeypatch.setitem(sys.modules, "torch", fake)
 
     def run(cmd, **kw):
@@ -95,7 +96,7 @@ def test_what_a_binding_is_built_for(tmp_path, monkeypatch):
         return json.loads(subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, check=True,
                                          cwd=tmp_path).stdout)
     got = target()
-    assert got[:3] == ["1.2+cu999", str(tmp_path / "torch"), "99.9"] and "cpython" in got[3]
+    assert got[:2] == ["1.2+cu999", "99.9"] and "cpython" in got[2]
     version.write_text("__version__ = '1.2'\ncuda = None\n")
     assert target() is None
 
@@ -104,6 +105,23 @@ def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
     import exact_tiled_attention_23_gb300 as fa
     fa.build()
     monkeypatch.setattr(fa, "_BINDING", None)
-    monkeypatch.setattr(_build, "binding_target", lambda: ["0.0", "/nowhere", "0.0", "abi"])
-    with pytest.raises(RuntimeError, match="not built for this torch"):
+    monkeypatch.setattr(_build, "binding_target", lambda: ["0.0", "0.0", "abi"])
+    with pytest.raises(RuntimeError, match="was built for"):
         fa._binding()
+
+
+def test_a_copied_tree_is_loaded_whatever_its_files_dates(tmp_path):
+    """A copy that dates the built files before the sources still runs."""
+    import shutil
+
+    import exact_tiled_attention_23_gb300 as fa
+    fa.build()
+    copy = tmp_path / "exact_tiled_attention_23_gb300"
+    shutil.copytree(_build.PKG, copy, ignore=shutil.ignore_patterns("_build", "__pycache__"))
+    shutil.copytree(_build.INCLUDE, tmp_path / "include")
+    for f in (copy / "lib").iterdir():
+        os.utime(f, (1, 1))
+    code = "import exact_tiled_attention_23_gb300 as fa; print(fa.__file__); fa._binding()"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=tmp_path,
+                       env=dict(os.environ, PYTHONPATH=str(tmp_path)))
+    assert r.returncode == 0 and str(copy) in r.stdout, r.stderr[-2000:]
