@@ -579,11 +579,11 @@ def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None,
 
     Hq is a multiple of the cache's Hkv.  causal: the queries are the last T
     tokens of their sequences; otherwise each sees all seq_len keys.  Queries
-    that see no key get O = 0 and LSE = -inf.  More than 32 query rows that share
-    keys (T * Hq / Hkv, times the batch over a prefix) run on the tensor cores with
-    weights of one 16-bit number, as in forward(); fewer with two (include/fa.h has
-    the errors).  The other arguments are forward()'s; q may have any strides, and out too (last dimension
-    contiguous).  The workspace (a CUDA tensor of at least
+    that see no key get O = 0 and LSE = -inf.  Up to 32 query rows of a sequence
+    that share a key (T * Hq / Hkv) have weights of two 16-bit numbers, so that
+    only O's own rounding shows; more have one, as in forward() (include/fa.h has
+    the errors).  The other arguments are forward()'s; q may have any strides, and
+    out too (last dimension contiguous).  The workspace (a CUDA tensor of at least
     cache.workspace_bytes(Hq, T) bytes) is allocated here when not given.
     """
     if stream is not None:

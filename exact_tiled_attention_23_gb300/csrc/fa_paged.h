@@ -123,11 +123,13 @@ struct Beside {
 constexpr int kRowsTile = 1, kBlocksTile = 5;
 
 // Own chunks and tiles (a chunk has 8 KB of keys and values at D = 64 and 128)
-// that cost an SM as much time as one block.  Geometric mean of ten shapes (32 to
-// 256 sequences of 100 to 4000 keys at most, prefixes of 1000 to 30000), with cold
-// caches and warm: 8: 60.0 and 47.2 us, 10: 58.6 and 45.0, 12: 58.9 and 44.1, 13:
-// 59.6 and 44.6.
-constexpr int kBlockCost = 10;
+// that cost an SM as much time as one block, with weights of two numbers.
+// Geometric means of ten shapes (32 to 256 sequences of 100 to 4000 keys at most,
+// prefixes of 1000 to 30000), in us on two GPUs, caches warm, and cold on one: 10:
+// 50.8, 49.6 and 61.2; 13: 47.8, 48.1 and 59.5; 14: 47.7, 48.5 and 59.5; 16: 47.3,
+// 49.7 and 60.2; 20: 51.8 and 61.7.  (With one number a weight 10 was best: 47.5,
+// 46.6 and 58.7.)
+constexpr int kBlockCost = 13;
 
 // SMs for the prefix beside `own` chunks and tiles of the sequences' own keys.
 #ifdef __CUDACC__
@@ -152,6 +154,7 @@ struct PagedParams {
     float scale_log2;
     int second;                        // 1: may start beside the kernel before, and ends after it
     int joined;                        // 1: every tile leaves its state in a slot for the merge
+    int two;                           // tensor-core kernel: weights of two 16-bit numbers
     Partials part;
     Beside beside;
     int team;                          // CTAs that share a tile (teams only: 1, 2, 4 or 8)

@@ -291,6 +291,8 @@ fa_status run(const fa_rows *Q, const fa_paged_kv *c, const int32_t *prefix_tabl
         p.beside.cap = (int)own_keys;
         p.beside.B = B;
         fa::PagedParams f = p;
+        // (as exact as the row kernel's own keys, whatever the batch stacks up to)
+        f.two = (int64_t)G * T <= kMostRows;
         f.c.table = prefix_table;
         f.c.table_width = (int)((prefix_len + (int64_t)c->page_size - 1) / c->page_size);
         f.c.table_stride = 0;

@@ -33,9 +33,14 @@
 // the hand-offs around it (tensor pipe 52 % busy).  Short calls pay ~10 us until
 // the pipeline runs, most of it instruction fetch.
 //
-// P is rounded to 16 bits for the second product and O divided by the sum of
-// the rounded weights, as in fa_fwd: the tensor cores take 16-bit operands, and
-// a second product for the rounding's rest would cost a third of the rate.
+// The tensor cores take 16-bit weights.  For the rows of a generation step over
+// a shared prefix a weight is the sum of two numbers, p = hi + lo, with a product
+// each, as in the row kernel that reads the sequences' own keys: the answer of a
+// sequence is as exact alone as among many (kTwo).  hi and lo take the two P tiles,
+// so that a block's weights wait for the products of the block before.  Beside the
+// own keys that costs 1 to 3 % (kBlockCost in fa_paged.h).  Pieces of a prompt would
+// go from 199 to 271 us: there P is rounded once and O divided by the sum of the
+// rounded weights, as in fa_fwd.
 //
 // Every mbarrier wait is bounded; a wait that runs out records the site in
 // this file's status word, raises the CTA's abort flag, and every role drains
@@ -112,6 +117,42 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_
 
 using BlockLine = Line<BN, kBlocksTile>;
 
+// OnlineRow::exp_pass for weights of two numbers: hi to the columns at t_hi, lo to
+// those at t_lo.  The sum of p serves O and the LSE.
+template <bool kF16, typename PreStore>
+__device__ __forceinline__ void exp_two(const uint32_t (&s)[2][32], float sl2, float m_ref, uint32_t t_hi, uint32_t t_lo,
+                                        float &sum, PreStore &pre_store)
+{
+    const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+    const uint64_t scale = ptx::pack2(sl2, sl2), less = ptx::pack2(-ref, -ref), minus = ptx::pack2(-1.f, -1.f);
+    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            float y0, y1, r0, r1;
+            ptx::unpack2(ptx::fma2(ptx::pack2(u2f(s[c][2 * t]), u2f(s[c][2 * t + 1])), scale, less), y0, y1);
+            const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
+            const uint64_t both = ptx::pack2(p0, p1);
+            acc[t & 3] = ptx::add2(acc[t & 3], both);
+            hi[t] = ptx::pack16x2<kF16>(p0, p1);
+            ptx::unpack2(ptx::fma2(ptx::widen16x2<kF16>(hi[t]), minus, both), r0, r1);
+            lo[t] = ptx::pack16x2<kF16>(r0, r1);
+        }
+        if (c == 0) pre_store();
+        ptx::tmem_st16(t_hi + c * 16, hi);
+        ptx::tmem_st16(t_lo + c * 16, lo);
+    }
+    sum = 0.f;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        float x, y;
+        ptx::unpack2(acc[a], x, y);
+        sum += x + y;
+    }
+}
+
 // A role's way along the CTA's piece of the line, tile by tile: what a block
 // needs beyond its number is found once per tile, because the issuing threads
 // run alone and every instruction between two products counts (a walk that
@@ -132,7 +173,7 @@ struct Walk {
     }
 };
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
 {
@@ -296,7 +337,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     } else if (warp == 1) {
         // ================= PV products =================
         // O_h += P_h V[64h ..]: K-steps 4h .. 4h+3 of the block, A from the
-        // half's 32 columns of P tile t % 2.  A tile's first products replace O,
+        // half's 32 columns of P tile t % 2 (kTwo: of both tiles, hi and lo of
+        // one block).  A tile's first products replace O,
         // once the softmax warps hold the tile before.  Lane 0 waits and
         // issues; the warp clears V behind a sequence's end together.
         constexpr uint32_t idesc = make_idesc(BM, D, 0, 1, kF16);
@@ -309,10 +351,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             for (int h = 0; h < 2; ++h) {
                 if (!wait_for(&p_full[h * 2 + buf], (t >> 1) & 1, limit, kSitePFull, ab)) return false;
                 ptx::tc_fence_after();
-                const uint32_t to = tmem + Lay::col_o(h), tp = tmem + Lay::col_p(buf, h);
+                const uint32_t to = tmem + Lay::col_o(h);
 #pragma unroll
-                for (int k = 0; k < kHalf / 16; ++k)
-                    ptx::mma_ts(to, tp + k * 8, vd + (uint64_t)(((4 * h + k) * 2048) >> 4), idesc, (!first || k > 0) ? 1u : 0u);
+                for (int n = 0; n < (kTwo ? 2 : 1); ++n) {
+                    const uint32_t tp = tmem + Lay::col_p(kTwo ? n : buf, h);
+#pragma unroll
+                    for (int k = 0; k < kHalf / 16; ++k)
+                        ptx::mma_ts(to, tp + k * 8, vd + (uint64_t)(((4 * h + k) * 2048) >> 4), idesc,
+                                    (!first || k > 0 || n > 0) ? 1u : 0u);
+                }
                 ptx::mma_commit(&pv_done[h * 2 + buf]);
             }
             ptx::mma_commit(&v_empty[t % RV]);
@@ -432,16 +479,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             OnlineRow<D, kF16, kHalf, kF16 ? kLiftF16 : 0> st;
             for (int j = 0; j < count; ++j, ++t) {
                 const int buf = t & 1;
-                const uint32_t tP = tmem + lane_off + Lay::col_p(buf, h);
+                const uint32_t tP = tmem + lane_off + Lay::col_p(kTwo ? 0 : buf, h);
+                const int reader = t - (kTwo ? 1 : 2);            // the last block whose products read it
                 const uint32_t tO = tmem + lane_off + Lay::col_o(h);
                 const bool got = wait_for(s_full, t & 1, limit, kSiteSFull, ab);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                // whether the last reader of P tile `buf` is done: tested now,
-                // waited for below only if it was not
-                const bool p_free = t < 2 || ptx::mbar_test(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1);
+                // whether that reader is done: tested now, waited for below only
+                // if it was not
+                const bool p_free = reader < 0 || ptx::mbar_test(&pv_done[h * 2 + (reader & 1)], (reader >> 1) & 1);
                 ptx::tc_fence_after();
                 // Hidden keys become -inf in TMEM, eight at a time and only in
                 // blocks that have some: selects on the 64 registers of the row
@@ -486,7 +534,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 };
                 auto before_p = [&] {
                     if (!__all_sync(0xffffffffu, p_free)) {
-                        hook_ok = wait_for(&pv_done[h * 2 + buf], ((t - 2) >> 1) & 1, limit, kSiteOFinal, ab) && hook_ok;
+                        hook_ok = wait_for(&pv_done[h * 2 + (reader & 1)], (reader >> 1) & 1, limit, kSiteOFinal, ab) && hook_ok;
                         ptx::tc_fence_after();
                     }
                 };
@@ -496,7 +544,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll 1
                 for (int turn = 0; turn < 2; ++turn) {
                     if (raise) st.raise(s_raw, sl2, j > 0, tO, before_o);
-                    st.template exp_pass<1>(s_raw, sl2, tP, sum, sum_o, before_p);
+                    if constexpr (kTwo) {
+                        exp_two<kF16>(s_raw, sl2, st.m_ref, tP, tmem + lane_off + Lay::col_p(1, h), sum, before_p);
+                        sum_o = sum;
+                    } else {
+                        st.template exp_pass<1>(s_raw, sl2, tP, sum, sum_o, before_p);
+                    }
                     raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kLazyLimitF16 : kLazyLimit)));
                     ptx::tmem_wait_st();      // the first turn's P stores land before new ones
                     if (!raise) break;
@@ -624,13 +677,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (p.second) ptx::wait_for_primary();
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kTwo>
 cudaError_t launch(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
 {
     static SharedMemory allowed;
-    const cudaError_t e = allowed.allow(paged_tc_kernel<D, kF16>, TcLayout<D>::kSmemBytes);
+    const cudaError_t e = allowed.allow(paged_tc_kernel<D, kF16, kTwo>, TcLayout<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_tc_kernel<D, kF16>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes, stream, tk, tv, p);
+    return launch_behind(paged_tc_kernel<D, kF16, kTwo>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes, stream, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t stream)
+{
+    if (p.two) return p.f16 ? launch<D, true, true>(p, tk, tv, ctas, stream) : launch<D, false, true>(p, tk, tv, ctas, stream);
+    return p.f16 ? launch<D, true, false>(p, tk, tv, ctas, stream) : launch<D, false, false>(p, tk, tv, ctas, stream);
 }
 
 }  // namespace
@@ -638,8 +698,7 @@ cudaError_t launch(const PagedParams &p, const CUtensorMap &tk, const CUtensorMa
 cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                             cudaStream_t stream)
 {
-    if (p.c.D <= 64) return p.f16 ? launch<64, true>(p, tk, tv, ctas, stream) : launch<64, false>(p, tk, tv, ctas, stream);
-    return p.f16 ? launch<128, true>(p, tk, tv, ctas, stream) : launch<128, false>(p, tk, tv, ctas, stream);
+    return p.c.D <= 64 ? launch_d<64>(p, tk, tv, ctas, stream) : launch_d<128>(p, tk, tv, ctas, stream);
 }
 
 cudaError_t read_and_clear_status_paged(uint32_t *out)

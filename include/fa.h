@@ -416,15 +416,14 @@ fa_status fa_kv_append(const fa_paged_kv *cache, const fa_rows *K, const fa_rows
  * Queries that see no key get O = +0.0 and LSE = -inf.  Results do not depend
  * on timing: partial states are joined in a fixed order.
  *
- * V is multiplied by 16-bit weights p.  Where more than 32 query rows share keys
- * (T * Hq / Hkv of them; times B over a prefix), D <= 128 and page_size is a
- * multiple of 8, a weight is one number, as in fa_fwd, and O is divided by the
- * sum of the rounded weights: beside its own rounding O is off by up to 2^-7
- * (fp16: 2^-10) of sum p |v| / sum p.  Elsewhere it is the sum of two numbers,
- * good to 2^-16 (2^-22), so that O's own rounding decides; a caller that needs
- * this of more tokens passes at most 32 * Hkv / Hq of them at a time.  A small
- * fp16 weight is off by 2^-37 of its row's largest instead where that is more
- * (one number: 2^-32).
+ * V is multiplied by 16-bit weights p.  A weight is the sum of two numbers, good
+ * to 2^-16 (fp16: 2^-22), so that O's own rounding decides.  Where more than 32
+ * query rows of a sequence share a key (T * Hq / Hkv), D <= 128 and page_size is a
+ * multiple of 8, it is one number, as in fa_fwd, and O is divided by the sum of the
+ * rounded weights: beside its own rounding O is then off by up to 2^-7 (2^-10) of
+ * sum p |v| / sum p.  A caller that needs more of such a call passes at most
+ * 32 * Hkv / Hq tokens at a time.  A small fp16 weight is off by 2^-32 of its row's
+ * largest instead where that is more.
  *
  * Returns as fa_fwd,
  * and FA_ERR_INVALID_ARG for a missing, misaligned or too small workspace, an

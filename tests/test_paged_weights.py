@@ -1,7 +1,8 @@
 """How exact the weights of the paged forward are.
 
-The row kernel (up to 32 stacked rows, alone or as a team) multiplies V by each
-weight as two 16-bit numbers, p = hi + lo.  The bounds here count that, and not
+The row kernel (up to 32 stacked rows, alone or as a team) and the tensor-core
+kernel over the prefix of such rows multiply V by each weight as two 16-bit
+numbers, p = hi + lo.  The bounds here count that, and not
 the single rounding of a weight that tests/paged_reference.py allows every
 kernel: a kernel without its second product does not keep them (which a model
 on the CPU shows first).
@@ -15,16 +16,17 @@ import exact_tiled_attention_23_gb300 as fa
 import paged_reference as ref
 from test_paged_gpu import BF16, F16, Pool
 
-# fp16: a row's largest weight is at least 2^LIFT in the row kernel's units
-LIFT = 12
+# fp16: a row's largest weight is at least 2^LIFT in the row kernel's units, and
+# 2^LIFT_TILES in the tensor-core kernel's
+LIFT, LIFT_TILES = 12, 7
 
 
-def bound_of(want, keys, dtype):
-    """The row kernel's |O - exact|.
+def bound_of(want, keys, dtype, lift=LIFT):
+    """|O - exact| with weights of two numbers.
 
     A weight is off by e as in check_attention().  hi is off by half a step u of
     p, and lo by half a step of that: u^2.  fp16 numbers below the normal range
-    are off by 2^-25 instead, 2^-(25 + LIFT) of the row's largest weight.  One
+    are off by 2^-25 instead, 2^-(25 + lift) of the row's largest weight.  One
     accumulator takes keys / 16 products of hi and as many of lo, each a sum of
     17 terms that are off by 2^-24 of the sum of magnitudes; the sum of weights
     is off by keys 2^-24.  The result is rounded once, half a step of itself."""
@@ -32,7 +34,7 @@ def bound_of(want, keys, dtype):
     u = ref.HALF_STEP[dtype]
     e = (o.shape[3] + 4) * 2.0 ** -24 * size + 2.0 ** -20
     c = (2 * -(-keys // 16) * 17 + keys) * 2.0 ** -24
-    tiny = keys * 2.0 ** -(25 + LIFT) * vmax + 2.0 ** -25 if dtype == F16 else 0 * vmax
+    tiny = keys * 2.0 ** -(25 + lift) * vmax + 2.0 ** -25 if dtype == F16 else 0 * vmax
     return u * o.abs() + 1.01 * ((2 * e[..., None] + u * u + c) * a + tiny[..., None])
 
 
@@ -92,4 +94,28 @@ def test_rows_keep_two_numbers_of_a_weight(lens, Hkv, group, T, D, page, width, 
             else fa.forward_paged(q.cuda(), cache))
     want = ref.attention(q, pool.k, pool.v, pool.table, pool.lens, prefix_table=pool.prefix_table, prefix_len=prefix)
     over = (o.double().cpu() - want[0]).abs() - bound_of(want, prefix + max(lens), dtype)
+    assert (over <= 0).all(), over.max()
+
+
+# Prefixes that the tensor cores read: more than 32 rows of all sequences together,
+# up to 32 of each.
+STACKED = [
+    # prefix, lens, Hkv, group, T, D, page
+    (40, [5, 30, 1, 0, 17, 9, 22, 3, 40], 1, 4, 1, 64, 16),
+    (130, [12] * 6, 1, 8, 1, 128, 16),
+    (17, [20, 1, 3], 2, 4, 3, 96, 8),
+    (64, [33, 2], 1, 4, 8, 128, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("prefix,lens,Hkv,group,T,D,page", STACKED)
+def test_a_prefix_is_as_exact_as_the_own_keys(prefix, lens, Hkv, group, T, D, page, dtype):
+    pool = Pool(lens, Hkv, D, page, dtype, seed=D + T + prefix, prefix=prefix, width=20000 // page)
+    q = pool.queries(Hkv * group, T)
+    fa.build()
+    o, _ = fa.forward_shared_prefix(q.cuda(), pool.gpu(), pool.prefix_table.cuda(), prefix)
+    want = ref.attention(q, pool.k, pool.v, pool.table, pool.lens, prefix_table=pool.prefix_table, prefix_len=prefix)
+    over = (o.double().cpu() - want[0]).abs() - bound_of(want, prefix + max(lens), dtype, LIFT_TILES)
     assert (over <= 0).all(), over.max()
