@@ -33,7 +33,7 @@ ROWS = [
 ]
 
 
-def check(B, n, gap, T, D, page, dtype, one_number, lift):
+def check(B, n, gap, T, D, page, dtype, one_number, lift, prefix=False):
     """A weight is off by 2^-20 of itself (the exponent's rounding) and by its
     16-bit form: half a step u, or u^2 as two numbers; in fp16 by 2^-25 against
     a largest weight of 2^lift where that is more.  One accumulator takes at most
@@ -50,8 +50,13 @@ def check(B, n, gap, T, D, page, dtype, one_number, lift):
     q = torch.zeros((B, group, T, D), dtype=dtype)
     q[..., 0] = 8
     table = torch.arange(k.shape[0], dtype=torch.int32).expand(B, -1).contiguous()
-    cache = fa.PagedKV(k.cuda(), v.cuda(), table.cuda(), torch.full((B,), n, dtype=torch.int32, device="cuda"))
-    o, lse = fa.forward_paged(q.cuda(), cache, causal=False, scale=1 / 8)      # a score is the key's first element
+    cache = fa.PagedKV(k.cuda(), v.cuda(), table.cuda(),
+                       torch.full((B,), 0 if prefix else n, dtype=torch.int32, device="cuda"))
+    scale = 1 / 8                                              # a score is the key's first element
+    if prefix:
+        o, lse = fa.forward_shared_prefix(q.cuda(), cache, table[0].cuda(), n, causal=False, scale=scale)
+    else:
+        o, lse = fa.forward_paged(q.cuda(), cache, causal=False, scale=scale)
     torch.cuda.synchronize()
     assert fa.fa_device_status(None) == fa.FA_OK
     tail = (n - 1) * math.exp(float(k[0, 0, 1, 0]))
@@ -80,3 +85,10 @@ def test_rows_keep_small_weights(B, n, gap, T, D, page, dtype):
 ])
 def test_tiles_keep_small_weights(B, n, gap, T, D, page, dtype):
     check(B, n, gap, T, D, page, dtype, True, LIFT_TILES)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B,n,gap,T,D,page", [(8192, 8192, 20.5, 1, 64, 16), (4096, 8192, 23.6, 2, 128, 16)])
+def test_a_prefix_keeps_small_weights(B, n, gap, T, D, page, dtype):
+    """All keys are the prefix's, which the tensor cores read with weights of two numbers."""
+    check(B, n, gap, T, D, page, dtype, False, LIFT_TILES, prefix=True)
