@@ -28,7 +28,7 @@
 //     while the first copies fly, decides whether the blocks have to ask.
 //
 // Measured: 1024 tokens over 16384 keys, 32 query and 8 key heads, D = 128, bf16,
-// 2.7e11 operations, 208 us with the merge, 1.28 PFLOP/s (a large matrix product:
+// 2.7e11 operations, 200 us with the merge, 1.33 PFLOP/s (a large matrix product:
 // 1.88); ~1680 clk per block, as in the split-row kernel, bound by the softmax and
 // the hand-offs around it (tensor pipe 52 % busy).  Short calls pay ~10 us until
 // the pipeline runs, most of it instruction fetch.
