@@ -11,8 +11,13 @@ and only marshal arguments through ctypes.  The torch conveniences on top:
   the computation;
 * ``backward()`` -- dQ, dK, dV by recomputation;
 * ``attention()`` -- a differentiable torch operation (forward + backward);
+* ``rotary()`` -- queries and keys turned by their positions on one or more
+  axes, differentiable;
 * ``PagedKV`` with ``kv_append()``, ``forward_paged()`` and
-  ``forward_shared_prefix()`` -- generation over a paged key/value cache.
+  ``forward_shared_prefix()`` -- generation over a paged key/value cache;
+* ``PagedKV4`` -- the same with keys and values held in 4 bits;
+* ``kv_grow()``, ``kv_fork()``, ``kv_free()``, ``kv_compact()``,
+  ``copy_pages()`` and ``kv_read()`` -- the pages of either.
 
 Every step of the computation runs in the library's CUDA kernels; there is no
 other code path, and calling without the built library raises.
@@ -34,7 +39,12 @@ __all__ = ["FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "
            "fa_fwd_from_host", "fa_fwd_from_host_auto_groups", "FA_MAX_HOST_GROUPS", "forward_from_host",
            "forward", "build", "fa_paged_kv", "fa_rows", "fa_kv_append", "fa_fwd_paged",
            "fa_fwd_paged_workspace_bytes", "fa_fwd_shared_prefix", "fa_fwd_shared_prefix_workspace_bytes",
-           "PagedKV", "kv_append", "forward_paged", "forward_shared_prefix"]
+           "PagedKV", "kv_append", "forward_paged", "forward_shared_prefix",
+           "fa_positions", "fa_paged_kv4", "fa_page_table", "fa_kv_append_at", "fa_rotary", "fa_kv_append_q4",
+           "fa_fwd_paged_q4", "fa_fwd_paged_q4_workspace_bytes", "fa_kv_read", "fa_kv_read_q4",
+           "fa_pages_workspace_bytes", "fa_kv_grow", "fa_kv_free", "fa_kv_fork", "fa_kv_compact", "fa_copy_pages",
+           "fa_copy_pages_q4", "PagedKV4", "rotary", "kv_read", "kv_grow", "kv_fork", "kv_free", "kv_compact",
+           "copy_pages"]
 
 FA_OK = 0
 FA_ERR_INVALID_ARG = 1
@@ -68,6 +78,30 @@ class fa_rows(ctypes.Structure):
     """A strided [B, H, N, D] array as the C entry points take it (include/fa.h)."""
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
                 ("stride_n", ctypes.c_int64)]
+
+
+class fa_positions(ctypes.Structure):
+    """Positions of tokens on one or more axes as the C entry points take them (include/fa.h)."""
+    _fields_ = [("n", ctypes.c_void_p), ("stride_axis", ctypes.c_int64), ("stride_b", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64), ("axes", ctypes.c_int), ("pair_axis", ctypes.c_void_p)]
+
+
+class fa_paged_kv4(ctypes.Structure):
+    """A paged cache of 4 bits as the C entry points take it (include/fa.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("stride_slot", ctypes.c_int64), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("scale_stride_page", ctypes.c_int64),
+                ("scale_stride_head", ctypes.c_int64), ("scale_stride_slot", ctypes.c_int64),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
+                ("seq_len", ctypes.c_void_p)]
+
+
+class fa_page_table(ctypes.Structure):
+    """A cache's table, lengths and page counts as the C entry points take them (include/fa.h)."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
+                ("B", ctypes.c_int), ("seq_len", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
 def library_path() -> str:
@@ -141,6 +175,27 @@ def load():
         lib.fa_fwd_shared_prefix.restype = i32
         lib.fa_fwd_shared_prefix_workspace_bytes.argtypes = [cache_p, i32, i32, i32, i32]
         lib.fa_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+        i64, size = ctypes.c_int64, ctypes.c_size_t
+        pos_p, cache4_p, table_p = (ctypes.POINTER(x) for x in (fa_positions, fa_paged_kv4, fa_page_table))
+        lib.fa_rotary.argtypes = [rows_p] * 4 + [i32] * 5 + [vp, i32, i32, pos_p, i64, i32, i32, vp]
+        lib.fa_kv_append_at.argtypes = [cache_p] + [rows_p] * 4 + [i32] * 3 + [vp, i32, i32, pos_p, i64, i32, vp]
+        lib.fa_kv_append_q4.argtypes = [cache4_p] + lib.fa_kv_append_at.argtypes[1:]
+        lib.fa_kv_read.argtypes = [cache_p, rows_p, rows_p, i32, i32, vp]
+        lib.fa_kv_read_q4.argtypes = [cache4_p, rows_p, rows_p, i32, i32, i32, vp]
+        lib.fa_fwd_paged_q4.argtypes = [rows_p, cache4_p, rows_p, vp, i32, i32, i32, i32, f32, i32, vp, size, vp]
+        lib.fa_fwd_paged_q4_workspace_bytes.argtypes = [cache4_p, i32, i32, i32]
+        lib.fa_pages_workspace_bytes.argtypes = [table_p, i32]
+        lib.fa_kv_grow.argtypes = [table_p, vp, vp, vp, size, vp]
+        lib.fa_kv_free.argtypes = [table_p, vp, i32, vp]
+        lib.fa_kv_fork.argtypes = [table_p, vp, vp, i32, vp, vp, vp, size, vp]
+        lib.fa_kv_compact.argtypes = [table_p, vp, vp, vp, vp, vp, size, vp]
+        lib.fa_copy_pages.argtypes = [cache_p, vp, vp, vp, i32, vp]
+        lib.fa_copy_pages_q4.argtypes = [cache4_p, vp, vp, vp, i32, vp]
+        for f in (lib.fa_rotary, lib.fa_kv_append_at, lib.fa_kv_append_q4, lib.fa_kv_read, lib.fa_kv_read_q4,
+                  lib.fa_fwd_paged_q4, lib.fa_kv_grow, lib.fa_kv_free, lib.fa_kv_fork, lib.fa_kv_compact,
+                  lib.fa_copy_pages, lib.fa_copy_pages_q4):
+            f.restype = i32
+        lib.fa_fwd_paged_q4_workspace_bytes.restype = lib.fa_pages_workspace_bytes.restype = size
         _lib = lib
         return lib
 
@@ -252,6 +307,81 @@ def fa_fwd_shared_prefix(Q, cache, prefix_table, prefix_len, O, LSE, B, Hq, T, c
 
 def fa_fwd_shared_prefix_workspace_bytes(cache, prefix_len, B, Hq, T) -> int:
     return int(load().fa_fwd_shared_prefix_workspace_bytes(cache, int(prefix_len), B, Hq, T))
+
+
+def fa_kv_append_at(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, interleaved, positions, position_offset,
+                    f16, stream) -> int:
+    """fa_kv_append with the tokens' positions (an fa_positions, or None)."""
+    return (_lib or load()).fa_kv_append_at(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, bool(interleaved),
+                                            positions, position_offset, bool(f16), stream)
+
+
+def fa_rotary(Q, Q_out, K, K_out, B, Hq, Hkv, T, D, inv_freq, rot_dim, interleaved, positions, position_offset,
+              inverse, f16, stream) -> int:
+    """Queries and keys turned by their positions (fa_rows; Hq or Hkv may be 0)."""
+    return (_lib or load()).fa_rotary(Q, Q_out, K, K_out, B, Hq, Hkv, T, D, inv_freq, rot_dim, bool(interleaved),
+                                      positions, position_offset, bool(inverse), bool(f16), stream)
+
+
+def fa_kv_append_q4(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, interleaved, positions, position_offset,
+                    f16, stream) -> int:
+    """fa_kv_append_at into an fa_paged_kv4."""
+    return (_lib or load()).fa_kv_append_q4(cache, K, V, Q, Q_out, B, Hq, T, inv_freq, rot_dim, bool(interleaved),
+                                            positions, position_offset, bool(f16), stream)
+
+
+def fa_fwd_paged_q4(Q, cache, O, LSE, B, Hq, T, causal, scale, f16, workspace, workspace_bytes, stream) -> int:
+    """fa_fwd_paged over an fa_paged_kv4."""
+    return (_lib or load()).fa_fwd_paged_q4(Q, cache, O, LSE, B, Hq, T, bool(causal), scale, bool(f16), workspace,
+                                            workspace_bytes, stream)
+
+
+def fa_fwd_paged_q4_workspace_bytes(cache, B, Hq, T) -> int:
+    return int(load().fa_fwd_paged_q4_workspace_bytes(cache, B, Hq, T))
+
+
+def fa_kv_read(cache, K, V, B, T, stream) -> int:
+    """The last T tokens of every sequence as rows."""
+    return (_lib or load()).fa_kv_read(cache, K, V, B, T, stream)
+
+
+def fa_kv_read_q4(cache, K, V, B, T, f16, stream) -> int:
+    """fa_kv_read of an fa_paged_kv4, decoded."""
+    return (_lib or load()).fa_kv_read_q4(cache, K, V, B, T, bool(f16), stream)
+
+
+def fa_pages_workspace_bytes(table, n) -> int:
+    return int(load().fa_pages_workspace_bytes(table, n))
+
+
+def fa_kv_grow(table, tokens, taken, workspace, workspace_bytes, stream) -> int:
+    """Pages for new tokens; `table` is an fa_page_table, tokens and taken device addresses."""
+    return (_lib or load()).fa_kv_grow(table, tokens, taken, workspace, workspace_bytes, stream)
+
+
+def fa_kv_free(table, rows, n, stream) -> int:
+    """Rows of an fa_page_table give up their pages."""
+    return (_lib or load()).fa_kv_free(table, rows, n, stream)
+
+
+def fa_kv_fork(table, parent, child, n, src, dst, workspace, workspace_bytes, stream) -> int:
+    """Rows of an fa_page_table become what others are; src and dst get the copies that it takes."""
+    return (_lib or load()).fa_kv_fork(table, parent, child, n, src, dst, workspace, workspace_bytes, stream)
+
+
+def fa_kv_compact(table, moved, src, dst, count, workspace, workspace_bytes, stream) -> int:
+    """The used pages of an fa_page_table to the pool's front; src, dst and count get the copies that it takes."""
+    return (_lib or load()).fa_kv_compact(table, moved, src, dst, count, workspace, workspace_bytes, stream)
+
+
+def fa_copy_pages(cache, src, dst, count, n, stream) -> int:
+    """Pages of an fa_paged_kv to others."""
+    return (_lib or load()).fa_copy_pages(cache, src, dst, count, n, stream)
+
+
+def fa_copy_pages_q4(cache, src, dst, count, n, stream) -> int:
+    """Pages of an fa_paged_kv4 to others."""
+    return (_lib or load()).fa_copy_pages_q4(cache, src, dst, count, n, stream)
 
 
 def fa_status_string(status: int) -> str:
@@ -438,6 +568,19 @@ def _fixed(name, doc):
     return property(get, put, doc=doc)
 
 
+def _table_sizes(block_table, seq_len):
+    import torch
+
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor [B, W]")
+    B, W = block_table.shape
+    if W > 1 and block_table.stride(1) != 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    if seq_len.dtype != torch.int32 or seq_len.dim() != 1 or seq_len.numel() != B or not seq_len.is_contiguous():
+        raise ValueError("seq_len must be a contiguous int32 tensor with B entries")
+    return B, W
+
+
 class PagedKV:
     """A paged key/value cache: a pool of pages and the pages of each sequence.
 
@@ -464,13 +607,7 @@ class PagedKV:
             raise ValueError("k_cache, v_cache must share dtype bfloat16 or float16")
         if k_cache.stride(3) != 1:
             raise ValueError("the last dimension of the caches must be contiguous")
-        if block_table.dtype != torch.int32 or block_table.dim() != 2:
-            raise ValueError("block_table must be an int32 tensor [B, W]")
-        B, W = block_table.shape
-        if W > 1 and block_table.stride(1) != 1:
-            raise ValueError("the rows of block_table must be contiguous")
-        if seq_len.dtype != torch.int32 or seq_len.dim() != 1 or seq_len.numel() != B or not seq_len.is_contiguous():
-            raise ValueError("seq_len must be a contiguous int32 tensor with B entries")
+        B, W = _table_sizes(block_table, seq_len)
         if not k_cache.is_cuda or any(x.device != k_cache.device for x in (v_cache, block_table, seq_len)):
             raise ValueError("the caches, block_table and seq_len must be CUDA tensors of one device")
         self._k_cache, self._v_cache, self._block_table, self._seq_len = k_cache, v_cache, block_table, seq_len
@@ -507,6 +644,80 @@ class PagedKV:
             return fa_fwd_shared_prefix_workspace_bytes(self._c, prefix_len, self.batch, Hq, T)
 
 
+class PagedKV4:
+    """A PagedKV whose keys and values are held in 4 bits.
+
+    k_cache, v_cache: uint8 CUDA tensors [pages, Hkv, page_size, P / 2], k_scales,
+    v_scales: uint8 [pages, Hkv, page_size, P / 16], each pair of one set of strides
+    (multiples of 16 and of P / 16 bytes), the last dimension contiguous.  P is 64, 128 or 256, the
+    least that holds the head dimension D (default P).  A row is held in groups of
+    16 elements, each a number of 4 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) times
+    its group's scale (include/fa.h has the format and the errors).  dtype: of the
+    queries, and of what is appended and read back, bfloat16 or float16.
+    block_table, seq_len and what may be done with them: as in PagedKV.
+
+    kv_append(), forward_paged(), kv_read() and the page operators take it in the
+    place of a PagedKV; forward_shared_prefix() does not (the sequences' tables may
+    share a prefix's pages instead).
+    """
+
+    def __init__(self, k_cache, v_cache, k_scales, v_scales, block_table, seq_len, D=None, dtype=None):
+        import torch
+
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be bfloat16 or float16")
+        for name, x, y in (("k_cache, v_cache", k_cache, v_cache), ("k_scales, v_scales", k_scales, v_scales)):
+            if x.dtype != torch.uint8 or y.dtype != torch.uint8 or x.dim() != 4 or x.shape != y.shape or x.stride() != y.stride():
+                raise ValueError(f"{name} must be uint8 tensors of one shape [pages, Hkv, page_size, bytes] and one set of strides")
+            if x.stride(3) != 1:
+                raise ValueError(f"the last dimension of {name} must be contiguous")
+        pages, Hkv, page_size, half = k_cache.shape
+        P = 2 * half
+        D = P if D is None else int(D)
+        if P not in (64, 128, 256) or not 0 < D <= P or (P > 64 and D <= P // 2):
+            raise ValueError("rows must have 64, 128 or 256 elements of 4 bits, the least that holds D")
+        if k_scales.shape != (pages, Hkv, page_size, P // 16):
+            raise ValueError("k_scales, v_scales must have shape [pages, Hkv, page_size, P / 16]")
+        B, W = _table_sizes(block_table, seq_len)
+        if not k_cache.is_cuda or any(x.device != k_cache.device for x in (v_cache, k_scales, v_scales, block_table, seq_len)):
+            raise ValueError("the caches, scales, block_table and seq_len must be CUDA tensors of one device")
+        self._k_cache, self._v_cache, self._k_scales, self._v_scales = k_cache, v_cache, k_scales, v_scales
+        self._block_table, self._seq_len = block_table, seq_len
+        self._batch, self._Hkv, self._D, self._dtype, self._device = B, Hkv, D, dtype, k_cache.device
+        # the stride of a dimension of one entry is never followed
+        strides = [[s if n > 1 else 0 for s, n in zip(x.stride(), (pages, Hkv, page_size))] for x in (k_cache, k_scales)]
+        self._c = fa_paged_kv4(k_cache.data_ptr(), v_cache.data_ptr(), *strides[0], k_scales.data_ptr(),
+                               v_scales.data_ptr(), *strides[1], pages, page_size, Hkv, D, block_table.data_ptr(),
+                               block_table.stride(0) if B > 1 else W, W, seq_len.data_ptr())
+        self._native = _binding().cache4(ctypes.addressof(self._c), k_cache, v_cache, k_scales, v_scales, block_table,
+                                         seq_len, dtype == torch.float16)
+
+    k_cache = _fixed("k_cache", "The pool of keys.")
+    v_cache = _fixed("v_cache", "The pool of values.")
+    k_scales = _fixed("k_scales", "The keys' scales.")
+    v_scales = _fixed("v_scales", "The values' scales.")
+    block_table = _fixed("block_table", "The pages of each sequence.")
+    seq_len = _fixed("seq_len", "Keys per sequence.")
+    batch = _fixed("batch", "Sequences.")
+    Hkv = _fixed("Hkv", "Key heads.")
+    D = _fixed("D", "Head dimension.")
+    dtype = _fixed("dtype", "Of queries and of what is read back.")
+    device = _fixed("device", "Of all tensors.")
+
+    @property
+    def c(self):
+        """The cache as the C entry points take it (a copy)."""
+        return fa_paged_kv4.from_buffer_copy(self._c)
+
+    def workspace_bytes(self, Hq: int, T: int) -> int:
+        """Bytes of workspace that forward_paged() needs for queries [B, Hq, T, D]."""
+        import torch
+
+        with torch.cuda.device(self.device):
+            return fa_fwd_paged_q4_workspace_bytes(self._c, self.batch, Hq, T)
+
+
 _BINDING = None
 
 
@@ -530,28 +741,32 @@ def _binding():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_torch", loader))
         loader.exec_module(module)
         module.init(*(ctypes.cast(f, ctypes.c_void_p).value
-                      for f in (lib.fa_kv_append, lib.fa_fwd_shared_prefix, lib.fa_fwd_shared_prefix_workspace_bytes)))
+                      for f in (lib.fa_kv_append_at, lib.fa_kv_append_q4, lib.fa_fwd_shared_prefix,
+                                lib.fa_fwd_shared_prefix_workspace_bytes, lib.fa_fwd_paged_q4,
+                                lib.fa_fwd_paged_q4_workspace_bytes, lib.fa_kv_read, lib.fa_kv_read_q4, lib.fa_rotary,
+                                lib.fa_pages_workspace_bytes, lib.fa_kv_grow, lib.fa_kv_free, lib.fa_kv_fork,
+                                lib.fa_kv_compact, lib.fa_copy_pages, lib.fa_copy_pages_q4)))
         _BINDING = module
     return _BINDING
 
 
-def _stream_context(cache, stream):
-    """torch's context for `stream` (a stream of the cache's device, or its
-    pointer): allocations and copies go there too."""
+def _stream_context(device, stream):
+    """torch's context for `stream` (a stream of the device, or its pointer):
+    allocations and copies go there too."""
     import torch
 
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(stream or 0, device=cache.device)
-    if stream.device != cache.device:
+        stream = torch.cuda.ExternalStream(stream or 0, device=device)
+    if stream.device != device:
         raise ValueError("stream must belong to the cache's device")
     return torch.cuda.stream(stream)
 
 
 def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, position_offset: int = 0,
-              q_out=None, stream=None):
-    """Put the keys and values of T new tokens per sequence into a PagedKV,
-    turned by their positions, and return the queries turned likewise (None
-    without q).
+              q_out=None, stream=None, positions=None, pair_axis=None):
+    """Put the keys and values of T new tokens per sequence into a PagedKV (or
+    PagedKV4), turned by their positions, and return the queries turned likewise
+    (None without q).
 
     k, v: [B, Hkv, T, D], q: [B, Hq, T, D], any strides (a [B, T, H, D]
     projection's transpose(1, 2) is read in place).  cache.seq_len already
@@ -561,13 +776,15 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
     position_offset: position of a sequence's first key; behind a shared prefix
     (forward_shared_prefix()) this is the prefix's length, since seq_len counts
     only the keys that follow it.  q_out: where to put
-    the queries, q itself for in place.  Runs asynchronously on `stream`
-    (default: torch's current stream of the cache's device).
+    the queries, q itself for in place.  positions, pair_axis: the tokens' own
+    positions, as in rotary(); None: their places in the sequences.  Runs
+    asynchronously on `stream` (default: torch's current stream of the cache's
+    device).
     """
     if stream is not None:
-        with _stream_context(cache, stream):
-            return kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out)
-    r = _BINDING.kv_append(cache._native, k, v, q, inv_freq, interleaved, position_offset, q_out)
+        with _stream_context(cache.device, stream):
+            return kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out, None, positions, pair_axis)
+    r = _BINDING.kv_append(cache._native, k, v, q, inv_freq, interleaved, position_offset, q_out, positions, pair_axis)
     if type(r) is int:
         raise FAError(r, "fa_kv_append")
     return r
@@ -575,7 +792,7 @@ def kv_append(cache, k, v, q=None, inv_freq=None, interleaved: bool = False, pos
 
 def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None, return_lse: bool = True,
                   workspace=None, stream=None):
-    """O, LSE = attention of q [B, Hq, T, D] over a PagedKV.
+    """O, LSE = attention of q [B, Hq, T, D] over a PagedKV or PagedKV4.
 
     Hq is a multiple of the cache's Hkv.  causal: the queries are the last T
     tokens of their sequences; otherwise each sees all seq_len keys.  Queries
@@ -587,7 +804,7 @@ def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None,
     cache.workspace_bytes(Hq, T) bytes) is allocated here when not given.
     """
     if stream is not None:
-        with _stream_context(cache, stream):
+        with _stream_context(cache.device, stream):
             return forward_paged(q, cache, causal, scale, out, lse, return_lse, workspace)
     r = _BINDING.forward(cache._native, q, None, 0, causal, scale, out, lse, return_lse, workspace)
     if type(r) is int:
@@ -606,7 +823,7 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     cache.workspace_bytes(Hq, T, prefix_len) bytes.
     """
     if stream is not None:
-        with _stream_context(cache, stream):
+        with _stream_context(cache.device, stream):
             return forward_shared_prefix(q, cache, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace)
     r = _BINDING.forward(cache._native, q, prefix_table, prefix_len, causal, scale, out, lse, return_lse, workspace)
     if type(r) is int:
@@ -614,7 +831,190 @@ def forward_shared_prefix(q, cache, prefix_table, prefix_len: int, causal: bool 
     return r
 
 
+def kv_read(cache, T: int, stream=None):
+    """Keys and values [B, Hkv, T, D] of the last T tokens of every sequence, as the
+    cache (PagedKV or PagedKV4) holds them; tokens that a sequence does not have are
+    zero."""
+    if stream is not None:
+        with _stream_context(cache.device, stream):
+            return kv_read(cache, T)
+    r = _BINDING.kv_read(cache._native, T)
+    if type(r) is int:
+        raise FAError(r, "fa_kv_read")
+    return r
+
+
+# ---------------------------------------------------------------- pages
+def _layers(cache):
+    """The caches of a call, which share one table."""
+    if not isinstance(cache, (list, tuple)):
+        return (cache,)
+    if not cache:
+        raise ValueError("at least one cache must be given")
+    first = cache[0]
+    for c in cache[1:]:
+        if (c.block_table is not first.block_table or c.seq_len is not first.seq_len
+                or c._c.num_pages != first._c.num_pages or c._c.page_size != first._c.page_size):
+            raise ValueError("the caches of one call must share block_table and seq_len and have pools of one size")
+    return cache
+
+
+def kv_grow(cache, refs, tokens, stream=None):
+    """Every sequence b grows by tokens[b] and gets the pages for them (the lowest
+    free ones, in the order of the sequences), so that kv_append() can follow.
+
+    cache: a PagedKV or PagedKV4, or a list of those that share block_table and seq_len
+    (a model's layers).  refs: int32 CUDA tensor [pages], how often each page is used: once per
+    table entry in front of a sequence's length, and whatever the caller adds (a
+    prefix's pages, say); 0: free.  tokens: int32 CUDA tensor [B].  block_table, seq_len and
+    refs are updated.  Returns an int32 tensor [B]: how many pages a sequence got, -2 if
+    it was not grown because its table row or the free pages do not suffice.  Runs
+    asynchronously, like all page operators: nothing waits for the GPU.
+    """
+    cache = _layers(cache)
+    if stream is not None:
+        with _stream_context(cache[0].device, stream):
+            return kv_grow(cache, refs, tokens)
+    r = _BINDING.grow(cache[0]._native, refs, tokens)
+    if type(r) is int:
+        raise FAError(r, "fa_kv_grow")
+    return r
+
+
+def kv_free(cache, refs, rows, stream=None):
+    """The sequences in `rows` (int32 CUDA tensor) give up their pages: refs falls by one
+    for each, their block_table entries become -1 and their seq_len 0.  cache, refs: as
+    in kv_grow()."""
+    cache = _layers(cache)
+    if stream is not None:
+        with _stream_context(cache[0].device, stream):
+            return kv_free(cache, refs, rows)
+    r = _BINDING.free(cache[0]._native, refs, rows)
+    if r != FA_OK:
+        raise FAError(r, "fa_kv_free")
+
+
+def kv_fork(cache, refs, parent, child, stream=None):
+    """Sequence child[i] becomes what parent[i] is.  Full pages are shared, and a last
+    page that is part full is copied (in every cache of a list), since both will write
+    behind it.
+
+    parent, child: int32 CUDA tensors of one length; a child is empty (kv_free()).
+    cache, refs: as in kv_grow().  Returns an int32 tensor: the page that was copied
+    to, -1 where none had to be, -2 where the fork was refused (no free page, a child
+    that is not empty, that comes twice or is another fork's parent, no such row).
+    """
+    cache = _layers(cache)
+    if stream is not None:
+        with _stream_context(cache[0].device, stream):
+            return kv_fork(cache, refs, parent, child)
+    r = _BINDING.fork(cache[0]._native, refs, parent, child)
+    if type(r) is int:
+        raise FAError(r, "fa_kv_fork")
+    src, dst = r
+    for c in cache:
+        copy_pages(c, src, dst)
+    return dst
+
+
+def kv_compact(cache, refs, stream=None):
+    """The pages in use move to the front of the pool (of every cache of a list): with L
+    of them, those from page L on to the free ones in front, both in order.
+
+    cache, refs: as in kv_grow().  Returns an int32 tensor [pages]: each page's number
+    afterwards, -1 for a free one, with which tables of the caller's own are mapped.
+    """
+    cache = _layers(cache)
+    if stream is not None:
+        with _stream_context(cache[0].device, stream):
+            return kv_compact(cache, refs)
+    r = _BINDING.compact(cache[0]._native, refs)
+    if type(r) is int:
+        raise FAError(r, "fa_kv_compact")
+    moved, src, dst, count = r
+    for c in cache:
+        copy_pages(c, src, dst, count)
+    return moved
+
+
+def copy_pages(cache, src, dst, count=None, stream=None):
+    """Page src[i] of the cache's pools to page dst[i], keys and values (and scales) of
+    all heads and slots.
+
+    src, dst: int32 CUDA tensors of one length; pairs with a number outside the pool are
+    skipped, and no page may be the target of two pairs or of one and the source of
+    another.  count: int32 CUDA tensor of one entry, how many pairs there are if not all.
+    """
+    if stream is not None:
+        with _stream_context(cache.device, stream):
+            return copy_pages(cache, src, dst, count)
+    r = _BINDING.copy_pages(cache._native, src, dst, count)
+    if r != FA_OK:
+        raise FAError(r, "fa_copy_pages")
+
+
 # ------------------------------------------------------------- autograd
+def _turned(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse):
+    r = (_BINDING or _binding()).rotary(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse)
+    if type(r) is int:
+        raise FAError(r, "fa_rotary")
+    return r
+
+
+def _rotary_function():
+    import torch
+
+    class _Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse):
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(inv_freq, positions, pair_axis)
+            ctx.how = interleaved, position_offset, inverse
+            return _turned(q, k, inv_freq, positions, pair_axis, *ctx.how)
+
+        @staticmethod
+        def backward(ctx, d_q, d_k):
+            if d_q is None and d_k is None:
+                return (None,) * 8
+            interleaved, position_offset, inverse = ctx.how
+            turned = _Rotary.apply(d_q, d_k, *ctx.saved_tensors, interleaved, position_offset, not inverse)
+            return *turned, None, None, None, None, None, None
+
+    return _Rotary
+
+
+_ROTARY = None
+
+
+def rotary(q, inv_freq, positions=None, k=None, pair_axis=None, interleaved: bool = False, position_offset: int = 0,
+           stream=None):
+    """q, or (q, k), turned by their positions: a differentiable torch operation, for
+    attention() and forward().
+
+    q: bf16 or fp16 CUDA tensor [B, Hq, T, D] (D a multiple of 8 up to 256), k: [B, Hkv,
+    T, D], any strides; the results are contiguous.  inv_freq: float32 CUDA tensor of the
+    angles per position, one per pair (2 * numel <= D elements of a head turn); pairs are
+    (p, p + numel), or neighbours if interleaved.  positions: int32 CUDA tensor [B, T], or
+    [axes, B, T] for positions on several axes (time, height and width, say); None: 0, 1,
+    2 ...  pair_axis: int32 CUDA tensor, the axis that each pair turns by (a pair whose
+    entry is no axis does not turn).  position_offset is added to every position.
+    Gradients reach q and k.
+    """
+    global _ROTARY
+    import torch
+
+    if stream is not None:
+        with _stream_context(q.device, stream):
+            return rotary(q, inv_freq, positions, k, pair_axis, interleaved, position_offset)
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if _ROTARY is None:
+            _ROTARY = _rotary_function()
+        r = _ROTARY.apply(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, False)
+    else:
+        r = _turned(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, False)
+    return r[0] if k is None else r
+
+
 def _attention_function():
     import torch
 

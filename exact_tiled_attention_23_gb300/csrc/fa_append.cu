@@ -1,12 +1,14 @@
-// fa_append.cu -- keys and values of new tokens into a paged cache, with the
-// position rotation of keys and queries applied on the way.
+// fa_append.cu -- keys and values of new tokens into a paged cache, of 16 or of 4 bits
+// (fa_four.cuh), with the position rotation of keys and queries applied on the way;
+// and the rotation alone.
 //
-// Token t of sequence b has the index i = seq_len[b] - T + t and the position
-// n = offset + i.  Pair p of its key (and query) head, (x, y), turns by the
-// angle a = n * inv_freq[p]:
-//     x' = x cos a - y sin a,    y' = y cos a + x sin a,
-// and the key and value go to slot i % page_size of page table[b][i / page_size].
+// Token t of sequence b has the index i = seq_len[b] - T + t; it turns by the position
+// n = offset + i, or by positions that the caller gives, and its key and value go to
+// slot i % page_size of page table[b][i / page_size].
 //
+// Pair p of a head, (x, y), turns by the angle a = n * inv_freq[p], n the token's
+// position (on the pair's axis, where there are several):
+//     x' = x cos a - y sin a,    y' = y cos a + x sin a.
 // A far position times a frequency loses its angle in fp32 (a product of 10^5
 // is good to 2^-7 radians), so the angle is kept as a fraction of a turn in 64
 // bits: inv_freq[p] / 2pi as a fixed-point number F of 2^-64 turns, and n * F
@@ -20,13 +22,13 @@
 // heads.  Two prompts of 8192 tokens, 32 query and 8 key heads, D = 128: 403 MB in
 // 62 us, 6.5 TB/s (a copy: 6.8).  One token: 3 us, a launch and four waits in turn
 // (length, page, values, stores).
-#include "fa_paged.h"
-#include "sm103_ptx.cuh"
+#include "fa_four.cuh"
 
 namespace fa {
 
 namespace {
 
+// Threads of a CTA that turns a token's heads.
 constexpr int kThreads = 128;
 
 // 2^128 / (2 pi): the bits of 1 / (2 pi) after the binary point.
@@ -81,6 +83,111 @@ __device__ __forceinline__ float widen1(uint16_t w)
 // 16-byte units; the same with any even rot.
 enum PairMode { kNeighbours = 0, kHalves = 1, kHalvesOdd = 2 };
 
+// The cosines and sines of token t of sequence b, `at` its place in the sequence,
+// into cs[rot / 2].
+__device__ __forceinline__ void turns_of(const TurnParams &p, int64_t b, int t, int64_t at, float2 *cs)
+{
+    for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) {
+        int64_t n = at;
+        float f = p.inv_freq[j];
+        if (p.pos) {
+            const int axis = p.pair_axis ? p.pair_axis[j] : 0;
+            const bool on = axis >= 0 && axis < p.axes;    // a pair of no axis does not turn
+            n = on ? p.pos[axis * p.pos_s[0] + b * p.pos_s[1] + t * p.pos_s[2]] : 0;
+            if (!on) f = 0.f;
+        }
+        float2 x = turn(p.offset + n, f);
+        if (p.inverse) x.y = -x.y;
+        cs[j] = x;
+    }
+}
+
+// Turns `heads` heads of D elements by cs, from source(head) to target(head), which
+// may be one place; all threads of the CTA call it.
+template <bool kF16, int kMode, typename Source, typename Target>
+__device__ __forceinline__ void turn_heads(int heads, int D, int rot, const float2 *cs, const Source &source,
+                                           const Target &target)
+{
+    const int half = rot / 2, units = D / 8;
+    if constexpr (kMode == kHalves) {
+        // a task is 8 pairs (two units), or one unit past the rotated part
+        const int pairs = half / 8, tasks = pairs + (D - rot) / 8;
+        for (int e = threadIdx.x; e < heads * tasks; e += kThreads) {
+            const int head = e / tasks, u = e % tasks;
+            const uint16_t *src = source(head);
+            uint16_t *dst = target(head);
+            if (u < pairs) {
+                const uint4 wx = *reinterpret_cast<const uint4 *>(src + u * 8);
+                const uint4 wy = *reinterpret_cast<const uint4 *>(src + half + u * 8);
+                float x[8], y[8], x2[8], y2[8];
+                widen8<kF16>(wx, x);
+                widen8<kF16>(wy, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 a = cs[u * 8 + j];
+                    x2[j] = x[j] * a.x - y[j] * a.y;
+                    y2[j] = y[j] * a.x + x[j] * a.y;
+                }
+                *reinterpret_cast<uint4 *>(dst + u * 8) = narrow8<kF16>(x2);
+                *reinterpret_cast<uint4 *>(dst + half + u * 8) = narrow8<kF16>(y2);
+            } else {
+                const int d = rot + (u - pairs) * 8;
+                *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
+            }
+        }
+    } else if constexpr (kMode == kNeighbours) {
+        for (int e = threadIdx.x; e < heads * units; e += kThreads) {
+            const int head = e / units, u = e % units;
+            const uint4 w = *reinterpret_cast<const uint4 *>(source(head) + u * 8);
+            uint4 out = w;
+            if (u * 8 < rot) {
+                float x[8], r[8];
+                widen8<kF16>(w, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = u * 8 + 2 * j < rot;
+                    const float2 a = in ? cs[u * 4 + j] : make_float2(1.f, 0.f);
+                    r[2 * j] = in ? x[2 * j] * a.x - x[2 * j + 1] * a.y : x[2 * j];
+                    r[2 * j + 1] = in ? x[2 * j + 1] * a.x + x[2 * j] * a.y : x[2 * j + 1];
+                }
+                out = narrow8<kF16>(r);
+            }
+            *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
+        }
+    } else {
+        // The halves of a pair are other threads' elements, which q_out = q
+        // overwrites: whole heads at a time, all read before any is written.
+        const int per = kThreads / units, mine = threadIdx.x / units, u = threadIdx.x % units;
+        for (int first = 0; first < heads; first += per) {
+            const int head = first + mine;
+            const bool on = mine < per && head < heads;
+            uint4 out = make_uint4(0u, 0u, 0u, 0u);
+            if (on) {
+                const uint16_t *src = source(head);
+                out = *reinterpret_cast<const uint4 *>(src + u * 8);
+                if (u * 8 < rot) {
+                    float r[8];
+                    widen8<kF16>(out, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int d = u * 8 + j;
+                        if (d < half) {
+                            const float y = widen1<kF16>(src[d + half]);
+                            r[j] = r[j] * cs[d].x - y * cs[d].y;
+                        } else if (d < rot) {
+                            const float y = widen1<kF16>(src[d - half]);
+                            r[j] = r[j] * cs[d - half].x + y * cs[d - half].y;
+                        }
+                    }
+                    out = narrow8<kF16>(r);
+                }
+            }
+            __syncthreads();
+            if (on) *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
+        }
+    }
+}
+
 // One CTA per token: its cosines and sines are computed once for all heads,
 // then each thread moves 16-byte units of q, k and v.
 template <bool kF16, int kMode>
@@ -91,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     const int64_t b = blockIdx.x / p.T;
     const int t = (int)(blockIdx.x % p.T);
     const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
-    const int half = p.rot / 2, D = p.c.D, Hkv = p.c.Hkv;
+    const int D = p.c.D, Hkv = p.c.Hkv;
     const int units = D / 8;
 
     if (i < 0) {                                            // no token here: its query is zero
@@ -106,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     if (at / size < (uint32_t)p.c.table_width) page = p.c.table[b * p.c.table_stride + at / size];
     const bool stored = page >= 0 && page < p.c.num_pages;   // otherwise the key and value are dropped
     const int64_t row = stored ? page * p.c.s_page + (int64_t)(at % size) * p.c.s_slot : 0;
-    for (int j = threadIdx.x; j < half; j += kThreads) cs[j] = turn(p.offset + i, p.inv_freq[j]);
+    turns_of(p.turn, b, t, i, cs);
     __syncthreads();
 
     // heads 0 .. Hkv-1: keys; Hkv .. Hkv+Hq-1: queries; then values
@@ -127,94 +234,161 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
             *reinterpret_cast<uint4 *>(p.c.v + row + head * p.c.s_head + u * 8) =
                 *reinterpret_cast<const uint4 *>(p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2] + u * 8);
         }
-    if constexpr (kMode == kHalves) {
-        // a task is 8 pairs (two units), or one unit past the rotated part
-        const int pairs = half / 8, tasks = pairs + (D - p.rot) / 8;
-        for (int e = threadIdx.x; e < (k_heads + q_heads) * tasks; e += kThreads) {
-            const int head = e / tasks, u = e % tasks;
-            const uint16_t *src = source(head);
-            uint16_t *dst = target(head);
-            if (u < pairs) {
-                const uint4 wx = *reinterpret_cast<const uint4 *>(src + u * 8);
-                const uint4 wy = *reinterpret_cast<const uint4 *>(src + half + u * 8);
-                float x[8], y[8], x2[8], y2[8];
-                widen8<kF16>(wx, x);
-                widen8<kF16>(wy, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 a = cs[u * 8 + j];
-                    x2[j] = x[j] * a.x - y[j] * a.y;
-                    y2[j] = y[j] * a.x + x[j] * a.y;
-                }
-                *reinterpret_cast<uint4 *>(dst + u * 8) = narrow8<kF16>(x2);
-                *reinterpret_cast<uint4 *>(dst + half + u * 8) = narrow8<kF16>(y2);
-            } else {
-                const int d = p.rot + (u - pairs) * 8;
-                *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
-            }
-        }
-    } else if constexpr (kMode == kNeighbours) {
-        for (int e = threadIdx.x; e < (k_heads + q_heads) * units; e += kThreads) {
-            const int head = e / units, u = e % units;
-            const uint4 w = *reinterpret_cast<const uint4 *>(source(head) + u * 8);
-            uint4 out = w;
-            if (u * 8 < p.rot) {
-                float x[8], r[8];
-                widen8<kF16>(w, x);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = u * 8 + 2 * j < p.rot;
-                    const float2 a = in ? cs[u * 4 + j] : make_float2(1.f, 0.f);
-                    r[2 * j] = in ? x[2 * j] * a.x - x[2 * j + 1] * a.y : x[2 * j];
-                    r[2 * j + 1] = in ? x[2 * j + 1] * a.x + x[2 * j] * a.y : x[2 * j + 1];
-                }
-                out = narrow8<kF16>(r);
-            }
-            *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
-        }
-    } else {
-        // The halves of a pair are other threads' elements, which q_out = q
-        // overwrites: whole heads at a time, all read before any is written.
-        const int per = kThreads / units, mine = threadIdx.x / units, u = threadIdx.x % units;
-        for (int first = 0; first < k_heads + q_heads; first += per) {
-            const int head = first + mine;
-            const bool on = mine < per && head < k_heads + q_heads;
-            uint4 out = make_uint4(0u, 0u, 0u, 0u);
-            if (on) {
-                const uint16_t *src = source(head);
-                out = *reinterpret_cast<const uint4 *>(src + u * 8);
-                if (u * 8 < p.rot) {
-                    float r[8];
-                    widen8<kF16>(out, r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int d = u * 8 + j;
-                        if (d < half) {
-                            const float y = widen1<kF16>(src[d + half]);
-                            r[j] = r[j] * cs[d].x - y * cs[d].y;
-                        } else if (d < p.rot) {
-                            const float y = widen1<kF16>(src[d - half]);
-                            r[j] = r[j] * cs[d - half].x + y * cs[d - half].y;
-                        }
-                    }
-                    out = narrow8<kF16>(r);
-                }
-            }
-            __syncthreads();
-            if (on) *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
-        }
-    }
+    turn_heads<kF16, kMode>(k_heads + q_heads, D, p.turn.rot, cs, source, target);
 }
 
 template <bool kF16>
 cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 {
     const dim3 grid((unsigned)((int64_t)p.B * p.T));
-    const size_t smem = (size_t)(p.rot / 2) * sizeof(float2);
-    if (p.interleaved || p.rot == 0)
+    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
+    if (p.turn.interleaved || p.turn.rot == 0)
         return launch_behind(append_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
-    if (p.rot % 16 == 0) return launch_behind(append_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
+    if (p.turn.rot % 16 == 0) return launch_behind(append_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
     return launch_behind(append_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
+}
+
+// ---------------------------------------------------------------- 4 bits
+// A key's pairs turn in fp32 and the result is rounded once, to 4 bits.  A thread
+// takes a group of 16 elements of a key or value, so that no thread needs another's
+// largest value (a key's partner elements are read a second time, from the L1).
+
+// Elements 8 u .. 8 u + 7 of a turned head.
+template <bool kF16, int kMode>
+__device__ __forceinline__ void turned8(const uint16_t *src, int u, int rot, const float2 *cs, float (&x)[8])
+{
+    widen8<kF16>(*reinterpret_cast<const uint4 *>(src + u * 8), x);
+    if (u * 8 >= rot) return;
+    const int half = rot / 2;
+    if constexpr (kMode == kHalves) {
+        const bool first = u * 8 < half;
+        const int from = first ? u * 8 : u * 8 - half;
+        float y[8];
+        widen8<kF16>(*reinterpret_cast<const uint4 *>(src + (first ? from + half : from)), y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 a = cs[from + j];
+            x[j] = first ? x[j] * a.x - y[j] * a.y : x[j] * a.x + y[j] * a.y;
+        }
+    } else if constexpr (kMode == kNeighbours) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (u * 8 + 2 * j >= rot) continue;
+            const float2 a = cs[u * 4 + j];
+            const float r = x[2 * j] * a.x - x[2 * j + 1] * a.y;
+            x[2 * j + 1] = x[2 * j + 1] * a.x + x[2 * j] * a.y;
+            x[2 * j] = r;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int d = u * 8 + j;
+            if (d < half)
+                x[j] = x[j] * cs[d].x - widen1<kF16>(src[d + half]) * cs[d].y;
+            else if (d < rot)
+                x[j] = x[j] * cs[d - half].x + widen1<kF16>(src[d - half]) * cs[d - half].y;
+        }
+    }
+}
+
+template <bool kF16, int kMode>
+__global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p)
+{
+    extern __shared__ float2 cs[];                          // [rot / 2]
+    ptx::wait_for_primary();
+    const int64_t b = blockIdx.x / p.T;
+    const int t = (int)(blockIdx.x % p.T);
+    const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
+    const int D = p.c.D, Hkv = p.c.Hkv, units = D / 8;
+
+    if (i < 0) {                                            // no token here: its query is zero
+        if (p.q)
+            for (int e = threadIdx.x; e < p.Hq * units; e += kThreads)
+                *reinterpret_cast<uint4 *>(p.q_out + b * p.qo_s[0] + (e / units) * p.qo_s[1] + t * p.qo_s[2] +
+                                           (e % units) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const uint32_t at = (uint32_t)i, size = (uint32_t)p.c.page_size;
+    int page = -1;
+    if (at / size < (uint32_t)p.c.table_width) page = p.c.table[b * p.c.table_stride + at / size];
+    const bool stored = page >= 0 && page < p.c.num_pages;   // otherwise the key and value are dropped
+    turns_of(p.turn, b, t, i, cs);
+    __syncthreads();
+
+    if (stored) {
+        const int64_t slot = at % size;
+        const int64_t row = page * p.c.s_page + slot * p.c.s_slot, scales = page * p.c.t_page + slot * p.c.t_slot;
+        const int groups = padded4(D) / kFourGroup;
+        for (int e = threadIdx.x; e < 2 * Hkv * groups; e += kThreads) {
+            const int which = e / groups, g = e % groups, head = which < Hkv ? which : which - Hkv;
+            float x[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int u = 2 * g + h;
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = 0.f;      // past the head: padding
+                if (u < units) {
+                    if (which < Hkv)
+                        turned8<kF16, kMode>(p.k + b * p.k_s[0] + head * p.k_s[1] + t * p.k_s[2], u, p.turn.rot, cs, y);
+                    else
+                        widen8<kF16>(*reinterpret_cast<const uint4 *>(p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2] + u * 8), y);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[8 * h + j] = y[j];
+            }
+            uint32_t code;
+            const uint2 w = to_four(x, code);
+            *reinterpret_cast<uint2 *>((which < Hkv ? p.c.k : p.c.v) + row + head * p.c.s_head + g * 8) = w;
+            ((which < Hkv ? p.c.ks : p.c.vs) + scales + head * p.c.t_head)[g] = (uint8_t)code;
+        }
+    }
+    const auto source = [&](int head) -> const uint16_t * { return p.q + b * p.q_s[0] + head * p.q_s[1] + t * p.q_s[2]; };
+    const auto target = [&](int head) -> uint16_t * { return p.q_out + b * p.qo_s[0] + head * p.qo_s[1] + t * p.qo_s[2]; };
+    turn_heads<kF16, kMode>(p.q ? p.Hq : 0, D, p.turn.rot, cs, source, target);
+}
+
+template <bool kF16>
+cudaError_t launch4(const Append4Params &p, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)p.B * p.T));
+    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
+    if (p.turn.interleaved || p.turn.rot == 0)
+        return launch_behind(append4_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
+    if (p.turn.rot % 16 == 0) return launch_behind(append4_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
+    return launch_behind(append4_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
+}
+
+// ---------------------------------------------------------------- no cache
+template <bool kF16, int kMode>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p)
+{
+    extern __shared__ float2 cs[];                          // [rot / 2]
+    ptx::wait_for_primary();
+    const int64_t b = blockIdx.x / p.T;
+    const int t = (int)(blockIdx.x % p.T);
+    turns_of(p.turn, b, t, t, cs);
+    __syncthreads();
+    const auto source = [&](int head) -> const uint16_t * {
+        const int i = head < p.H[0] ? 0 : 1;
+        return p.x[i] + b * p.x_s[i][0] + (head - i * p.H[0]) * p.x_s[i][1] + t * p.x_s[i][2];
+    };
+    const auto target = [&](int head) -> uint16_t * {
+        const int i = head < p.H[0] ? 0 : 1;
+        return p.y[i] + b * p.y_s[i][0] + (head - i * p.H[0]) * p.y_s[i][1] + t * p.y_s[i][2];
+    };
+    turn_heads<kF16, kMode>(p.H[0] + p.H[1], p.D, p.turn.rot, cs, source, target);
+}
+
+template <bool kF16>
+cudaError_t launch_turn(const RotaryParams &p, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)p.B * p.T));
+    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
+    if (p.turn.interleaved || p.turn.rot == 0)
+        return launch_behind(rotary_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
+    if (p.turn.rot % 16 == 0) return launch_behind(rotary_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
+    return launch_behind(rotary_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
 }
 
 }  // namespace
@@ -222,6 +396,16 @@ cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream)
 {
     return p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+cudaError_t launch_append4(const Append4Params &p, cudaStream_t stream)
+{
+    return p.f16 ? launch4<true>(p, stream) : launch4<false>(p, stream);
+}
+
+cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream)
+{
+    return p.f16 ? launch_turn<true>(p, stream) : launch_turn<false>(p, stream);
 }
 
 }  // namespace fa

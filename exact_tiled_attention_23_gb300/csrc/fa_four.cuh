@@ -1,0 +1,91 @@
+// fa_four.cuh -- the numbers of a 4-bit cache.
+//
+// A row is padded to 64, 128 or 256 elements and held in groups of 16: element d is
+// u s, where u has 4 bits (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6; an even d is the lower half of its byte) and the group's scale s has 8
+// (5 exponent bits, 3 mantissa bits: the upper bits of an IEEE half, whose sign is
+// never set).  s is largest / 6, rounded to nearest, and u is x / s, rounded to
+// nearest; halfway goes to the even mantissa, and past 6 to 6.
+//
+// u s has at most 6 significant bits and lies between 2^-18 and 6 * 10240 = 61440, so
+// that it is exact as an IEEE half and as a bf16 number.
+#pragma once
+
+#include "fa_paged.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+// The largest scale, 10240: what it stands for with u = 6 is below fp16's largest.
+constexpr uint32_t kLargestScale = 226;
+
+// The scale for a group whose largest magnitude is `largest` (infinities: the
+// largest scale; a NaN among the values is not counted).
+__device__ __forceinline__ uint32_t scale_code(float largest)
+{
+    const float t = __fdiv_rn(largest, 6.f);
+    if (t < 6.103515625e-5f) return (uint32_t)__float2int_rn(t * 131072.f);     // below 2^-14: multiples of 2^-17
+    const uint32_t bits = __float_as_uint(t);
+    const uint32_t up = (bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20;          // 3 mantissa bits, to nearest
+    return min(up - ((127u - 15u) << 3), kLargestScale);
+}
+
+__device__ __forceinline__ float scale_value(uint32_t code)
+{
+    return __half2float(__ushort_as_half((unsigned short)(code << 7)));
+}
+
+// 16 values in 4 bits each, and their scale.
+__device__ __forceinline__ uint2 to_four(const float (&x)[16], uint32_t &code)
+{
+    float largest = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) largest = fmaxf(largest, fabsf(x[i]));
+    code = scale_code(largest);
+    if (code == 0) return make_uint2(0u, 0u);
+    const float s = scale_value(code);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        w[h] = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // (a division: x / s halfway between two numbers stays halfway)
+            const float a = __fdiv_rn(x[8 * h + 2 * i], s), b = __fdiv_rn(x[8 * h + 2 * i + 1], s);
+            w[h] |= ptx::pack_e2m1x2(a, b) << (8 * i);
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// 8 elements of 4 bits times `scale` (a pair of equal halves), as 16-bit pairs of
+// neighbours.
+__device__ __forceinline__ void from_four(uint32_t w, __half2 scale, __half2 (&x)[4])
+{
+    uint32_t r[4];
+    ptx::unpack_e2m1x8(w, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __hmul2(*reinterpret_cast<const __half2 *>(&r[i]), scale);
+}
+
+// The same values in the 16-bit type of the queries.
+template <bool kF16>
+__device__ __forceinline__ uint4 rows_from_four(uint32_t w, uint32_t code)
+{
+    const uint32_t pair = (code << 7) * 0x10001u;
+    __half2 x[4];
+    from_four(w, *reinterpret_cast<const __half2 *>(&pair), x);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kF16) {
+            r[i] = *reinterpret_cast<const uint32_t *>(&x[i]);
+        } else {
+            const float2 f = __half22float2(x[i]);
+            r[i] = ptx::pack_bf16x2(f.x, f.y);
+        }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+}  // namespace fa

@@ -1,0 +1,28 @@
+// fa_four_rows.h -- parameters of the attention kernels over a 4-bit cache, shared by
+// their host checks (fa_four_api.cu) and the kernels (not part of the public C ABI).
+#pragma once
+
+#include "fa_paged.h"
+
+namespace fa {
+
+// p.c has the table, the lengths and the sizes; c the pools.
+struct FourParams {
+    PagedParams p;
+    PagedCache4 c;
+};
+
+struct WidenParams {
+    PagedCache4 c;
+    uint16_t *k, *v;                   // [B * width, Hkv, page_size, D]
+    int32_t *table, *seq_len;          // [B, width], [B]
+    int f16;
+};
+
+int four_rows_per_tile(int D, int64_t rows);
+int four_rows_chunk(int D);
+int four_rows_ctas_per_sm(int D, int rows);
+cudaError_t launch_four_rows(const FourParams &f, int ctas, cudaStream_t stream);
+cudaError_t launch_widen_pages(const WidenParams &p, int64_t pages, cudaStream_t stream);
+
+}  // namespace fa

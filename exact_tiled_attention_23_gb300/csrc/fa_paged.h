@@ -47,14 +47,73 @@ struct PagedCache {
     int Hkv, D;
 };
 
+// How a token's heads turn (fa_append.cu).
+struct TurnParams {
+    const float *inv_freq;             // [rot / 2]
+    const int32_t *pos;                // positions by axis, sequence, token; null: the place in the sequence
+    int64_t pos_s[3];
+    const int32_t *pair_axis;          // [rot / 2], null: axis 0
+    int64_t offset;                    // added to every position
+    int axes, rot, interleaved, inverse;
+};
+
 struct AppendParams {
     PagedCache c;
+    TurnParams turn;
     const uint16_t *k, *v, *q;         // [B, H, T, D] through the strides below; q may be null
     uint16_t *q_out;
     int64_t k_s[3], v_s[3], q_s[3], qo_s[3];   // batch, head, token
-    const float *inv_freq;             // [rot / 2]
-    int64_t offset;                    // position of a sequence's first key
-    int B, T, Hq, rot, interleaved, f16;
+    int B, T, Hq, f16;
+};
+
+// A row of a 4-bit cache: padded to 64, 128 or 256 elements, groups of 16.
+constexpr int kFourGroup = 16;
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int padded4(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// A 4-bit cache through the page table; strides in bytes.
+struct PagedCache4 {
+    uint8_t *k, *v, *ks, *vs;
+    int64_t s_page, s_head, s_slot;    // of k and v
+    int64_t t_page, t_head, t_slot;    // of their scales
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *seq_len;
+    int table_width;
+    int num_pages, page_size;
+    FastDiv by_page;                   // page_size
+    int Hkv, D;
+};
+
+struct Append4Params {
+    PagedCache4 c;
+    TurnParams turn;
+    const uint16_t *k, *v, *q;         // [B, H, T, D] through the strides below; q may be null
+    uint16_t *q_out;
+    int64_t k_s[3], v_s[3], q_s[3], qo_s[3];   // batch, head, token
+    int B, T, Hq, f16;
+};
+
+// Positions of q and k turned without a cache.
+struct RotaryParams {
+    TurnParams turn;
+    const uint16_t *x[2];              // q, k: [B, H, T, D] through the strides below; H may be 0
+    uint16_t *y[2];
+    int64_t x_s[2][3], y_s[2][3];      // batch, head, token
+    int H[2];
+    int B, T, D, f16;
+};
+
+// The last T tokens of a cache, as 16-bit rows [B, Hkv, T, D] (a token that the
+// sequence does not have, or whose page is not there, is zero).
+struct ReadParams {
+    PagedCache c;                      // one of the two
+    PagedCache4 c4;
+    uint16_t *k, *v;
+    int64_t k_s[3], v_s[3];
+    int B, T, f16;
 };
 
 // Where a tile's partial states are: from which slot on, and how many.
@@ -241,6 +300,9 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 }
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_append4(const Append4Params &p, cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryParams &p, cudaStream_t stream);
+cudaError_t launch_read(const ReadParams &p, bool four, cudaStream_t stream);
 // (tk, tv are read only where p.box_rows > 0)
 cudaError_t launch_paged_rows(const PagedParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int ctas,
                               cudaStream_t stream);

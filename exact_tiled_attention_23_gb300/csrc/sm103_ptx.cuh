@@ -293,6 +293,24 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
+// Two fp32 values -> two e2m1 values in a byte (nearest even, at most 6 in
+// magnitude); `lo` in bits 0-3.
+__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The eight e2m1 values of `w` as f16x2 words of neighbours.
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&r)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+
 // The 16-bit pair of the operand type: f16 when kF16, else bf16.
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack16x2(float lo, float hi)

@@ -1,6 +1,6 @@
 // torch_binding.cpp -- torch tensors into the paged-cache entry points of
-// libfa.so: the work behind kv_append(), forward_paged() and
-// forward_shared_prefix() of the Python package.
+// libfa.so: the work behind kv_append(), forward_paged(), forward_shared_prefix(),
+// kv_read(), rotary() and the page operators of the Python package.
 //
 // A generation step is a few microseconds of GPU time, and the same checks,
 // allocations and argument passing took 15 to 19 us per call in Python (4 to 9
@@ -24,14 +24,23 @@
 
 namespace {
 
-using KvAppend = decltype(&fa_kv_append);
-using FwdSharedPrefix = decltype(&fa_fwd_shared_prefix);
-using WorkspaceBytes = decltype(&fa_fwd_shared_prefix_workspace_bytes);
-
 // The entry points of the libfa.so that the package has loaded.
-KvAppend g_kv_append = nullptr;
-FwdSharedPrefix g_fwd = nullptr;
-WorkspaceBytes g_workspace_bytes = nullptr;
+decltype(&fa_kv_append_at) g_kv_append = nullptr;
+decltype(&fa_kv_append_q4) g_kv_append_q4 = nullptr;
+decltype(&fa_fwd_shared_prefix) g_fwd = nullptr;
+decltype(&fa_fwd_shared_prefix_workspace_bytes) g_workspace_bytes = nullptr;
+decltype(&fa_fwd_paged_q4) g_fwd_q4 = nullptr;
+decltype(&fa_fwd_paged_q4_workspace_bytes) g_workspace_bytes_q4 = nullptr;
+decltype(&fa_kv_read) g_kv_read = nullptr;
+decltype(&fa_kv_read_q4) g_kv_read_q4 = nullptr;
+decltype(&fa_rotary) g_rotary = nullptr;
+decltype(&fa_pages_workspace_bytes) g_pages_bytes = nullptr;
+decltype(&fa_kv_grow) g_grow = nullptr;
+decltype(&fa_kv_free) g_free = nullptr;
+decltype(&fa_kv_fork) g_fork = nullptr;
+decltype(&fa_kv_compact) g_compact = nullptr;
+decltype(&fa_copy_pages) g_copy = nullptr;
+decltype(&fa_copy_pages_q4) g_copy_q4 = nullptr;
 
 // Calls on the default stream run one after another and share a workspace up
 // to this size; another stream's calls, or a graph captured on one, may run
@@ -44,6 +53,9 @@ struct Cache {
     at::ScalarType dtype;
     c10::DeviceIndex device;
     at::Tensor k, v, table, seq_len;       // what c points to
+    bool four = false;                     // a 4-bit cache: c4, and c's sizes and table
+    fa_paged_kv4 c4{};
+    at::Tensor ks, vs;
     std::mutex mutex;        // keeps the launches of two host threads' calls apart
     at::Tensor workspace;
 
@@ -52,7 +64,8 @@ struct Cache {
     bool in_place() const
     {
         return k.const_data_ptr() == c.k && v.const_data_ptr() == c.v && table.const_data_ptr() == c.table &&
-               seq_len.const_data_ptr() == c.seq_len;
+               seq_len.const_data_ptr() == c.seq_len &&
+               (!four || (ks.const_data_ptr() == c4.k_scales && vs.const_data_ptr() == c4.v_scales));
     }
 };
 
@@ -162,20 +175,92 @@ PyObject *new_cache(PyObject *, PyObject *args)
         }
     const at::Tensor &k = THPVariable_Unpack(x[0]), &seq_len = THPVariable_Unpack(x[3]);
     Cache *cache = new Cache{*reinterpret_cast<const fa_paged_kv *>(address), seq_len.numel(), k.scalar_type(),
-                             k.get_device(), k, THPVariable_Unpack(x[1]), THPVariable_Unpack(x[2]), seq_len, {}, {}};
+                             k.get_device(), k, THPVariable_Unpack(x[1]), THPVariable_Unpack(x[2]), seq_len};
     PyObject *capsule = PyCapsule_New(cache, kCapsule, free_cache);
     if (!capsule) delete cache;
     return capsule;
     END_HANDLE_TH_ERRORS
 }
 
-// kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out) ->
-// q_out (None without q), or a status
+// cache4(address of an fa_paged_kv4, k, v, k_scales, v_scales, table, seq_len, whether
+// queries are fp16) -> capsule
+PyObject *new_cache4(PyObject *, PyObject *args)
+{
+    HANDLE_TH_ERRORS
+    unsigned long long address;
+    PyObject *x[6];
+    int f16;
+    if (!PyArg_ParseTuple(args, "KOOOOOOp", &address, &x[0], &x[1], &x[2], &x[3], &x[4], &x[5], &f16)) return nullptr;
+    for (PyObject *o : x)
+        if (!THPVariable_Check(o)) {
+            PyErr_SetString(PyExc_TypeError, "the caches, scales, block_table and seq_len must be tensors");
+            return nullptr;
+        }
+    const fa_paged_kv4 &c4 = *reinterpret_cast<const fa_paged_kv4 *>(address);
+    fa_paged_kv c{};
+    c.k = c4.k;
+    c.v = c4.v;
+    c.num_pages = c4.num_pages;
+    c.page_size = c4.page_size;
+    c.Hkv = c4.Hkv;
+    c.D = c4.D;
+    c.table = c4.table;
+    c.table_stride = c4.table_stride;
+    c.table_width = c4.table_width;
+    c.seq_len = c4.seq_len;
+    const at::Tensor &k = THPVariable_Unpack(x[0]), &seq_len = THPVariable_Unpack(x[5]);
+    Cache *cache = new Cache{c, seq_len.numel(), f16 ? at::kHalf : at::kBFloat16, k.get_device(), k, THPVariable_Unpack(x[1]),
+                             THPVariable_Unpack(x[4]), seq_len, true, c4, THPVariable_Unpack(x[2]), THPVariable_Unpack(x[3])};
+    PyObject *capsule = PyCapsule_New(cache, kCapsule, free_cache);
+    if (!capsule) delete cache;
+    return capsule;
+    END_HANDLE_TH_ERRORS
+}
+
+// Positions and the axes of the pairs (either may be None) of tokens [B, T] on a device.
+struct Positions {
+    at::Tensor n, pair_axis;
+    fa_positions p{};
+    const fa_positions *get() const { return n.defined() ? &p : nullptr; }
+};
+
+bool positions_of(PyObject *object, PyObject *axes, int64_t B, int64_t T, int64_t pairs, const at::Device &device, Positions &x)
+{
+    if (object == Py_None) return axes == Py_None || value_error("pair_axis needs positions");
+    if (!THPVariable_Check(object)) {
+        PyErr_SetString(PyExc_TypeError, "positions must be a tensor");
+        return false;
+    }
+    x.n = THPVariable_Unpack(object);
+    const int64_t d = x.n.dim();
+    if (x.n.scalar_type() != at::kInt || x.n.device() != device || (d != 2 && d != 3) || x.n.size(d - 2) != B ||
+        x.n.size(d - 1) != T || (d == 3 && (x.n.size(0) < 1 || x.n.size(0) > INT32_MAX)))
+        return value_error("positions must be an int32 tensor [B, T] or [axes, B, T] on the same device");
+    x.p.n = x.n.const_data_ptr<int32_t>();
+    x.p.axes = d == 3 ? (int)x.n.size(0) : 1;
+    x.p.stride_axis = d == 3 ? x.n.stride(0) : 0;
+    x.p.stride_b = x.n.stride(d - 2);
+    x.p.stride_t = x.n.stride(d - 1);
+    if (axes == Py_None) return x.p.axes == 1 || value_error("positions of several axes need pair_axis");
+    if (!THPVariable_Check(axes)) {
+        PyErr_SetString(PyExc_TypeError, "pair_axis must be a tensor");
+        return false;
+    }
+    x.pair_axis = THPVariable_Unpack(axes);
+    if (x.pair_axis.scalar_type() != at::kInt || x.pair_axis.dim() != 1 || x.pair_axis.numel() != pairs || x.pair_axis.device() != device)
+        return value_error("pair_axis must be an int32 tensor with an entry for each of inv_freq's, on the same device");
+    x.pair_axis = x.pair_axis.contiguous();
+    x.p.pair_axis = x.pair_axis.const_data_ptr<int32_t>();
+    return true;
+}
+
+// kv_append(cache, k, v, q, inv_freq, interleaved, position_offset, q_out, positions,
+// pair_axis) -> q_out (None without q), or a status
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "kv_append takes 8 arguments");
+    if (n != 10) {
+        PyErr_SetString(PyExc_TypeError, "kv_append takes 10 arguments");
         return nullptr;
     }
     Cache *cache = cache_of(a[0]);
@@ -201,6 +286,8 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         value_error("sizes must fit 32 bits");
         return nullptr;
     }
+    Positions positions;
+    if (!positions_of(a[8], a[9], cache->B, T, freq.defined() ? freq.numel() : 0, k.device(), positions)) return nullptr;
     const fa_rows rk = rows_of(k), rv = rows_of(v);
     fa_rows rq{}, ro{};
     if (queries) {
@@ -210,9 +297,12 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n)
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
     fa_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = g_kv_append(&cache->c, &rk, &rv, queries ? &rq : nullptr, queries ? &ro : nullptr, (int)cache->B,
-                     queries ? (int)q.size(1) : 0, (int)T, freq.defined() ? freq.const_data_ptr<float>() : nullptr,
-                     freq.defined() ? 2 * (int)freq.numel() : 0, interleaved, offset, cache->dtype == at::kHalf, stream);
+    const auto run = [&](auto call, auto *c) {
+        return call(c, &rk, &rv, queries ? &rq : nullptr, queries ? &ro : nullptr, (int)cache->B, queries ? (int)q.size(1) : 0,
+                    (int)T, freq.defined() ? freq.const_data_ptr<float>() : nullptr, freq.defined() ? 2 * (int)freq.numel() : 0,
+                    interleaved, positions.get(), offset, cache->dtype == at::kHalf, stream);
+    };
+    st = cache->four ? run(g_kv_append_q4, &cache->c4) : run(g_kv_append, &cache->c);
     Py_END_ALLOW_THREADS
     if (st != FA_OK) return PyLong_FromLong(st);
     if (!queries) Py_RETURN_NONE;
@@ -252,6 +342,10 @@ PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         value_error("prefix_len must lie in [0, what prefix_table's pages hold]");
         return nullptr;
     }
+    if (cache->four && pages.defined()) {
+        value_error("a 4-bit cache takes no prefix_table: the sequences' tables may share a prefix's pages");
+        return nullptr;
+    }
     const int causal = PyObject_IsTrue(a[4]), return_lse = PyObject_IsTrue(a[8]);
     const double scale = a[5] == Py_None ? NAN : PyFloat_AsDouble(a[5]);
     if (causal < 0 || return_lse < 0 || PyErr_Occurred()) return nullptr;
@@ -288,7 +382,8 @@ PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         size = workspace.nbytes();
     } else {
-        size = g_workspace_bytes(&cache->c, (int)prefix, (int)B, (int)Hq, (int)T);
+        size = cache->four ? g_workspace_bytes_q4(&cache->c4, (int)B, (int)Hq, (int)T)
+                           : g_workspace_bytes(&cache->c, (int)prefix, (int)B, (int)Hq, (int)T);
         kept = stream == nullptr && size <= kKeptWorkspace;
         if (!kept) workspace = bytes(size);
     }
@@ -308,8 +403,11 @@ PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
             if (!cache->workspace.defined() || (size_t)cache->workspace.numel() < size) cache->workspace = bytes(size);
             workspace = cache->workspace;
         }
-        st = g_fwd(&rq, &cache->c, table, (int)prefix, &ro, lse_ptr, (int)B, (int)Hq, (int)T, causal, (float)scale,
-                   cache->dtype == at::kHalf, workspace.data_ptr(), size, stream);
+        const int f16 = cache->dtype == at::kHalf;
+        st = cache->four ? g_fwd_q4(&rq, &cache->c4, &ro, lse_ptr, (int)B, (int)Hq, (int)T, causal, (float)scale, f16,
+                                    workspace.data_ptr(), size, stream)
+                         : g_fwd(&rq, &cache->c, table, (int)prefix, &ro, lse_ptr, (int)B, (int)Hq, (int)T, causal,
+                                 (float)scale, f16, workspace.data_ptr(), size, stream);
     }
     if (st != FA_OK) return PyLong_FromLong(st);
     if (!return_lse) return THPVariable_Wrap(out);
@@ -321,23 +419,326 @@ PyObject *forward(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// init(addresses of fa_kv_append, fa_fwd_shared_prefix and
-// fa_fwd_shared_prefix_workspace_bytes)
+// kv_read(cache, T) -> (k, v), or a status
+PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 2) {
+        PyErr_SetString(PyExc_TypeError, "kv_read takes 2 arguments");
+        return nullptr;
+    }
+    Cache *cache = cache_of(a[0]);
+    if (!cache) return nullptr;
+    const long long T = PyLong_AsLongLong(a[1]);
+    if (T == -1 && PyErr_Occurred()) return nullptr;
+    if (T < 0 || T > INT32_MAX) {
+        value_error("T must lie in [0, 2^31)");
+        return nullptr;
+    }
+    const c10::cuda::CUDAGuard guard(cache->device);
+    const auto like = at::TensorOptions().dtype(cache->dtype).device(cache->k.device());
+    at::Tensor k = at::empty({cache->B, cache->c.Hkv, T, cache->c.D}, like), v = at::empty_like(k);
+    const fa_rows rk = rows_of(k), rv = rows_of(v);
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    fa_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = cache->four ? g_kv_read_q4(&cache->c4, &rk, &rv, (int)cache->B, (int)T, cache->dtype == at::kHalf, stream)
+                     : g_kv_read(&cache->c, &rk, &rv, (int)cache->B, (int)T, stream);
+    Py_END_ALLOW_THREADS
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject *pair = PyTuple_New(2);
+    if (!pair) return nullptr;
+    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(k));
+    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(v));
+    return pair;
+    END_HANDLE_TH_ERRORS
+}
+
+// rotary(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse)
+// -> (q, k) turned, None for one that is None, or a status
+PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "rotary takes 8 arguments");
+        return nullptr;
+    }
+    at::Tensor x[2], y[2];
+    fa_rows in[2]{}, out[2]{};
+    const at::Tensor *first = nullptr;
+    for (int i = 0; i < 2; ++i) {
+        if (a[i] == Py_None) continue;
+        if (!THPVariable_Check(a[i])) {
+            PyErr_SetString(PyExc_TypeError, "q and k must be tensors");
+            return nullptr;
+        }
+        x[i] = THPVariable_Unpack(a[i]);
+        if (!x[i].is_cuda() || x[i].dim() != 4 || (x[i].scalar_type() != at::kHalf && x[i].scalar_type() != at::kBFloat16)) {
+            value_error("q and k must be bf16 or fp16 CUDA tensors [B, heads, T, D]");
+            return nullptr;
+        }
+        if (!first) first = &x[i];
+        if (x[i].scalar_type() != first->scalar_type() || x[i].device() != first->device() || x[i].size(0) != first->size(0) ||
+            x[i].size(2) != first->size(2) || x[i].size(3) != first->size(3) || x[i].size(1) > INT32_MAX) {
+            value_error("q and k must share dtype, device, B, T and D");
+            return nullptr;
+        }
+    }
+    if (!first) {
+        value_error("q or k must be given");
+        return nullptr;
+    }
+    const int64_t B = first->size(0), T = first->size(2), D = first->size(3);
+    const c10::cuda::CUDAGuard guard(first->device());
+    if (!THPVariable_Check(a[2])) {
+        PyErr_SetString(PyExc_TypeError, "inv_freq must be a tensor");
+        return nullptr;
+    }
+    at::Tensor freq = THPVariable_Unpack(a[2]);
+    if (freq.scalar_type() != at::kFloat || freq.dim() != 1 || freq.device() != first->device() || freq.numel() > INT32_MAX / 2) {
+        value_error("inv_freq must be a float32 tensor of one dimension on the device of q and k");
+        return nullptr;
+    }
+    freq = freq.contiguous();
+    Positions positions;
+    if (!positions_of(a[3], a[4], B, T, freq.numel(), first->device(), positions)) return nullptr;
+    const int interleaved = PyObject_IsTrue(a[5]);
+    const long long offset = PyLong_AsLongLong(a[6]);
+    const int inverse = PyObject_IsTrue(a[7]);
+    if (interleaved < 0 || inverse < 0 || (offset == -1 && PyErr_Occurred())) return nullptr;
+    if (B > INT32_MAX || T > INT32_MAX || D > INT32_MAX) {
+        value_error("sizes must fit 32 bits");
+        return nullptr;
+    }
+    for (int i = 0; i < 2; ++i) {
+        if (!x[i].defined()) continue;
+        if (!followable(x[i])) x[i] = x[i].clone(at::MemoryFormat::Contiguous);
+        y[i] = at::empty(x[i].sizes(), at::TensorOptions().dtype(x[i].scalar_type()).device(x[i].device()));
+        in[i] = rows_of(x[i]);
+        out[i] = rows_of(y[i]);
+    }
+    const auto heads = [&](int i) { return x[i].defined() ? (int)x[i].size(1) : 0; };
+    void *stream = c10::cuda::getCurrentCUDAStream(first->get_device()).stream();
+    fa_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = g_rotary(&in[0], &out[0], &in[1], &out[1], (int)B, heads(0), heads(1), (int)T, (int)D, freq.const_data_ptr<float>(),
+                  2 * (int)freq.numel(), interleaved, positions.get(), offset, inverse, first->scalar_type() == at::kHalf, stream);
+    Py_END_ALLOW_THREADS
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject *pair = PyTuple_New(2);
+    if (!pair) return nullptr;
+    for (int i = 0; i < 2; ++i) {
+        PyObject *o = y[i].defined() ? THPVariable_Wrap(y[i]) : Py_NewRef(Py_None);
+        PyTuple_SET_ITEM(pair, i, o);
+    }
+    return pair;
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------- pages
+// An int32 vector of the cache's device, of `count` entries (< 0: any), contiguous.
+bool entries(PyObject *object, const char *what, int64_t count, const Cache &cache, bool written, at::Tensor &x)
+{
+    if (!THPVariable_Check(object)) {
+        PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
+        return false;
+    }
+    x = THPVariable_Unpack(object);
+    if (x.scalar_type() != at::kInt || x.dim() != 1 || !x.is_cuda() || x.get_device() != cache.device ||
+        (count >= 0 && x.numel() != count) || x.numel() > INT32_MAX || (written && !x.is_contiguous())) {
+        if (count >= 0)
+            PyErr_Format(PyExc_ValueError, "%s must be a%s int32 tensor with %lld entries on the cache's device", what,
+                         written ? " contiguous" : "n", (long long)count);
+        else
+            PyErr_Format(PyExc_ValueError, "%s must be an int32 tensor of one dimension on the cache's device", what);
+        return false;
+    }
+    x = x.contiguous();
+    return true;
+}
+
+bool table_of(const Cache &cache, PyObject *refs, at::Tensor &counts, fa_page_table &t)
+{
+    if (!entries(refs, "refs", cache.c.num_pages, cache, true, counts)) return false;
+    t = fa_page_table{const_cast<int32_t *>(cache.c.table), cache.c.table_stride, cache.c.table_width, (int)cache.B,
+                      const_cast<int32_t *>(cache.c.seq_len), counts.mutable_data_ptr<int32_t>(), cache.c.num_pages, cache.c.page_size};
+    return true;
+}
+
+at::Tensor numbers(const Cache &cache, int64_t n)
+{
+    return at::empty({n}, at::TensorOptions().dtype(at::kInt).device(cache.k.device()));
+}
+
+// run(workspace, bytes) with a workspace of a page operator: the cache's own on the
+// default stream, else a new one.
+template <typename Run>
+fa_status with_workspace(Cache &cache, const fa_page_table &t, int n, void *stream, const Run &run)
+{
+    const size_t size = g_pages_bytes(&t, n);
+    const auto bytes = [&] { return at::empty({(int64_t)size}, at::TensorOptions().dtype(at::kByte).device(cache.k.device())); };
+    const bool kept = stream == nullptr && size <= kKeptWorkspace;
+    at::Tensor workspace;
+    if (!kept) workspace = bytes();
+    struct Released {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Released() { PyEval_RestoreThread(state); }
+    } released;
+    std::unique_lock<std::mutex> lock(cache.mutex, std::defer_lock);
+    if (kept) {
+        lock.lock();
+        if (!cache.workspace.defined() || (size_t)cache.workspace.numel() < size) cache.workspace = bytes();
+        workspace = cache.workspace;
+    }
+    return run(workspace.data_ptr(), (size_t)workspace.nbytes());
+}
+
+// grow(cache, refs, tokens) -> taken, or a status
+PyObject *grow(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Cache *cache = n == 3 ? cache_of(a[0]) : nullptr;
+    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "grow takes 3 arguments"), nullptr);
+    const c10::cuda::CUDAGuard guard(cache->device);
+    at::Tensor refs, tokens;
+    fa_page_table t;
+    if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "tokens", cache->B, *cache, false, tokens)) return nullptr;
+    at::Tensor taken = numbers(*cache, cache->B);
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    const fa_status st = with_workspace(*cache, t, 0, stream, [&](void *w, size_t size) {
+        return g_grow(&t, tokens.const_data_ptr<int32_t>(), taken.mutable_data_ptr<int32_t>(), w, size, stream);
+    });
+    return st != FA_OK ? PyLong_FromLong(st) : THPVariable_Wrap(taken);
+    END_HANDLE_TH_ERRORS
+}
+
+// free(cache, refs, rows) -> status
+PyObject *free_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Cache *cache = n == 3 ? cache_of(a[0]) : nullptr;
+    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "free takes 3 arguments"), nullptr);
+    const c10::cuda::CUDAGuard guard(cache->device);
+    at::Tensor refs, rows;
+    fa_page_table t;
+    if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "rows", -1, *cache, false, rows)) return nullptr;
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    return PyLong_FromLong(g_free(&t, rows.const_data_ptr<int32_t>(), (int)rows.numel(), stream));
+    END_HANDLE_TH_ERRORS
+}
+
+// fork(cache, refs, parent, child) -> (src, dst), or a status
+PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Cache *cache = n == 4 ? cache_of(a[0]) : nullptr;
+    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "fork takes 4 arguments"), nullptr);
+    const c10::cuda::CUDAGuard guard(cache->device);
+    at::Tensor refs, parent, child;
+    fa_page_table t;
+    if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "parent", -1, *cache, false, parent) ||
+        !entries(a[3], "child", parent.numel(), *cache, false, child))
+        return nullptr;
+    at::Tensor src = numbers(*cache, parent.numel()), dst = numbers(*cache, parent.numel());
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    const fa_status st = with_workspace(*cache, t, (int)parent.numel(), stream, [&](void *w, size_t size) {
+        return g_fork(&t, parent.const_data_ptr<int32_t>(), child.const_data_ptr<int32_t>(), (int)parent.numel(),
+                      src.mutable_data_ptr<int32_t>(), dst.mutable_data_ptr<int32_t>(), w, size, stream);
+    });
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject *pair = PyTuple_New(2);
+    if (!pair) return nullptr;
+    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(src));
+    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(dst));
+    return pair;
+    END_HANDLE_TH_ERRORS
+}
+
+// compact(cache, refs) -> (moved, src, dst, count), or a status
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Cache *cache = n == 2 ? cache_of(a[0]) : nullptr;
+    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "compact takes 2 arguments"), nullptr);
+    const c10::cuda::CUDAGuard guard(cache->device);
+    at::Tensor refs;
+    fa_page_table t;
+    if (!table_of(*cache, a[1], refs, t)) return nullptr;
+    at::Tensor out[4];
+    for (int i = 0; i < 4; ++i) out[i] = numbers(*cache, i < 3 ? cache->c.num_pages : 1);
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    const fa_status st = with_workspace(*cache, t, 0, stream, [&](void *w, size_t size) {
+        return g_compact(&t, out[0].mutable_data_ptr<int32_t>(), out[1].mutable_data_ptr<int32_t>(),
+                         out[2].mutable_data_ptr<int32_t>(), out[3].mutable_data_ptr<int32_t>(), w, size, stream);
+    });
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject *all = PyTuple_New(4);
+    if (!all) return nullptr;
+    for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(all, i, THPVariable_Wrap(out[i]));
+    return all;
+    END_HANDLE_TH_ERRORS
+}
+
+// copy_pages(cache, src, dst, count) -> status
+PyObject *copy_pages(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Cache *cache = n == 4 ? cache_of(a[0]) : nullptr;
+    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "copy_pages takes 4 arguments"), nullptr);
+    const c10::cuda::CUDAGuard guard(cache->device);
+    at::Tensor src, dst, count;
+    if (!entries(a[1], "src", -1, *cache, false, src) || !entries(a[2], "dst", src.numel(), *cache, false, dst)) return nullptr;
+    if (a[3] != Py_None && !entries(a[3], "count", 1, *cache, false, count)) return nullptr;
+    const int32_t *m = count.defined() ? count.const_data_ptr<int32_t>() : nullptr;
+    void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
+    const auto run = [&](auto call, auto *c) {
+        return call(c, src.const_data_ptr<int32_t>(), dst.const_data_ptr<int32_t>(), m, (int)src.numel(), stream);
+    };
+    return PyLong_FromLong(cache->four ? run(g_copy_q4, &cache->c4) : run(g_copy, &cache->c));
+    END_HANDLE_TH_ERRORS
+}
+
+// init(addresses of the entry points, in the order below)
 PyObject *init(PyObject *, PyObject *args)
 {
-    unsigned long long x, y, z;
-    if (!PyArg_ParseTuple(args, "KKK", &x, &y, &z)) return nullptr;
-    g_kv_append = reinterpret_cast<KvAppend>(x);
-    g_fwd = reinterpret_cast<FwdSharedPrefix>(y);
-    g_workspace_bytes = reinterpret_cast<WorkspaceBytes>(z);
+    unsigned long long x[16];
+    if (!PyArg_ParseTuple(args, "KKKKKKKKKKKKKKKK", &x[0], &x[1], &x[2], &x[3], &x[4], &x[5], &x[6], &x[7], &x[8], &x[9],
+                          &x[10], &x[11], &x[12], &x[13], &x[14], &x[15]))
+        return nullptr;
+    int i = 0;
+    const auto put = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(x[i++]); };
+    put(g_kv_append);
+    put(g_kv_append_q4);
+    put(g_fwd);
+    put(g_workspace_bytes);
+    put(g_fwd_q4);
+    put(g_workspace_bytes_q4);
+    put(g_kv_read);
+    put(g_kv_read_q4);
+    put(g_rotary);
+    put(g_pages_bytes);
+    put(g_grow);
+    put(g_free);
+    put(g_fork);
+    put(g_compact);
+    put(g_copy);
+    put(g_copy_q4);
     Py_RETURN_NONE;
 }
 
 PyMethodDef g_methods[] = {
     {"init", init, METH_VARARGS, nullptr},
     {"cache", new_cache, METH_VARARGS, nullptr},
+    {"cache4", new_cache4, METH_VARARGS, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"forward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(forward)), METH_FASTCALL, nullptr},
+    {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read)), METH_FASTCALL, nullptr},
+    {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotary)), METH_FASTCALL, nullptr},
+    {"grow", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grow)), METH_FASTCALL, nullptr},
+    {"free", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(free_rows)), METH_FASTCALL, nullptr},
+    {"fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(fork_rows)), METH_FASTCALL, nullptr},
+    {"compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(compact)), METH_FASTCALL, nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(copy_pages)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -459,6 +459,189 @@ fa_status fa_fwd_shared_prefix(const fa_rows *Q, const fa_paged_kv *cache, const
 /* Bytes of workspace fa_fwd_shared_prefix needs (0 for invalid or empty sizes). */
 size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix_len, int B, int Hq, int T);
 
+/*
+ * Positions that the caller gives, on one or more axes (time, height and width of a
+ * video's patches, say): token t of sequence b is at
+ *     n[axis * stride_axis + b * stride_b + t * stride_t]
+ * on each axis, plus the call's position_offset (any int32; the axes' entries may
+ * repeat through strides of 0).  Pair p of a head turns by its position on axis
+ * pair_axis[p] (device memory, rot_dim / 2 entries; a pair whose entry is no axis
+ * does not turn).  pair_axis = NULL: axis 0.
+ */
+typedef struct fa_positions {
+    const int32_t *n;
+    int64_t stride_axis, stride_b, stride_t;    /* >= 0 */
+    int axes;                                   /* >= 1 */
+    const int32_t *pair_axis;
+} fa_positions;
+
+/* fa_kv_append with the tokens' positions given (NULL: their places in the
+ * sequences, as fa_kv_append). */
+fa_status fa_kv_append_at(const fa_paged_kv *cache, const fa_rows *K, const fa_rows *V, const fa_rows *Q,
+                          const fa_rows *Q_out, int B, int Hq, int T, const float *inv_freq, int rot_dim, int interleaved,
+                          const fa_positions *positions, int64_t position_offset, int f16, void *stream);
+
+/*
+ * fa_rotary -- the position rotation of fa_kv_append on queries and keys without a
+ * cache, for training and for attention over whole sequences (fa_fwd).
+ *
+ *   Q, Q_out         [B, Hq, T, D], and where to put them turned; Q_out may be Q
+ *                    (same address and strides) and may not overlap an input
+ *                    otherwise.  Not looked at where Hq is 0.
+ *   K, K_out         [B, Hkv, T, D], likewise.
+ *   D                a multiple of 8 up to 256.
+ *   inv_freq, rot_dim, interleaved, position_offset: as in fa_kv_append.
+ *   positions        NULL: token t is at position_offset + t.
+ *   inverse          nonzero: turned back, which is the gradient of the rotation.
+ * One kernel; sines, cosines and products are fp32 until they are rounded once.
+ */
+fa_status fa_rotary(const fa_rows *Q, const fa_rows *Q_out, const fa_rows *K, const fa_rows *K_out, int B, int Hq, int Hkv,
+                    int T, int D, const float *inv_freq, int rot_dim, int interleaved, const fa_positions *positions,
+                    int64_t position_offset, int inverse, int f16, void *stream);
+
+/*
+ * ------------------------------------------------------------- 4-bit cache
+ * A paged cache (above) whose rows are held in 4 bits: at D = 128 a key and its value
+ * take 144 bytes a head, where 16 bits take 512.
+ *
+ * A row of D elements is padded with zeros to P = 64, 128 or 256 (the least that
+ * holds it), in groups of 16.  Element d is u * s: u is nibble d of the row's P / 2
+ * bytes (an even d is the lower half of byte d / 2), s its group's scale, byte d / 16
+ * of the row's P / 16 bytes of scales.
+ *   u  sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   s  5 exponent bits, 3 mantissa bits, no sign: the IEEE half with the bits s << 7.
+ *      At most 10240 (byte 226); larger bytes are undefined.
+ * u * s is exact as an IEEE half and as bf16.  Appending, s is the group's largest
+ * magnitude / 6 and u the element / s, both rounded to nearest (halfway to the even
+ * mantissa bit), u at most 6: an element is off by at most 1/5 of its group's largest
+ * and about 1/12 of itself if it is not small beside that; magnitudes below 2^-19
+ * are lost and those above 61440 are held as that.  Elements have to be finite
+ * (others become some finite value).
+ *
+ * The pools' rows are
+ *     k + page * stride_page + head * stride_head + slot * stride_slot
+ *     k_scales + page * scale_stride_page + head * scale_stride_head + slot * scale_stride_slot
+ * (bytes; multiples of 16, and of P / 16), and v and v_scales likewise.
+ */
+typedef struct fa_paged_kv4 {
+    void *k, *v;                 /* 16-byte aligned */
+    int64_t stride_page, stride_head, stride_slot;
+    void *k_scales, *v_scales;   /* 16-byte aligned */
+    int64_t scale_stride_page, scale_stride_head, scale_stride_slot;
+    int num_pages, page_size;
+    int Hkv, D;                  /* as in fa_paged_kv, and so are the following */
+    const int32_t *table;
+    int64_t table_stride;
+    int table_width;
+    const int32_t *seq_len;
+} fa_paged_kv4;
+
+/* fa_kv_append_at into a 4-bit cache.  A key turns in fp32 and is rounded once, to 4
+ * bits; the queries are as in fa_kv_append. */
+fa_status fa_kv_append_q4(const fa_paged_kv4 *cache, const fa_rows *K, const fa_rows *V, const fa_rows *Q,
+                          const fa_rows *Q_out, int B, int Hq, int T, const float *inv_freq, int rot_dim, int interleaved,
+                          const fa_positions *positions, int64_t position_offset, int f16, void *stream);
+
+/*
+ * fa_fwd_paged_q4 -- fa_fwd_paged over a 4-bit cache: exact attention over the rows
+ * that it holds.  Arguments, workspace rules and errors as fa_fwd_paged.
+ *
+ * Up to 32 query rows of a sequence that share a key (T * Hq / Hkv), D = 256, or a
+ * page_size that is no multiple of 8: a weight is off by 2^-11 (bf16) or 2^-22 (fp16)
+ * relative, or by 2^-37 of its row's largest where that is more, so that O's own
+ * rounding decides.  Else the rows are decoded to 16 bits in the workspace, up to 256
+ * MB of them at a time (a whole sequence at least), and the errors are fa_fwd_paged's.
+ */
+fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_rows *O, float *LSE, int B, int Hq, int T,
+                          int causal, float scale, int f16, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_fwd_paged_q4 needs on the current device (0 for invalid or
+ * empty sizes).  They depend on the sizes, not on seq_len's contents. */
+size_t fa_fwd_paged_q4_workspace_bytes(const fa_paged_kv4 *cache, int B, int Hq, int T);
+
+/*
+ * fa_kv_read -- the keys and values of the last T tokens of every sequence as rows
+ * K, V [B, Hkv, T, D], aligned at their end like an append's tokens.  Tokens that a
+ * sequence does not have, or whose page holds nothing, are zero.  fa_kv_read_q4: of a
+ * 4-bit cache, decoded (exactly) to IEEE halves (f16) or bf16.  One kernel.
+ */
+fa_status fa_kv_read(const fa_paged_kv *cache, const fa_rows *K, const fa_rows *V, int B, int T, void *stream);
+fa_status fa_kv_read_q4(const fa_paged_kv4 *cache, const fa_rows *K, const fa_rows *V, int B, int T, int f16, void *stream);
+
+/*
+ * ------------------------------------------------------------- pages
+ * Which pages sequences have, kept on the device: no call waits for the GPU, and all
+ * can be captured into a graph.
+ *
+ * refs[p] counts the uses of page p: one for each table entry in front of a
+ * sequence's length (entry e of row b with e < ceil(seq_len[b] / page_size)), and what
+ * the caller adds for uses of its own, a shared prefix say.  A page whose count is 0
+ * (or less) is free.  Calls that take pages take the lowest free ones, in order, so
+ * that results depend on nothing but the inputs.  Layers with caches of their own
+ * share one table: its calls are made once, and the copies that they list are made in
+ * every cache with fa_copy_pages.
+ */
+typedef struct fa_page_table {
+    int32_t *table;              /* [B, table_width], rows table_stride entries apart */
+    int64_t table_stride;
+    int table_width;             /* table_width * page_size <= 2^31 - 4096 */
+    int B;
+    int32_t *seq_len;            /* [B] */
+    int32_t *refs;               /* [num_pages] */
+    int num_pages, page_size;
+} fa_page_table;
+
+/* Bytes of workspace (16-byte aligned; its contents do not matter, and calls that may
+ * overlap need separate ones) that the calls below need, for n forks. */
+size_t fa_pages_workspace_bytes(const fa_page_table *table, int n);
+
+/*
+ * fa_kv_grow -- every sequence b grows by tokens[b] (0 or less: not), and gets the
+ * pages for them: what an append needs.  taken[b] is how many pages it got, or -2 if
+ * it was not grown: the table's row or the free pages do not suffice.  Pages are given
+ * in the order of the sequences; behind one that they did not suffice for, only
+ * sequences that need none are sure to grow.
+ */
+fa_status fa_kv_grow(const fa_page_table *table, const int32_t *tokens, int32_t *taken, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * fa_kv_free -- rows [n] give up their pages: counts fall by one, the rows' entries
+ * become -1 and their lengths 0.  A row that is listed twice, or is none, counts once,
+ * or not at all.
+ */
+fa_status fa_kv_free(const fa_page_table *table, const int32_t *rows, int n, void *stream);
+
+/*
+ * fa_kv_fork -- row child[i] becomes what row parent[i] is, for i < n.  Full pages are
+ * shared; a last page that is part full is copied to a free one, since both rows will
+ * write behind it.  src[i] and dst[i] are that copy, which the caller makes with
+ * fa_copy_pages, or -1 for none.  dst[i] = -2: not forked, because no page was free,
+ * the child was not empty (seq_len 0), a row is none, or the child is another fork's
+ * parent or an earlier one's child.
+ */
+fa_status fa_kv_fork(const fa_page_table *table, const int32_t *parent, const int32_t *child, int n, int32_t *src, int32_t *dst,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * fa_kv_compact -- with L pages in use, those from page L on move to the free ones in
+ * front of it, both in order, so that the pool's end is free.  moved[p] is page p's new
+ * number (-1 if it is free); counts and the sequences' entries follow, other tables are
+ * the caller's to map.  *count copies from src[] to dst[] (num_pages entries each) are
+ * the caller's to make with fa_copy_pages.
+ */
+fa_status fa_kv_compact(const fa_page_table *table, int32_t *moved, int32_t *src, int32_t *dst, int32_t *count, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * fa_copy_pages -- page src[i] of a cache's pools to page dst[i], keys and values of
+ * all heads and slots, for i < n (or *count, device memory, where that is less; NULL:
+ * n).  Pairs with a number outside the pool are skipped.  No page may be the target of
+ * two pairs or of one and the source of another: its contents would be undefined.
+ */
+fa_status fa_copy_pages(const fa_paged_kv *cache, const int32_t *src, const int32_t *dst, const int32_t *count, int n, void *stream);
+fa_status fa_copy_pages_q4(const fa_paged_kv4 *cache, const int32_t *src, const int32_t *dst, const int32_t *count, int n, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *fa_status_string(fa_status s);
 
