@@ -954,38 +954,6 @@ def copy_pages(cache, src, dst, count=None, stream=None):
 
 
 # ------------------------------------------------------------- autograd
-def _turned(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse):
-    r = (_BINDING or _binding()).rotary(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse)
-    if type(r) is int:
-        raise FAError(r, "fa_rotary")
-    return r
-
-
-def _rotary_function():
-    import torch
-
-    class _Rotary(torch.autograd.Function):
-        @staticmethod
-        def forward(ctx, q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse):
-            ctx.set_materialize_grads(False)
-            ctx.save_for_backward(inv_freq, positions, pair_axis)
-            ctx.how = interleaved, position_offset, inverse
-            return _turned(q, k, inv_freq, positions, pair_axis, *ctx.how)
-
-        @staticmethod
-        def backward(ctx, d_q, d_k):
-            if d_q is None and d_k is None:
-                return (None,) * 8
-            interleaved, position_offset, inverse = ctx.how
-            turned = _Rotary.apply(d_q, d_k, *ctx.saved_tensors, interleaved, position_offset, not inverse)
-            return *turned, None, None, None, None, None, None
-
-    return _Rotary
-
-
-_ROTARY = None
-
-
 def rotary(q, inv_freq, positions=None, k=None, pair_axis=None, interleaved: bool = False, position_offset: int = 0,
            stream=None):
     """q, or (q, k), turned by their positions: a differentiable torch operation, for
@@ -1000,18 +968,12 @@ def rotary(q, inv_freq, positions=None, k=None, pair_axis=None, interleaved: boo
     entry is no axis does not turn).  position_offset is added to every position.
     Gradients reach q and k.
     """
-    global _ROTARY
-    import torch
-
     if stream is not None:
         with _stream_context(q.device, stream):
             return rotary(q, inv_freq, positions, k, pair_axis, interleaved, position_offset)
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
-        if _ROTARY is None:
-            _ROTARY = _rotary_function()
-        r = _ROTARY.apply(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, False)
-    else:
-        r = _turned(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, False)
+    r = (_BINDING or _binding()).rotary(q, k, inv_freq, positions, pair_axis, interleaved, position_offset)
+    if type(r) is int:
+        raise FAError(r, "fa_rotary")
     return r[0] if k is None else r
 
 

@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p
     if (stored) {
         const int64_t slot = at % size;
         const int64_t row = page * p.c.s_page + slot * p.c.s_slot, scales = page * p.c.t_page + slot * p.c.t_slot;
-        const int groups = padded4(D) / kFourGroup;
-        for (int e = threadIdx.x; e < 2 * Hkv * groups; e += kThreads) {
-            const int which = e / groups, g = e % groups, head = which < Hkv ? which : which - Hkv;
+        const int groups = D <= 64 ? 2 : D <= 128 ? 3 : 4;  // (the logarithm of how many a row has)
+        for (int e = threadIdx.x; e < (2 * Hkv) << groups; e += kThreads) {
+            const int which = e >> groups, g = e & ((1 << groups) - 1), head = which < Hkv ? which : which - Hkv;
             float x[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

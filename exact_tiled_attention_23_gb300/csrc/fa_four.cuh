@@ -19,11 +19,20 @@ namespace fa {
 // The largest scale, 10240: what it stands for with u = 6 is below fp16's largest.
 constexpr uint32_t kLargestScale = 226;
 
+// x / s to nearest, from y = 1 / s to nearest: P. Markstein's correction of a quotient
+// by its remainder (1990).  (s not so small or large that a step leaves the normal
+// range; a quotient that small is 0 in 4 bits.)
+__device__ __forceinline__ float quotient(float x, float s, float y)
+{
+    const float q = x * y;
+    return fmaf(fmaf(-q, s, x), y, q);
+}
+
 // The scale for a group whose largest magnitude is `largest` (infinities: the
 // largest scale; a NaN among the values is not counted).
 __device__ __forceinline__ uint32_t scale_code(float largest)
 {
-    const float t = __fdiv_rn(largest, 6.f);
+    const float t = largest < INFINITY ? quotient(largest, 6.f, 1.f / 6.f) : largest;
     if (t < 6.103515625e-5f) return (uint32_t)__float2int_rn(t * 131072.f);     // below 2^-14: multiples of 2^-17
     const uint32_t bits = __float_as_uint(t);
     const uint32_t up = (bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20;          // 3 mantissa bits, to nearest
@@ -43,17 +52,15 @@ __device__ __forceinline__ uint2 to_four(const float (&x)[16], uint32_t &code)
     for (int i = 0; i < 16; ++i) largest = fmaxf(largest, fabsf(x[i]));
     code = scale_code(largest);
     if (code == 0) return make_uint2(0u, 0u);
-    const float s = scale_value(code);
+    // (exact quotients: x / s halfway between two numbers stays halfway)
+    const float s = scale_value(code), y = __frcp_rn(s);
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        w[h] = 0u;
+        float q[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (a division: x / s halfway between two numbers stays halfway)
-            const float a = __fdiv_rn(x[8 * h + 2 * i], s), b = __fdiv_rn(x[8 * h + 2 * i + 1], s);
-            w[h] |= ptx::pack_e2m1x2(a, b) << (8 * i);
-        }
+        for (int i = 0; i < 8; ++i) q[i] = fabsf(x[8 * h + i]) < INFINITY ? quotient(x[8 * h + i], s, y) : x[8 * h + i];
+        w[h] = ptx::pack_e2m1x8(q);
     }
     return make_uint2(w[0], w[1]);
 }

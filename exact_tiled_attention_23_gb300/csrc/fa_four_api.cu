@@ -83,6 +83,7 @@ fa_status read_rows(fa::ReadParams &p, const C *cache, const fa_rows *K, const f
     strides_of(p.k_s, *K);
     p.v = static_cast<uint16_t *>(V->ptr);
     strides_of(p.v_s, *V);
+    p.by_groups = fa::make_fast_div((uint32_t)(cache->D + 15) / 16);
     p.B = B;
     p.T = T;
     return fa::launch_read(p, four, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -250,6 +251,9 @@ fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_
     const bool given = scale > 0.f && !std::isinf(scale);
     p.scale_log2 = (given ? scale : 1.0f / std::sqrt((float)D)) * 1.4426950408889634f;
     p.part = plan.rows.part;
+    p.wait_limit_ns = fa::wait_budget_ns();
+    p.team = team_size(D, plan.rows, (own_keys + p.part.chunk - 1) / p.part.chunk, fa::four_teams_at_once);
+    if (p.team) return fa::launch_four_team(f, (int)plan.rows.items * p.team, cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     if (fa::launch_four_rows(f, (int)plan.rows.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
 
     fa::MergeParams m{};

@@ -23,6 +23,9 @@ int four_rows_per_tile(int D, int64_t rows);
 int four_rows_chunk(int D);
 int four_rows_ctas_per_sm(int D, int rows);
 cudaError_t launch_four_rows(const FourParams &f, int ctas, cudaStream_t stream);
+// A team of p.team CTAs per tile of 8 rows, and how many teams fit the device together.
+cudaError_t launch_four_team(const FourParams &f, int ctas, cudaStream_t stream);
+int four_teams_at_once(int device, int team);
 cudaError_t launch_widen_pages(const WidenParams &p, int64_t pages, cudaStream_t stream);
 
 }  // namespace fa

@@ -129,5 +129,7 @@ cudaError_t read_and_clear_status_halves(uint32_t *out);
 cudaError_t read_and_clear_status_paged(uint32_t *out);
 // The paged row kernel's status word (call after read_and_clear_status).
 cudaError_t read_and_clear_status_paged_rows(uint32_t *out);
+// The 4-bit cache's row kernel's status word (call after read_and_clear_status).
+cudaError_t read_and_clear_status_four(uint32_t *out);
 
 }  // namespace fa

@@ -113,6 +113,7 @@ struct ReadParams {
     PagedCache4 c4;
     uint16_t *k, *v;
     int64_t k_s[3], v_s[3];
+    FastDiv by_groups;                 // 16 elements, of a row
     int B, T, f16;
 };
 
@@ -297,6 +298,29 @@ template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
 {
     return launch_clusters(kernel, 1, grid, threads, smem, stream, args...);
+}
+
+// Clusters of `team` CTAs of a kernel that fit the current device together; 0 if it
+// cannot be known.
+template <typename... P>
+int clusters_at_once(void (*kernel)(P...), int team, int threads, int smem)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)team);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)team;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess)
+        return clusters;
+    (void)cudaGetLastError();                       // the line serves every call
+    return 0;
 }
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);

@@ -285,4 +285,26 @@ struct Plan {
     }
 };
 
+// CTAs of a team per tile, 0 where teams do not pay.  A team's tile has up to 8
+// rows, so that its states fit the stages.  All teams are on the GPU at once
+// (16 teams of 8 where 15 fit: 10.1 us, as teams of 4: 6.3), and a warp has at
+// most eight chunks of the longest sequence that the table allows.  With 8 of
+// 128 tiles of 1024 keys: 12.0 us, cut as a line 18.4, and where one sequence
+// alone is that long 11.2 and 10.2, since a line spreads it over the GPU; with 16
+// of 2048 keys 24.3 and 29.9, but 18.9 and 13.6.
+inline int team_size(int D, const Plan &own, int64_t chunks, int (*at_once)(int device, int team))
+{
+    constexpr int kMostChunks = 8;
+    if (D > 128 || own.part.rows != 8 || own.part.tiles != 1) return 0;
+    const int device = fa::current_device();
+    if (own.items > fa::sm_count_of(device)) return 0;
+    int team = 0;
+    for (int t = 1; t <= fa::kMostTeam && own.items <= at_once(device, t); t *= 2) {
+        const int64_t each = (chunks + t * fa::kTeamWarps - 1) / (t * fa::kTeamWarps);
+        if (each <= kMostChunks) team = t;
+        if (each <= 1) break;
+    }
+    return team;
+}
+
 }  // namespace fa::paged

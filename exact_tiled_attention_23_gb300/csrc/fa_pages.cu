@@ -52,11 +52,18 @@ __device__ __forceinline__ N scan(N x, N &base, N (*sums)[kWarps], int &turn)
 // Live pages of [first, last), summed over the CTA.
 __device__ int count_live(const int32_t *refs, int first, int last)
 {
+    constexpr int kWide = 8;               // loads together
     __shared__ int total;
     if (threadIdx.x == 0) total = 0;
     __syncthreads();
     int n = 0;
-    for (int64_t p = first + (int64_t)threadIdx.x; p < last; p += kThreads) n += refs[p] > 0;
+    for (int64_t at = first + (int64_t)threadIdx.x; at < last; at += kThreads * kWide) {
+        bool live[kWide];
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) live[i] = at + i * kThreads < last && refs[at + i * kThreads] > 0;
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) n += live[i];
+    }
     n = __reduce_add_sync(0xffffffffu, n);
     if (threadIdx.x % 32 == 0 && n) atomicAdd(&total, n);
     __syncthreads();
@@ -66,13 +73,19 @@ __device__ int count_live(const int32_t *refs, int first, int last)
 }
 
 // each(p, live, live pages of [first, last) in front of p) for every page of
-// [first, last), `before` added.
+// [first, last), `before` added, until `enough` pages were free.  Returns how many
+// pages were live, `before` added, and `last` or how far it came.
 template <typename Each>
-__device__ __forceinline__ void walk(const int32_t *refs, int first, int last, int before, int (*sums)[kWarps], int &turn,
-                                     const Each &each)
+__device__ __forceinline__ int walk(const int32_t *refs, int first, int &last, int before, int64_t enough, int (*sums)[kWarps],
+                                    int &turn, const Each &each)
 {
     constexpr int kWide = 8;           // pages of a thread, loaded together
+    const int from = first - before;
     for (int64_t at = first; at < last; at += kThreads * kWide) {
+        if (at - before - from >= enough) {
+            last = (int)at;
+            break;
+        }
         const int64_t p = at + (int64_t)threadIdx.x * kWide;
         bool live[kWide];
         int n = 0;
@@ -87,6 +100,7 @@ __device__ __forceinline__ void walk(const int32_t *refs, int first, int last, i
             front += live[i];
         }
     }
+    return before;
 }
 
 __device__ __forceinline__ int segment_first(const PagesParams &p, int s) { return (int)min((int64_t)s * p.segment, (int64_t)p.num_pages); }
@@ -110,14 +124,16 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const PagesParams p)
     if (threadIdx.x == 0) p.counts[blockIdx.x] = n;
 }
 
-// The free pages of [first, last) in order, after `before` live pages in front.
-__device__ __forceinline__ void list_free(const PagesParams &p, int first, int last, int before)
+// The free pages of [first, last) in order, after `before` live pages in front, until
+// there are `enough`.  Returns how many were listed.
+__device__ __forceinline__ int list_free(const PagesParams &p, int first, int last, int before, int64_t enough)
 {
     __shared__ int sums[2][kWarps];
     int turn = 0;
-    walk(p.refs, first, last, before, sums, turn, [&](int page, bool live, int front) {
-        if (!live) p.list[page - front] = page;
+    const int live = walk(p.refs, first, last, before, enough, sums, turn, [&](int page, bool is, int front) {
+        if (!is) p.list[page - front] = page;
     });
+    return last - first - (live - before);
 }
 
 __global__ void __launch_bounds__(kThreads) list_kernel(const PagesParams p)
@@ -125,19 +141,19 @@ __global__ void __launch_bounds__(kThreads) list_kernel(const PagesParams p)
     ptx::wait_for_primary();
     int all;
     const int before = live_before(p, all);
-    list_free(p, segment_first(p, blockIdx.x), segment_first(p, blockIdx.x + 1), before);
+    list_free(p, segment_first(p, blockIdx.x), segment_first(p, blockIdx.x + 1), before, INT32_MAX);
 }
 
-// How many free pages p.list has; lists them where no kernel before did.
-__device__ __forceinline__ int free_pages(const PagesParams &p)
+// How many free pages p.list has, `enough` or all; lists them where no kernel before
+// did.
+__device__ __forceinline__ int free_pages(const PagesParams &p, int64_t enough)
 {
     if (p.segments > 1) {
         int all;
         live_before(p, all);
         return p.num_pages - all;
     }
-    list_free(p, 0, p.num_pages, 0);
-    return p.num_pages - count_live(p.refs, 0, p.num_pages);
+    return list_free(p, 0, p.num_pages, 0, enough);
 }
 
 __device__ __forceinline__ int64_t capacity(const PagesParams &p) { return (int64_t)p.width * p.page_size; }
@@ -150,41 +166,76 @@ __device__ __forceinline__ int64_t length_of(const PagesParams &p, int b)
 
 __device__ __forceinline__ int64_t pages_of(const PagesParams &p, int64_t n) { return (n + p.page_size - 1) / p.page_size; }
 
-// Sequences grow: who gets which free pages is the prefix sum of what they need.
+// What sequence b has, what it needs to grow (none where its row is too short), and
+// whether that is so.
+struct Growth {
+    int64_t n, then, have, need;
+    bool room;
+};
+
+__device__ __forceinline__ Growth growth_of(const PagesParams &p, int64_t b)
+{
+    Growth g{0, 0, 0, 0, false};
+    if (b >= p.B) return g;
+    g.n = length_of(p, (int)b);
+    g.then = g.n + max(p.tokens[b], 0);
+    g.room = g.then <= capacity(p);
+    g.have = pages_of(p, g.n);
+    if (g.room) g.need = pages_of(p, g.then) - g.have;
+    return g;
+}
+
+// Sequences grow: who gets which free pages is the prefix sum of what they need.  A
+// thread has a sequence, and takes one page itself; more are a warp's work.
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesParams p)
 {
     __shared__ int64_t sums[2][kWarps];
     int turn = 0;
-    int64_t base = 0;
+    int64_t total = 0;
     ptx::wait_for_primary();
+    const int lane = threadIdx.x % 32;
+    Growth g{};
+    int64_t first = 0;
     for (int64_t at = 0; at < p.B; at += kThreads) {
-        const int64_t b = at + threadIdx.x;
-        int64_t need = 0;
-        if (b < p.B) {
-            const int64_t n = length_of(p, (int)b), then = n + max(p.tokens[b], 0);
-            if (then <= capacity(p)) need = pages_of(p, then) - pages_of(p, n);
-        }
-        const int64_t first = scan(need, base, sums, turn);
-        if (b < p.B) p.first[b] = first;
+        g = growth_of(p, at + threadIdx.x);
+        first = scan(g.need, total, sums, turn);
+        if (p.B > kThreads && at + threadIdx.x < p.B) p.first[at + threadIdx.x] = first;
     }
     __syncthreads();
-    const int found = free_pages(p);
+    const int found = free_pages(p, total);
     __syncthreads();
-    const int lane = threadIdx.x % 32;
-    for (int64_t b = threadIdx.x / 32; b < p.B; b += kWarps) {
-        const int64_t n = length_of(p, (int)b), then = n + max(p.tokens[b], 0);
-        const int64_t have = pages_of(p, n), need = then <= capacity(p) ? pages_of(p, then) - have : 0;
-        const bool fits = then <= capacity(p) && (need == 0 || p.first[b] + need <= found);
-        if (fits)
-            for (int64_t i = lane; i < need; i += 32) {
-                const int page = p.list[p.first[b] + i];
-                p.table[b * p.table_stride + have + i] = page;
+    for (int64_t at = 0; at < p.B; at += kThreads) {
+        const int64_t b = at + threadIdx.x;
+        if (p.B > kThreads) {
+            g = growth_of(p, b);
+            first = b < p.B ? p.first[b] : 0;
+        }
+        const bool fits = g.room && (g.need == 0 || first + g.need <= found);
+        if (b < p.B) {
+            if (fits && g.need == 1) {
+                const int page = p.list[first];
+                p.table[b * p.table_stride + g.have] = page;
                 p.refs[page] = 1;
             }
-        __syncwarp();
-        if (lane == 0) {
-            if (fits && then > n) p.seq_len[b] = (int)then;
-            p.taken[b] = fits ? (int)need : kRefused;
+            if (fits && g.then > g.n) p.seq_len[b] = (int)g.then;
+            p.taken[b] = fits ? (int)g.need : kRefused;
+        }
+        for (unsigned many = __ballot_sync(0xffffffffu, fits && g.need > 1); many; many &= many - 1) {
+            const int of = __ffs(many) - 1;
+            const int64_t need = __shfl_sync(0xffffffffu, g.need, of), from = __shfl_sync(0xffffffffu, first, of);
+            int32_t *entry = p.table + (b - lane + of) * p.table_stride + __shfl_sync(0xffffffffu, g.have, of);
+            constexpr int kWide = 4;       // loads together
+            for (int64_t i = lane; i < need; i += 32 * kWide) {
+                int page[kWide];
+#pragma unroll
+                for (int j = 0; j < kWide; ++j) page[j] = i + 32 * j < need ? p.list[from + i + 32 * j] : -1;
+#pragma unroll
+                for (int j = 0; j < kWide; ++j)
+                    if (page[j] >= 0) {
+                        entry[i + 32 * j] = page[j];
+                        p.refs[page[j]] = 1;
+                    }
+            }
         }
     }
 }
@@ -229,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PagesParams p
         if (y >= 0 && y < p.B) atomicMin(p.mark + y, i);
     }
     __syncthreads();
-    const int found = free_pages(p);
+    const int found = free_pages(p, p.n);
     __syncthreads();
     for (int at = 0; at < p.n; at += kThreads) {
         const int i = at + threadIdx.x;
@@ -279,19 +330,11 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const PagesParams p)
     if (threadIdx.x == 0) p.seq_len[y] = (int)n;
 }
 
-// The moves that are listed: new numbers and counts.
-__device__ __forceinline__ void finish_moves(const PagesParams &p, int64_t from, int64_t step)
-{
-    for (int64_t j = from; j < *p.count; j += step) {
-        const int src = p.src[j], dst = p.list[j];
-        p.taken[src] = dst;
-        p.refs[dst] = p.refs[src];
-        p.refs[src] = 0;
-    }
-}
-
 // With L live pages, the live pages from L on move into the holes in front of L, both
-// in order: p.src and p.list.
+// in order: p.src and p.list.  p.taken has a page's new number, or kMove less its place
+// in the lists until finish_kernel has been there.
+constexpr int kMove = -3;
+
 __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesParams p)
 {
     __shared__ int sums[2][kWarps];
@@ -311,39 +354,42 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesParams p)
             first = segment_first(p, s + 1);
         }
     kept += count_live(p.refs, first, live);
-    walk(p.refs, segment_first(p, blockIdx.x), segment_first(p, blockIdx.x + 1), before, sums, turn,
-         [&](int page, bool is, int front) {
-             p.taken[page] = is && page < live ? page : -1;
-             if (!is && page < live) p.list[page - front] = page;
-             if (is && page >= live) p.src[front - kept] = page;
-         });
+    int last = segment_first(p, blockIdx.x + 1);
+    walk(p.refs, segment_first(p, blockIdx.x), last, before, INT32_MAX, sums, turn, [&](int page, bool is, int front) {
+        p.taken[page] = !is ? -1 : page < live ? page : kMove - (front - kept);
+        if (!is && page < live) p.list[page - front] = page;
+        if (is && page >= live) p.src[front - kept] = page;
+    });
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = live - kept;
-    if (alone) {
-        __syncthreads();
-        finish_moves(p, threadIdx.x, kThreads);
-    }
 }
 
-__global__ void __launch_bounds__(256) moves_kernel(const PagesParams p)
-{
-    ptx::wait_for_primary();
-    finish_moves(p, blockIdx.x * 256ll + threadIdx.x, gridDim.x * 256ll);
-}
-
-// The tables follow: a CTA per row and kRemap entries.
+// Numbers and counts of the pages that move (the first CTAs), and the tables (the
+// rest: one per row and kRemap entries).  An entry's page has its new number in
+// p.taken, or still its place in the list.
 constexpr int kRemap = 2048;
 
-__global__ void __launch_bounds__(256) remap_kernel(const PagesParams p)
+__global__ void __launch_bounds__(256) finish_kernel(const PagesParams p, const int movers)
 {
     ptx::wait_for_primary();
-    const int parts = (p.width + kRemap - 1) / kRemap, b = blockIdx.x / parts, part = blockIdx.x % parts;
+    if ((int)blockIdx.x < movers) {
+        for (int64_t j = blockIdx.x * 256ll + threadIdx.x; j < *p.count; j += movers * 256ll) {
+            const int src = p.src[j], dst = p.list[j];
+            p.taken[src] = dst;
+            p.refs[dst] = p.refs[src];
+            p.refs[src] = 0;
+        }
+        return;
+    }
+    const int block = (int)blockIdx.x - movers;
+    const int parts = (p.width + kRemap - 1) / kRemap, b = block / parts, part = block % parts;
     const int64_t have = pages_of(p, length_of(p, b)), first = (int64_t)part * kRemap;
     for (int64_t e = first + threadIdx.x; e < min(have, first + kRemap); e += 256) {
         int32_t *entry = p.table + b * p.table_stride + e;
         const int page = *entry;
         if (page < 0 || page >= p.num_pages) continue;
-        const int to = p.taken[page];
-        if (to >= 0 && to != page) *entry = to;            // (a page that nobody counted stays)
+        const int t = __ldcg(p.taken + page);               // (other CTAs write it)
+        const int to = t <= kMove ? p.list[kMove - t] : t;
+        if (to >= 0 && to != page) *entry = to;             // (a page that nobody counted stays)
     }
 }
 
@@ -449,10 +495,9 @@ cudaError_t launch_compact(const PagesParams &p, cudaStream_t stream)
 {
     cudaError_t e = count_segments(p, stream);
     if (e == cudaSuccess) e = launch_behind(compact_kernel, dim3((unsigned)p.segments), kThreads, 0, stream, p);
-    if (e == cudaSuccess && p.segments > 1)
-        e = launch_behind(moves_kernel, dim3((unsigned)p.segments), 256, 0, stream, p);
     const int64_t rows = (int64_t)p.B * ((p.width + kRemap - 1) / kRemap);
-    if (e == cudaSuccess && rows > 0) e = launch_behind(remap_kernel, dim3((unsigned)rows), 256, 0, stream, p);
+    const int movers = p.num_pages / 2048 + 1 < 152 ? p.num_pages / 2048 + 1 : 152;
+    if (e == cudaSuccess) e = launch_behind(finish_kernel, dim3((unsigned)(movers + rows)), 256, 0, stream, p, movers);
     return e;
 }
 

@@ -18,7 +18,7 @@ fa_status check_table(const fa_page_table *t)
     if (t->B > 1 && t->table_stride < t->table_width) return FA_ERR_INVALID_ARG;
     if ((int64_t)t->table_width * t->page_size > kMostKeys) return FA_ERR_INVALID_ARG;
     const int64_t parts = (t->table_width + 2047ll) / 2048;
-    if (parts * t->B > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (parts * t->B > INT32_MAX - 1024) return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 

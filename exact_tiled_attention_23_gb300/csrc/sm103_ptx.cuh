@@ -293,12 +293,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-// Two fp32 values -> two e2m1 values in a byte (nearest even, at most 6 in
-// magnitude); `lo` in bits 0-3.
-__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi)
+// Eight fp32 values -> e2m1 values (nearest even, at most 6 in magnitude), the first
+// in bits 0-3.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8])
 {
     uint32_t r;
-    asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %1, %2;\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
 

@@ -15,12 +15,16 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "fa.h"
 
+#include <array>
 #include <cmath>
 #include <mutex>
+#include <optional>
+#include <vector>
 
 namespace {
 
@@ -454,20 +458,105 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// rotary(q, k, inv_freq, positions, pair_axis, interleaved, position_offset, inverse)
-// -> (q, k) turned, None for one that is None, or a status
+// ---------------------------------------------------------------- rotation
+// What the C ABI refused.
+struct Refused {
+    fa_status status;
+};
+
+// q and k (either may be undefined) turned; the arguments have been checked.
+struct Turn {
+    at::Tensor freq, n, pair_axis;
+    bool interleaved, inverse;
+    int64_t offset;
+
+    std::array<at::Tensor, 2> operator()(std::array<at::Tensor, 2> x) const
+    {
+        std::array<at::Tensor, 2> y;
+        fa_rows in[2]{}, out[2]{};
+        int heads[2]{};
+        const at::Tensor &first = x[0].defined() ? x[0] : x[1];
+        const c10::cuda::CUDAGuard guard(first.device());
+        for (int i = 0; i < 2; ++i) {
+            if (!x[i].defined()) continue;
+            if (!followable(x[i])) x[i] = x[i].clone(at::MemoryFormat::Contiguous);
+            y[i] = at::empty(x[i].sizes(), at::TensorOptions().dtype(x[i].scalar_type()).device(x[i].device()));
+            in[i] = rows_of(x[i]);
+            out[i] = rows_of(y[i]);
+            heads[i] = (int)x[i].size(1);
+        }
+        fa_positions p{};
+        if (n.defined()) {
+            const int64_t d = n.dim();
+            p = fa_positions{n.const_data_ptr<int32_t>(), d == 3 ? n.stride(0) : 0, n.stride(d - 2), n.stride(d - 1),
+                             d == 3 ? (int)n.size(0) : 1, pair_axis.defined() ? pair_axis.const_data_ptr<int32_t>() : nullptr};
+        }
+        const at::Tensor &like = x[0].defined() ? x[0] : x[1];
+        const fa_status st = g_rotary(&in[0], &out[0], &in[1], &out[1], (int)like.size(0), heads[0], heads[1], (int)like.size(2),
+                                      (int)like.size(3), freq.const_data_ptr<float>(), 2 * (int)freq.numel(), interleaved,
+                                      n.defined() ? &p : nullptr, offset, inverse, like.scalar_type() == at::kHalf,
+                                      c10::cuda::getCurrentCUDAStream(like.get_device()).stream());
+        if (st != FA_OK) throw Refused{st};
+        return y;
+    }
+};
+
+// The same as an operation whose gradient turns back.  (The first tensor is defined.)
+struct Rotary : torch::autograd::Function<Rotary> {
+    static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const at::Tensor &a,
+                                                  const std::optional<at::Tensor> &b, const Turn &turn)
+    {
+        ctx->set_materialize_grads(false);
+        torch::autograd::variable_list saved{turn.freq};
+        if (turn.n.defined()) saved.push_back(turn.n);
+        if (turn.pair_axis.defined()) saved.push_back(turn.pair_axis);
+        ctx->save_for_backward(saved);
+        ctx->saved_data["how"] = (int64_t)turn.interleaved | (int64_t)turn.inverse << 1;
+        ctx->saved_data["offset"] = turn.offset;
+        const auto y = turn({a, b.value_or(at::Tensor())});
+        torch::autograd::variable_list out{y[0]};
+        if (b.has_value()) out.push_back(y[1]);
+        return out;
+    }
+
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list d)
+    {
+        torch::autograd::variable_list grads(3);
+        std::vector<int> which;
+        for (int i = 0; i < (int)d.size(); ++i)
+            if (d[i].defined()) which.push_back(i);
+        if (which.empty()) return grads;
+        const auto saved = ctx->get_saved_variables();
+        const int64_t how = ctx->saved_data["how"].toInt();
+        const Turn back{saved[0], saved.size() > 1 ? saved[1] : at::Tensor(), saved.size() > 2 ? saved[2] : at::Tensor(),
+                        (how & 1) != 0, (how & 2) == 0, ctx->saved_data["offset"].toInt()};
+        std::optional<at::Tensor> second;
+        if (which.size() > 1) second = d[which[1]];
+        try {
+            const auto y = at::GradMode::is_enabled() ? apply(d[which[0]], second, back) : as_list(back({d[which[0]], second.value_or(at::Tensor())}));
+            for (size_t i = 0; i < which.size(); ++i) grads[which[i]] = y[i];
+        } catch (const Refused &r) {
+            TORCH_CHECK(false, "the gradient of rotary: status ", (int)r.status);
+        }
+        return grads;
+    }
+
+    static torch::autograd::variable_list as_list(const std::array<at::Tensor, 2> &y) { return {y[0], y[1]}; }
+};
+
+// rotary(q, k or None, inv_freq, positions, pair_axis, interleaved, position_offset) ->
+// (q, k or None) turned, or a status
 PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "rotary takes 8 arguments");
+    if (n != 7) {
+        PyErr_SetString(PyExc_TypeError, "rotary takes 7 arguments");
         return nullptr;
     }
-    at::Tensor x[2], y[2];
-    fa_rows in[2]{}, out[2]{};
-    const at::Tensor *first = nullptr;
+    at::Tensor x[2];
+    const at::Tensor *first = &x[0];
     for (int i = 0; i < 2; ++i) {
-        if (a[i] == Py_None) continue;
+        if (i == 1 && a[i] == Py_None) continue;
         if (!THPVariable_Check(a[i])) {
             PyErr_SetString(PyExc_TypeError, "q and k must be tensors");
             return nullptr;
@@ -477,19 +566,17 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
             value_error("q and k must be bf16 or fp16 CUDA tensors [B, heads, T, D]");
             return nullptr;
         }
-        if (!first) first = &x[i];
         if (x[i].scalar_type() != first->scalar_type() || x[i].device() != first->device() || x[i].size(0) != first->size(0) ||
-            x[i].size(2) != first->size(2) || x[i].size(3) != first->size(3) || x[i].size(1) > INT32_MAX) {
+            x[i].size(2) != first->size(2) || x[i].size(3) != first->size(3)) {
             value_error("q and k must share dtype, device, B, T and D");
             return nullptr;
         }
+        for (int d = 0; d < 4; ++d)
+            if (x[i].size(d) > INT32_MAX) {
+                value_error("sizes must fit 32 bits");
+                return nullptr;
+            }
     }
-    if (!first) {
-        value_error("q or k must be given");
-        return nullptr;
-    }
-    const int64_t B = first->size(0), T = first->size(2), D = first->size(3);
-    const c10::cuda::CUDAGuard guard(first->device());
     if (!THPVariable_Check(a[2])) {
         PyErr_SetString(PyExc_TypeError, "inv_freq must be a tensor");
         return nullptr;
@@ -499,38 +586,36 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
         value_error("inv_freq must be a float32 tensor of one dimension on the device of q and k");
         return nullptr;
     }
+    const c10::cuda::CUDAGuard guard(first->device());
     freq = freq.contiguous();
     Positions positions;
-    if (!positions_of(a[3], a[4], B, T, freq.numel(), first->device(), positions)) return nullptr;
+    if (!positions_of(a[3], a[4], first->size(0), first->size(2), freq.numel(), first->device(), positions)) return nullptr;
     const int interleaved = PyObject_IsTrue(a[5]);
     const long long offset = PyLong_AsLongLong(a[6]);
-    const int inverse = PyObject_IsTrue(a[7]);
-    if (interleaved < 0 || inverse < 0 || (offset == -1 && PyErr_Occurred())) return nullptr;
-    if (B > INT32_MAX || T > INT32_MAX || D > INT32_MAX) {
-        value_error("sizes must fit 32 bits");
-        return nullptr;
+    if (interleaved < 0 || (offset == -1 && PyErr_Occurred())) return nullptr;
+    std::array<at::Tensor, 2> y;
+    fa_status st = FA_OK;
+    {
+        struct Released {
+            PyThreadState *state = PyEval_SaveThread();
+            ~Released() { PyEval_RestoreThread(state); }
+        } released;
+        try {
+            const Turn turn{freq.detach(), positions.n, positions.pair_axis, interleaved != 0, false, offset};
+            if (at::GradMode::is_enabled() && (x[0].requires_grad() || (x[1].defined() && x[1].requires_grad()))) {
+                const auto r = Rotary::apply(x[0], x[1].defined() ? std::optional<at::Tensor>(x[1]) : std::nullopt, turn);
+                y = {r[0], r.size() > 1 ? r[1] : at::Tensor()};
+            } else {
+                y = turn({x[0], x[1]});
+            }
+        } catch (const Refused &r) {
+            st = r.status;
+        }
     }
-    for (int i = 0; i < 2; ++i) {
-        if (!x[i].defined()) continue;
-        if (!followable(x[i])) x[i] = x[i].clone(at::MemoryFormat::Contiguous);
-        y[i] = at::empty(x[i].sizes(), at::TensorOptions().dtype(x[i].scalar_type()).device(x[i].device()));
-        in[i] = rows_of(x[i]);
-        out[i] = rows_of(y[i]);
-    }
-    const auto heads = [&](int i) { return x[i].defined() ? (int)x[i].size(1) : 0; };
-    void *stream = c10::cuda::getCurrentCUDAStream(first->get_device()).stream();
-    fa_status st;
-    Py_BEGIN_ALLOW_THREADS
-    st = g_rotary(&in[0], &out[0], &in[1], &out[1], (int)B, heads(0), heads(1), (int)T, (int)D, freq.const_data_ptr<float>(),
-                  2 * (int)freq.numel(), interleaved, positions.get(), offset, inverse, first->scalar_type() == at::kHalf, stream);
-    Py_END_ALLOW_THREADS
     if (st != FA_OK) return PyLong_FromLong(st);
     PyObject *pair = PyTuple_New(2);
     if (!pair) return nullptr;
-    for (int i = 0; i < 2; ++i) {
-        PyObject *o = y[i].defined() ? THPVariable_Wrap(y[i]) : Py_NewRef(Py_None);
-        PyTuple_SET_ITEM(pair, i, o);
-    }
+    for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(pair, i, y[i].defined() ? THPVariable_Wrap(y[i]) : Py_NewRef(Py_None));
     return pair;
     END_HANDLE_TH_ERRORS
 }
