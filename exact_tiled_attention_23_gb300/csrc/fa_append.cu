@@ -253,11 +253,11 @@ cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 // takes a group of 16 elements of a key or value, so that no thread needs another's
 // largest value (a key's partner elements are read a second time, from the L1).
 
-// Elements 8 u .. 8 u + 7 of a turned head.
+// Elements 8 u .. 8 u + 7 of a turned head, which are `w` before.
 template <bool kF16, int kMode>
-__device__ __forceinline__ void turned8(const uint16_t *src, int u, int rot, const float2 *cs, float (&x)[8])
+__device__ __forceinline__ void turned8(const uint16_t *src, int u, uint4 w, int rot, const float2 *cs, float (&x)[8])
 {
-    widen8<kF16>(*reinterpret_cast<const uint4 *>(src + u * 8), x);
+    widen8<kF16>(w, x);
     if (u * 8 >= rot) return;
     const int half = rot / 2;
     if constexpr (kMode == kHalves) {
@@ -291,15 +291,30 @@ __device__ __forceinline__ void turned8(const uint16_t *src, int u, int rot, con
     }
 }
 
+// (A thread's first group is read before it is known where it goes: two waits less.)
 template <bool kF16, int kMode>
 __global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p)
 {
     extern __shared__ float2 cs[];                          // [rot / 2]
     ptx::wait_for_primary();
-    const int64_t b = blockIdx.x / p.T;
-    const int t = (int)(blockIdx.x % p.T);
-    const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
+    const int b = p.by_t.quotient((int)blockIdx.x), t = (int)blockIdx.x - b * p.T;
     const int D = p.c.D, Hkv = p.c.Hkv, units = D / 8;
+    // keys, then values; groups of a head
+    const int groups = D <= 64 ? 2 : D <= 128 ? 3 : 4;      // (the logarithm of how many a row has)
+    const auto source = [&](int which) {
+        return which < Hkv ? p.k + b * p.k_s[0] + which * p.k_s[1] + t * p.k_s[2]
+                           : p.v + b * p.v_s[0] + (which - Hkv) * p.v_s[1] + t * p.v_s[2];
+    };
+    uint4 w[2];
+    const auto fetch = [&](int e) {
+        const uint16_t *src = source(e >> groups);
+        const int u = 2 * (e & ((1 << groups) - 1));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)                          // past the head: padding
+            w[h] = u + h < units ? *reinterpret_cast<const uint4 *>(src + (u + h) * 8) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if ((int)threadIdx.x < (2 * Hkv) << groups) fetch(threadIdx.x);
+    const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
 
     if (i < 0) {                                            // no token here: its query is zero
         if (p.q)
@@ -308,44 +323,38 @@ __global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p
                                            (e % units) * 8) = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
-    const uint32_t at = (uint32_t)i, size = (uint32_t)p.c.page_size;
+    const int entry = p.c.by_page.quotient(i);
     int page = -1;
-    if (at / size < (uint32_t)p.c.table_width) page = p.c.table[b * p.c.table_stride + at / size];
-    const bool stored = page >= 0 && page < p.c.num_pages;   // otherwise the key and value are dropped
+    if (entry < p.c.table_width) page = p.c.table[b * p.c.table_stride + entry];
     turns_of(p.turn, b, t, i, cs);
     __syncthreads();
 
-    if (stored) {
-        const int64_t slot = at % size;
+    if (page >= 0 && page < p.c.num_pages) {                // otherwise the key and value are dropped
+        const int64_t slot = i - entry * p.c.page_size;
         const int64_t row = page * p.c.s_page + slot * p.c.s_slot, scales = page * p.c.t_page + slot * p.c.t_slot;
-        const int groups = D <= 64 ? 2 : D <= 128 ? 3 : 4;  // (the logarithm of how many a row has)
         for (int e = threadIdx.x; e < (2 * Hkv) << groups; e += kThreads) {
+            if (e != (int)threadIdx.x) fetch(e);
             const int which = e >> groups, g = e & ((1 << groups) - 1), head = which < Hkv ? which : which - Hkv;
             float x[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int u = 2 * g + h;
                 float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = 0.f;      // past the head: padding
-                if (u < units) {
-                    if (which < Hkv)
-                        turned8<kF16, kMode>(p.k + b * p.k_s[0] + head * p.k_s[1] + t * p.k_s[2], u, p.turn.rot, cs, y);
-                    else
-                        widen8<kF16>(*reinterpret_cast<const uint4 *>(p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2] + u * 8), y);
-                }
+                if (which < Hkv && 2 * g + h < units)
+                    turned8<kF16, kMode>(source(which), 2 * g + h, w[h], p.turn.rot, cs, y);
+                else
+                    widen8<kF16>(w[h], y);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[8 * h + j] = y[j];
             }
             uint32_t code;
-            const uint2 w = to_four(x, code);
-            *reinterpret_cast<uint2 *>((which < Hkv ? p.c.k : p.c.v) + row + head * p.c.s_head + g * 8) = w;
+            const uint2 four = to_four(x, code);
+            *reinterpret_cast<uint2 *>((which < Hkv ? p.c.k : p.c.v) + row + head * p.c.s_head + g * 8) = four;
             ((which < Hkv ? p.c.ks : p.c.vs) + scales + head * p.c.t_head)[g] = (uint8_t)code;
         }
     }
-    const auto source = [&](int head) -> const uint16_t * { return p.q + b * p.q_s[0] + head * p.q_s[1] + t * p.q_s[2]; };
+    const auto from = [&](int head) -> const uint16_t * { return p.q + b * p.q_s[0] + head * p.q_s[1] + t * p.q_s[2]; };
     const auto target = [&](int head) -> uint16_t * { return p.q_out + b * p.qo_s[0] + head * p.qo_s[1] + t * p.qo_s[2]; };
-    turn_heads<kF16, kMode>(p.q ? p.Hq : 0, D, p.turn.rot, cs, source, target);
+    turn_heads<kF16, kMode>(p.q ? p.Hq : 0, D, p.turn.rot, cs, from, target);
 }
 
 template <bool kF16>

@@ -20,19 +20,26 @@ namespace fa {
 constexpr uint32_t kLargestScale = 226;
 
 // x / s to nearest, from y = 1 / s to nearest: P. Markstein's correction of a quotient
-// by its remainder (1990).  (s not so small or large that a step leaves the normal
-// range; a quotient that small is 0 in 4 bits.)
+// by its remainder (1990).  (s is not so small or large that a step leaves the normal
+// range, and a quotient that small is 0 in 4 bits.)
 __device__ __forceinline__ float quotient(float x, float s, float y)
 {
     const float q = x * y;
     return fmaf(fmaf(-q, s, x), y, q);
 }
 
+// Two of them; s as (-s, -s), y as (y, y).
+__device__ __forceinline__ uint64_t quotient2(uint64_t x, uint64_t minus_s, uint64_t y)
+{
+    const uint64_t q = ptx::mul2(x, y);
+    return ptx::fma2(ptx::fma2(q, minus_s, x), y, q);
+}
+
 // The scale for a group whose largest magnitude is `largest` (infinities: the
 // largest scale; a NaN among the values is not counted).
 __device__ __forceinline__ uint32_t scale_code(float largest)
 {
-    const float t = largest < INFINITY ? quotient(largest, 6.f, 1.f / 6.f) : largest;
+    const float t = quotient(largest, 6.f, 1.f / 6.f);        // (NaN: the largest scale)
     if (t < 6.103515625e-5f) return (uint32_t)__float2int_rn(t * 131072.f);     // below 2^-14: multiples of 2^-17
     const uint32_t bits = __float_as_uint(t);
     const uint32_t up = (bits + 0x7ffffu + ((bits >> 20) & 1u)) >> 20;          // 3 mantissa bits, to nearest
@@ -47,19 +54,21 @@ __device__ __forceinline__ float scale_value(uint32_t code)
 // 16 values in 4 bits each, and their scale.
 __device__ __forceinline__ uint2 to_four(const float (&x)[16], uint32_t &code)
 {
-    float largest = 0.f;
+    float largest = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) largest = fmaxf(largest, fabsf(x[i]));
+    for (int i = 2; i < 16; i += 2) largest = ptx::max3(largest, fabsf(x[i]), fabsf(x[i + 1]));
     code = scale_code(largest);
     if (code == 0) return make_uint2(0u, 0u);
     // (exact quotients: x / s halfway between two numbers stays halfway)
     const float s = scale_value(code), y = __frcp_rn(s);
+    const uint64_t minus_s2 = ptx::pack2(-s, -s), y2 = ptx::pack2(y, y);
     uint32_t w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = fabsf(x[8 * h + i]) < INFINITY ? quotient(x[8 * h + i], s, y) : x[8 * h + i];
+        for (int i = 0; i < 8; i += 2)
+            ptx::unpack2(quotient2(ptx::pack2(x[8 * h + i], x[8 * h + i + 1]), minus_s2, y2), q[i], q[i + 1]);
         w[h] = ptx::pack_e2m1x8(q);
     }
     return make_uint2(w[0], w[1]);

@@ -35,7 +35,7 @@ struct FourPlan {
         const int64_t page = (int64_t)c.Hkv * c.page_size * c.D, each = page * c.table_width * 4;
         group = (int)std::max<int64_t>(1, std::min<int64_t>(B, kWide / each));
         const int64_t pages = (int64_t)group * c.table_width;
-        if (pages > INT32_MAX || page > INT32_MAX) {
+        if (pages * c.Hkv > INT32_MAX || 2 * page > INT32_MAX) {
             ok = false;
             return;
         }
@@ -143,6 +143,7 @@ fa_status fa_kv_append_q4(const fa_paged_kv4 *cache, const fa_rows *K, const fa_
     if (st != FA_OK) return st;
     p.c = cache4_of(*cache);
     put_rows(p, K, V, queries ? Q : nullptr, Q_out);
+    p.by_t = fa::make_fast_div((uint32_t)T);
     p.B = B;
     p.T = T;
     p.Hq = queries ? Hq : 0;

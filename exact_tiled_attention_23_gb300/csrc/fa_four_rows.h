@@ -17,6 +17,9 @@ struct WidenParams {
     uint16_t *k, *v;                   // [B * width, Hkv, page_size, D]
     int32_t *table, *seq_len;          // [B, width], [B]
     int f16;
+    // set by the launcher: 16 elements, of a row; heads of a CTA, CTAs of a page
+    FastDiv by_groups;
+    int heads, parts;
 };
 
 int four_rows_per_tile(int D, int64_t rows);
@@ -26,6 +29,6 @@ cudaError_t launch_four_rows(const FourParams &f, int ctas, cudaStream_t stream)
 // A team of p.team CTAs per tile of 8 rows, and how many teams fit the device together.
 cudaError_t launch_four_team(const FourParams &f, int ctas, cudaStream_t stream);
 int four_teams_at_once(int device, int team);
-cudaError_t launch_widen_pages(const WidenParams &p, int64_t pages, cudaStream_t stream);
+cudaError_t launch_widen_pages(WidenParams p, int64_t pages, cudaStream_t stream);
 
 }  // namespace fa

@@ -93,6 +93,7 @@ struct Append4Params {
     const uint16_t *k, *v, *q;         // [B, H, T, D] through the strides below; q may be null
     uint16_t *q_out;
     int64_t k_s[3], v_s[3], q_s[3], qo_s[3];   // batch, head, token
+    FastDiv by_t;                      // T
     int B, T, Hq, f16;
 };
 

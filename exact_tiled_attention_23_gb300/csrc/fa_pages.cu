@@ -19,7 +19,9 @@ constexpr int kThreads = 1024;         // of a CTA that sums
 constexpr int kWarps = kThreads / 32;
 constexpr int kOneList = 65536;        // pages that one CTA lists by itself
 constexpr int kSegment = 16384;        // pages of a CTA's segment at least, beyond that
-constexpr int kMostSegments = 128;
+// Where all pages are looked at, not only as many as are needed (15678 pages, a
+// compaction's lists: one CTA 19 us, four 10).
+constexpr int kAllSegment = 4096;
 
 // The sums of x over the threads in front of each, after `base`, which the sum of all
 // is added to.  `sums` has two rows that take turns, so that one barrier is enough.
@@ -186,14 +188,21 @@ __device__ __forceinline__ Growth growth_of(const PagesParams &p, int64_t b)
 }
 
 // Sequences grow: who gets which free pages is the prefix sum of what they need.  A
-// thread has a sequence, and takes one page itself; more are a warp's work.
+// thread has a sequence, and takes one page itself; the pages of those that need more
+// are all warps' work, 32 at a time.
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesParams p)
 {
     __shared__ int64_t sums[2][kWarps];
+    struct Many {
+        int sequence, have, need, first;
+    };
+    __shared__ Many many[kThreads];
+    __shared__ int queued;
     int turn = 0;
     int64_t total = 0;
+    if (threadIdx.x == 0) queued = 0;
     ptx::wait_for_primary();
-    const int lane = threadIdx.x % 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Growth g{};
     int64_t first = 0;
     for (int64_t at = 0; at < p.B; at += kThreads) {
@@ -220,23 +229,21 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesParams p)
             if (fits && g.then > g.n) p.seq_len[b] = (int)g.then;
             p.taken[b] = fits ? (int)g.need : kRefused;
         }
-        for (unsigned many = __ballot_sync(0xffffffffu, fits && g.need > 1); many; many &= many - 1) {
-            const int of = __ffs(many) - 1;
-            const int64_t need = __shfl_sync(0xffffffffu, g.need, of), from = __shfl_sync(0xffffffffu, first, of);
-            int32_t *entry = p.table + (b - lane + of) * p.table_stride + __shfl_sync(0xffffffffu, g.have, of);
-            constexpr int kWide = 4;       // loads together
-            for (int64_t i = lane; i < need; i += 32 * kWide) {
-                int page[kWide];
-#pragma unroll
-                for (int j = 0; j < kWide; ++j) page[j] = i + 32 * j < need ? p.list[from + i + 32 * j] : -1;
-#pragma unroll
-                for (int j = 0; j < kWide; ++j)
-                    if (page[j] >= 0) {
-                        entry[i + 32 * j] = page[j];
-                        p.refs[page[j]] = 1;
-                    }
+        if (fits && g.need > 1) many[atomicAdd(&queued, 1)] = Many{(int)b, (int)g.have, (int)g.need, (int)first};
+        __syncthreads();
+        const int items = queued;
+        for (int i = 0; i < items; ++i) {
+            const Many x = many[i];
+            // (another warp begins each, so that short ones are spread, too)
+            for (int64_t j = (int64_t)((warp - i) & (kWarps - 1)) * 32 + lane; j < x.need; j += kThreads) {
+                const int page = p.list[x.first + j];
+                p.table[x.sequence * p.table_stride + x.have + j] = page;
+                p.refs[page] = 1;
             }
         }
+        __syncthreads();
+        if (threadIdx.x == 0) queued = 0;
+        __syncthreads();
     }
 }
 
@@ -463,10 +470,11 @@ cudaError_t list_segments(const PagesParams &p, cudaStream_t stream)
 
 }  // namespace
 
-int page_segments(int num_pages)
+int page_segments(int num_pages, bool all)
 {
-    if (num_pages <= kOneList) return 1;
-    const int n = (num_pages - 1) / kSegment + 1;
+    const int size = all ? kAllSegment : kSegment;
+    if (num_pages <= (all ? kAllSegment : kOneList)) return 1;
+    const int n = (num_pages - 1) / size + 1;
     return n < kMostSegments ? n : kMostSegments;
 }
 

@@ -45,8 +45,10 @@ struct CopyParams {
     const int32_t *src, *dst, *count;  // count: how many pairs, if not n
 };
 
-// Segments that a pool is listed in, and parts of a page of so many bytes.
-int page_segments(int num_pages);
+// Segments that a pool is listed in (all: to its end, whatever is needed), and parts of
+// a page of so many bytes.
+constexpr int kMostSegments = 128;
+int page_segments(int num_pages, bool all);
 int64_t copy_parts(int64_t bytes);
 
 cudaError_t launch_grow(const PagesParams &p, cudaStream_t stream);

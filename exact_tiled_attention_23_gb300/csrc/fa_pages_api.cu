@@ -23,7 +23,7 @@ fa_status check_table(const fa_page_table *t)
 }
 
 // The table, and the workspace's parts in order; returns its bytes.
-size_t place(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace)
+size_t place(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace, bool all = false)
 {
     p.table = t.table;
     p.table_stride = t.table_stride;
@@ -34,7 +34,7 @@ size_t place(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace)
     p.num_pages = t.num_pages;
     p.page_size = t.page_size;
     p.n = n;
-    p.segments = fa::page_segments(t.num_pages);
+    p.segments = fa::page_segments(t.num_pages, all);
     p.segment = (t.num_pages + p.segments - 1) / p.segments;
     uint8_t *base = static_cast<uint8_t *>(workspace);
     size_t at = 0;
@@ -43,7 +43,7 @@ size_t place(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace)
         at += round_up(bytes);
         return r;
     };
-    p.counts = static_cast<int32_t *>(take((size_t)p.segments * 4));
+    p.counts = static_cast<int32_t *>(take((size_t)fa::kMostSegments * 4));
     p.count = static_cast<int32_t *>(take(4));
     p.list = static_cast<int32_t *>(take((size_t)t.num_pages * 4));
     p.src = static_cast<int32_t *>(take((size_t)std::max(t.num_pages, n) * 4));
@@ -52,9 +52,9 @@ size_t place(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace)
     return at;
 }
 
-fa_status with_workspace(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace, size_t bytes)
+fa_status with_workspace(fa::PagesParams &p, const fa_page_table &t, int n, void *workspace, size_t bytes, bool all = false)
 {
-    const size_t need = place(p, t, n, workspace);
+    const size_t need = place(p, t, n, workspace, all);
     return workspace && aligned(workspace, 16) && bytes >= need ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
@@ -159,7 +159,7 @@ fa_status fa_kv_compact(const fa_page_table *table, int32_t *moved, int32_t *src
         !aligned(count, 4))
         return FA_ERR_INVALID_ARG;
     fa::PagesParams p{};
-    st = with_workspace(p, *table, 0, workspace, workspace_bytes);
+    st = with_workspace(p, *table, 0, workspace, workspace_bytes, true);
     if (st != FA_OK) return st;
     p.taken = moved;
     p.src = src;

@@ -9,59 +9,89 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// A CTA per token; a thread takes 16 elements of a key or value.
-template <bool kFour, bool kF16>
+// A CTA has kTokens tokens; a thread takes 16 elements of a key or value of each, all
+// read before any is written.
+template <bool kFour, bool kF16, int kTokens>
 __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p)
 {
     ptx::wait_for_primary();
-    const int64_t b = blockIdx.x / (unsigned)p.T;
-    const int t = (int)(blockIdx.x - b * p.T);
+    const int parts = (p.T + kTokens - 1) / kTokens;
+    const int64_t b = blockIdx.x / (unsigned)parts;
+    const int t0 = (int)(blockIdx.x - b * parts) * kTokens;
     const int32_t *seq_len = kFour ? p.c4.seq_len : p.c.seq_len, *table = kFour ? p.c4.table : p.c.table;
-    const int i = max(seq_len[b], -1) - p.T + t;
-    const uint32_t at = (uint32_t)max(i, 0), size = (uint32_t)(kFour ? p.c4.page_size : p.c.page_size);
-    int page = -1;
-    if (i >= 0 && at / size < (uint32_t)(kFour ? p.c4.table_width : p.c.table_width))
-        page = table[b * (kFour ? p.c4.table_stride : p.c.table_stride) + at / size];
-    const bool there = page >= 0 && page < (kFour ? p.c4.num_pages : p.c.num_pages);
-    const int64_t slot = there ? at % size : 0;
-    if (!there) page = 0;
+    const uint32_t size = (uint32_t)(kFour ? p.c4.page_size : p.c.page_size);
+    const int n = max(seq_len[b], -1) - p.T;
+    int page[kTokens], slot[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+        const int i = n + t0 + k;
+        const uint32_t at = (uint32_t)max(i, 0);
+        page[k] = -1;
+        slot[k] = (int)(at % size);
+        if (t0 + k < p.T && i >= 0 && at / size < (uint32_t)(kFour ? p.c4.table_width : p.c.table_width))
+            page[k] = table[b * (kFour ? p.c4.table_stride : p.c.table_stride) + at / size];
+    }
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k)
+        if (page[k] >= (kFour ? p.c4.num_pages : p.c.num_pages)) page[k] = -1;
     const int D = kFour ? p.c4.D : p.c.D, Hkv = kFour ? p.c4.Hkv : p.c.Hkv;
     for (int e = threadIdx.x; e < 2 * Hkv * (int)p.by_groups.by; e += kThreads) {
         const int which = p.by_groups.quotient(e), g = e - which * (int)p.by_groups.by, head = which < Hkv ? which : which - Hkv;
         const bool both = 16 * g + 8 < D;           // (a last group may have 8)
-        uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (there) {
+        uint4 w[kTokens][2];
+        uint2 four[kTokens];
+        uint32_t scale[kTokens];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            w[k][0] = w[k][1] = make_uint4(0u, 0u, 0u, 0u);
+            four[k] = make_uint2(0u, 0u);
+            scale[k] = 0;
+            if (page[k] < 0) continue;
             if constexpr (kFour) {
                 const PagedCache4 &c = p.c4;
-                const uint8_t *row = (which < Hkv ? c.k : c.v) + page * c.s_page + slot * c.s_slot + head * c.s_head;
-                const uint8_t *scales = (which < Hkv ? c.ks : c.vs) + page * c.t_page + slot * c.t_slot + head * c.t_head;
-                const uint2 x = *reinterpret_cast<const uint2 *>(row + 8 * g);
-                const uint32_t scale = scales[g];
-                w[0] = rows_from_four<kF16>(x.x, scale);
-                w[1] = rows_from_four<kF16>(x.y, scale);
+                four[k] = *reinterpret_cast<const uint2 *>((which < Hkv ? c.k : c.v) + page[k] * c.s_page + slot[k] * c.s_slot +
+                                                           head * c.s_head + 8 * g);
+                scale[k] = ((which < Hkv ? c.ks : c.vs) + page[k] * c.t_page + slot[k] * c.t_slot + head * c.t_head)[g];
             } else {
                 const PagedCache &c = p.c;
-                const uint4 *row = reinterpret_cast<const uint4 *>((which < Hkv ? c.k : c.v) + page * c.s_page + slot * c.s_slot +
-                                                                   head * c.s_head + 16 * g);
-                w[0] = row[0];
-                if (both) w[1] = row[1];
+                const uint4 *row = reinterpret_cast<const uint4 *>((which < Hkv ? c.k : c.v) + page[k] * c.s_page +
+                                                                   slot[k] * c.s_slot + head * c.s_head + 16 * g);
+                w[k][0] = row[0];
+                if (both) w[k][1] = row[1];
             }
         }
-        uint4 *dst = reinterpret_cast<uint4 *>((which < Hkv ? p.k + b * p.k_s[0] + head * p.k_s[1] + t * p.k_s[2]
-                                                            : p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2]) + 16 * g);
-        dst[0] = w[0];
-        if (both) dst[1] = w[1];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int t = t0 + k;
+            if (t >= p.T) continue;
+            if constexpr (kFour) {
+                w[k][0] = rows_from_four<kF16>(four[k].x, scale[k]);
+                w[k][1] = rows_from_four<kF16>(four[k].y, scale[k]);
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>((which < Hkv ? p.k + b * p.k_s[0] + head * p.k_s[1] + t * p.k_s[2]
+                                                                : p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2]) + 16 * g);
+            dst[0] = w[k][0];
+            if (both) dst[1] = w[k][1];
+        }
     }
+}
+
+template <int kTokens>
+cudaError_t launch(const ReadParams &p, bool four, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)((int64_t)p.B * ((p.T + kTokens - 1) / kTokens)));
+    if (!four) return launch_behind(read_kernel<false, false, kTokens>, grid, kThreads, 0, stream, p);
+    return p.f16 ? launch_behind(read_kernel<true, true, kTokens>, grid, kThreads, 0, stream, p)
+                 : launch_behind(read_kernel<true, false, kTokens>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_read(const ReadParams &p, bool four, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.B * p.T));
-    if (!four) return launch_behind(read_kernel<false, false>, grid, kThreads, 0, stream, p);
-    return p.f16 ? launch_behind(read_kernel<true, true>, grid, kThreads, 0, stream, p)
-                 : launch_behind(read_kernel<true, false>, grid, kThreads, 0, stream, p);
+    // Few tokens: a CTA each, the shortest way; many: four, whose reads wait together.
+    const bool many = p.T >= 4 && (int64_t)p.B * p.T > 4 * 16 * (int64_t)sm_count_of(current_device());
+    return many ? launch<4>(p, four, stream) : launch<1>(p, four, stream);
 }
 
 }  // namespace fa
