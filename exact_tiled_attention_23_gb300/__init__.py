@@ -797,9 +797,9 @@ def forward_paged(q, cache, causal: bool = True, scale=None, out=None, lse=None,
     Hq is a multiple of the cache's Hkv.  causal: the queries are the last T
     tokens of their sequences; otherwise each sees all seq_len keys.  Queries
     that see no key get O = 0 and LSE = -inf.  Up to 32 query rows of a sequence
-    that share a key (T * Hq / Hkv) have weights of two 16-bit numbers, so that
-    only O's own rounding shows; more have one, as in forward() (include/fa.h has
-    the errors).  The other arguments are forward()'s; q may have any strides, and
+    that share a key (T * Hq / Hkv) have weights of two 16-bit numbers (of a PagedKV4
+    with bf16 queries, of one fp16 number), so that only O's own rounding shows; more
+    have one, as in forward() (include/fa.h has the errors).  The other arguments are forward()'s; q may have any strides, and
     out too (last dimension contiguous).  The workspace (a CUDA tensor of at least
     cache.workspace_bytes(Hq, T) bytes) is allocated here when not given.
     """

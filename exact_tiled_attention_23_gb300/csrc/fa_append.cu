@@ -293,7 +293,7 @@ __device__ __forceinline__ void turned8(const uint16_t *src, int u, uint4 w, int
 
 // (A thread's first group is read before it is known where it goes: two waits less.)
 template <bool kF16, int kMode>
-__global__ void __launch_bounds__(kThreads) append4_kernel(const Append4Params p)
+__global__ void __launch_bounds__(kThreads, 10) append4_kernel(const Append4Params p)
 {
     extern __shared__ float2 cs[];                          // [rot / 2]
     ptx::wait_for_primary();

@@ -104,4 +104,17 @@ __device__ __forceinline__ uint4 rows_from_four(uint32_t w, uint32_t code)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// The power of two that takes a row of bf16 queries whose largest magnitude is
+// `largest` to halves (2^14 .. 2^15 at most), and its inverse.
+struct RowScale {
+    float up, down;
+};
+
+__device__ __forceinline__ RowScale row_scale(float largest)
+{
+    int up = 127 + 14 - (int)(__float_as_uint(largest) >> 23);
+    up = largest == 0.f ? 0 : max(-112, min(up, 100));
+    return RowScale{__uint_as_float((uint32_t)(127 + up) << 23), __uint_as_float((uint32_t)(127 - up) << 23)};
+}
+
 }  // namespace fa

@@ -10,35 +10,38 @@ namespace {
 
 using namespace fa::paged;
 
-// Sequences whose keys are decoded to 16 bits at a time, for the tensor cores: as many
-// as have kWide bytes of them at most, one at least.
-constexpr int64_t kWide = (int64_t)256 << 20;
+// Sequences whose keys are decoded to 16 bits at a time: as many as have kWide bytes of
+// them at most, one at least, if that has kMostWide at most.
+constexpr int64_t kWide = (int64_t)256 << 20, kMostWide = (int64_t)1 << 30;
+
+// Row tiles of a sequence up to which each decodes its keys itself on the tensor cores;
+// more read keys that are decoded once.  1, 2, 3, 4 and 8 tiles, themselves against
+// once, in us: 8 sequences of 4000 to 8000 keys 55 and 100, 91 and 120, 126 and 137,
+// 163 and 161, 312 and 237; 64 of up to 8000 (4 tiles) 957 and 1017; one of 16384 (2, 4
+// and 8) 40 and 53, 64 and 62, 112 and 85.
+constexpr int kDirectTiles = 4;
 
 // How a forward over a 4-bit cache is cut, and its workspace.
 struct FourPlan {
-    bool wide = false;      // decoded first, and then the tensor-core kernel
-    Plan rows;              // else
+    bool wide = false;      // decoded first, and then the tensor-core kernel of 16-bit caches
+    Plan direct;            // else: the row kernel, or the tensor-core kernel that decodes
     int group = 0;          // sequences at a time
     fa_paged_kv pool{};     // of a group, without its places in the workspace
     size_t pool_bytes = 0, table_bytes = 0, len_bytes = 0, inner = 0, bytes = 0;
     bool ok = true;
 
-    FourPlan(const fa_paged_kv4 &c, int B, int Hq, int T) : rows(B, c.Hkv, c.D, (int64_t)(Hq / c.Hkv) * T, (int64_t)c.table_width * c.page_size)
+    FourPlan(const fa_paged_kv4 &c, int B, int Hq, int T) : direct(B, c, (int64_t)(Hq / c.Hkv) * T, (int64_t)c.table_width * c.page_size)
     {
         const int64_t R = (int64_t)(Hq / c.Hkv) * T;
-        wide = R > kMostRows && c.D <= 128 && c.page_size % 8 == 0 && c.table_width > 0;
-        if (!wide) {
-            ok = rows.ok;
-            bytes = rows.bytes;
-            return;
-        }
         const int64_t page = (int64_t)c.Hkv * c.page_size * c.D, each = page * c.table_width * 4;
-        group = (int)std::max<int64_t>(1, std::min<int64_t>(B, kWide / each));
-        const int64_t pages = (int64_t)group * c.table_width;
-        if (pages * c.Hkv > INT32_MAX || 2 * page > INT32_MAX) {
-            ok = false;
+        wide = direct.tc && direct.part.tiles > kDirectTiles && each > 0 && each <= kMostWide;
+        if (!wide) {
+            ok = direct.ok;
+            bytes = direct.bytes;
             return;
         }
+        group = (int)std::max<int64_t>(1, std::min<int64_t>(B, kWide / each));
+        const int64_t pages = (int64_t)group * c.table_width;       // (2^30 bytes of rows of 64 at least: fewer than 2^24)
         pool.stride_page = page;
         pool.stride_head = (int64_t)c.page_size * c.D;
         pool.stride_slot = c.D;
@@ -188,26 +191,28 @@ fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_
     const int D = cache->D;
     if (!rows_ok(Q, B, Hq, T, D, false) || !rows_ok(O, B, Hq, T, D, true)) return FA_ERR_INVALID_ARG;
     if (LSE && !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
-    FourPlan plan(*cache, B, Hq, T);
-    if (!plan.ok || !workspace || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return FA_ERR_INVALID_ARG;
+    const int64_t own_keys = (int64_t)cache->table_width * cache->page_size;
+    const int G = Hq / cache->Hkv;
+    FourPlan whole(*cache, B, Hq, T);
+    if (!whole.ok || !workspace || !aligned(workspace, 16) || workspace_bytes < whole.bytes) return FA_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
-    if (plan.wide) {
+    if (whole.wide) {
         uint8_t *at = static_cast<uint8_t *>(workspace);
         fa::WidenParams w{};
         w.f16 = f16 ? 1 : 0;
         w.k = reinterpret_cast<uint16_t *>(at);
-        w.v = reinterpret_cast<uint16_t *>(at + plan.pool_bytes);
-        w.table = reinterpret_cast<int32_t *>(at + 2 * plan.pool_bytes);
-        w.seq_len = reinterpret_cast<int32_t *>(at + 2 * plan.pool_bytes + plan.table_bytes);
-        uint8_t *inner = at + 2 * plan.pool_bytes + plan.table_bytes + plan.len_bytes;
-        fa_paged_kv pool = plan.pool;
+        w.v = reinterpret_cast<uint16_t *>(at + whole.pool_bytes);
+        w.table = reinterpret_cast<int32_t *>(at + 2 * whole.pool_bytes);
+        w.seq_len = reinterpret_cast<int32_t *>(at + 2 * whole.pool_bytes + whole.table_bytes);
+        uint8_t *inner = at + 2 * whole.pool_bytes + whole.table_bytes + whole.len_bytes;
+        fa_paged_kv pool = whole.pool;
         pool.k = w.k;
         pool.v = w.v;
         pool.table = w.table;
         pool.seq_len = w.seq_len;
-        for (int b = 0; b < B; b += plan.group) {
-            const int n = std::min(plan.group, B - b);
+        for (int b = 0; b < B; b += whole.group) {
+            const int n = std::min(whole.group, B - b);
             fa_paged_kv4 part = *cache;
             part.table += (int64_t)b * cache->table_stride;
             part.seq_len += b;
@@ -215,15 +220,14 @@ fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_
             if (fa::launch_widen_pages(w, (int64_t)n * cache->table_width, cs) != cudaSuccess) return FA_ERR_CUDA;
             const fa_rows q = from_sequence(*Q, b), o = from_sequence(*O, b);
             const fa_status s = fa_fwd_paged(&q, &pool, &o, LSE ? LSE + (int64_t)b * Hq * T : nullptr, n, Hq, T, causal, scale,
-                                             f16, inner, plan.inner, stream);
+                                             f16, inner, whole.inner, stream);
             if (s != FA_OK) return s;
         }
         return FA_OK;
     }
 
-    plan.rows.place(static_cast<uint8_t *>(workspace), D);
-    const int64_t own_keys = (int64_t)cache->table_width * cache->page_size;
-    const int G = Hq / cache->Hkv;
+    Plan &plan = whole.direct;
+    plan.place(static_cast<uint8_t *>(workspace), D);
     fa::FourParams f{};
     f.c = cache4_of(*cache);
     fa::PagedParams &p = f.p;
@@ -251,14 +255,14 @@ fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_
     p.f16 = f16 ? 1 : 0;
     const bool given = scale > 0.f && !std::isinf(scale);
     p.scale_log2 = (given ? scale : 1.0f / std::sqrt((float)D)) * 1.4426950408889634f;
-    p.part = plan.rows.part;
+    p.part = plan.part;
     p.wait_limit_ns = fa::wait_budget_ns();
-    p.team = team_size(D, plan.rows, (own_keys + p.part.chunk - 1) / p.part.chunk, fa::four_teams_at_once);
-    if (p.team) return fa::launch_four_team(f, (int)plan.rows.items * p.team, cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-    if (fa::launch_four_rows(f, (int)plan.rows.ctas, cs) != cudaSuccess) return FA_ERR_CUDA;
+    p.team = plan.tc ? 0 : team_size(D, plan, (own_keys + p.part.chunk - 1) / p.part.chunk, fa::four_teams_at_once);
+    if (p.team) return fa::launch_four_team(f, (int)plan.items * p.team, cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if ((plan.tc ? fa::launch_four_tc(f, (int)plan.ctas, cs) : fa::launch_four_rows(f, (int)plan.ctas, cs)) != cudaSuccess) return FA_ERR_CUDA;
 
     fa::MergeParams m{};
-    m.src[m.n_src++] = plan.rows.part;
+    m.src[m.n_src++] = plan.part;
     m.seq_len = cache->seq_len;
     m.max_len = (int)own_keys;
     m.o = p.o;
@@ -273,7 +277,7 @@ fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_
     m.D = D;
     m.causal = p.causal;
     m.f16 = p.f16;
-    const int64_t states = plan.rows.pieces / plan.rows.items + 1;
+    const int64_t states = plan.pieces / plan.items + 1;
     return fa::launch_paged_merge(m, (int)states, fa::sm_count_of(fa::current_device()), cs) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -29,6 +29,8 @@ cudaError_t launch_four_rows(const FourParams &f, int ctas, cudaStream_t stream)
 // A team of p.team CTAs per tile of 8 rows, and how many teams fit the device together.
 cudaError_t launch_four_team(const FourParams &f, int ctas, cudaStream_t stream);
 int four_teams_at_once(int device, int team);
+// Tiles of 128 rows on the tensor cores (fa_paged_tc.cu), D <= 128.
+cudaError_t launch_four_tc(const FourParams &f, int ctas, cudaStream_t stream);
 cudaError_t launch_widen_pages(WidenParams p, int64_t pages, cudaStream_t stream);
 
 }  // namespace fa

@@ -232,12 +232,13 @@ struct Plan {
         cut(nseq, c.Hkv, D, rows, keys, stacked, joined, tc ? 1 : fa::paged_rows_ctas_per_sm(D, part.rows));
     }
 
-    // The row kernel over a 4-bit cache.
-    Plan(int nseq, int Hkv, int D, int64_t rows, int64_t keys)
+    // Over a 4-bit cache.
+    Plan(int nseq, const fa_paged_kv4 &c, int64_t rows, int64_t keys)
     {
-        part.rows = fa::four_rows_per_tile(D, rows);
-        part.chunk = fa::four_rows_chunk(D);
-        cut(nseq, Hkv, D, rows, keys, false, false, fa::four_rows_ctas_per_sm(D, part.rows));
+        tc = rows > kMostRows && c.D <= 128 && c.page_size % 8 == 0;
+        part.rows = tc ? 128 : fa::four_rows_per_tile(c.D, rows);
+        part.chunk = tc ? fa::kBlockKeys : fa::four_rows_chunk(c.D);
+        cut(nseq, c.Hkv, c.D, rows, keys, false, false, tc ? 1 : fa::four_rows_ctas_per_sm(c.D, part.rows));
     }
 
     void cut(int nseq, int Hkv, int D, int64_t rows, int64_t keys, bool stacked, bool joined, int ctas_per_sm)

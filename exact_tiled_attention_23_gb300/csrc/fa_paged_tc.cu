@@ -45,6 +45,8 @@
 // Every mbarrier wait is bounded; a wait that runs out records the site in
 // this file's status word, raises the CTA's abort flag, and every role drains
 // its copies / MMAs, frees TMEM and exits.
+#include "fa_four.cuh"
+#include "fa_four_rows.h"
 #include "fa_fwd_softmax.cuh"
 #include "fa_internal.h"
 #include "fa_paged.h"
@@ -91,7 +93,8 @@ struct TcLayout {
     // q_full, k_full/k_empty[RK], v_full/v_empty[RV], s_full, s_read,
     // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
     static constexpr int kBars = 1 + 2 * (kRingK + kRingV) + 2 + 4 + 4 + 4;
-    static constexpr int kSmemBytes = kBarOff + 512 + 1024;    // + alignment slack
+    static constexpr int kScaleOff = kBarOff + 512;            // 4-bit cache: what a tile's rows of Q are divided by, twice
+    static constexpr int kSmemBytes = kScaleOff + 1024 + 1024; // + alignment slack
     __device__ static constexpr uint32_t col_o(int h) { return kColO + (uint32_t)(h * D); }
     __device__ static constexpr uint32_t col_p(int buf, int h) { return kColP + (uint32_t)(buf * 64 + h * 32); }
     static_assert(D == 64 || D == 128, "head dim");
@@ -107,12 +110,6 @@ __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t 
                                        bool follow_abort)
 {
     return wait_bounded(bar, parity, limit_ns, site, ab, follow_abort);
-}
-
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort ab,
-                                         bool follow_abort = true)
-{
-    return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, ab, follow_abort);
 }
 
 using BlockLine = Line<BN, kBlocksTile>;
@@ -173,10 +170,17 @@ struct Walk {
     }
 };
 
-template <int D, bool kF16, bool kTwo>
+// kFour: a 4-bit cache, whose rows warps 12-15 decode into the K and V slots as IEEE
+// halves, for queries and outputs of kIo16 (fp16, else bf16).  Everything else is then
+// fp16: a bf16 row of Q is multiplied by the power of two that takes its largest
+// element to 2^14 .. 2^15 (exact, but for what lies 2^-39 below that), its scores are
+// divided by it.
+template <int D, bool kF16, bool kTwo, bool kFour = false, bool kIo16 = kF16>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedParams p,
+                const PagedCache4 four)
 {
+    static_assert(!kFour || (kF16 && !kTwo), "a 4-bit cache is decoded to halves");
     using Lay = TcLayout<D>;
     constexpr int kChunks = Lay::kChunks, kTileBytes = Lay::kTileBytes, RK = Lay::kRingK, RV = Lay::kRingV;
     constexpr int kQOff = Lay::kQOff, kKOff = Lay::kKOff, kVOff = Lay::kVOff;
@@ -202,6 +206,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int *hidden_word = abort_word + 1;
     const Abort ab{abort_word, &g_status_paged};
     const uint64_t limit = p.wait_limit_ns;
+    // (a call does not go with registers that move between warps)
+    auto wait_for = [](uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort to, bool follow_abort = true) {
+        return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, to, follow_abort);
+    };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -216,8 +224,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         *abort_word = 0;
         *hidden_word = 0;
         ptx::fence_mbarrier_init();
-        ptx::tma_prefetch_desc(&tm_k);
-        ptx::tma_prefetch_desc(&tm_v);
+        if constexpr (!kFour) {
+            ptx::tma_prefetch_desc(&tm_k);
+            ptx::tma_prefetch_desc(&tm_v);
+        }
     }
     if (!p.second) ptx::wait_for_primary();
     ptx::launch_dependents();
@@ -250,8 +260,107 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-
-    if (warp == 0 || warp == 2) {
+    if (kFour && (warp == 0 || warp == 2)) {
+        if constexpr (kFour) {
+            // ================= K (warp 0) and V (warp 2) of a 4-bit cache =================
+            // A lane has four rows of a block, 32 apart: what it reads is fetched a
+            // block ahead, its pages two.  (Neighbouring lanes write neighbouring
+            // rows, whose swizzle keeps the banks apart.)
+            constexpr int kUnits = D / 32, kRows = BN / 32;         // 16 bytes of a row
+            const uint8_t *const data = warp == 0 ? four.k : four.v, *const scales = warp == 0 ? four.ks : four.vs;
+            uint64_t *full = warp == 0 ? k_full : v_full, *empty = warp == 0 ? k_empty : v_empty;
+            const uint32_t slots = ptx::smem_u32(smem + (warp == 0 ? kKOff : kVOff));
+            const int ring = warp == 0 ? RK : RV;
+            struct Source {
+                int page[kRows], slot[kRows], h;    // page < 0: not a key that the tile sees
+            };
+            struct Raw {
+                uint4 w[kRows][kUnits];
+                uint32_t scales[kRows][kUnits / 2];                 // four groups each
+            };
+            int looked = 0;                                         // blocks
+            auto look_up = [&](Source &x) {
+                x.h = walk.u.h;
+                const int32_t *table = p.c.table + (int64_t)(walk.u.g / p.part.tiles) * p.c.table_stride;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const int64_t key = (int64_t)walk.u.c * BN + i * 32 + lane;
+                    x.page[i] = -1;
+                    x.slot[i] = 0;
+                    if (looked < blocks && key < walk.u.keys) {
+                        const int which = p.c.by_page.quotient((int)key);
+                        x.page[i] = table[which];
+                        x.slot[i] = (int)key - which * p.c.page_size;
+                    }
+                }
+                if (looked < blocks && ++looked < blocks) line.advance(walk.u);
+            };
+            auto fetch = [&](const Source &x, Raw &r) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) r.w[i][u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int u = 0; u < kUnits / 2; ++u) r.scales[i][u] = 0u;
+                    if (x.page[i] < 0 || x.page[i] >= p.c.num_pages) continue;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(data + x.page[i] * four.s_page + x.h * four.s_head + x.slot[i] * four.s_slot);
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) r.w[i][u] = src[u];
+                    const uint32_t *s = reinterpret_cast<const uint32_t *>(scales + x.page[i] * four.t_page + x.h * four.t_head + x.slot[i] * four.t_slot);
+#pragma unroll
+                    for (int u = 0; u < kUnits / 2; ++u) r.scales[i][u] = s[u];
+                }
+            };
+            Source next;
+            Raw raw;
+            look_up(next);
+            fetch(next, raw);
+            look_up(next);
+            for (int t = 0, slot = 0, phase = 1; t < blocks; ++t) {
+                bool ok = true;
+                if (t >= ring && lane == 0) ok = wait_for(&empty[slot], phase, limit, kSiteSlotEmpty, ab);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                // (a row's units lie at its address with their number's low bits changed)
+                const uint32_t dst = slots + slot * kTileBytes + lane * 128 + ((lane & 7) << 4);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint32_t words[4] = {raw.w[i][u].x, raw.w[i][u].y, raw.w[i][u].z, raw.w[i][u].w};
+                        uint32_t x[4][4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ptx::unpack_e2m1x8(words[j], x[j]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int group = (4 * u + j) / 2;
+                            // the scale's byte in both halves, and to a half's place
+                            const uint32_t pair = __byte_perm(raw.scales[i][group / 4], 0u, 0x4040u | (group % 4) * 0x101u) * 128u;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[j][e]), *reinterpret_cast<const __half2 *>(&pair));
+                                x[j][e] = *reinterpret_cast<const uint32_t *>(&y);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int unit = 4 * u + j;
+                            ptx::st_shared_v4((dst ^ ((unit % 8) << 4)) + (unit / 8) * kChunkBytes + i * 32 * 128, x[j][0], x[j][1], x[j][2], x[j][3]);
+                        }
+                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&full[slot]);
+                fetch(next, raw);                                   // (past the last block: nothing)
+                look_up(next);
+                if (++slot == ring) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp < kSoftmaxWarp0) {
+        if (warp == 0 || warp == 2) {
         // ================= K copies (warp 0), V copies (warp 2) =================
         // Lane i < boxes finds box i of a block; lane 0 copies them all.  One
         // warp each: a copy costs its issuing thread ~100 clk, and with pages
@@ -371,7 +480,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // Rows of the last block's V that hold what lies behind the
             // sequence's last key: from there to the end of the box it is in.
             const int from = walk.u.len - (walk.u.c + count - 1) * BN;
-            const bool rest = from < BN && (from & (p.box_rows - 1)) != 0;      // (a box has a power of two rows)
+            // (a box has a power of two rows; what is decoded has zeros there)
+            const bool rest = !kFour && from < BN && (from & (p.box_rows - 1)) != 0;
             const int to = rest ? (from | (p.box_rows - 1)) + 1 : from;
             bool ok = true;
             if (lane == 0) {
@@ -405,6 +515,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             wait_for(mma_drain, 0, limit, kSiteDrain, ab, false);
         }
         __syncwarp();
+        }
     } else {
         // ================= online softmax of one key half + epilogue =================
         const int h = (warp - kSoftmaxWarp0) / 4;     // key half: columns 64h .. 64h+63 of every block
@@ -413,12 +524,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int thread = threadIdx.x - 32 * kSoftmaxWarp0;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lane_off + kColS + (uint32_t)(h * kHalf);
-        const float sl2 = p.scale_log2;
+        float sl2 = p.scale_log2;
+        float *const q_scale = reinterpret_cast<float *>(smem + Lay::kScaleOff);     // [2][BM], tiles in turn
 
         // The rows of the walk's tile into the Q buffer, in the 128-byte-swizzled
         // layout; rows past the last and columns past D are zero.  The products
         // that read the buffer before are done.
-        auto copy_q = [&] {
+        auto copy_q = [&](int tile) {
             // two threads per row, so that a row's place is found once
             const int b = walk.u.g / p.part.tiles, row = thread >> 1, idx = (walk.u.g - b * p.part.tiles) * BM + row;
             constexpr int kUnits = D / 16;                        // 16-byte units per thread
@@ -433,6 +545,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 for (int i = 0; i < kUnits; ++i)
                     if ((unit0 + i) * 8 < p.c.D) w[i] = *reinterpret_cast<const uint4 *>(src + (unit0 + i) * 8);
             }
+            if constexpr (kFour && !kIo16) {
+                float largest = 0.f;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+                    for (const uint32_t x : {w[i].x, w[i].y, w[i].z, w[i].w})
+                        largest = ptx::max3(largest, fabsf(u2f(x << 16)), fabsf(u2f(x & 0xffff0000u)));
+                largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
+                const RowScale by = row_scale(largest);
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i)
+                    for (uint32_t *x : {&w[i].x, &w[i].y, &w[i].z, &w[i].w})
+                        *x = ptx::pack_f16x2(u2f(*x << 16) * by.up, u2f(*x & 0xffff0000u) * by.up);
+                if ((thread & 1) == 0) q_scale[(tile & 1) * BM + row] = by.down;
+            }
             const uint32_t dst = ptx::smem_u32(smem + kQOff) + row * 128;
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
@@ -445,7 +571,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         };
 
         // the first tile's Q, and whether any page of this piece is hidden
-        copy_q();
+        copy_q(0);
         bool hidden = false;
         {
             Walk s = walk;
@@ -470,6 +596,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int tile = 0;; ++tile) {
             const int count = walk.count();
             const int b = walk.u.g / p.part.tiles, row0 = (walk.u.g - b * p.part.tiles) * BM;
+            // (written before the barriers that lie behind)
+            if constexpr (kFour && !kIo16) sl2 = p.scale_log2 * q_scale[(tile & 1) * BM + r_local];
             const int row = row0 + r_local;
             const int lim = min(walk.u.len, line.masked ? walk.u.len - p.T + p.by_g.quotient(row) + 1 : walk.u.len);
             // Blocks from t_mask on have keys that some row of the tile does
@@ -569,7 +697,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             // products run.
             const LineCursor was = walk.u;
             const bool more = walk.next_tile(line, count);
-            if (ok && more) copy_q();
+            if (ok && more) copy_q(tile + 1);
 
             // ---- join the halves: m = max(m_A, m_B), w_h = 2^(m_h - m),
             // O = (w_A O_A + w_B O_B) / (w_A l_oA + w_B l_oB)
@@ -652,8 +780,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                     for (int e = 0; e < 8; ++e) x[e] = empty ? 0.f : fmaf(c0, u2f(oa[8 * k + e]), c1 * u2f(ob[8 * k + e]));
                     if (direct) {
                         *reinterpret_cast<uint4 *>(o_row + col + 8 * k) =
-                            make_uint4(ptx::pack16x2<kF16>(x[0], x[1]), ptx::pack16x2<kF16>(x[2], x[3]),
-                                       ptx::pack16x2<kF16>(x[4], x[5]), ptx::pack16x2<kF16>(x[6], x[7]));
+                            make_uint4(ptx::pack16x2<kIo16>(x[0], x[1]), ptx::pack16x2<kIo16>(x[2], x[3]),
+                                       ptx::pack16x2<kIo16>(x[4], x[5]), ptx::pack16x2<kIo16>(x[6], x[7]));
                     } else {
                         float4 *dst = reinterpret_cast<float4 *>(p.part.o) +
                                       (slot * (p.c.D / 4) + (col + 8 * k) / 4) * BM + r_local;
@@ -683,7 +811,17 @@ cudaError_t launch(const PagedParams &p, const CUtensorMap &tk, const CUtensorMa
     static SharedMemory allowed;
     const cudaError_t e = allowed.allow(paged_tc_kernel<D, kF16, kTwo>, TcLayout<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_tc_kernel<D, kF16, kTwo>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes, stream, tk, tv, p);
+    return launch_behind(paged_tc_kernel<D, kF16, kTwo>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes, stream, tk, tv, p, PagedCache4{});
+}
+
+template <int D, bool kIo16>
+cudaError_t launch_four(const PagedParams &p, const PagedCache4 &four, int ctas, cudaStream_t stream)
+{
+    static SharedMemory allowed;
+    const cudaError_t e = allowed.allow(paged_tc_kernel<D, true, false, true, kIo16>, TcLayout<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_behind(paged_tc_kernel<D, true, false, true, kIo16>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes,
+                         stream, CUtensorMap{}, CUtensorMap{}, p, four);
 }
 
 template <int D>
@@ -699,6 +837,13 @@ cudaError_t launch_paged_tc(const PagedParams &p, const CUtensorMap &tk, const C
                             cudaStream_t stream)
 {
     return p.c.D <= 64 ? launch_d<64>(p, tk, tv, ctas, stream) : launch_d<128>(p, tk, tv, ctas, stream);
+}
+
+cudaError_t launch_four_tc(const FourParams &f, int ctas, cudaStream_t stream)
+{
+    if (f.p.c.D <= 64)
+        return f.p.f16 ? launch_four<64, true>(f.p, f.c, ctas, stream) : launch_four<64, false>(f.p, f.c, ctas, stream);
+    return f.p.f16 ? launch_four<128, true>(f.p, f.c, ctas, stream) : launch_four<128, false>(f.p, f.c, ctas, stream);
 }
 
 cudaError_t read_and_clear_status_paged(uint32_t *out)

@@ -546,11 +546,13 @@ fa_status fa_kv_append_q4(const fa_paged_kv4 *cache, const fa_rows *K, const fa_
  * fa_fwd_paged_q4 -- fa_fwd_paged over a 4-bit cache: exact attention over the rows
  * that it holds.  Arguments, workspace rules and errors as fa_fwd_paged.
  *
- * Up to 32 query rows of a sequence that share a key (T * Hq / Hkv), D = 256, or a
- * page_size that is no multiple of 8: a weight is off by 2^-11 (bf16) or 2^-22 (fp16)
- * relative, or by 2^-37 of its row's largest where that is more, so that O's own
- * rounding decides.  Else the rows are decoded to 16 bits in the workspace, up to 256
- * MB of them at a time (a whole sequence at least), and the errors are fa_fwd_paged's.
+ * A weight is off by 2^-11 relative, for fp16 queries by 2^-22, or by 2^-37 of its
+ * row's largest where that is more.  Where more than 32 query rows of a sequence share
+ * a key (T * Hq / Hkv), D <= 128 and page_size is a multiple of 8, it is off by 2^-11
+ * in either type, or by 2^-32 of the largest, and O is divided by the sum of the
+ * rounded weights.  Beyond 512 such rows the keys are decoded once to 16 bits in the
+ * workspace, 256 MB of them at a time (or a sequence, if its row of the table takes up
+ * to 1 GB; one with more keys is not decoded first), and the errors are fa_fwd_paged's.
  */
 fa_status fa_fwd_paged_q4(const fa_rows *Q, const fa_paged_kv4 *cache, const fa_rows *O, float *LSE, int B, int Hq, int T,
                           int causal, float scale, int f16, void *workspace, size_t workspace_bytes, void *stream);

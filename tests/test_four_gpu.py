@@ -404,3 +404,18 @@ def test_refusals():
     ks.data = ks.clone()
     with pytest.raises(ValueError):
         fa.kv_read(cache, 1)
+
+
+def test_tables_without_pages_and_an_empty_batch():
+    pools = empty_pools(4, 2, 16, 128)
+    for B, W, T in ((2, 0, 1), (2, 0, 40), (2, 0, 300), (0, 3, 1)):
+        table = torch.zeros((B, W), dtype=torch.int32, device="cuda")
+        cache = fa.PagedKV4(*pools, table, torch.full((B,), 5, dtype=torch.int32, device="cuda"))
+        q = torch.ones((B, 4, T, 128), dtype=BF16, device="cuda")
+        o, lse = fa.forward_paged(q, cache)
+        assert o.shape == q.shape and not o.any() and bool(torch.isneginf(lse).all())
+        x = torch.ones((B, 2, T, 128), dtype=BF16, device="cuda")
+        fa.kv_append(cache, x, x)
+        assert not pools[0].any()
+        k, v = fa.kv_read(cache, 3)
+        assert k.shape == (B, 2, 3, 128) and not k.any()
