@@ -908,13 +908,10 @@ def kv_fork(cache, refs, parent, child, stream=None):
     if stream is not None:
         with _stream_context(cache[0].device, stream):
             return kv_fork(cache, refs, parent, child)
-    r = _BINDING.fork(cache[0]._native, refs, parent, child)
+    r = _BINDING.fork(tuple([c._native for c in cache]), refs, parent, child)
     if type(r) is int:
         raise FAError(r, "fa_kv_fork")
-    src, dst = r
-    for c in cache:
-        copy_pages(c, src, dst)
-    return dst
+    return r
 
 
 def kv_compact(cache, refs, stream=None):
@@ -928,13 +925,10 @@ def kv_compact(cache, refs, stream=None):
     if stream is not None:
         with _stream_context(cache[0].device, stream):
             return kv_compact(cache, refs)
-    r = _BINDING.compact(cache[0]._native, refs)
+    r = _BINDING.compact(tuple([c._native for c in cache]), refs)
     if type(r) is int:
         raise FAError(r, "fa_kv_compact")
-    moved, src, dst, count = r
-    for c in cache:
-        copy_pages(c, src, dst, count)
-    return moved
+    return r
 
 
 def copy_pages(cache, src, dst, count=None, stream=None):

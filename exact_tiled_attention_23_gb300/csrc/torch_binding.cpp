@@ -655,14 +655,15 @@ at::Tensor numbers(const Cache &cache, int64_t n)
     return at::empty({n}, at::TensorOptions().dtype(at::kInt).device(cache.k.device()));
 }
 
-// run(workspace, bytes) with a workspace of a page operator: the cache's own on the
-// default stream, else a new one.
+// run(workspace, bytes, more) with a workspace of a page operator and `extra` bytes
+// more behind it, the interpreter's lock released: the cache's own on the default
+// stream, else a new one.
 template <typename Run>
-fa_status with_workspace(Cache &cache, const fa_page_table &t, int n, void *stream, const Run &run)
+fa_status with_workspace(Cache &cache, const fa_page_table &t, int n, size_t extra, void *stream, const Run &run)
 {
     const size_t size = g_pages_bytes(&t, n);
-    const auto bytes = [&] { return at::empty({(int64_t)size}, at::TensorOptions().dtype(at::kByte).device(cache.k.device())); };
-    const bool kept = stream == nullptr && size <= kKeptWorkspace;
+    const auto bytes = [&] { return at::empty({(int64_t)(size + extra)}, at::TensorOptions().dtype(at::kByte).device(cache.k.device())); };
+    const bool kept = stream == nullptr && size + extra <= kKeptWorkspace;
     at::Tensor workspace;
     if (!kept) workspace = bytes();
     struct Released {
@@ -672,10 +673,34 @@ fa_status with_workspace(Cache &cache, const fa_page_table &t, int n, void *stre
     std::unique_lock<std::mutex> lock(cache.mutex, std::defer_lock);
     if (kept) {
         lock.lock();
-        if (!cache.workspace.defined() || (size_t)cache.workspace.numel() < size) cache.workspace = bytes();
+        if (!cache.workspace.defined() || (size_t)cache.workspace.numel() < size + extra) cache.workspace = bytes();
         workspace = cache.workspace;
     }
-    return run(workspace.data_ptr(), (size_t)workspace.nbytes());
+    uint8_t *w = static_cast<uint8_t *>(workspace.data_ptr());
+    return run(w, size, reinterpret_cast<int32_t *>(w + size));        // (size is a multiple of 256)
+}
+
+// The caches in a tuple (a model's layers, whose pools are of one size and whose table
+// is the first's); false with an error set.
+bool layers_of(PyObject *object, std::vector<Cache *> &all)
+{
+    if (!PyTuple_Check(object) || PyTuple_GET_SIZE(object) == 0) return value_error("at least one cache must be given");
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(object); ++i) {
+        Cache *c = cache_of(PyTuple_GET_ITEM(object, i));
+        if (!c) return false;
+        all.push_back(c);
+    }
+    return true;
+}
+
+// The pages that a call listed, in every cache.
+fa_status copy_listed(const std::vector<Cache *> &all, const int32_t *src, const int32_t *dst, const int32_t *count, int n, void *stream)
+{
+    for (Cache *c : all) {
+        const fa_status st = c->four ? g_copy_q4(&c->c4, src, dst, count, n, stream) : g_copy(&c->c, src, dst, count, n, stream);
+        if (st != FA_OK) return st;
+    }
+    return FA_OK;
 }
 
 // grow(cache, refs, tokens) -> taken, or a status
@@ -690,7 +715,7 @@ PyObject *grow(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "tokens", cache->B, *cache, false, tokens)) return nullptr;
     at::Tensor taken = numbers(*cache, cache->B);
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
-    const fa_status st = with_workspace(*cache, t, 0, stream, [&](void *w, size_t size) {
+    const fa_status st = with_workspace(*cache, t, 0, 0, stream, [&](void *w, size_t size, int32_t *) {
         return g_grow(&t, tokens.const_data_ptr<int32_t>(), taken.mutable_data_ptr<int32_t>(), w, size, stream);
     });
     return st != FA_OK ? PyLong_FromLong(st) : THPVariable_Wrap(taken);
@@ -712,55 +737,53 @@ PyObject *free_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// fork(cache, refs, parent, child) -> (src, dst), or a status
+// fork(caches, refs, parent, child) -> the pages that were copied to, or a status
 PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    Cache *cache = n == 4 ? cache_of(a[0]) : nullptr;
-    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "fork takes 4 arguments"), nullptr);
+    std::vector<Cache *> all;
+    if (n != 4) return PyErr_SetString(PyExc_TypeError, "fork takes 4 arguments"), nullptr;
+    if (!layers_of(a[0], all)) return nullptr;
+    Cache *cache = all[0];
     const c10::cuda::CUDAGuard guard(cache->device);
     at::Tensor refs, parent, child;
     fa_page_table t;
     if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "parent", -1, *cache, false, parent) ||
         !entries(a[3], "child", parent.numel(), *cache, false, child))
         return nullptr;
-    at::Tensor src = numbers(*cache, parent.numel()), dst = numbers(*cache, parent.numel());
+    const int count = (int)parent.numel();
+    at::Tensor dst = numbers(*cache, count);
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
-    const fa_status st = with_workspace(*cache, t, (int)parent.numel(), stream, [&](void *w, size_t size) {
-        return g_fork(&t, parent.const_data_ptr<int32_t>(), child.const_data_ptr<int32_t>(), (int)parent.numel(),
-                      src.mutable_data_ptr<int32_t>(), dst.mutable_data_ptr<int32_t>(), w, size, stream);
+    const fa_status st = with_workspace(*cache, t, count, 4 * (size_t)count, stream, [&](void *w, size_t size, int32_t *src) {
+        const fa_status s = g_fork(&t, parent.const_data_ptr<int32_t>(), child.const_data_ptr<int32_t>(), count, src,
+                                   dst.mutable_data_ptr<int32_t>(), w, size, stream);
+        return s != FA_OK ? s : copy_listed(all, src, dst.const_data_ptr<int32_t>(), nullptr, count, stream);
     });
-    if (st != FA_OK) return PyLong_FromLong(st);
-    PyObject *pair = PyTuple_New(2);
-    if (!pair) return nullptr;
-    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(src));
-    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(dst));
-    return pair;
+    return st != FA_OK ? PyLong_FromLong(st) : THPVariable_Wrap(dst);
     END_HANDLE_TH_ERRORS
 }
 
-// compact(cache, refs) -> (moved, src, dst, count), or a status
+// compact(caches, refs) -> moved, or a status
 PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    Cache *cache = n == 2 ? cache_of(a[0]) : nullptr;
-    if (!cache) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_TypeError, "compact takes 2 arguments"), nullptr);
+    std::vector<Cache *> all;
+    if (n != 2) return PyErr_SetString(PyExc_TypeError, "compact takes 2 arguments"), nullptr;
+    if (!layers_of(a[0], all)) return nullptr;
+    Cache *cache = all[0];
     const c10::cuda::CUDAGuard guard(cache->device);
     at::Tensor refs;
     fa_page_table t;
     if (!table_of(*cache, a[1], refs, t)) return nullptr;
-    at::Tensor out[4];
-    for (int i = 0; i < 4; ++i) out[i] = numbers(*cache, i < 3 ? cache->c.num_pages : 1);
+    const int pages = cache->c.num_pages;
+    at::Tensor moved = numbers(*cache, pages);
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
-    const fa_status st = with_workspace(*cache, t, 0, stream, [&](void *w, size_t size) {
-        return g_compact(&t, out[0].mutable_data_ptr<int32_t>(), out[1].mutable_data_ptr<int32_t>(),
-                         out[2].mutable_data_ptr<int32_t>(), out[3].mutable_data_ptr<int32_t>(), w, size, stream);
+    const fa_status st = with_workspace(*cache, t, 0, 8 * (size_t)pages + 4, stream, [&](void *w, size_t size, int32_t *src) {
+        int32_t *dst = src + pages, *count = dst + pages;
+        const fa_status s = g_compact(&t, moved.mutable_data_ptr<int32_t>(), src, dst, count, w, size, stream);
+        return s != FA_OK ? s : copy_listed(all, src, dst, count, pages, stream);
     });
-    if (st != FA_OK) return PyLong_FromLong(st);
-    PyObject *all = PyTuple_New(4);
-    if (!all) return nullptr;
-    for (int i = 0; i < 4; ++i) PyTuple_SET_ITEM(all, i, THPVariable_Wrap(out[i]));
-    return all;
+    return st != FA_OK ? PyLong_FromLong(st) : THPVariable_Wrap(moved);
     END_HANDLE_TH_ERRORS
 }
 
