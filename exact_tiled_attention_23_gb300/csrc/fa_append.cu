@@ -251,7 +251,9 @@ cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 // ---------------------------------------------------------------- 4 bits
 // A key's pairs turn in fp32 and the result is rounded once, to 4 bits.  A thread
 // takes a group of 16 elements of a key or value, so that no thread needs another's
-// largest value (a key's partner elements are read a second time, from the L1).
+// largest value (a key's partner elements are read a second time, from the L1).  Two
+// prompts of 8192 tokens as above: 354 MB in 65 us, 5.4 TB/s (8 instead of 10 CTAs an
+// SM 67; with a division per element 74).  One token of 256 sequences: 3.5 us.
 
 // Elements 8 u .. 8 u + 7 of a turned head, which are `w` before.
 template <bool kF16, int kMode>
@@ -369,6 +371,8 @@ cudaError_t launch4(const Append4Params &p, cudaStream_t stream)
 }
 
 // ---------------------------------------------------------------- no cache
+// 32760 tokens, 16 query and 16 key heads, D = 128, three axes: 537 MB in 84 us, 6.4
+// TB/s; turned back the same.
 template <bool kF16, int kMode>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p)
 {

@@ -42,6 +42,13 @@
 // go from 199 to 271 us: there P is rounded once and O divided by the sum of the
 // rounded weights, as in fa_fwd.
 //
+// Over a 4-bit cache (kFour) warps 0 and 2 decode what they copy else, a step of 128
+// keys in ~3200 clk where a block takes 1680, so that calls of many row tiles have
+// their keys decoded once, elsewhere (kDirectTiles in fa_four_api.cu).  36 rows over 64
+// sequences of up to 8191 keys: 243 us, decoded elsewhere first 627 (16 bits: 176).
+// (Four more warps for it leave 128 registers a thread; moved between the roles they
+// spilled in the issuing threads' loops: 241, and 345 instead of 387 for 32 tiles.)
+//
 // Every mbarrier wait is bounded; a wait that runs out records the site in
 // this file's status word, raises the CTA's abort flag, and every role drains
 // its copies / MMAs, frees TMEM and exits.
