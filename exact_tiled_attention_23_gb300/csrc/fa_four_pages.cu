@@ -2,8 +2,8 @@
 // calls whose many row tiles would each decode them again (fa_paged_tc.cu).
 //
 // Bound by memory: 144 bytes read and 512 written per key and head at D = 128 (a
-// sequence of 16384 keys, 8 heads: 86 MB, 17 us; one thread per element group at a
-// time, 45).
+// sequence of 16384 keys, 8 heads: 86 MB, 23 us with cold caches; with one group of a
+// thread in flight instead of four, and a CTA for all heads of a page, 45).
 #include "fa_four.cuh"
 #include "fa_four_rows.h"
 
