@@ -513,9 +513,9 @@ fa_status fa_rotary(const fa_rows *Q, const fa_rows *Q_out, const fa_rows *K, co
  *      At most 10240 (byte 226); larger bytes are undefined.
  * u * s is exact as an IEEE half and as bf16.  Appending, s is the group's largest
  * magnitude / 6 and u the element / s, both rounded to nearest (halfway to the even
- * mantissa bit), u at most 6: an element is off by at most 1/5 of its group's largest
- * and about 1/12 of itself if it is not small beside that; magnitudes below 2^-19
- * are lost and those above 61440 are held as that.  Elements have to be finite
+ * mantissa bit), u at most 6: an element is off by at most 0.18 of its group's largest
+ * (0.23 where that is below 2^-11).  A group whose largest is 6 * 2^-18 or less is held
+ * as zeros, and magnitudes above 61440 are held as that.  Elements have to be finite
  * (others become some finite value).
  *
  * The pools' rows are
