@@ -100,13 +100,14 @@ struct TcLayout {
     // q_full, k_full/k_empty[RK], v_full/v_empty[RV], s_full, s_read,
     // p_full[2][2], pv_done[2][2], o_final, o_read, mma_drain, mma_drain_s
     static constexpr int kBars = 1 + 2 * (kRingK + kRingV) + 2 + 4 + 4 + 4;
-    static constexpr int kScaleOff = kBarOff + 512;            // 4-bit cache: what a tile's rows of Q are divided by, twice
-    static constexpr int kSmemBytes = kScaleOff + 1024 + 1024; // + alignment slack
+    static constexpr int kSmemBytes = kBarOff + 512 + 1024;    // + alignment slack
+    // 4-bit cache: what a tile's rows of Q are multiplied by, of two tiles in turn
+    static constexpr int kScaleOff = kBarOff + 512, kFourSmemBytes = kSmemBytes + 2 * BM * 4;
     __device__ static constexpr uint32_t col_o(int h) { return kColO + (uint32_t)(h * D); }
     __device__ static constexpr uint32_t col_p(int buf, int h) { return kColP + (uint32_t)(buf * 64 + h * 32); }
     static_assert(D == 64 || D == 128, "head dim");
     static_assert(kColO + 2 * D <= kTmemCols, "TMEM columns");
-    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static_assert(kFourSmemBytes <= 232448, "shared memory budget");
     static_assert(kBars * 8 + 16 <= 512, "barrier area");
 };
 
@@ -117,6 +118,12 @@ __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, uint64_t 
                                        bool follow_abort)
 {
     return wait_bounded(bar, parity, limit_ns, site, ab, follow_abort);
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort ab,
+                                         bool follow_abort = true)
+{
+    return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, ab, follow_abort);
 }
 
 using BlockLine = Line<BN, kBlocksTile>;
@@ -213,10 +220,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int *hidden_word = abort_word + 1;
     const Abort ab{abort_word, &g_status_paged};
     const uint64_t limit = p.wait_limit_ns;
-    // (a call does not go with registers that move between warps)
-    auto wait_for = [](uint64_t *bar, uint32_t parity, uint64_t limit_ns, uint32_t site, Abort to, bool follow_abort = true) {
-        return ptx::mbar_test(bar, parity) || wait_long(bar, parity, limit_ns, site, to, follow_abort);
-    };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -366,8 +369,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
                 }
             }
         }
-    } else if (warp < kSoftmaxWarp0) {
-        if (warp == 0 || warp == 2) {
+    } else if (warp == 0 || warp == 2) {
         // ================= K copies (warp 0), V copies (warp 2) =================
         // Lane i < boxes finds box i of a block; lane 0 copies them all.  One
         // warp each: a copy costs its issuing thread ~100 clk, and with pages
@@ -522,7 +524,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             wait_for(mma_drain, 0, limit, kSiteDrain, ab, false);
         }
         __syncwarp();
-        }
     } else {
         // ================= online softmax of one key half + epilogue =================
         const int h = (warp - kSoftmaxWarp0) / 4;     // key half: columns 64h .. 64h+63 of every block
@@ -825,9 +826,9 @@ template <int D, bool kIo16>
 cudaError_t launch_four(const PagedParams &p, const PagedCache4 &four, int ctas, cudaStream_t stream)
 {
     static SharedMemory allowed;
-    const cudaError_t e = allowed.allow(paged_tc_kernel<D, true, false, true, kIo16>, TcLayout<D>::kSmemBytes);
+    const cudaError_t e = allowed.allow(paged_tc_kernel<D, true, false, true, kIo16>, TcLayout<D>::kFourSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_behind(paged_tc_kernel<D, true, false, true, kIo16>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kSmemBytes,
+    return launch_behind(paged_tc_kernel<D, true, false, true, kIo16>, dim3((unsigned)ctas), kThreads, TcLayout<D>::kFourSmemBytes,
                          stream, CUtensorMap{}, CUtensorMap{}, p, four);
 }
 
