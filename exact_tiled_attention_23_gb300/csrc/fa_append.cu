@@ -18,18 +18,55 @@
 // 2^-24 at the farthest position, 2^40 + 2^31.
 //
 // Bound by memory: every value is read once and written once, whole 16-byte units
-// at a time.  One CTA per token, so that a token's angles are computed once for all
-// heads.  Two prompts of 8192 tokens, 32 query and 8 key heads, D = 128: 403 MB in
-// 62 us, 6.5 TB/s (a copy: 6.8).  One token: 3 us, a launch and four waits in turn
-// (length, page, values, stores).
+// at a time.  One CTA per token (where tokens have little, a warp), so that a token's
+// angles are computed once for all heads.  Two prompts of 8192 tokens, 32 query and 8
+// key heads, D = 128: 403 MB in 62 us, 6.5 TB/s (a copy: 6.8).  One token: 3 us, a
+// launch and four waits in turn (length, page, values, stores).
 #include "fa_four.cuh"
+
+#include <type_traits>
 
 namespace fa {
 
 namespace {
 
-// Threads of a CTA that turns a token's heads.
+// Threads of a CTA, and of those the ones that have a token: all, or where tokens are
+// many and have little, a warp each (kGroup below).
 constexpr int kThreads = 128;
+
+template <int kGroup>
+__device__ __forceinline__ int group_thread()
+{
+    return kGroup == kThreads ? (int)threadIdx.x : (int)threadIdx.x % kGroup;
+}
+
+template <int kGroup>
+__device__ __forceinline__ void group_sync()
+{
+    if constexpr (kGroup == 32)
+        __syncwarp();
+    else
+        __syncthreads();
+}
+
+// The token of a thread's group; false past the last.  (kFast: where the CTA's sequence
+// is on the way to its first read.  Without, a division of the grid's index, which every
+// thread has in the same register, leaves more to the rest: 32 registers, not 36, in the
+// kernel without a cache, 84.5 and not 91.4 us in the case below.)
+template <int kGroup, bool kFast = false>
+__device__ __forceinline__ bool group_token(int64_t tokens, FastDiv by_t, int64_t &b, int &t)
+{
+    const int token = kGroup == kThreads ? (int)blockIdx.x : (int)blockIdx.x * (kThreads / kGroup) + (int)threadIdx.x / kGroup;
+    if constexpr (kGroup == kThreads && !kFast) {
+        b = blockIdx.x / (int)by_t.by;
+        t = (int)(blockIdx.x % (int)by_t.by);
+    } else {
+        const int at = by_t.quotient(token);
+        b = at;
+        t = token - at * (int)by_t.by;
+    }
+    return kGroup == kThreads || token < tokens;
+}
 
 // 2^128 / (2 pi): the bits of 1 / (2 pi) after the binary point.
 constexpr uint64_t kInvTwoPiHi = 0x28be60db9391054aull, kInvTwoPiLo = 0x7f09d5f47d4d3770ull;
@@ -85,9 +122,10 @@ enum PairMode { kNeighbours = 0, kHalves = 1, kHalvesOdd = 2 };
 
 // The cosines and sines of token t of sequence b, `at` its place in the sequence,
 // into cs[rot / 2].
+template <int kGroup>
 __device__ __forceinline__ void turns_of(const TurnParams &p, int64_t b, int t, int64_t at, float2 *cs)
 {
-    for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) {
+    for (int j = group_thread<kGroup>(); j < p.rot / 2; j += kGroup) {
         int64_t n = at;
         float f = p.inv_freq[j];
         if (p.pos) {
@@ -103,8 +141,8 @@ __device__ __forceinline__ void turns_of(const TurnParams &p, int64_t b, int t, 
 }
 
 // Turns `heads` heads of D elements by cs, from source(head) to target(head), which
-// may be one place; all threads of the CTA call it.
-template <bool kF16, int kMode, typename Source, typename Target>
+// may be one place; all threads of the group call it.
+template <bool kF16, int kMode, int kGroup, typename Source, typename Target>
 __device__ __forceinline__ void turn_heads(int heads, int D, int rot, const float2 *cs, const Source &source,
                                            const Target &target)
 {
@@ -112,7 +150,7 @@ __device__ __forceinline__ void turn_heads(int heads, int D, int rot, const floa
     if constexpr (kMode == kHalves) {
         // a task is 8 pairs (two units), or one unit past the rotated part
         const int pairs = half / 8, tasks = pairs + (D - rot) / 8;
-        for (int e = threadIdx.x; e < heads * tasks; e += kThreads) {
+        for (int e = group_thread<kGroup>(); e < heads * tasks; e += kGroup) {
             const int head = e / tasks, u = e % tasks;
             const uint16_t *src = source(head);
             uint16_t *dst = target(head);
@@ -136,7 +174,7 @@ __device__ __forceinline__ void turn_heads(int heads, int D, int rot, const floa
             }
         }
     } else if constexpr (kMode == kNeighbours) {
-        for (int e = threadIdx.x; e < heads * units; e += kThreads) {
+        for (int e = group_thread<kGroup>(); e < heads * units; e += kGroup) {
             const int head = e / units, u = e % units;
             const uint4 w = *reinterpret_cast<const uint4 *>(source(head) + u * 8);
             uint4 out = w;
@@ -157,7 +195,7 @@ __device__ __forceinline__ void turn_heads(int heads, int D, int rot, const floa
     } else {
         // The halves of a pair are other threads' elements, which q_out = q
         // overwrites: whole heads at a time, all read before any is written.
-        const int per = kThreads / units, mine = threadIdx.x / units, u = threadIdx.x % units;
+        const int per = kGroup / units, mine = group_thread<kGroup>() / units, u = group_thread<kGroup>() % units;
         for (int first = 0; first < heads; first += per) {
             const int head = first + mine;
             const bool on = mine < per && head < heads;
@@ -182,28 +220,30 @@ __device__ __forceinline__ void turn_heads(int heads, int D, int rot, const floa
                     out = narrow8<kF16>(r);
                 }
             }
-            __syncthreads();
+            group_sync<kGroup>();
             if (on) *reinterpret_cast<uint4 *>(target(head) + u * 8) = out;
         }
     }
 }
 
-// One CTA per token: its cosines and sines are computed once for all heads,
-// then each thread moves 16-byte units of q, k and v.
-template <bool kF16, int kMode>
+// A token's cosines and sines are computed once for all heads, then each thread of
+// its group moves 16-byte units of q, k and v.
+template <bool kF16, int kMode, int kGroup>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
 {
-    extern __shared__ float2 cs[];                          // [rot / 2]
+    extern __shared__ float2 all_cs[];                      // [groups][rot / 2]
+    float2 *const cs = kGroup == kThreads ? all_cs : all_cs + (int)threadIdx.x / kGroup * (p.turn.rot / 2);
     ptx::wait_for_primary();
-    const int64_t b = blockIdx.x / p.T;
-    const int t = (int)(blockIdx.x % p.T);
+    int64_t b;
+    int t;
+    if (!group_token<kGroup>((int64_t)p.B * p.T, p.by_t, b, t)) return;
     const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
     const int D = p.c.D, Hkv = p.c.Hkv;
     const int units = D / 8;
 
     if (i < 0) {                                            // no token here: its query is zero
         if (p.q)
-            for (int e = threadIdx.x; e < p.Hq * units; e += kThreads)
+            for (int e = group_thread<kGroup>(); e < p.Hq * units; e += kGroup)
                 *reinterpret_cast<uint4 *>(p.q_out + b * p.qo_s[0] + (e / units) * p.qo_s[1] + t * p.qo_s[2] +
                                            (e % units) * 8) = make_uint4(0u, 0u, 0u, 0u);
         return;
@@ -213,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     if (at / size < (uint32_t)p.c.table_width) page = p.c.table[b * p.c.table_stride + at / size];
     const bool stored = page >= 0 && page < p.c.num_pages;   // otherwise the key and value are dropped
     const int64_t row = stored ? page * p.c.s_page + (int64_t)(at % size) * p.c.s_slot : 0;
-    turns_of(p.turn, b, t, i, cs);
-    __syncthreads();
+    turns_of<kGroup>(p.turn, b, t, i, cs);
+    group_sync<kGroup>();
 
     // heads 0 .. Hkv-1: keys; Hkv .. Hkv+Hq-1: queries; then values
     const int q_heads = p.q ? p.Hq : 0;
@@ -229,23 +269,62 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p)
     };
 
     if (stored)
-        for (int e = threadIdx.x; e < Hkv * units; e += kThreads) {
+        for (int e = group_thread<kGroup>(); e < Hkv * units; e += kGroup) {
             const int head = e / units, u = e % units;
             *reinterpret_cast<uint4 *>(p.c.v + row + head * p.c.s_head + u * 8) =
                 *reinterpret_cast<const uint4 *>(p.v + b * p.v_s[0] + head * p.v_s[1] + t * p.v_s[2] + u * 8);
         }
-    turn_heads<kF16, kMode>(k_heads + q_heads, D, p.turn.rot, cs, source, target);
+    turn_heads<kF16, kMode, kGroup>(k_heads + q_heads, D, p.turn.rot, cs, source, target);
+}
+
+// Whether a warp per token serves: where tokens have little and are many, the more the
+// more they have.  A CTA and a warp per token, us, into 16 bits, into 4, and without a
+// cache (`units`: 16-byte units of a token, of q, k and v in the first two, of q and k
+// in the third):
+//   tokens   units         into 16        into 4         without
+//   500      64, 64, 48    3.3 and 3.3    3.3 and 3.3    2.5 and 2.5
+//   2000     15, 15, 10    4.1 and 3.3    5.8 and 4.2    3.3 and 2.9
+//   2000     64, 64, 48    4.1 and 3.7    5.8 and 4.2    3.3 and 2.9
+//   2000     192, 192, 160 5.0 and 5.4    6.3 and 5.4    3.8 and 4.6
+//   5000     192, 192, 160 8.7 and 7.8    11.1 and 8.3   6.6 and 7.0
+//   50000    64, 64, 48    48 and 31      62 and 41      28 and 20
+//   50000    192, 192, 160 69 and 60      78 and 56      48 and 47
+//   16384    768, 768, -   62 and 68      65 and 69
+//   32760    -, -, 512                                   84.5 and 87.5
+bool warp_per_token(int64_t tokens, int64_t units)
+{
+    return units <= 192 && tokens > (units <= 64 ? 8 : 64) * (int64_t)sm_count_of(current_device()) &&
+           tokens < (int64_t)1 << 30;
+}
+
+// kernel(mode, group) with a token per CTA, or per warp.
+template <typename P, typename Launch>
+cudaError_t launch_tokens(const P &p, int64_t units, const Launch &launch)
+{
+    const int64_t tokens = (int64_t)p.B * p.T;
+    const bool warps = warp_per_token(tokens, units);
+    const int per = warps ? kThreads / 32 : 1;
+    const dim3 grid((unsigned)((tokens + per - 1) / per));
+    const size_t smem = (size_t)per * (p.turn.rot / 2) * sizeof(float2);
+    const int mode = p.turn.interleaved || p.turn.rot == 0 ? kNeighbours : p.turn.rot % 16 == 0 ? kHalves : kHalvesOdd;
+    using std::integral_constant;
+    const auto with_group = [&](auto m) {
+        return warps ? launch(m, integral_constant<int, 32>{}, grid, smem)
+                     : launch(m, integral_constant<int, kThreads>{}, grid, smem);
+    };
+    switch (mode) {
+    case kNeighbours: return with_group(integral_constant<int, kNeighbours>{});
+    case kHalves: return with_group(integral_constant<int, kHalves>{});
+    default: return with_group(integral_constant<int, kHalvesOdd>{});
+    }
 }
 
 template <bool kF16>
 cudaError_t launch(const AppendParams &p, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.B * p.T));
-    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
-    if (p.turn.interleaved || p.turn.rot == 0)
-        return launch_behind(append_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
-    if (p.turn.rot % 16 == 0) return launch_behind(append_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
-    return launch_behind(append_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
+    return launch_tokens(p, (p.Hq + (int64_t)2 * p.c.Hkv) * (p.c.D / 8), [&](auto mode, auto group, dim3 grid, size_t smem) {
+        return launch_behind(append_kernel<kF16, decltype(mode)::value, decltype(group)::value>, grid, kThreads, smem, stream, p);
+    });
 }
 
 // ---------------------------------------------------------------- 4 bits
@@ -294,12 +373,16 @@ __device__ __forceinline__ void turned8(const uint16_t *src, int u, uint4 w, int
 }
 
 // (A thread's first group is read before it is known where it goes: two waits less.)
-template <bool kF16, int kMode>
+template <bool kF16, int kMode, int kGroup>
 __global__ void __launch_bounds__(kThreads, 10) append4_kernel(const Append4Params p)
 {
-    extern __shared__ float2 cs[];                          // [rot / 2]
+    extern __shared__ float2 all_cs[];                      // [groups][rot / 2]
+    float2 *const cs = kGroup == kThreads ? all_cs : all_cs + (int)threadIdx.x / kGroup * (p.turn.rot / 2);
+    const int thread = group_thread<kGroup>();
     ptx::wait_for_primary();
-    const int b = p.by_t.quotient((int)blockIdx.x), t = (int)blockIdx.x - b * p.T;
+    int64_t b;
+    int t;
+    if (!group_token<kGroup, true>((int64_t)p.B * p.T, p.by_t, b, t)) return;
     const int D = p.c.D, Hkv = p.c.Hkv, units = D / 8;
     // keys, then values; groups of a head
     const int groups = D <= 64 ? 2 : D <= 128 ? 3 : 4;      // (the logarithm of how many a row has)
@@ -315,12 +398,12 @@ __global__ void __launch_bounds__(kThreads, 10) append4_kernel(const Append4Para
         for (int h = 0; h < 2; ++h)                          // past the head: padding
             w[h] = u + h < units ? *reinterpret_cast<const uint4 *>(src + (u + h) * 8) : make_uint4(0u, 0u, 0u, 0u);
     };
-    if ((int)threadIdx.x < (2 * Hkv) << groups) fetch(threadIdx.x);
+    if (thread < (2 * Hkv) << groups) fetch(thread);
     const int i = max(p.c.seq_len[b], -1) - p.T + t;        // (-1 - T at least: no overflow)
 
     if (i < 0) {                                            // no token here: its query is zero
         if (p.q)
-            for (int e = threadIdx.x; e < p.Hq * units; e += kThreads)
+            for (int e = thread; e < p.Hq * units; e += kGroup)
                 *reinterpret_cast<uint4 *>(p.q_out + b * p.qo_s[0] + (e / units) * p.qo_s[1] + t * p.qo_s[2] +
                                            (e % units) * 8) = make_uint4(0u, 0u, 0u, 0u);
         return;
@@ -328,14 +411,14 @@ __global__ void __launch_bounds__(kThreads, 10) append4_kernel(const Append4Para
     const int entry = p.c.by_page.quotient(i);
     int page = -1;
     if (entry < p.c.table_width) page = p.c.table[b * p.c.table_stride + entry];
-    turns_of(p.turn, b, t, i, cs);
-    __syncthreads();
+    turns_of<kGroup>(p.turn, b, t, i, cs);
+    group_sync<kGroup>();
 
     if (page >= 0 && page < p.c.num_pages) {                // otherwise the key and value are dropped
         const int64_t slot = i - entry * p.c.page_size;
         const int64_t row = page * p.c.s_page + slot * p.c.s_slot, scales = page * p.c.t_page + slot * p.c.t_slot;
-        for (int e = threadIdx.x; e < (2 * Hkv) << groups; e += kThreads) {
-            if (e != (int)threadIdx.x) fetch(e);
+        for (int e = thread; e < (2 * Hkv) << groups; e += kGroup) {
+            if (e != thread) fetch(e);
             const int which = e >> groups, g = e & ((1 << groups) - 1), head = which < Hkv ? which : which - Hkv;
             float x[16];
 #pragma unroll
@@ -356,32 +439,31 @@ __global__ void __launch_bounds__(kThreads, 10) append4_kernel(const Append4Para
     }
     const auto from = [&](int head) -> const uint16_t * { return p.q + b * p.q_s[0] + head * p.q_s[1] + t * p.q_s[2]; };
     const auto target = [&](int head) -> uint16_t * { return p.q_out + b * p.qo_s[0] + head * p.qo_s[1] + t * p.qo_s[2]; };
-    turn_heads<kF16, kMode>(p.q ? p.Hq : 0, D, p.turn.rot, cs, from, target);
+    turn_heads<kF16, kMode, kGroup>(p.q ? p.Hq : 0, D, p.turn.rot, cs, from, target);
 }
 
 template <bool kF16>
 cudaError_t launch4(const Append4Params &p, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.B * p.T));
-    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
-    if (p.turn.interleaved || p.turn.rot == 0)
-        return launch_behind(append4_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
-    if (p.turn.rot % 16 == 0) return launch_behind(append4_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
-    return launch_behind(append4_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
+    return launch_tokens(p, (p.Hq + (int64_t)2 * p.c.Hkv) * (p.c.D / 8), [&](auto mode, auto group, dim3 grid, size_t smem) {
+        return launch_behind(append4_kernel<kF16, decltype(mode)::value, decltype(group)::value>, grid, kThreads, smem, stream, p);
+    });
 }
 
 // ---------------------------------------------------------------- no cache
 // 32760 tokens, 16 query and 16 key heads, D = 128, three axes: 537 MB in 84 us, 6.4
 // TB/s; turned back the same.
-template <bool kF16, int kMode>
+template <bool kF16, int kMode, int kGroup>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p)
 {
-    extern __shared__ float2 cs[];                          // [rot / 2]
+    extern __shared__ float2 all_cs[];                      // [groups][rot / 2]
+    float2 *const cs = kGroup == kThreads ? all_cs : all_cs + (int)threadIdx.x / kGroup * (p.turn.rot / 2);
     ptx::wait_for_primary();
-    const int64_t b = blockIdx.x / p.T;
-    const int t = (int)(blockIdx.x % p.T);
-    turns_of(p.turn, b, t, t, cs);
-    __syncthreads();
+    int64_t b;
+    int t;
+    if (!group_token<kGroup>((int64_t)p.B * p.T, p.by_t, b, t)) return;
+    turns_of<kGroup>(p.turn, b, t, t, cs);
+    group_sync<kGroup>();
     const auto source = [&](int head) -> const uint16_t * {
         const int i = head < p.H[0] ? 0 : 1;
         return p.x[i] + b * p.x_s[i][0] + (head - i * p.H[0]) * p.x_s[i][1] + t * p.x_s[i][2];
@@ -390,18 +472,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p)
         const int i = head < p.H[0] ? 0 : 1;
         return p.y[i] + b * p.y_s[i][0] + (head - i * p.H[0]) * p.y_s[i][1] + t * p.y_s[i][2];
     };
-    turn_heads<kF16, kMode>(p.H[0] + p.H[1], p.D, p.turn.rot, cs, source, target);
+    turn_heads<kF16, kMode, kGroup>(p.H[0] + p.H[1], p.D, p.turn.rot, cs, source, target);
 }
 
 template <bool kF16>
 cudaError_t launch_turn(const RotaryParams &p, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((int64_t)p.B * p.T));
-    const size_t smem = (size_t)(p.turn.rot / 2) * sizeof(float2);
-    if (p.turn.interleaved || p.turn.rot == 0)
-        return launch_behind(rotary_kernel<kF16, kNeighbours>, grid, kThreads, smem, stream, p);
-    if (p.turn.rot % 16 == 0) return launch_behind(rotary_kernel<kF16, kHalves>, grid, kThreads, smem, stream, p);
-    return launch_behind(rotary_kernel<kF16, kHalvesOdd>, grid, kThreads, smem, stream, p);
+    return launch_tokens(p, (int64_t)(p.H[0] + p.H[1]) * (p.D / 8), [&](auto mode, auto group, dim3 grid, size_t smem) {
+        return launch_behind(rotary_kernel<kF16, decltype(mode)::value, decltype(group)::value>, grid, kThreads, smem, stream, p);
+    });
 }
 
 }  // namespace

@@ -122,6 +122,7 @@ fa_status fa_rotary(const fa_rows *Q, const fa_rows *Q_out, const fa_rows *K, co
     }
     if (Hq && Hkv && Q_out->ptr == K_out->ptr) return FA_ERR_INVALID_ARG;
     p.turn.inverse = inverse ? 1 : 0;
+    p.by_t = fa::make_fast_div((uint32_t)T);
     p.B = B;
     p.T = T;
     p.D = D;

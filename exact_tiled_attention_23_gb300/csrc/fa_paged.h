@@ -63,6 +63,7 @@ struct AppendParams {
     const uint16_t *k, *v, *q;         // [B, H, T, D] through the strides below; q may be null
     uint16_t *q_out;
     int64_t k_s[3], v_s[3], q_s[3], qo_s[3];   // batch, head, token
+    FastDiv by_t;                      // T
     int B, T, Hq, f16;
 };
 
@@ -104,6 +105,7 @@ struct RotaryParams {
     uint16_t *y[2];
     int64_t x_s[2][3], y_s[2][3];      // batch, head, token
     int H[2];
+    FastDiv by_t;                      // T
     int B, T, D, f16;
 };
 

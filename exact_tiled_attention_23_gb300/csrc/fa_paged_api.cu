@@ -188,6 +188,7 @@ fa_status fa_kv_append_at(const fa_paged_kv *cache, const fa_rows *K, const fa_r
 
     p.c = cache_of(*cache);
     put_rows(p, K, V, queries ? Q : nullptr, Q_out);
+    p.by_t = fa::make_fast_div((uint32_t)T);
     p.B = B;
     p.T = T;
     p.Hq = queries ? Hq : 0;
