@@ -10,6 +10,9 @@ namespace {
 
 using namespace fa::paged;
 
+// (Kernels count pages, rows and forks in 32 bits, a CTA's threads at a time.)
+constexpr int kMostEntries = INT32_MAX - 1024;
+
 fa_status check_table(const fa_page_table *t)
 {
     if (!t || t->B < 0 || t->table_width < 0 || t->num_pages < 0 || t->page_size <= 0) return FA_ERR_INVALID_ARG;
@@ -18,7 +21,7 @@ fa_status check_table(const fa_page_table *t)
     if (t->B > 1 && t->table_stride < t->table_width) return FA_ERR_INVALID_ARG;
     if ((int64_t)t->table_width * t->page_size > kMostKeys) return FA_ERR_INVALID_ARG;
     const int64_t parts = (t->table_width + 2047ll) / 2048;
-    if (parts * t->B > INT32_MAX - 1024) return FA_ERR_INVALID_ARG;
+    if (parts * t->B > kMostEntries || t->num_pages > kMostEntries) return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
@@ -58,7 +61,7 @@ fa_status with_workspace(fa::PagesParams &p, const fa_page_table &t, int n, void
     return workspace && aligned(workspace, 16) && bytes >= need ? FA_OK : FA_ERR_INVALID_ARG;
 }
 
-bool vector_ok(const int32_t *x, int n) { return n == 0 || (x && aligned(x, 4)); }
+bool vector_ok(const int32_t *x, int n) { return n == 0 || (n <= kMostEntries && x && aligned(x, 4)); }
 
 fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
@@ -101,7 +104,7 @@ extern "C" {
 
 size_t fa_pages_workspace_bytes(const fa_page_table *table, int n)
 {
-    if (check_table(table) != FA_OK || n < 0) return 0;
+    if (check_table(table) != FA_OK || n < 0 || n > kMostEntries) return 0;
     fa::PagesParams p{};
     return place(p, *table, n, nullptr);
 }

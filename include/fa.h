@@ -590,7 +590,7 @@ typedef struct fa_page_table {
     int B;
     int32_t *seq_len;            /* [B] */
     int32_t *refs;               /* [num_pages] */
-    int num_pages, page_size;
+    int num_pages, page_size;    /* num_pages, and the entries of the calls' vectors, <= 2^31 - 1025 */
 } fa_page_table;
 
 /* Bytes of workspace (16-byte aligned; its contents do not matter, and calls that may

@@ -145,6 +145,20 @@ def test_bad_page_calls(lib):
     assert fa.fa_copy_pages_q4(cache4(), None, None, None, 0, None) == fa.FA_OK
 
 
+@cuda_toolkit
+def test_counts_that_32_bits_do_not_hold_a_block_further(lib):
+    most = 2 ** 31 - 1025
+    assert fa.fa_pages_workspace_bytes(table(num_pages=most), most) > 0
+    for pages in (most + 1, 2 ** 31 - 1):
+        t = table(num_pages=pages)
+        assert fa.fa_pages_workspace_bytes(t, 0) == 0 and fa.fa_kv_grow(t, P, P, P, 2 ** 40, None) == BAD
+        assert fa.fa_kv_compact(t, P, P, P, P, P, 2 ** 40, None) == BAD
+    for n in (most + 1, 2 ** 31 - 1):
+        assert fa.fa_pages_workspace_bytes(table(), n) == 0 and fa.fa_kv_free(table(), P, n, None) == BAD
+        assert fa.fa_kv_fork(table(), P, P, n, P, P, P, 2 ** 40, None) == BAD
+        assert fa.fa_copy_pages_q4(cache4(), P, P, None, n, None) == BAD
+
+
 def test_the_references_format():
     """Every number of the format is itself, and halfway goes to the even one."""
     s = ref.scales()
