@@ -47,7 +47,10 @@
 // their keys decoded once, elsewhere (kDirectTiles in fa_four_api.cu).  36 rows over 64
 // sequences of up to 8191 keys: 243 us, decoded elsewhere first 627 (16 bits: 176).
 // (Four more warps for it leave 128 registers a thread; moved between the roles they
-// spilled in the issuing threads' loops: 241, and 345 instead of 387 for 32 tiles.)
+// spilled in the issuing threads' loops: 241, and 345 instead of 387 for 32 tiles.
+// The bytes' way is not what it waits for: beside 247, copied by blocks into shared
+// memory a block ahead 242, by 16 bytes 289; a row's loads as soon as it is decoded
+// 257; whole rows by neighbouring lanes 262.)
 //
 // Every mbarrier wait is bounded; a wait that runs out records the site in
 // this file's status word, raises the CTA's abort flag, and every role drains
@@ -184,7 +187,7 @@ struct Walk {
     }
 };
 
-// kFour: a 4-bit cache, whose rows warps 12-15 decode into the K and V slots as IEEE
+// kFour: a 4-bit cache, whose rows warps 0 and 2 decode into the K and V slots as IEEE
 // halves, for queries and outputs of kIo16 (fp16, else bf16).  Everything else is then
 // fp16: a bf16 row of Q is multiplied by the power of two that takes its largest
 // element to 2^14 .. 2^15 (exact, but for what lies 2^-39 below that), its scores are
