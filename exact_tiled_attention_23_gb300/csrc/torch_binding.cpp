@@ -24,6 +24,7 @@
 #include <cmath>
 #include <mutex>
 #include <optional>
+#include <tuple>
 #include <vector>
 
 namespace {
@@ -501,6 +502,8 @@ struct Turn {
     }
 };
 
+std::array<at::Tensor, 2> turned(const std::array<at::Tensor, 2> &x, const Turn &turn);
+
 // The same as an operation whose gradient turns back.  (The first tensor is defined.)
 struct Rotary : torch::autograd::Function<Rotary> {
     static torch::autograd::variable_list forward(torch::autograd::AutogradContext *ctx, const at::Tensor &a,
@@ -530,19 +533,42 @@ struct Rotary : torch::autograd::Function<Rotary> {
         const int64_t how = ctx->saved_data["how"].toInt();
         const Turn back{saved[0], saved.size() > 1 ? saved[1] : at::Tensor(), saved.size() > 2 ? saved[2] : at::Tensor(),
                         (how & 1) != 0, (how & 2) == 0, ctx->saved_data["offset"].toInt()};
-        std::optional<at::Tensor> second;
-        if (which.size() > 1) second = d[which[1]];
         try {
-            const auto y = at::GradMode::is_enabled() ? apply(d[which[0]], second, back) : as_list(back({d[which[0]], second.value_or(at::Tensor())}));
+            const auto y = turned({d[which[0]], which.size() > 1 ? d[which[1]] : at::Tensor()}, back);
             for (size_t i = 0; i < which.size(); ++i) grads[which[i]] = y[i];
         } catch (const Refused &r) {
             TORCH_CHECK(false, "the gradient of rotary: status ", (int)r.status);
         }
         return grads;
     }
-
-    static torch::autograd::variable_list as_list(const std::array<at::Tensor, 2> &y) { return {y[0], y[1]}; }
 };
+
+// q and k (either may be undefined) turned, differentiable both ways: through Rotary
+// where a gradient may be asked for, and a forward-mode tangent turns as its tensor
+// does, since the operation is linear.
+std::array<at::Tensor, 2> turned(const std::array<at::Tensor, 2> &x, const Turn &turn)
+{
+    const auto is_dual = [](const at::Tensor &t) { return t.defined() && t._fw_grad(0).defined(); };
+    if (is_dual(x[0]) || is_dual(x[1])) {
+        std::array<at::Tensor, 2> value = x, tangent;
+        for (int i = 0; i < 2; ++i)
+            if (is_dual(x[i])) std::tie(value[i], tangent[i]) = at::_unpack_dual(x[i], 0);
+        auto y = turned(value, turn);
+        const auto t = turned(tangent, turn);
+        for (int i = 0; i < 2; ++i)
+            if (t[i].defined()) y[i] = at::_make_dual(y[i], t[i], 0);
+        return y;
+    }
+    const auto asks = [](const at::Tensor &t) { return t.defined() && t.requires_grad(); };
+    if (!at::GradMode::is_enabled() || !(asks(x[0]) || asks(x[1]))) return turn(x);
+    const int first = x[0].defined() ? 0 : 1;
+    const bool both = first == 0 && x[1].defined();
+    const auto r = Rotary::apply(x[first], both ? std::optional<at::Tensor>(x[1]) : std::nullopt, turn);
+    std::array<at::Tensor, 2> y;
+    y[first] = r[0];
+    if (both) y[1] = r[1];
+    return y;
+}
 
 // rotary(q, k or None, inv_freq, positions, pair_axis, interleaved, position_offset) ->
 // (q, k or None) turned, or a status
@@ -602,12 +628,7 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
         } released;
         try {
             const Turn turn{freq.detach(), positions.n, positions.pair_axis, interleaved != 0, false, offset};
-            if (at::GradMode::is_enabled() && (x[0].requires_grad() || (x[1].defined() && x[1].requires_grad()))) {
-                const auto r = Rotary::apply(x[0], x[1].defined() ? std::optional<at::Tensor>(x[1]) : std::nullopt, turn);
-                y = {r[0], r.size() > 1 ? r[1] : at::Tensor()};
-            } else {
-                y = turn({x[0], x[1]});
-            }
+            y = turned({x[0], x[1]}, turn);
         } catch (const Refused &r) {
             st = r.status;
         }
