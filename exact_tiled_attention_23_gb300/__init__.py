@@ -960,7 +960,8 @@ def rotary(q, inv_freq, positions=None, k=None, pair_axis=None, interleaved: boo
     [axes, B, T] for positions on several axes (time, height and width, say); None: 0, 1,
     2 ...  pair_axis: int32 CUDA tensor, the axis that each pair turns by (a pair whose
     entry is no axis does not turn).  position_offset is added to every position.
-    Gradients reach q and k, and forward-mode tangents of them turn, too.
+    Gradients reach q and k, and forward-mode tangents of them turn, too; inv_freq gets
+    none, and one that requires grad is refused (ValueError).
     """
     if stream is not None:
         with _stream_context(q.device, stream):

@@ -612,6 +612,11 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n)
         value_error("inv_freq must be a float32 tensor of one dimension on the device of q and k");
         return nullptr;
     }
+    // (a gradient that is asked for must not be missed without a word)
+    if ((at::GradMode::is_enabled() && freq.requires_grad()) || freq._fw_grad(0).defined()) {
+        value_error("rotary gives inv_freq no gradient: pass inv_freq.detach()");
+        return nullptr;
+    }
     const c10::cuda::CUDAGuard guard(first->device());
     freq = freq.contiguous();
     Positions positions;
