@@ -103,7 +103,7 @@ fa_status fa_rotary(const fa_rows *Q, const fa_rows *Q_out, const fa_rows *K, co
     if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || D <= 0) return FA_ERR_INVALID_ARG;
     if (D % 8 != 0 || D > 256) return FA_ERR_UNSUPPORTED;
     fa::RotaryParams p{};
-    const fa_status st = check_turn(p.turn, D, inv_freq, rot_dim, interleaved, positions, position_offset);
+    const fa_status st = check_turn(p.turn, (int64_t)B * T, D, inv_freq, rot_dim, interleaved, positions, position_offset);
     if (st != FA_OK) return st;
     if ((int64_t)B * T > INT32_MAX || (int64_t)Hq + Hkv > INT32_MAX / D) return FA_ERR_INVALID_ARG;
     if ((int64_t)B * T == 0 || Hq + Hkv == 0) return FA_OK;
@@ -138,7 +138,7 @@ fa_status fa_kv_append_q4(const fa_paged_kv4 *cache, const fa_rows *K, const fa_
     fa_status st = check_cache4(cache, B);
     if (st != FA_OK) return st;
     fa::Append4Params p{};
-    st = check_turn(p.turn, cache->D, inv_freq, rot_dim, interleaved, positions, position_offset);
+    st = check_turn(p.turn, (int64_t)B * T, cache->D, inv_freq, rot_dim, interleaved, positions, position_offset);
     if (st != FA_OK) return st;
     if ((int64_t)B * T > INT32_MAX) return FA_ERR_INVALID_ARG;
     if ((int64_t)B * T == 0) return FA_OK;

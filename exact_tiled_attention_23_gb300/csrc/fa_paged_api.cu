@@ -178,7 +178,7 @@ fa_status fa_kv_append_at(const fa_paged_kv *cache, const fa_rows *K, const fa_r
     fa_status st = check_cache(cache, B);
     if (st != FA_OK) return st;
     fa::AppendParams p{};
-    st = check_turn(p.turn, cache->D, inv_freq, rot_dim, interleaved, positions, position_offset);
+    st = check_turn(p.turn, (int64_t)B * T, cache->D, inv_freq, rot_dim, interleaved, positions, position_offset);
     if (st != FA_OK) return st;
     if ((int64_t)B * T > INT32_MAX) return FA_ERR_INVALID_ARG;
     if ((int64_t)B * T == 0) return FA_OK;

@@ -134,8 +134,9 @@ inline bool same_rows(const fa_rows &x, const fa_rows &y, int B, int H, int T)
 
 inline size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// The rotation's arguments, checked.
-inline fa_status check_turn(fa::TurnParams &t, int D, const float *inv_freq, int rot_dim, int interleaved,
+// The rotation's arguments for so many tokens, checked.  (Positions of no tokens need
+// no memory.)
+inline fa_status check_turn(fa::TurnParams &t, int64_t tokens, int D, const float *inv_freq, int rot_dim, int interleaved,
                             const fa_positions *positions, int64_t position_offset)
 {
     if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0) return FA_ERR_INVALID_ARG;
@@ -147,7 +148,7 @@ inline fa_status check_turn(fa::TurnParams &t, int D, const float *inv_freq, int
     t.rot = rot_dim;
     t.interleaved = interleaved ? 1 : 0;
     if (positions) {
-        if (!positions->n || !aligned(positions->n, 4) || positions->axes < 1 || !aligned(positions->pair_axis, 4)) return FA_ERR_INVALID_ARG;
+        if ((tokens > 0 && !positions->n) || !aligned(positions->n, 4) || positions->axes < 1 || !aligned(positions->pair_axis, 4)) return FA_ERR_INVALID_ARG;
         if (positions->stride_axis < 0 || positions->stride_b < 0 || positions->stride_t < 0) return FA_ERR_INVALID_ARG;
         t.pos = positions->n;
         t.pos_s[0] = positions->stride_axis;

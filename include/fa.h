@@ -469,7 +469,7 @@ size_t fa_fwd_shared_prefix_workspace_bytes(const fa_paged_kv *cache, int prefix
  * does not turn).  pair_axis = NULL: axis 0.
  */
 typedef struct fa_positions {
-    const int32_t *n;
+    const int32_t *n;                           /* (may be NULL where there are no tokens) */
     int64_t stride_axis, stride_b, stride_t;    /* >= 0 */
     int axes;                                   /* >= 1 */
     const int32_t *pair_axis;
