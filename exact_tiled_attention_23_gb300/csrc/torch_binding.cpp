@@ -719,6 +719,17 @@ bool layers_of(PyObject *object, std::vector<Cache *> &all)
     return true;
 }
 
+// Whether every cache's pages can be copied, known before the table changes (no pairs: the
+// C ABI's checks alone).
+fa_status check_copies(const std::vector<Cache *> &all)
+{
+    for (const Cache *c : all) {
+        const fa_status st = c->four ? g_copy_q4(&c->c4, nullptr, nullptr, nullptr, 0, nullptr) : g_copy(&c->c, nullptr, nullptr, nullptr, 0, nullptr);
+        if (st != FA_OK) return st;
+    }
+    return FA_OK;
+}
+
 // The pages that a call listed, in every cache.
 fa_status copy_listed(const std::vector<Cache *> &all, const int32_t *src, const int32_t *dst, const int32_t *count, int n, void *stream)
 {
@@ -777,6 +788,8 @@ PyObject *fork_rows(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (!table_of(*cache, a[1], refs, t) || !entries(a[2], "parent", -1, *cache, false, parent) ||
         !entries(a[3], "child", parent.numel(), *cache, false, child))
         return nullptr;
+    const fa_status copies = check_copies(all);
+    if (copies != FA_OK) return PyLong_FromLong(copies);
     const int count = (int)parent.numel();
     at::Tensor dst = numbers(*cache, count);
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
@@ -801,6 +814,8 @@ PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n)
     at::Tensor refs;
     fa_page_table t;
     if (!table_of(*cache, a[1], refs, t)) return nullptr;
+    const fa_status copies = check_copies(all);
+    if (copies != FA_OK) return PyLong_FromLong(copies);
     const int pages = cache->c.num_pages;
     at::Tensor moved = numbers(*cache, pages);
     void *stream = c10::cuda::getCurrentCUDAStream(cache->device).stream();
