@@ -902,7 +902,8 @@ def kv_fork(cache, refs, parent, child, stream=None):
     parent, child: int32 CUDA tensors of one length; a child is empty (kv_free()).
     cache, refs: as in kv_grow().  Returns an int32 tensor: the page that was copied
     to, -1 where none had to be, -2 where the fork was refused (no free page, a child
-    that is not empty, that comes twice or is another fork's parent, no such row).
+    that is not empty or is an earlier fork's, a parent that is among the children, no
+    such row).
     """
     cache = _layers(cache)
     if stream is not None:

@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PagesParams p
     __shared__ int sums[2][kWarps];
     int turn = 0, base = 0;
     ptx::wait_for_primary();
-    // a row that is a child twice, or a child and a parent, would depend on the order
+    // a child has its first fork's number, all other rows none: what a second fork of a
+    // child, or a fork of a child, gives would depend on the order
     for (int i = threadIdx.x; i < p.n; i += kThreads) {
         const int x = p.parent[i], y = p.rows[i];
         if (x >= 0 && x < p.B) p.mark[x] = INT32_MAX;

@@ -619,8 +619,9 @@ fa_status fa_kv_free(const fa_page_table *table, const int32_t *rows, int n, voi
  * shared; a last page that is part full is copied to a free one, since both rows will
  * write behind it.  src[i] and dst[i] are that copy, which the caller makes with
  * fa_copy_pages, or -1 for none.  dst[i] = -2: not forked, because no page was free,
- * the child was not empty (seq_len 0), a row is none, or the child is another fork's
- * parent or an earlier one's child.
+ * the child was not empty (seq_len 0), a row is none, the child is an earlier fork's
+ * child, or the parent is a fork's child in the same call (whether that one is done or
+ * not).
  */
 fa_status fa_kv_fork(const fa_page_table *table, const int32_t *parent, const int32_t *child, int n, int32_t *src, int32_t *dst,
                      void *workspace, size_t workspace_bytes, void *stream);
