@@ -513,10 +513,10 @@ fa_status fa_rotary(const fa_rows *Q, const fa_rows *Q_out, const fa_rows *K, co
  *      At most 10240 (byte 226); larger bytes are undefined.
  * u * s is exact as an IEEE half and as bf16.  Appending, s is the group's largest
  * magnitude / 6 and u the element / s, both rounded to nearest (halfway to the even
- * mantissa bit), u at most 6: an element is off by at most 0.18 of its group's largest
- * (0.23 where that is below 2^-11).  A group whose largest is 6 * 2^-18 or less is held
- * as zeros, and magnitudes above 61440 are held as that.  Elements have to be finite
- * (others become some finite value).
+ * mantissa bit), u at most 6: an element is off by at most 0.18 of its group's largest,
+ * by 0.2 where that is below 6 * 2^-14, and by 1/3 below 9 * 2^-17.  A group whose
+ * largest is 6 * 2^-18 or less is held as zeros, and magnitudes above 61440 are held as
+ * that.  Elements have to be finite (others become some finite value).
  *
  * The pools' rows are
  *     k + page * stride_page + head * stride_head + slot * stride_slot
