@@ -868,8 +868,12 @@ def kv_grow(cache, refs, tokens, stream=None):
     table entry in front of a sequence's length, and whatever the caller adds (a
     prefix's pages, say); 0: free.  tokens: int32 CUDA tensor [B].  block_table, seq_len and
     refs are updated.  Returns an int32 tensor [B]: how many pages a sequence got, -2 if
-    it was not grown because its table row or the free pages do not suffice.  Runs
-    asynchronously, like all page operators: nothing waits for the GPU.
+    it was not grown: its table row is too short, or the free pages do not suffice for
+    what it and all sequences in front of it ask for (four free pages: of needs of 9, 1
+    and 1 pages none is met, of 1, 1 and 9 the first two).  kv_append() writes the last T
+    tokens of every sequence, also of one that was not grown: give that one the tokens
+    that it has.  Runs asynchronously, like all page operators:
+    nothing waits for the GPU.
     """
     cache = _layers(cache)
     if stream is not None:

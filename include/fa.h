@@ -600,9 +600,9 @@ size_t fa_pages_workspace_bytes(const fa_page_table *table, int n);
 /*
  * fa_kv_grow -- every sequence b grows by tokens[b] (0 or less: not), and gets the
  * pages for them: what an append needs.  taken[b] is how many pages it got, or -2 if
- * it was not grown: the table's row or the free pages do not suffice.  Pages are given
- * in the order of the sequences; behind one that they did not suffice for, only
- * sequences that need none are sure to grow.
+ * it was not grown: the table's row is too short (it asks for no pages then), or the
+ * free pages do not suffice for what it and all sequences in front of it ask for.
+ * Pages are given in the order of the sequences.
  */
 fa_status fa_kv_grow(const fa_page_table *table, const int32_t *tokens, int32_t *taken, void *workspace, size_t workspace_bytes,
                      void *stream);
