@@ -658,7 +658,10 @@ class PagedKV4:
 
     kv_append(), forward_paged(), kv_read() and the page operators take it in the
     place of a PagedKV; forward_shared_prefix() does not (the sequences' tables may
-    share a prefix's pages instead).
+    share a prefix's pages instead).  forward_paged() takes less time than over a PagedKV
+    where up to 32 query rows of a sequence share a key (T * Hq / Hkv), and mostly more
+    beyond that.  Beyond 512 rows its workspace and time grow with the width of
+    block_table: make that no wider than the sequences need (include/fa.h has figures).
     """
 
     def __init__(self, k_cache, v_cache, k_scales, v_scales, block_table, seq_len, D=None, dtype=None):
@@ -868,12 +871,12 @@ def kv_grow(cache, refs, tokens, stream=None):
     table entry in front of a sequence's length, and whatever the caller adds (a
     prefix's pages, say); 0: free.  tokens: int32 CUDA tensor [B].  block_table, seq_len and
     refs are updated.  Returns an int32 tensor [B]: how many pages a sequence got, -2 if
-    it was not grown: its table row is too short, or the free pages do not suffice for
-    what it and all sequences in front of it ask for (four free pages: of needs of 9, 1
-    and 1 pages none is met, of 1, 1 and 9 the first two).  kv_append() writes the last T
-    tokens of every sequence, also of one that was not grown: give that one the tokens
-    that it has.  Runs asynchronously, like all page operators:
-    nothing waits for the GPU.
+    it was not grown: its table row is too short, or it needs pages and the free ones do
+    not suffice for what it and all sequences in front of it ask for (four free pages: of
+    needs of 9, 1 and 1 pages none is met, of 1, 1 and 9 the first two).  kv_append()
+    writes the last T tokens of every sequence, also of one that was not grown: give that
+    one the tokens that it has.  Runs asynchronously, like all page operators: nothing
+    waits for the GPU.
     """
     cache = _layers(cache)
     if stream is not None:

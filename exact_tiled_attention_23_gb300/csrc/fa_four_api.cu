@@ -11,7 +11,14 @@ namespace {
 using namespace fa::paged;
 
 // Sequences whose keys are decoded to 16 bits at a time: as many as have kWide bytes of
-// them at most, one at least, if that has kMostWide at most.
+// them at most, one at least, if that has kMostWide at most.  A sequence counts with all
+// keys that its row of the table can hold, since its length is on the device: at D = 128
+// and 8 key heads a row for 131072 keys takes 512 MB of workspace, whatever it holds, and
+// its sequences are decoded and attended to one after another.  256 tokens of 64
+// sequences of 500 keys, with rows for 512, 16384, 131072 and 262144 keys: 382, 717, 2198
+// and 3066 us, and for more, where every tile decodes its keys itself, 419; of 8 of 4000
+// keys 225 (rows for 4000), 261, 456, 565 and 243.  Tables no wider than the longest
+// sequence needs are what this is for.
 constexpr int64_t kWide = (int64_t)256 << 20, kMostWide = (int64_t)1 << 30;
 
 // Row tiles of a sequence up to which each decodes its keys itself on the tensor cores;

@@ -45,12 +45,16 @@
 // Over a 4-bit cache (kFour) warps 0 and 2 decode what they copy else, a step of 128
 // keys in ~3200 clk where a block takes 1680, so that calls of many row tiles have
 // their keys decoded once, elsewhere (kDirectTiles in fa_four_api.cu).  36 rows over 64
-// sequences of up to 8191 keys: 243 us, decoded elsewhere first 627 (16 bits: 176).
+// sequences of up to 8191 keys: 243 to 260 us, decoded elsewhere first 627 (16 bits:
+// 176).  Of 259 us, and 514 for two tiles, parts left out in a copy of the kernel leave:
+// the numbers' conversions and products 215 and 421, the loads 194 and 386, both and
+// the stores 121 and 279.  What the two warps do decides, and its parts come in turn,
+// not beside each other.
 // (Four more warps for it leave 128 registers a thread; moved between the roles they
 // spilled in the issuing threads' loops: 241, and 345 instead of 387 for 32 tiles.
-// The bytes' way is not what it waits for: beside 247, copied by blocks into shared
-// memory a block ahead 242, by 16 bytes 289; a row's loads as soon as it is decoded
-// 257; whole rows by neighbouring lanes 262.)
+// Other ways of the bytes, beside 247: copied by blocks into shared memory a block
+// ahead 242, by 16 bytes 289; a row's loads as soon as it is decoded 257; whole rows by
+// neighbouring lanes 262.)
 //
 // Every mbarrier wait is bounded; a wait that runs out records the site in
 // this file's status word, raises the CTA's abort flag, and every role drains
