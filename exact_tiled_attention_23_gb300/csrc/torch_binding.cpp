@@ -480,7 +480,8 @@ struct Turn {
         const c10::cuda::CUDAGuard guard(first.device());
         for (int i = 0; i < 2; ++i) {
             if (!x[i].defined()) continue;
-            if (!followable(x[i])) x[i] = x[i].clone(at::MemoryFormat::Contiguous);
+            // (a tangent of zeros may have no memory)
+            if (x[i]._is_zerotensor() || !followable(x[i])) x[i] = x[i].clone(at::MemoryFormat::Contiguous);
             y[i] = at::empty(x[i].sizes(), at::TensorOptions().dtype(x[i].scalar_type()).device(x[i].device()));
             in[i] = rows_of(x[i]);
             out[i] = rows_of(y[i]);

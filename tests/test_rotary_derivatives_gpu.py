@@ -89,3 +89,14 @@ def test_the_gradient_of_a_tangent():
         up = torch.randn_like(q)
         gq, gt = torch.autograd.grad((r.primal, r.tangent), (q, tq), (up, 2 * up))
     assert torch.equal(gq, back(up, freq, how)) and torch.equal(gt, back(2 * up, freq, how))
+
+
+def test_tangents_that_have_no_memory():
+    """Zeros that torch keeps without memory turn into zeros."""
+    q, _, k, tk, freq, how = made(BF16, False)
+    want = fa.rotary(tk, freq, **how)
+    with fwd.dual_level():
+        zeros = torch._efficientzerotensor(q.shape, dtype=q.dtype, device=q.device)
+        a, b = fa.rotary(fwd.make_dual(q, zeros), freq, k=fwd.make_dual(k, tk), **how)
+        t = fwd.unpack_dual(a).tangent
+        assert (t is None or not t.any()) and torch.equal(fwd.unpack_dual(b).tangent, want)
