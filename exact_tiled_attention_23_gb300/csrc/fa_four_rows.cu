@@ -32,9 +32,9 @@
 // memory and control.  No unit is full: 59 % of the issue slots, 51 % of the integer pipe
 // and two thirds of DRAM are used.  12 us are spent before the first and behind the last
 // keys.  fp16 queries, with a second product per value, take 73 and 40 us; D = 256, with
-// chunks of 16 keys, 161 and 85 (16 bits: 330 and 170), in fp16 171 and 91.  Not kept: a step's scores beside the values of the step
-// before (71 us), two accumulators per score (68), 16 or 14 warps an SM instead of 12
-// (68, 74).
+// chunks of 16 keys, 161 and 85 (16 bits: 330 and 170), in fp16 171 and 91.  Not kept: a
+// step's scores beside the values of the step before (71 us), two accumulators per score
+// (68), 16 or 14 warps an SM instead of 12 (68, 74).
 #include "fa_four.cuh"
 #include "fa_four_rows.h"
 #include "fa_paged_line.cuh"
